@@ -32,7 +32,8 @@ ZS_FUSED_AUTO, ZS_FUSED_LDG, ZS_FUSED_TMA = 0, 1, 2
 ZS_BUCKETS_ONE_WALK, ZS_BUCKETS_PER_BUCKET = 0, 1
 ZS_LAYOUT_FSDP1, ZS_LAYOUT_FSDP2 = 0, 1
 ZS_DEVERR_NONE, ZS_DEVERR_PRODUCER_WAIT, ZS_DEVERR_CONSUMER_WAIT, ZS_DEVERR_SELFTEST = 0, 1, 2, 3
-ZS_DEVERR_GATHER_WAIT = 4
+ZS_DEVERR_GATHER_WAIT, ZS_DEVERR_MATMUL_WAIT = 4, 5
+ZS_Q8_BLOCK, ZS_Q8_MAX_PARTIALS = 128, 608
 
 c_i32, c_i64, c_f32, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 P_i64 = ctypes.POINTER(c_i64)
@@ -47,6 +48,10 @@ class ZsError(RuntimeError):
 
 class zs_adamw_hparams(ctypes.Structure):
     _fields_ = [("lr", c_f32), ("beta1", c_f32), ("beta2", c_f32), ("eps", c_f32), ("weight_decay", c_f32)]
+
+
+class zs_q8(ctypes.Structure):
+    _fields_ = [("codes", c_vp), ("scales", c_vp), ("ld", c_i64), ("ld_scales", c_i64)]
 
 
 def _sig(name, args, res=c_i32):
@@ -106,6 +111,15 @@ _sig("zs_set_fused_variant", [c_i32])
 _sig("zs_set_dependent_launch", [c_i32])
 _sig("zs_device_status", [ctypes.POINTER(ctypes.c_uint32), c_i32])
 _sig("zs_selftest_wait_timeout", [c_i64, c_vp])
+_sig("zs_q8_encode", [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp])
+_sig("zs_q8_decode", [c_vp, c_i64, c_i64, c_vp, c_i64, c_vp])
+_sig("zs_q8_transpose", [c_vp, c_i64, c_i64, c_vp, c_vp])
+_sig("zs_q8_matmul", [c_vp, c_vp, c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_i64, c_vp])
+_sig("zs_rmsnorm_q8", [c_vp, c_i64, c_vp, c_i64, c_vp, c_f32, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp])
+_sig("zs_rmsnorm_backward", [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp,
+                             c_f32, c_i32, c_vp, c_i64, c_vp])
+_sig("zs_swiglu_q8", [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp])
+_sig("zs_swiglu_backward_q8", [c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp])
 
 EXPORTED = [
     "zs_plan_create", "zs_plan_destroy", "zs_plan_info", "zs_plan_unit", "zs_plan_bucket",
@@ -117,7 +131,8 @@ EXPORTED = [
     "zs_checkpoint_save", "zs_checkpoint_load", "zs_zero2_step_host_noalloc", "zs_all_reduce_mean",
     "zs_dp_step", "zs_plan_create_fsdp2", "zs_plan_layout", "zs_plan_param_rows", "zs_plan_pad_ranges",
     "zs_fsdp2_chunk_cat", "zs_fsdp2_copy_out", "zs_fused_step_buckets", "zs_set_dependent_launch",
-    "zs_rank_shard_step", "zs_fused_step_accumulate",
+    "zs_rank_shard_step", "zs_fused_step_accumulate", "zs_q8_encode", "zs_q8_decode", "zs_q8_transpose",
+    "zs_q8_matmul", "zs_rmsnorm_q8", "zs_rmsnorm_backward", "zs_swiglu_q8", "zs_swiglu_backward_q8",
 ]
 
 
@@ -626,3 +641,152 @@ def zs_selftest_wait_timeout(limit_cycles, stream=None):
 
 __all__ = ["Plan", "ZsError", "zs_adamw_hparams", "LIB_PATH"] + EXPORTED + [
     n for n in dir() if n.startswith("ZS_")]
+
+
+# ------------------------------------------------------------------ 8-bit training operators
+#
+# An 8-bit matrix is a pair (codes, scales): codes a CUDA tensor [rows, cols] of one byte per value
+# (uint8 or float8_e4m3fn), rows 16 bytes apart or a multiple; scales [rows, ceil(cols / 128)] (uint8 or
+# float8_e8m0fnu).  Both may be views (row or column ranges) of larger ones.  bf16 matrices are CUDA
+# tensors [rows, cols] whose rows are contiguous.
+
+def q8_empty(rows, cols, device="cuda"):
+    """An 8-bit matrix (codes, scales) of rows x cols to write into: rows of codes padded to 16 bytes."""
+    import torch
+    codes = torch.empty((rows, max(16, (cols + 15) // 16 * 16)), dtype=torch.uint8, device=device)[:, :cols]
+    scales = torch.empty((rows, (cols + ZS_Q8_BLOCK - 1) // ZS_Q8_BLOCK), dtype=torch.uint8, device=device)
+    return codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu)
+
+
+def _row_distance(x, rows, cols, size, what):
+    """Checks a CUDA matrix of rows x cols with contiguous rows; the elements between its rows."""
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+        raise ValueError("%s must be %d x %d, not %s" % (what, rows, cols, tuple(x.shape)))
+    if x.element_size() != size:
+        raise ValueError("%s must have %d-byte elements" % (what, size))
+    ld, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s must have contiguous rows" % what)
+    if rows < 2:
+        return max(ld, cols)                 # one row: its distance is never used
+    if ld < cols:
+        raise ValueError("%s: rows overlap" % what)
+    return ld
+
+
+def _bf16(x, rows, cols, what):
+    import torch
+    if x.dtype is not torch.bfloat16:
+        raise ValueError("%s must be bfloat16" % what)
+    return x.data_ptr(), _row_distance(x, rows, cols, 2, what)
+
+
+def _vector(x, n, size, what):
+    if x is None:
+        return None
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if not x.is_contiguous() or x.element_size() != size or x.numel() != n:
+        raise ValueError("%s must be %d contiguous %d-byte elements" % (what, n, size))
+    return x.data_ptr()
+
+
+def _q8(q, rows, cols, what):
+    """A zs_q8 of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
+    if q is None:
+        return None
+    codes, scales = q
+    ld = _row_distance(codes, rows, cols, 1, what + " codes")
+    if rows < 2:
+        ld = (ld + 15) // 16 * 16
+    lds = _row_distance(scales, rows, (cols + ZS_Q8_BLOCK - 1) // ZS_Q8_BLOCK, 1, what + " scales")
+    return ctypes.byref(zs_q8(codes.data_ptr(), scales.data_ptr(), ld, lds))
+
+
+def _shape(x, what):
+    if x.dim() != 2:
+        raise ValueError("%s must be a matrix" % what)
+    return x.shape
+
+
+def zs_q8_encode(x, q=None, q_t=None, stream=None):
+    """x (bf16 [rows, cols]) in 8 bits: as it is into q, transposed into q_t ([cols, rows])."""
+    rows, cols = _shape(x, "x")
+    p, ld = _bf16(x, rows, cols, "x")
+    return _check(_lib.zs_q8_encode(p, ld, rows, cols, _q8(q, rows, cols, "q"), _q8(q_t, cols, rows, "q_t"),
+                                    _stream(stream)))
+
+
+def zs_q8_decode(q, y, stream=None):
+    """The values of q into y (bf16, same shape)."""
+    rows, cols = _shape(y, "y")
+    p, ld = _bf16(y, rows, cols, "y")
+    return _check(_lib.zs_q8_decode(_q8(q, rows, cols, "q"), rows, cols, p, ld, _stream(stream)))
+
+
+def zs_q8_transpose(q, q_t, stream=None):
+    """q ([rows, cols]) encoded again as its transpose q_t ([cols, rows])."""
+    rows, cols = _shape(q[0], "q")
+    return _check(_lib.zs_q8_transpose(_q8(q, rows, cols, "q"), rows, cols, _q8(q_t, cols, rows, "q_t"),
+                                       _stream(stream)))
+
+
+def zs_q8_matmul(a, b, out, scale=1.0, first=True, stream=None):
+    """out (bf16 [m, n]) = (0 if first else out) + scale * a b^T for 8-bit a ([m, k]) and b ([n, k])."""
+    m, n = _shape(out, "out")
+    k = _shape(a[0], "a")[1]
+    p, ld = _bf16(out, m, n, "out")
+    return _check(_lib.zs_q8_matmul(_q8(a, m, k, "a"), _q8(b, n, k, "b"), m, n, k, float(scale), 1 if first else 0, p, ld,
+                                    _stream(stream)))
+
+
+def zs_rmsnorm_q8(x, residual, weight, eps, y, s=None, rstd=None, s_q8=None, stream=None):
+    """RMS norm of x + residual (residual may be None) in 8 bits into y; the sum into s (bf16) and s_q8
+    (8 bits), the rows' reciprocal norms into rstd (fp32), each when given."""
+    rows, cols = _shape(x, "x")
+    px, ldx = _bf16(x, rows, cols, "x")
+    pr, ldr = (None, 0) if residual is None else _bf16(residual, rows, cols, "residual")
+    ps, lds = (None, 0) if s is None else _bf16(s, rows, cols, "s")
+    return _check(_lib.zs_rmsnorm_q8(px, ldx, pr, ldr, _vector(weight, cols, 2, "weight"), float(eps), rows, cols,
+                                     _q8(y, rows, cols, "y"), ps, lds, _q8(s_q8, rows, cols, "s_q8"),
+                                     _vector(rstd, rows, 4, "rstd"), _stream(stream)))
+
+
+def zs_rmsnorm_backward(dy, s, weight, rstd, dx, dw, partials, ds=None, scale=1.0, first=True, stream=None):
+    """Backward pass of zs_rmsnorm_q8.  s: the sum, a bf16 matrix or an 8-bit pair; partials: fp32 scratch
+    [n, cols]; ds: gradient reaching the sum past the norm, added to dx."""
+    rows, cols = _shape(dy, "dy")
+    py, ldy = _bf16(dy, rows, cols, "dy")
+    if isinstance(s, tuple):
+        ps, lds, qs = None, 0, _q8(s, rows, cols, "s")
+    else:
+        (ps, lds), qs = _bf16(s, rows, cols, "s"), None
+    pd, ldd = (None, 0) if ds is None else _bf16(ds, rows, cols, "ds")
+    px, ldx = _bf16(dx, rows, cols, "dx")
+    n = _shape(partials, "partials")[0]
+    return _check(_lib.zs_rmsnorm_backward(
+        py, ldy, ps, lds, qs, _vector(weight, cols, 2, "weight"), _vector(rstd, rows, 4, "rstd"), pd, ldd, rows, cols,
+        px, ldx, _vector(dw, cols, 2, "dw"), float(scale), 1 if first else 0, _vector(partials, n * cols, 4, "partials"),
+        n, _stream(stream)))
+
+
+def zs_swiglu_q8(gate, up, h, gate_q=None, up_q=None, stream=None):
+    """h = gate * sigmoid(gate) * up in 8 bits; gate and up kept in 8 bits where gate_q, up_q are given."""
+    rows, cols = _shape(gate, "gate")
+    pg, ldg = _bf16(gate, rows, cols, "gate")
+    pu, ldu = _bf16(up, rows, cols, "up")
+    return _check(_lib.zs_swiglu_q8(pg, ldg, pu, ldu, rows, cols, _q8(h, rows, cols, "h"),
+                                    _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), _stream(stream)))
+
+
+def zs_swiglu_backward_q8(dh, gate_q, up_q, dgate=None, dup=None, dgate_t=None, dup_t=None, h_t=None, stream=None):
+    """Backward pass of zs_swiglu_q8 from the kept gate and up: the gradients in 8 bits as they are and
+    transposed, and h recomputed and transposed, each where given."""
+    rows, cols = _shape(dh, "dh")
+    p, ld = _bf16(dh, rows, cols, "dh")
+    return _check(_lib.zs_swiglu_backward_q8(
+        p, ld, _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), rows, cols,
+        _q8(dgate, rows, cols, "dgate"), _q8(dup, rows, cols, "dup"), _q8(dgate_t, cols, rows, "dgate_t"),
+        _q8(dup_t, cols, rows, "dup_t"), _q8(h_t, cols, rows, "h_t"), _stream(stream)))

@@ -1995,4 +1995,11 @@ cudaError_t read_device_error(unsigned int* out, bool clear) {
     return cudaMemcpyToSymbol(g_zs_device_error, &zero, sizeof(unsigned int));
 }
 
+cudaError_t device_error_word(unsigned int** out) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_zs_device_error);
+    *out = (unsigned int*)p;
+    return e;
+}
+
 }  // namespace zs

@@ -179,6 +179,8 @@ cudaError_t launch_dp_tma(const BView& g, const BView& out, float* const* master
 cudaError_t launch_dp_step(const BView& g, const BView& out, float* const* master, float* const* m, float* const* v,
                            const Range& r, const AdamScalars& s, int nd, cudaStream_t st);
 cudaError_t read_device_error(unsigned int* out, bool clear);
+// Device address of the current device's status word, for kernels of other translation units.
+cudaError_t device_error_word(unsigned int** out);
 
 // Which fused kernel zs_fused_step / zs_zero3_rs_step_unit use (ZS_FUSED_*).
 void set_fused_variant(int v);

@@ -52,7 +52,8 @@
  *             use a second stream order it after the first with events.  The
  *             checkpoint calls are the exception: they synchronise their stream
  *             and return with the data in place.  A plan owns host tables only.
- * Alignment.  Every device pointer must be 16-byte aligned.
+ * Alignment.  Every device pointer must be 16-byte aligned, unless a call says
+ *             otherwise.
  * Aliasing.   Inputs and outputs must not overlap unless a call says so.
  * Step.       The AdamW step t is 1-based.
  * Errors.     Every entry point returns ZS_OK or a negative status.  Argument
@@ -112,6 +113,7 @@ extern "C" {
 #define ZS_DEVERR_CONSUMER_WAIT 2u   /* a staged kernel's consumer gave up waiting for its data     */
 #define ZS_DEVERR_SELFTEST      3u   /* zs_selftest_wait_timeout ran its wait out (expected)         */
 #define ZS_DEVERR_GATHER_WAIT   4u   /* a bulk-store gather gave up waiting for its tile             */
+#define ZS_DEVERR_MATMUL_WAIT   5u   /* zs_q8_matmul gave up waiting for a tile or an accumulator    */
 
 typedef struct zs_plan_s* zs_plan_t;
 
@@ -594,6 +596,130 @@ int zs_zero3_step(zs_plan_t plan, void* shards, float* master, float* m, float* 
                   const void* const* unit_grads, void* const* pool, int32_t pool_slots,
                   int32_t reshard_after_forward, const zs_adamw_hparams* hp, int64_t step,
                   void* main_stream, void* side_stream);
+
+/* ------------------------------------------------------------------ 8-bit training operators
+ *
+ * What a unit's forward and backward pass run between zs_zero3_gather_unit and
+ * zs_zero3_rs_step_unit, with activations, weights and gradients of the matrix
+ * products in 8 bits and what the backward pass needs kept in 8 bits.  One
+ * format serves all of it: the norm's output is the next product's operand and
+ * the kept activation at once.
+ *
+ * Format (zs_q8).  A matrix of `rows` x `cols` values is
+ *     codes   one e4m3 byte per value, codes[r * ld + c]
+ *     scales  one e8m0 byte per row and block of ZS_Q8_BLOCK columns,
+ *             scales[r * ld_scales + c / ZS_Q8_BLOCK]; byte b stands for 2^(b - 127)
+ *     value   = e4m3(code) * 2^(scale - 127)
+ * Encoding a block of fp32 values: e is the smallest integer >= -127 with
+ * max|value| <= 448 * 2^e over the block's finite values (-127 when there are
+ * none but zeros), the scale byte is e + 127 and each code is value * 2^-e
+ * rounded to nearest even.  Scales are powers of two so the multiplication is
+ * exact, and so that a kept matrix can be encoded again along its other
+ * direction with no loss but what falls below the new block's smallest normal
+ * code.  NaN and infinities encode as the e4m3 NaN (0x7f or 0xff) and leave
+ * their block's scale alone; a scale byte of 255 stands for NaN and is read as
+ * such, never written.
+ *   ld         bytes between rows of codes: >= cols and a multiple of 16;
+ *              codes 16-byte aligned (so a matrix may be a column range of a
+ *              larger one that starts at a multiple of 16).
+ *   ld_scales  bytes between rows of scales, >= ceil(cols / ZS_Q8_BLOCK).
+ * Only the rows x cols codes and their scales are read or written.
+ *
+ * bf16 matrices are given by a 2-byte aligned pointer and the elements between
+ * rows (>= cols): views into flat parameter and gradient buffers at any
+ * element.  Kernels move 16 bytes per access where pointer and row distance
+ * are multiples of 16 bytes and single elements elsewhere.  Sums are fp32.
+ * rows and cols are at most 2^31 - 256; cols >= 1; rows = 0 is an empty matrix
+ * (nothing is read or written unless a call says so).  Inputs and outputs must
+ * not overlap unless a call says so.  The calls only enqueue work on `stream`,
+ * allocate nothing and give the same bits whenever they are repeated.
+ * Errors: ZS_ERR_INVALID (nothing enqueued), ZS_ERR_CUDA. */
+#define ZS_Q8_BLOCK 128
+
+typedef struct {
+    void* codes;
+    void* scales;
+    int64_t ld;
+    int64_t ld_scales;
+} zs_q8;
+
+/* A bf16 matrix x (rows x cols, ldx) in 8 bits: as it is into q and transposed
+ * (cols x rows, blocks of 128 along x's rows) into q_t, in one pass over x; either
+ * may be NULL.  The two are the forward and the input-gradient operand of a
+ * weight, or the input- and weight-gradient operand of an output gradient. */
+int zs_q8_encode(const void* x, int64_t ldx, int64_t rows, int64_t cols, const zs_q8* q, const zs_q8* q_t,
+                 void* stream);
+
+/* The values of q (rows x cols) as bf16 (e4m3 values times a power of two are
+ * bf16 values; only what falls below bf16's subnormals is rounded). */
+int zs_q8_decode(const zs_q8* q, int64_t rows, int64_t cols, void* y, int64_t ldy, void* stream);
+
+/* q (rows x cols) encoded again as its transpose q_t (cols x rows, blocks of 128
+ * along q's rows): a kept activation as the weight gradient's operand. */
+int zs_q8_transpose(const zs_q8* q, int64_t rows, int64_t cols, const zs_q8* q_t, void* stream);
+
+/* Product of two 8-bit matrices over their common columns: with a (m x k) and
+ * b (n x k),
+ *     out[i][j] = bf16( (first ? 0 : out[i][j]) + scale * sum over l of a[i][l] * b[j][l] )
+ * with an fp32 sum (out is only written when first != 0).  Forward: a = the
+ * activations, b = the weight (out features x in features).  Input gradient:
+ * a = the output gradient, b = the weight's transpose.  Weight gradient: a =
+ * the output gradient's transpose, b = the activations' transpose, out = the
+ * weight's place in a flat gradient buffer, scale = 1/n_micro and first as in
+ * zs_accumulate_grad (here the running sum and the product are added in fp32
+ * and rounded once).  k = 0 is the empty sum.  out: ldo elements between rows. */
+int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n, int64_t k, float scale, int32_t first,
+                 void* out, int64_t ldo, void* stream);
+
+/* Residual addition and root-mean-square norm, output in 8 bits.  Per row, with
+ * t = fp32(x) + fp32(residual) (t = fp32(x) when residual is NULL):
+ *     r = 1 / sqrt( mean over columns of t^2 + eps )
+ *     y = t * r * weight  in 8 bits
+ *     s = bf16(t), s_q8 = t in 8 bits, rstd = r     (each only when not NULL)
+ * weight: cols bf16 values; rstd: rows floats; eps >= 0, finite.  s may be x or
+ * residual (same row distance). */
+int zs_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, float eps,
+                  int64_t rows, int64_t cols, const zs_q8* y, void* s, int64_t lds, const zs_q8* s_q8,
+                  float* rstd, void* stream);
+
+/* Backward pass of zs_rmsnorm_q8, from the gradient dy of its output, the sum s
+ * (bf16, or s_q8 in 8 bits: exactly one of the two) and rstd.  Per row, with
+ * xh = s * rstd, g = dy * weight and c = mean over columns of g * xh:
+ *     dx = bf16( rstd * (g - xh * c) + ds )
+ *     dw = bf16( (first ? 0 : dw) + scale * sum over rows of dy * xh )
+ * dx is the gradient of x and of residual alike; ds (NULL: none) is the gradient
+ * that reaches the sum past the norm.  dw (cols bf16 values, e.g. the weight's
+ * place in a flat gradient buffer) takes scale and first as zs_q8_matmul's out;
+ * with rows = 0 it gets the empty sum.
+ *   partials    caller's scratch: n_partials x cols floats, 16-byte aligned; the
+ *               sum over rows is formed in up to n_partials pieces (at most
+ *               ZS_Q8_MAX_PARTIALS are used; fewer make the call slower), added
+ *               in a fixed order.
+ * dx may be dy or ds (same row distance). */
+#define ZS_Q8_MAX_PARTIALS 608
+int zs_rmsnorm_backward(const void* dy, int64_t lddy, const void* s, int64_t lds, const zs_q8* s_q8,
+                        const void* weight, const float* rstd, const void* ds, int64_t ldds, int64_t rows,
+                        int64_t cols, void* dx, int64_t lddx, void* dw, float scale, int32_t first, float* partials,
+                        int64_t n_partials, void* stream);
+
+/* h = gate * sigmoid(gate) * up in 8 bits, and gate and up kept in 8 bits for the
+ * backward pass (gate_q and up_q: NULL when not wanted).  gate and up (rows x cols)
+ * may be the two halves of one product's result. */
+int zs_swiglu_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64_t rows, int64_t cols,
+                 const zs_q8* h, const zs_q8* gate_q, const zs_q8* up_q, void* stream);
+
+/* Backward pass of zs_swiglu_q8 from the kept gate and up and the gradient dh
+ * (bf16) of h, with p = sigmoid(gate):
+ *     dgate = dh * up * p * (1 + gate * (1 - p)),   dup = dh * gate * p
+ * each in 8 bits as it is (dgate, dup: rows x cols, the input gradient's operands)
+ * and transposed (dgate_t, dup_t: cols x rows, the weight gradient's), and h
+ * itself, recomputed from the kept values, transposed (h_t: the weight-gradient
+ * operand of the layer after).  Outputs that are NULL are not written; at least
+ * one is not.  dgate and dup may be the column halves of one matrix when cols is
+ * a multiple of 128, dgate_t and dup_t the row halves of one at any size. */
+int zs_swiglu_backward_q8(const void* dh, int64_t lddh, const zs_q8* gate_q, const zs_q8* up_q, int64_t rows,
+                          int64_t cols, const zs_q8* dgate, const zs_q8* dup, const zs_q8* dgate_t,
+                          const zs_q8* dup_t, const zs_q8* h_t, void* stream);
 
 #ifdef __cplusplus
 }
