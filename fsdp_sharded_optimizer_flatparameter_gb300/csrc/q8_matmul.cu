@@ -20,7 +20,6 @@ namespace zs {
 
 namespace {
 
-constexpr int kMmThreads = 256;
 constexpr int kMaxDevices = 64;
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -99,6 +98,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// One thread of a converged warp.  The product and copy roles run as whole warps, and only their issue is
+// one thread's: what the instructions take then sits in uniform registers.  (With the role's loop run by
+// lane 0 alone, issuing one block's four products took 350 cycles instead of well under the 450 they run.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 // Every thread of the cluster; orders shared-memory writes before it against reads after it.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -134,6 +141,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* b, uint32_t parity, 
     }
     return true;
 }
+// A whole warp waits, and agrees on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, long long limit) {
+    return __all_sync(~0u, mbar_wait(b, parity, limit));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* b, uint32_t parity, long long limit) {
+    return __all_sync(~0u, mbar_wait_cluster(b, parity, limit));
+}
 // tma_load whose bytes count on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -163,21 +177,65 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         : "memory");
 }
 
-// 32 columns of this warp's 32 accumulator rows.
-__device__ __forceinline__ void tmem_load32(uint32_t tmem, float (&f)[32]) {
-    uint32_t r[32];
+// 16 columns of this warp's 32 accumulator rows.
+__device__ __forceinline__ void tmem_load16(uint32_t tmem, float (&f)[16]) {
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(tmem));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
+
+// Writes 16 columns of 32 rows of the result, one row per lane in f: row r of the warp at out + r * ldo.
+// `rows` and `n` are what is valid of them (the same in every lane).  With `align` 32 or 16, rows start at
+// multiples of that many bytes and a lane stores its own segment (a full sector at 32).  Otherwise the
+// values go through 2 KB of the warp's shared memory, so that neighbouring lanes store neighbouring
+// columns: one 2-byte store per lane and row cost 15 of 27 us for 160 x 339 x 4096.
+__device__ __forceinline__ void store_rows16(uint16_t* out, int64_t ldo, const float (&f)[16], int rows, int n, int align,
+                                             float scale, int first, float* stage) {
+    const int lane = threadIdx.x & 31;
+    if (rows <= 0 || n <= 0) return;
+    if (align && n >= 16) {
+        if (lane >= rows) return;
+        uint16_t* o = out + lane * ldo;
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint4* v = reinterpret_cast<uint4*>(o);
+        if (!first) {
+            const uint4 x = v[0], y = v[1];
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(fmaf(f[2 * j], scale, bf16_lo(w[j])), fmaf(f[2 * j + 1], scale, bf16_hi(w[j])));
+        if (align == 32) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        } else {
+            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 16 + (j ^ (lane & 15))] = f[j];
+    __syncwarp();
+    const int c = lane & 15;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (r < rows && c < n) {
+            uint16_t* o = out + r * ldo + c;
+            o[0] = f32_to_bf16(fmaf(stage[r * 16 + (c ^ (r & 15))], scale, first ? 0.f : bf16_to_f32(o[0])));
+        }
+    }
+    __syncwarp();
+}
+constexpr int kStoreStage = 32 * 16;             // floats of shared memory per storing warp
 
 // Position in a ring of stages: the stage and how often the ring has gone round.
 struct Ring {
@@ -196,51 +254,41 @@ struct MmArgs {
     const uint8_t *sp, *sq;      // scales of the P and Q operands
     int64_t ldsp, ldsq;
     int rows_p, rows_q;          // valid rows
-    int kblocks, blocks;         // 128-column blocks of the sum (the products stop at the last; scales exist for it)
-    int tiles_q;                 // tiles of Q: tile t is P tile t / tiles_q, Q tile t % tiles_q
+    int kblocks;                 // 128-column blocks of the sum
+    int tiles_q;                 // tiles of Q
+    int split;                   // CTAs that share a tile's sum
     uint16_t* out;
     int64_t ldo;
     int transposed;              // 0: out[p][q], 1: out[q][p]
-    int wide;                    // rows of out take 16-byte stores
+    int align;                   // rows of out start at multiples of 32 or 16 bytes; 0: neither
     float scale;
     int first;
     unsigned int* error;
     long long wait_limit;
 };
 
-template <int BN, int STAGES>
-struct MmShape {
-    static constexpr int kStageBytes = 128 * 128 + BN * 128;
-    static constexpr int kQChunks = (BN + 127) / 128;
-    static constexpr int kScaleBytes = 512 * (1 + kQChunks);
-    static constexpr int kScaleCols = 4 * (1 + kQChunks);
-    static constexpr int kTmemCols = BN + 2 * kScaleCols <= 32 ? 32 : BN + 2 * kScaleCols <= 64 ? 64
-                                     : BN + 2 * kScaleCols <= 128 ? 128 : BN + 2 * kScaleCols <= 256 ? 256 : 512;
-    static constexpr int kSmem = 1024 + STAGES * kStageBytes + 2 * kScaleBytes + 256;
-};
-
-// One row's scale bytes, kBatch groups of four blocks at a time.  Rows of scales start at any byte, so a
-// group is cut out of two neighbouring aligned words; every word is loaded once.  Words that reach over
-// either end of the matrix of scales are put together from its bytes.  Blocks past the row's last give
-// scale byte 0, and so do rows past the matrix (their codes read as 0).
+// One row's scale bytes, kBatch groups of four blocks (16 bytes) at a time.  Rows of scales start at any
+// byte, so a batch is cut out of two neighbouring aligned 16-byte chunks, and every chunk is loaded once:
+// the lanes of a warp read different rows, a line each, and such loads share the shared memory's bandwidth,
+// which the products and the tiles' arrival need nearly all of.  (A 4-byte load per group: 333 us for
+// 8192^3.)  Chunks that reach over either end of the matrix of scales are put together from its
+// bytes.  Blocks past the row's last give scale byte 0, and so do rows past the matrix (their codes read
+// as 0).
 constexpr int kBatch = 4;
 struct ScaleRow {
-    const uint8_t *at, *lo, *hi;     // word to load next; the matrix of scales
-    uint32_t w[kBatch + 1], shift;
+    const uint8_t *at, *lo, *hi;     // chunk to load next; the matrix of scales
+    uint4 c0, c1;
+    uint32_t off;                    // bytes of c0 before the batch
     int left;                        // blocks from the current batch on
-    __device__ __forceinline__ uint32_t load() {
+    __device__ __forceinline__ uint4 load() {
         const uint8_t* p = at;
-        at += 4;
-        if (p >= lo && p + 4 <= hi) return *reinterpret_cast<const uint32_t*>(p);
-        uint32_t x = 0;
+        at += 16;
+        if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4*>(p);
+        uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (p + k >= lo && p + k < hi) x |= (uint32_t)p[k] << (8 * k);
-        return x;
-    }
-    __device__ __forceinline__ void fill() {                 // w[1 ..], after w[0]
-#pragma unroll
-        for (int j = 1; j <= kBatch; ++j) w[j] = left > 4 * (j - 1) ? load() : 0;
+        for (int k = 0; k < 16; ++k)
+            if (p + k >= lo && p + k < hi) x[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+        return make_uint4(x[0], x[1], x[2], x[3]);
     }
     // Row `row` of s from block `first` on, `blocks` of them; the rows have `all`.
     __device__ __forceinline__ void start(const uint8_t* s, int64_t ld, int64_t row, int rows, int first, int blocks, int all) {
@@ -248,47 +296,83 @@ struct ScaleRow {
         lo = s;
         hi = left ? s + (int64_t)(rows - 1) * ld + all : s;
         const uint8_t* p = left ? s + row * ld + first : s;
-        shift = (uint32_t)((uintptr_t)p & 3) * 8;
-        at = (const uint8_t*)((uintptr_t)p & ~(uintptr_t)3);
-        w[0] = load();
-        fill();
+        off = (uint32_t)((uintptr_t)p & 15);
+        at = (const uint8_t*)((uintptr_t)p & ~(uintptr_t)15);
+        c0 = load();
+        c1 = (int)(16 - off) < left ? load() : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ uint32_t take(int j) const {
-        const uint32_t x = __funnelshift_r(w[j], w[j + 1], shift);
-        const int n = left - 4 * j;
-        return n >= 4 ? x : n > 0 ? x & ((1u << (8 * n)) - 1) : 0;
+    __device__ __forceinline__ void take(uint32_t (&w)[kBatch]) const {
+        uint32_t x[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        if (off & 8) {
+#pragma unroll
+            for (int k = 0; k < 6; ++k) x[k] = x[k + 2];
+        }
+        if (off & 4) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k) x[k] = x[k + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int n = left - 4 * k;
+            const uint32_t v = __funnelshift_r(x[k], x[k + 1], 8 * (off & 3));
+            w[k] = n >= 4 ? v : n > 0 ? v & ((1u << (8 * n)) - 1) : 0;
+        }
     }
     __device__ __forceinline__ void advance() {
         left -= 4 * kBatch;
-        w[0] = w[kBatch];
-        fill();
+        c0 = c1;
+        if ((int)(16 - off) < left) c1 = load();
     }
 };
 
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int64_t row, int rows, int group, int blocks) {
-    if (row >= rows) return 0;
-    const uint8_t* p = s + row * ld + group * 4;
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (group * 4 + k < blocks) w |= (uint32_t)p[k] << (8 * k);
-    return w;
+// ------------------------------------------------------------------ small products: the sum split over a cluster
+
+// Tile of 128 P rows x BN Q rows; the blocks of the sum are split over the CTAs of a cluster, so that a
+// product with few tiles (few rows, a weight of a few thousand) still loads through every SM.  Each CTA
+// keeps its part in tensor memory; the parts meet in shared memory, where every CTA adds one share of the
+// tile's columns over all CTAs in rank order (the same bits in every run) and writes it.  No workspace and
+// no second launch.  About 100 KB per CTA, so that one CTA's start and end overlap another's loads.
+constexpr int kSplitThreads = 320;
+constexpr int kSplitMost = 8;        // CTAs of a cluster
+template <int BN, int STAGES>
+struct SplitShape {
+    static constexpr int kStageBytes = 128 * 128 + BN * 128;
+    static constexpr int kScaleBytes = 1024;
+    static constexpr int kScaleCols = 8;
+    static constexpr int kTmemCols = BN + kBatch * kScaleCols <= 64 ? 64 : BN + kBatch * kScaleCols <= 128 ? 128 : 256;
+    static constexpr int kSmem = 1024 + STAGES * kStageBytes + 2 * kBatch * kScaleBytes + 256;
+    static_assert(BN * 512 <= STAGES * kStageBytes, "the parts meet where the tiles were");
+    static_assert(BN % 16 == 0 && BN <= 128, "one chunk of scales");
+    static_assert(2 * kBatch * kScaleBytes >= 4 * kStoreStage * 4, "staging of the stores");
+};
+
+__device__ __forceinline__ float cluster_ld(uint32_t at) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
+    return x;
 }
 
 template <int BN, int STAGES>
-__global__ void __launch_bounds__(kMmThreads, 1) k_q8_matmul(const __grid_constant__ CUtensorMap map_p,
-                                                             const __grid_constant__ CUtensorMap map_q,
-                                                             const __grid_constant__ MmArgs a) {
-    using S = MmShape<BN, STAGES>;
+__global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __grid_constant__ CUtensorMap map_p,
+                                                                      const __grid_constant__ CUtensorMap map_q,
+                                                                      const __grid_constant__ MmArgs a) {
+    using S = SplitShape<BN, STAGES>;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (su32(raw) & 1023)) & 1023);
     uint8_t* scale_sh = base + STAGES * S::kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(scale_sh + 2 * S::kScaleBytes);
+    float* store_sh = reinterpret_cast<float*>(scale_sh);                        // once the products are done
+    uint64_t* full = reinterpret_cast<uint64_t*>(scale_sh + 2 * kBatch * S::kScaleBytes);
     uint64_t* empty = full + STAGES;
     uint64_t* sfull = empty + STAGES;
     uint64_t* sempty = sfull + 2;
-    uint64_t* done = sempty + 2;                 // the accumulator is complete
+    uint64_t* done = sempty + 2;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+    uint32_t* gave_up = tmem_at + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -297,14 +381,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_q8_matmul(const __grid_consta
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(sfull + i, 1);
+            mbar_init(sfull + i, 4);             // the scale warps
             mbar_init(sempty + i, 1);
         }
         mbar_init(done, 1);
+        *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     dependent_launch_prologue();
-    if (warp == 3) {
+    if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_at)),
                      "r"((uint32_t)S::kTmemCols)
                      : "memory");
@@ -313,128 +398,198 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_q8_matmul(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at;
-    const uint32_t tmem_scales = tmem + BN;
-    const int tp = blockIdx.x / a.tiles_q, tq = blockIdx.x - tp * a.tiles_q;
-    const int p0 = tp * 128, q0 = tq * BN;
-    const int groups = (a.kblocks + 3) / 4;
+    const uint32_t tmem = *tmem_at, tmem_scales = tmem + BN;
+    const int split = a.split, rank = blockIdx.x % split, tile = blockIdx.x / split;
+    const int p0 = tile / a.tiles_q * 128, q0 = tile % a.tiles_q * BN;
+    const int kb0 = (int)((int64_t)a.kblocks * rank / split), kbs = (int)((int64_t)a.kblocks * (rank + 1) / split) - kb0;
+    const int groups = (kbs + 3) / 4;
+    auto fail = [&] {
+        atomicExch(gave_up, 1u);
+        atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
+    };
 
-    if (warp == 0 && lane == 0) {
-        int issued = 0;
-        for (; issued < a.kblocks; ++issued) {
-            const int s = issued % STAGES;
-            if (issued >= STAGES && !mbar_wait(empty + s, ((issued / STAGES) - 1) & 1, a.wait_limit)) {
-                atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
-                for (int k = issued - STAGES; k < issued; ++k)       // let the copies in flight land
-                    mbar_wait(full + k % STAGES, (k / STAGES) & 1, a.wait_limit);
-                break;
-            }
-            uint8_t* at = base + s * S::kStageBytes;
-            mbar_expect_tx(full + s, S::kStageBytes);
-            tma_load(at, &map_p, issued * 128, p0, full + s);
-            tma_load(at + 128 * 128, &map_q, issued * 128, q0, full + s);
-        }
-    } else if (warp == 1 && lane == 0) {
-        const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+    if (warp == 0) {
+        Ring ring;
         bool ok = true;
-        for (int kb = 0; kb < a.kblocks && ok; ++kb) {
-            const int s = kb % STAGES, g = kb >> 2, slot = g & 1;
-            const uint32_t sfa = tmem_scales + slot * S::kScaleCols, sfb = sfa + 4;
-            if ((kb & 3) == 0) {
-                if (!(ok = mbar_wait(sfull + slot, (g >> 1) & 1, a.wait_limit))) break;
-                tc_fence_after();
-                const uint32_t at = su32(scale_sh + slot * S::kScaleBytes);
-                tmem_copy_scales(sfa, scales_desc(at));
-#pragma unroll
-                for (int c = 0; c < S::kQChunks; ++c) tmem_copy_scales(sfb + 4 * c, scales_desc(at + 512 * (1 + c)));
-                mma_commit(sempty + slot);
+        for (int kb = 0; kb < kbs; ++kb) {
+            if (ring.round > 0 && !(ok = warp_wait(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
+            uint8_t* at = base + ring.at * S::kStageBytes;
+            if (elect_one()) {
+                mbar_expect_tx(full + ring.at, S::kStageBytes);
+                tma_load(at, &map_p, (kb0 + kb) * 128, p0, full + ring.at);
+                tma_load(at + 128 * 128, &map_q, (kb0 + kb) * 128, q0, full + ring.at);
             }
-            if (!(ok = mbar_wait(full + s, (kb / STAGES) & 1, a.wait_limit))) break;
-            tc_fence_after();
-            const uint32_t at = su32(base + s * S::kStageBytes);
-            const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * 128);
-            const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_scaled(tmem, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > 0 || k > 0);
-            mma_commit(empty + s);
+            __syncwarp();
+            ring.next(STAGES);
         }
-        if (!ok) atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
-        mma_commit(done);
-    } else if (warp == 2) {
-        for (int g = 0; g < groups; ++g) {
-            const int slot = g & 1;
-            uint32_t w[1 + S::kQChunks][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[0][i] = scale_word(a.sp, a.ldsp, (int64_t)p0 + lane + 32 * i, a.rows_p, g, a.blocks);
-#pragma unroll
-            for (int c = 0; c < S::kQChunks; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = c * 128 + lane + 32 * i;
-                    w[1 + c][i] = r < BN ? scale_word(a.sq, a.ldsq, (int64_t)q0 + r, a.rows_q, g, a.blocks) : 0;
+        if (!ok && lane == 0) fail();
+        const bool wrapped = ring.round > 0;     // let every copy land before the CTA may go on
+        for (int k = 0; k < STAGES; ++k) {
+            if (k < ring.at) warp_wait(full + k, ring.parity(), a.wait_limit);
+            else if (wrapped) warp_wait(full + k, ring.parity() ^ 1, a.wait_limit);
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+        const uint64_t desc0 = operand_desc(su32(base)), sdesc0 = scales_desc(su32(scale_sh));
+        bool ok = true;
+        Ring ring, slots;
+        for (int kb = 0; kb < kbs; ++kb) {
+            const int in = (kb >> 2) & (kBatch - 1);
+            const uint32_t sfa = tmem_scales + in * S::kScaleCols;
+            if ((kb & 3) == 0) {
+                if (in == 0) {
+                    if (!(ok = warp_wait(sfull + slots.at, slots.parity(), a.wait_limit))) break;
+                    tc_fence_after();
                 }
-            bool ok = true;
-            if (g >= 2) ok = mbar_wait(sempty + slot, ((g >> 1) - 1) & 1, a.wait_limit);
-            if (!__all_sync(~0u, ok)) {
-                if (lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
-                break;
+                const bool last = in == kBatch - 1 || kb + 4 >= kbs;
+                if (elect_one()) {
+                    const uint64_t from = sdesc0 + (((slots.at * kBatch + in) * S::kScaleBytes) >> 4);
+                    tmem_copy_scales(sfa, from);
+                    tmem_copy_scales(sfa + 4, from + (512 >> 4));
+                    if (last) mma_commit(sempty + slots.at);
+                }
+                __syncwarp();
+                if (last) slots.next(2);
             }
-            uint4* at = reinterpret_cast<uint4*>(scale_sh + slot * S::kScaleBytes);
+            if (!(ok = warp_wait(full + ring.at, ring.parity(), a.wait_limit))) break;
+            tc_fence_after();
+            const uint64_t da = desc0 + ((ring.at * S::kStageBytes) >> 4), db = da + ((128 * 128) >> 4);
+            const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < 1 + S::kQChunks; ++c) at[c * 32 + lane] = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+                for (int k = 0; k < 4; ++k) mma_scaled(tmem, da + 2 * k, db + 2 * k, id, sfa, sfa + 4, kb > 0 || k > 0);
+                mma_commit(empty + ring.at);
+            }
+            __syncwarp();
+            ring.next(STAGES);
+        }
+        if (!ok && lane == 0) fail();
+        if (ok && elect_one()) mma_commit(done);
+        __syncwarp();
+    } else if (warp < 6) {
+        // thread r of 128: P row r and Q row r of the tile (see the scale copy's layout below)
+        Ring slots;
+        bool ok = true;
+        const int r = threadIdx.x - 64;
+        uint8_t* mine = scale_sh + (r & 31) * 16 + (r >> 5) * 4;
+        ScaleRow row[2];
+        row[0].start(a.sp, a.ldsp, (int64_t)p0 + r, a.rows_p, kb0, kbs, a.kblocks);
+        row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, r < BN ? a.rows_q : 0, kb0, kbs, a.kblocks);
+        for (int g = 0; g < groups; g += kBatch) {
+            if (slots.round > 0 && !(ok = warp_wait(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[kBatch];
+                row[c].take(w);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    *reinterpret_cast<uint32_t*>(mine + (slots.at * kBatch + j) * S::kScaleBytes + c * 512) = w[j];
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(sfull + slot);
+            if (lane == 0) mbar_arrive(sfull + slots.at);
+            slots.next(2);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) row[c].advance();
         }
-    } else if (warp >= 4) {
-        const bool ok = mbar_wait(done, 0, a.wait_limit + a.wait_limit);
-        if (!__all_sync(~0u, ok)) {
-            if (lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
+        if (!ok && lane == 0) fail();
+    } else {
+        const int sub = warp & 3;
+        const uint32_t from = tmem + ((uint32_t)(sub * 32) << 16);
+        if (!warp_wait(done, 0, a.wait_limit)) {
+            if (lane == 0) fail();
         } else {
             tc_fence_after();
-            const int sub = warp - 4;
-            const int64_t p = (int64_t)p0 + sub * 32 + lane;
+            if (split == 1) {
+                const int64_t p = (int64_t)p0 + sub * 32;                        // the warp's first row
+                const int n = a.rows_q - q0, rows = a.rows_p - p < 32 ? (int)(a.rows_p - p) : 32;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                float f[32];
-                if (q0 + c >= a.rows_q) break;
-                tmem_load32(tmem + ((uint32_t)(sub * 32) << 16) + c, f);
-                const int n = a.rows_q - q0 - c < (BN < 32 ? BN : 32) ? a.rows_q - q0 - c : (BN < 32 ? BN : 32);
-                if (p >= a.rows_p) continue;
-                if (a.transposed) {
-                    uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p;
+                for (int c = 0; c < BN; c += 16) {
+                    float f[16];
+                    tmem_load16(from + c, f);
+                    if (a.transposed) {
+                        uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p + lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n) {
-                            const float old = a.first ? 0.f : bf16_to_f32(o[j * a.ldo]);
-                            o[j * a.ldo] = f32_to_bf16(fmaf(f[j], a.scale, old));
-                        }
-                } else {
-                    uint16_t* o = a.out + p * a.ldo + q0 + c;
-                    if (a.wide && n == 32) {
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            float e[8], old[8];
-                            if (!a.first) unpack(BfVec<8>{reinterpret_cast<const uint4*>(o)[v]}, old);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) e[i] = fmaf(f[v * 8 + i], a.scale, a.first ? 0.f : old[i]);
-                            reinterpret_cast<uint4*>(o)[v] = pack(e).w;
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            if (c + j < n && lane < rows)
+                                o[j * a.ldo] = f32_to_bf16(fmaf(f[j], a.scale, a.first ? 0.f : bf16_to_f32(o[j * a.ldo])));
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < n) {
-                                const float old = a.first ? 0.f : bf16_to_f32(o[j]);
-                                o[j] = f32_to_bf16(fmaf(f[j], a.scale, old));
-                            }
+                        store_rows16(a.out + p * a.ldo + q0 + c, a.ldo, f, rows, n - c, a.align, a.scale, a.first,
+                                     store_sh + sub * kStoreStage);
                     }
+                }
+            } else {
+                float* part = reinterpret_cast<float*>(base) + sub * 32 + lane;      // [column][128 rows]
+#pragma unroll 1
+                for (int c = 0; c < BN; c += 16) {
+                    float f[16];
+                    tmem_load16(from + c, f);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * 128] = f[j];
                 }
             }
             tc_fence_before();
         }
     }
+    if (split > 1) {
+        __syncthreads();
+        cluster_sync();
+        bool ok = true;
+        for (int k = 0; k < split; ++k) {
+            uint32_t bad;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad) : "r"(at_rank(gave_up, k)));
+            ok = ok && bad == 0;
+        }
+        const int share = BN / split, c0 = rank * share, n = a.rows_q - q0;
+        if (ok && a.transposed) {
+            // four rows of a column per thread: they are neighbours in out
+            for (int i = threadIdx.x; i < share * 32; i += kSplitThreads) {
+                const int c = c0 + (i >> 5), r = (i & 31) * 4;
+                const int64_t p = (int64_t)p0 + r;
+                if (c >= n || p >= a.rows_p) continue;
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < split; ++k) {
+                    const float4 x = cluster_ld4(at_rank(base + (c * 128 + r) * 4, k));
+                    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                }
+                uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = v[j] * a.scale;
+                if (a.first && ((uintptr_t)o & 7) == 0 && p + 4 <= a.rows_p) {
+                    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (p + j < a.rows_p) o[j] = f32_to_bf16(a.first ? v[j] : v[j] + bf16_to_f32(o[j]));
+                }
+            }
+        } else if (ok) {
+            // 16 columns of a row per thread; the four warps that own staging memory
+            if (warp >= 6) {
+                const int r0 = (warp - 6) * 32;
+                const int64_t p = (int64_t)p0 + r0;
+                const int rows = a.rows_p - p < 32 ? (int)(a.rows_p - p) : 32;
+                for (int c = c0; c < c0 + share; c += 16) {
+                    float f[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] = 0.f;
+                    for (int k = 0; k < split; ++k) {
+                        const uint32_t at = at_rank(base + (c * 128 + r0 + lane) * 4, k);
+                        float x[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = cluster_ld(at + j * 512);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] += x[j];
+                    }
+                    store_rows16(a.out + p * a.ldo + q0 + c, a.ldo, f, rows, n - c, a.align, a.scale, a.first,
+                                 store_sh + (warp - 6) * kStoreStage);
+                }
+            }
+        }
+        cluster_sync();                          // no CTA leaves while another reads its part
+    }
     __syncthreads();
-    if (warp == 3) {
+    if (warp == 2) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kTmemCols));
     }
@@ -442,40 +597,42 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_q8_matmul(const __grid_consta
 
 // ------------------------------------------------------------------ large products: a persistent CTA pair per tile
 
-// Tile of 256 P rows x 256 Q rows per pair of CTAs.  Each CTA loads its 128 P rows and half of the Q rows
-// (32 KB per 128 columns; the tensor cores read the other half of Q from the other CTA), one thread of the
-// leading CTA issues the products for both, and each CTA keeps 128 x 256 fp32 accumulators in its own
-// tensor memory.  The pairs are persistent.  The accumulator takes half the tensor memory and the scales
-// some of the rest, so it is not doubled: the eight warps that read it move it into registers as bf16,
-// release it, and store while the next tile's products run.
+// Tile of 256 P rows x BN Q rows per pair of CTAs.  Each CTA loads its 128 P rows and half of the Q rows
+// (the tensor cores read the other half of Q from the other CTA), one thread of the leading CTA issues the
+// products for both, and each CTA keeps 128 x BN fp32 accumulators in its own tensor memory.  The pairs are
+// persistent and the accumulators doubled, so that eight warps write a tile out while the next one's
+// products run; that and the scales leave BN at 224 or less (256 columns undoubled lost about 1 us per
+// tile to the read-out).
 constexpr int kPairThreads = 448;
-constexpr int kPairN = 256;
 constexpr int kPairStages = 6;
-constexpr int kPairStageBytes = 128 * 128 + (kPairN / 2) * 128;
 constexpr int kPairScaleBytes = 512 * 3;
 constexpr int kPairSlots = 2;         // batches of scales in flight
-constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + kPairSlots * kBatch * kPairScaleBytes + 256;
+constexpr int kPairTmemScales = 12;  // columns of one group's scales
+template <int BN>
+struct PairShape {
+    static constexpr int kStageBytes = 128 * 128 + (BN / 2) * 128;
+    static constexpr int kSmem = 1024 + kPairStages * kStageBytes + kPairSlots * kBatch * kPairScaleBytes + 8 * kStoreStage * 4 + 256;
+    static_assert(2 * BN + kBatch * kPairTmemScales <= 512, "tensor memory");
+    static_assert(BN % 32 == 0 && (BN / 2) % 16 == 0, "halves of whole 16-column loads");
+};
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
 
-__device__ __forceinline__ void store_pairs16(uint16_t* o, const uint32_t* w) {      // 16 bf16 values, 32-byte aligned
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
+template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ MmArgs a) {
+    constexpr int kStageBytes = PairShape<BN>::kStageBytes;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (su32(raw) & 1023)) & 1023);
-    uint8_t* scale_sh = base + kPairStages * kPairStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(scale_sh + kPairSlots * kBatch * kPairScaleBytes);   // leader: both CTAs' tiles landed
+    uint8_t* scale_sh = base + kPairStages * kStageBytes;
+    float* store_sh = reinterpret_cast<float*>(scale_sh + kPairSlots * kBatch * kPairScaleBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(store_sh + 8 * kStoreStage);   // leader: both CTAs' tiles landed
     uint64_t* empty = full + kPairStages;        // each CTA: the products have read the stage
     uint64_t* sfull = empty + kPairStages;       // leader: both CTAs' scales are in shared memory
     uint64_t* sempty = sfull + kPairSlots;       // each CTA: they are copied out
-    uint64_t* done = sempty + kPairSlots;        // each CTA: the accumulator is complete
-    uint64_t* acc_free = done + 1;               // leader: both CTAs' accumulators are read
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 1);
+    uint64_t* done = sempty + kPairSlots;        // each CTA: an accumulator is complete
+    uint64_t* acc_free = done + 2;               // leader: both CTAs have read it
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 2);
     uint32_t* gave_up = tmem_at + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -489,8 +646,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(sfull + i, 8);             // the four scale warps of both CTAs
             mbar_init(sempty + i, 1);
         }
-        mbar_init(done, 1);
-        mbar_init(acc_free, 16);                 // the eight reading warps of both CTAs
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(done + i, 1);
+            mbar_init(acc_free + i, 16);         // the eight reading warps of both CTAs
+        }
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -503,7 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at, tmem_scales = tmem + kPairN;
+    const uint32_t tmem = *tmem_at, tmem_scales = tmem + 2 * BN;
     const int groups = (a.kblocks + 3) / 4;
     const int tiles_p = (a.rows_p + 255) / 256;
     const int64_t tiles = (int64_t)tiles_p * a.tiles_q;
@@ -514,30 +673,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int g = (int)(t / per), in = (int)(t - g * per);
         const int width = tiles_p - g * kPairGroup < kPairGroup ? tiles_p - g * kPairGroup : kPairGroup;
         p0 = (g * kPairGroup + in % width) * 256;
-        q0 = (in / width) * kPairN;
+        q0 = (in / width) * BN;
     };
     auto fail = [&] {
         atomicExch(gave_up, 1u);
         atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
     };
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         Ring ring;
         bool ok = true;
+        const uint32_t full0 = at_rank(full, 0);
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
             int p0, q0;
             place(t, p0, q0);
             for (int kb = 0; kb < a.kblocks; ++kb) {
-                if (ring.round > 0 && !(ok = mbar_wait(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
-                uint8_t* at = base + ring.at * kPairStageBytes;
-                const uint32_t bar = at_rank(full + ring.at, 0);
-                if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kPairStageBytes);
-                tma_load_pair(at, &map_p, kb * 128, p0 + (int)rank * 128, bar);
-                tma_load_pair(at + 128 * 128, &map_q, kb * 128, q0 + (int)rank * (kPairN / 2), bar);
+                if (ring.round > 0 && !(ok = warp_wait(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
+                uint8_t* at = base + ring.at * kStageBytes;
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kStageBytes);
+                    tma_load_pair(at, &map_p, kb * 128, p0 + (int)rank * 128, full0 + ring.at * 8);
+                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
+                }
+                __syncwarp();
                 ring.next(kPairStages);
             }
         }
-        if (!ok) fail();
+        if (!ok && lane == 0) fail();
         if (rank == 0) {                         // let every copy land before the CTAs may exit
             const bool wrapped = ring.round > 0;
             for (int k = 0; k < kPairStages; ++k) {
@@ -545,50 +707,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 else if (wrapped) mbar_wait(full + k, ring.parity() ^ 1, a.wait_limit);
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        const uint32_t idesc = ((uint32_t)(kPairN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
-        const uint32_t base32 = su32(base), scale32 = su32(scale_sh);
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
+        const uint64_t desc0 = operand_desc(su32(base));
+        const uint64_t sdesc0 = scales_desc(su32(scale_sh));
         bool ok = true;
-        Ring ring, slots;
-        uint32_t tile_parity = 0;
+        Ring ring, slots, acc;
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
-            if (t != first_tile) {
-                if (!(ok = mbar_wait_cluster(acc_free, tile_parity, a.wait_limit))) break;
-                tile_parity ^= 1;
-            }
+            if (acc.round > 0 && !(ok = warp_wait_cluster(acc_free + acc.at, acc.parity() ^ 1, a.wait_limit))) break;
             tc_fence_after();
-            uint32_t sfa = 0;
+            const uint32_t sums = tmem + acc.at * BN;
             for (int kb = 0; kb < a.kblocks; ++kb) {
+                const int in = (kb >> 2) & (kBatch - 1);             // group of the batch
+                const uint32_t sfa = tmem_scales + in * kPairTmemScales;
                 if ((kb & 3) == 0) {
-                    const int in = (kb >> 2) & (kBatch - 1);
                     if (in == 0) {
-                        if (!(ok = mbar_wait_cluster(sfull + slots.at, slots.parity(), a.wait_limit))) break;
+                        if (!(ok = warp_wait_cluster(sfull + slots.at, slots.parity(), a.wait_limit))) break;
                         tc_fence_after();
                     }
-                    const uint32_t at = scale32 + (slots.at * kBatch + in) * kPairScaleBytes;
-                    sfa = tmem_scales + in * 12;
-                    tmem_copy_scales_pair(sfa, scales_desc(at));
-                    tmem_copy_scales_pair(sfa + 4, scales_desc(at + 512));
-                    tmem_copy_scales_pair(sfa + 8, scales_desc(at + 1024));
-                    if (in == kBatch - 1 || kb + 4 >= a.kblocks) {
-                        mma_commit_pair(sempty + slots.at);
-                        slots.next(kPairSlots);
+                    const bool last = in == kBatch - 1 || kb + 4 >= a.kblocks;
+                    if (elect_one()) {
+                        const uint64_t from = sdesc0 + (((slots.at * kBatch + in) * kPairScaleBytes) >> 4);
+                        tmem_copy_scales_pair(sfa, from);
+                        tmem_copy_scales_pair(sfa + 4, from + (512 >> 4));
+                        tmem_copy_scales_pair(sfa + 8, from + (1024 >> 4));
+                        if (last) mma_commit_pair(sempty + slots.at);
                     }
+                    __syncwarp();
+                    if (last) slots.next(kPairSlots);
                 }
-                if (!(ok = mbar_wait(full + ring.at, ring.parity(), a.wait_limit))) break;
+                if (!(ok = warp_wait(full + ring.at, ring.parity(), a.wait_limit))) break;
                 tc_fence_after();
-                const uint32_t at = base32 + ring.at * kPairStageBytes;
-                const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * 128);
+                const uint64_t da = desc0 + ((ring.at * kStageBytes) >> 4), db = da + ((128 * 128) >> 4);
                 const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_scaled_pair(tmem, da + 2 * k, db + 2 * k, id, sfa, sfa + 4, kb > 0 || k > 0);
-                mma_commit_pair(empty + ring.at);
+                    for (int k = 0; k < 4; ++k) mma_scaled_pair(sums, da + 2 * k, db + 2 * k, id, sfa, sfa + 4, kb > 0 || k > 0);
+                    mma_commit_pair(empty + ring.at);
+                }
+                __syncwarp();
                 ring.next(kPairStages);
             }
             if (!ok) break;
-            mma_commit_pair(done);
+            if (elect_one()) mma_commit_pair(done + acc.at);
+            __syncwarp();
+            acc.next(2);
         }
-        if (!ok) fail();
+        if (!ok && lane == 0) fail();
     } else if (warp >= 2 && warp < 6) {
         // thread r of 128: P row r, Q rows r and 128 + r of the tile; the scale copy wants row r's word at
         // (r % 32) * 16 + (r / 32) * 4
@@ -600,18 +765,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             int p0, q0;
             place(t, p0, q0);
             ScaleRow row[3];
-            row[0].start(a.sp, a.ldsp, (int64_t)p0 + rank * 128 + r, a.rows_p, 0, a.blocks, a.blocks);
-            row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, a.rows_q, 0, a.blocks, a.blocks);
-            row[2].start(a.sq, a.ldsq, (int64_t)q0 + 128 + r, a.rows_q, 0, a.blocks, a.blocks);
+            row[0].start(a.sp, a.ldsp, (int64_t)p0 + rank * 128 + r, a.rows_p, 0, a.kblocks, a.kblocks);
+            row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, a.rows_q, 0, a.kblocks, a.kblocks);
+            row[2].start(a.sq, a.ldsq, (int64_t)q0 + 128 + r, BN > 128 + r ? a.rows_q : 0, 0, a.kblocks, a.kblocks);
             for (int g = 0; g < groups; g += kBatch) {
-                if (slots.round > 0) ok = mbar_wait(sempty + slots.at, slots.parity() ^ 1, a.wait_limit);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
+                if (slots.round > 0 && !(ok = warp_wait(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
+                for (int c = 0; c < 3; ++c) {
+                    uint32_t w[kBatch];
+                    row[c].take(w);
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)
-                        *reinterpret_cast<uint32_t*>(mine + (slots.at * kBatch + j) * kPairScaleBytes + c * 512) = row[c].take(j);
+                    for (int j = 0; j < kBatch; ++j)
+                        *reinterpret_cast<uint32_t*>(mine + (slots.at * kBatch + j) * kPairScaleBytes + c * 512) = w[j];
+                }
                 // This fence waits for every load of its thread as well: the next batch's are issued after it,
                 // and a batch, not a group, is handed over at a time so that their latency is paid once per
                 // 2,048 columns.  (One group at a time: 383 us for 8192^3 against 297 with no scales at all.)
@@ -625,57 +791,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= 6) {
+        constexpr int kHalf = BN / 2;            // columns of one warp
         const int sub = warp & 3, half = (warp - 6) >> 2;
-        const uint32_t free_bar = at_rank(acc_free, 0);
-        int64_t i = 0;
-        for (int64_t t = first_tile; t < tiles; t += step, ++i) {
+        Ring acc;
+        for (int64_t t = first_tile; t < tiles; t += step, acc.next(2)) {
             int p0, q0;
             place(t, p0, q0);
-            bool ok = mbar_wait(done, i & 1, a.wait_limit);
-            // the products of a tile may be many: wait on while the tile still makes progress is not
-            // needed, a tile of 2^31 columns ends well within the limit
-            if (!__all_sync(~0u, ok)) {
+            if (!warp_wait(done + acc.at, acc.parity(), a.wait_limit)) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
-            const int64_t p = (int64_t)p0 + rank * 128 + sub * 32 + lane;
-            const int qh = q0 + half * 128;
-            const bool row_ok = p < a.rows_p;
+            const int64_t p = (int64_t)p0 + rank * 128 + sub * 32;               // the warp's first row
+            const int rows = a.rows_p - p < 32 ? (int)(a.rows_p - p) : 32;
+            const int qh = q0 + half * kHalf;
             uint16_t* o = a.out + p * a.ldo + qh;
-            uint32_t w[64];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float f[32];
-                tmem_load32(tmem + ((uint32_t)(sub * 32) << 16) + half * 128 + c * 32, f);
-                if (a.first) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[c * 16 + j] = pack_bf16x2(f[2 * j] * a.scale, f[2 * j + 1] * a.scale);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int q = qh + c * 32 + 2 * j;
-                        const float lo = row_ok && q < a.rows_q ? bf16_to_f32(o[c * 32 + 2 * j]) : 0.f;
-                        const float hi = row_ok && q + 1 < a.rows_q ? bf16_to_f32(o[c * 32 + 2 * j + 1]) : 0.f;
-                        w[c * 16 + j] = pack_bf16x2(fmaf(f[2 * j], a.scale, lo), fmaf(f[2 * j + 1], a.scale, hi));
-                    }
-                }
+            const uint32_t from = tmem + acc.at * BN + half * kHalf + ((uint32_t)(sub * 32) << 16);
+#pragma unroll 2
+            for (int c = 0; c < kHalf; c += 16) {
+                float f[16];
+                tmem_load16(from + c, f);
+                store_rows16(o + c, a.ldo, f, rows, a.rows_q - qh - c, a.align, a.scale, a.first,
+                             store_sh + (warp - 6) * kStoreStage);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(free_bar);
-            if (!row_ok) continue;
-            const int n = a.rows_q - qh;         // valid columns of this half
-            if (a.wide && n >= 128) {
-#pragma unroll
-                for (int v = 0; v < 8; ++v) store_pairs16(o + v * 16, w + v * 8);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    if (2 * j < n) o[2 * j] = (uint16_t)w[j];
-                    if (2 * j + 1 < n) o[2 * j + 1] = (uint16_t)(w[j] >> 16);
-                }
-            }
+            if (lane == 0) mbar_arrive_cluster(at_rank(acc_free + acc.at, 0));
         }
     }
     __syncthreads();
@@ -715,47 +856,105 @@ bool make_map(CUtensorMap* map, const Q8& q, int64_t rows, int64_t cols, int box
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)q.ld};
     const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, unit[2] = {1, 1};
     return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.codes, dims, strides, box, unit,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int STAGES>
-cudaError_t launch_mm(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
-    using S = MmShape<BN, STAGES>;
-    static std::atomic<uint64_t> ready{0};
+// Raises a kernel's dynamic shared-memory limit once per device.
+cudaError_t ready_once(std::atomic<uint64_t>& ready, const void* kern, int smem) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(k_q8_matmul<BN, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
-    }
-    CUtensorMap mp, mq;
-    if (!encode_tiled() || !make_map(&mp, p, a.rows_p, k, 128) || !make_map(&mq, q, a.rows_q, k, BN)) return cudaErrorInvalidValue;
-    a.tiles_q = (a.rows_q + BN - 1) / BN;
-    const int64_t tiles = (int64_t)((a.rows_p + 127) / 128) * a.tiles_q;
-    if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_kernel(k_q8_matmul<BN, STAGES>, dim3((unsigned)tiles), dim3(kMmThreads), S::kSmem, st, mp, mq, a);
+    if (dev < kMaxDevices && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < kMaxDevices) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return e;
 }
 
-cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
-    static std::atomic<uint64_t> ready{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(k_q8_matmul_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+// The two operands' tensor maps.  A thread that has made no CUDA call of its own yet has no current
+// context, which the driver call needs; the runtime binds the device's own on cudaSetDevice.
+cudaError_t make_maps(CUtensorMap* mp, CUtensorMap* mq, const Q8& p, const Q8& q, const MmArgs& a, int64_t k, int box_p, int box_q) {
+    if (!encode_tiled()) return cudaErrorNotSupported;
+    if (!make_map(mp, p, a.rows_p, k, box_p)) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaSetDevice(dev);
         if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+        if (!make_map(mp, p, a.rows_p, k, box_p)) return cudaErrorInvalidValue;
     }
+    return make_map(mq, q, a.rows_q, k, box_q) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BN, int STAGES>
+cudaError_t launch_mm_split(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
+    using S = SplitShape<BN, STAGES>;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = ready_once(ready, (const void*)k_q8_matmul_split<BN, STAGES>, S::kSmem);
+    if (e != cudaSuccess) return e;
     CUtensorMap mp, mq;
-    if (!encode_tiled() || !make_map(&mp, p, a.rows_p, k, 128) || !make_map(&mq, q, a.rows_q, k, kPairN / 2)) return cudaErrorInvalidValue;
-    a.tiles_q = (a.rows_q + kPairN - 1) / kPairN;
+    e = make_maps(&mp, &mq, p, q, a, k, 128, BN);
+    if (e != cudaSuccess) return e;
+    a.tiles_q = (a.rows_q + BN - 1) / BN;
+    const int64_t tiles = (int64_t)((a.rows_p + 127) / 128) * a.tiles_q;
+    // Split while the CTAs still fit one per SM and keep at least five blocks each: joining the parts costs
+    // 2-4 us, which more CTAs than SMs do not earn back (1 x 22016 x 4096: 17.8 us unsplit, 22.5 and 31.7 in
+    // 2 and 8 parts; 1 x 4096 x 4096, 32 tiles: 11.4 unsplit, 6.3 in 4).
+    a.split = 1;
+    while (a.split < kSplitMost && tiles * a.split * 2 <= q8_host::sm_count() && a.kblocks >= a.split * 2 * 5 &&
+           BN / (a.split * 2) >= (a.transposed ? 1 : 16))
+        a.split *= 2;
+    if (tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * a.split));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = dependent_launch() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_q8_matmul_split<BN, STAGES>, mp, mq, a);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
+template <int BN>
+cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
+    constexpr int smem = PairShape<BN>::kSmem;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = ready_once(ready, (const void*)k_q8_matmul_pair<BN>, smem);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mp, mq;
+    e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2);
+    if (e != cudaSuccess) return e;
+    a.tiles_q = (a.rows_q + BN - 1) / BN;
     const int64_t tiles = (int64_t)((a.rows_p + 255) / 256) * a.tiles_q;
     const int64_t pairs = q8_host::sm_count() / 2;
-    return launch_kernel(k_q8_matmul_pair, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads), kPairSmem, st, mp,
+    return launch_kernel(k_q8_matmul_pair<BN>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads), smem, st, mp,
                          mq, a);
+}
+
+// The tile width with the least time in the busiest pair: rounds of tiles times the time of one block of
+// one tile, which is that of its products (1.11 ns per column) or of its loads (per row of the CTA's two
+// tiles 0.92 ns, and 1.7 where rows are not 128 bytes apart or a multiple and each touches two lines).
+int pair_width(int64_t rows_p, int64_t rows_q, bool lines) {
+    const int64_t pairs = q8_host::sm_count() / 2, tp = (rows_p + 255) / 256;
+    int best = 224;
+    double least = 1e300;
+    for (int bn : {224, 192, 160, 128}) {
+        const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + pairs - 1) / pairs;
+        const double products = 1.11 * bn, loads = (lines ? 0.92 : 1.7) * (128 + bn / 2);
+        const double cost = (double)rounds * (products > loads ? products : loads);
+        if (cost < least) {
+            least = cost;
+            best = bn;
+        }
+    }
+    return best;
 }
 
 cudaError_t error_word(unsigned int** out) {
@@ -806,22 +1005,31 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     g.ldsq = q.lds;
     g.rows_p = (int)(swap ? n : m);
     g.rows_q = (int)(swap ? m : n);
-    g.kblocks = g.blocks = (int)((k + 127) / 128);
+    g.kblocks = (int)((k + 127) / 128);
     g.out = (uint16_t*)out;
     g.ldo = ldo;
     g.transposed = swap;
-    g.wide = wide(out, ldo);
+    g.align = ((uintptr_t)out & 31) == 0 && (ldo & 15) == 0 ? 32 : wide(out, ldo) ? 16 : 0;
     g.scale = scale;
     g.first = first != 0;
     g.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
     cudaError_t e;
-    g.wide = wide(out, ldo);
-    if (!swap && m >= 192 && n >= 192 && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
-        g.wide = ((uintptr_t)out & 31) == 0 && (ldo & 15) == 0;
-        e = zs::launch_mm_pair(p, q, k, g, st);
-    } else if (g.rows_q <= 32) e = zs::launch_mm<32, 6>(p, q, k, g, st);
-    else if (g.rows_q <= 64) e = zs::launch_mm<64, 6>(p, q, k, g, st);
-    else e = zs::launch_mm<128, 6>(p, q, k, g, st);
+    if (!swap && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
+        switch (zs::pair_width(m, n, ((qa.ld | qb.ld) & 127) == 0)) {
+            case 224: e = zs::launch_mm_pair<224>(p, q, k, g, st); break;
+            case 192: e = zs::launch_mm_pair<192>(p, q, k, g, st); break;
+            case 160: e = zs::launch_mm_pair<160>(p, q, k, g, st); break;
+            default: e = zs::launch_mm_pair<128>(p, q, k, g, st); break;
+        }
+    } else if (g.rows_q <= 16) {
+        e = zs::launch_mm_split<16, 4>(p, q, k, g, st);
+    } else if (g.rows_q <= 32) {
+        e = zs::launch_mm_split<32, 4>(p, q, k, g, st);
+    } else if (g.rows_q <= 64) {
+        e = zs::launch_mm_split<64, 4>(p, q, k, g, st);
+    } else {
+        e = zs::launch_mm_split<128, 3>(p, q, k, g, st);
+    }
     return cuda_status(fn, e);
 }
