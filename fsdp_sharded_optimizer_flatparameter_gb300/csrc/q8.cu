@@ -7,61 +7,6 @@ namespace zs {
 
 namespace {
 
-enum { kFromBf16Wide = 0, kFromBf16 = 1, kFromQ8 = 2 };
-
-struct TileArgs {
-    const uint16_t* x;       // bf16 input, ldx elements between rows
-    int64_t ldx;
-    Q8 in;                   // 8-bit input
-    Q8 q, q_t;               // outputs; codes == nullptr: not wanted
-    int64_t rows, cols, tiles_c;
-};
-
-template <int FROM>
-__global__ void __launch_bounds__(kTileThreads) k_q8_tile(const __grid_constant__ TileArgs a) {
-    __shared__ TileShared sh;
-    dependent_launch_prologue();
-    const TilePos t = tile_pos(blockIdx.x, a.tiles_c, a.rows, a.cols);
-    const int n = t.chunk();
-    float v[4][16];
-    if constexpr (FROM == kFromQ8) {
-        uint4 w[4];
-        uint32_t byte[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int64_t r = t.r0 + t.rg * 4 + p;
-            const bool ok = t.row_ok(p);
-            w[p] = load_codes(a.in.codes + r * a.in.ld + t.c0 + t.cc * 16, ok ? n : 0);
-            byte[p] = ok ? a.in.scales[r * a.in.lds + (t.c0 >> 7)] : 0;
-        }
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float s = q8_scale(byte[p]);
-            q8_unpack4(w[p].x, s, v[p]);
-            q8_unpack4(w[p].y, s, v[p] + 4);
-            q8_unpack4(w[p].z, s, v[p] + 8);
-            q8_unpack4(w[p].w, s, v[p] + 12);
-        }
-    } else {
-        uint32_t w[4][8];
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-            load_bf16_16<FROM == kFromBf16Wide>(a.x + (t.r0 + t.rg * 4 + p) * a.ldx + t.c0 + t.cc * 16,
-                                                t.row_ok(p) ? n : 0, w[p]);
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[p][2 * i] = bf16_lo(w[p][i]);
-                v[p][2 * i + 1] = bf16_hi(w[p][i]);
-            }
-    }
-    float top[4];
-    tile_row_tops(v, top);
-    if (a.q.codes) tile_store_rows(t, v, top, a.q);
-    if (a.q_t.codes) tile_store_columns(t, v, a.q_t, sh);
-}
-
 struct DecodeArgs {
     Q8 q;
     uint16_t* y;
@@ -95,19 +40,6 @@ __global__ void __launch_bounds__(256) k_q8_decode(const __grid_constant__ Decod
     }
 }
 
-int launch_tiles(const char* fn, int from, TileArgs& a, cudaStream_t st) {
-    if (a.rows == 0) return ZS_OK;
-    a.tiles_c = (a.cols + 127) / 128;
-    const int64_t tiles = a.tiles_c * ((a.rows + 127) / 128);
-    if (tiles > 0x7fffffffLL) return q8_host::fail(fn, "matrix too large for one launch");
-    const dim3 grid((unsigned)tiles), block(kTileThreads);
-    switch (from) {
-        case kFromBf16Wide: return q8_host::cuda_status(fn, launch_kernel(k_q8_tile<kFromBf16Wide>, grid, block, 0, st, a));
-        case kFromBf16: return q8_host::cuda_status(fn, launch_kernel(k_q8_tile<kFromBf16>, grid, block, 0, st, a));
-        default: return q8_host::cuda_status(fn, launch_kernel(k_q8_tile<kFromQ8>, grid, block, 0, st, a));
-    }
-}
-
 }  // namespace
 
 }  // namespace zs
@@ -123,14 +55,16 @@ extern "C" int zs_q8_encode(const void* x, int64_t ldx, int64_t rows, int64_t co
     ZS_Q8_TRY(check_dim(fn, "rows", rows, 0));
     ZS_Q8_TRY(check_dim(fn, "cols", cols, 1));
     ZS_Q8_TRY(check_bf16(fn, "x", x, ldx, rows, cols));
-    ZS_Q8_TRY(check_q8(fn, "q", q, rows, cols, true, &a.q));
-    ZS_Q8_TRY(check_q8(fn, "q_t", q_t, cols, rows, true, &a.q_t));
+    ZS_Q8_TRY(check_q8(fn, "q", q, rows, cols, true, &a.rows_out[0]));
+    ZS_Q8_TRY(check_q8(fn, "q_t", q_t, cols, rows, true, &a.cols_out[0]));
     if (!q && !q_t) return fail(fn, "q and q_t are both NULL");
+    if (rows == 0) return ZS_OK;
     a.x = (const uint16_t*)x;
     a.ldx = ldx;
     a.rows = rows;
     a.cols = cols;
-    return zs::launch_tiles(fn, wide(x, ldx) ? zs::kFromBf16Wide : zs::kFromBf16, a, (cudaStream_t)stream);
+    const cudaStream_t st = (cudaStream_t)stream;
+    return cuda_status(fn, wide(x, ldx) ? zs::launch_tiles<zs::kTileEncode, true>(a, st) : zs::launch_tiles<zs::kTileEncode, false>(a, st));
 }
 
 extern "C" int zs_q8_transpose(const zs_q8* q, int64_t rows, int64_t cols, const zs_q8* q_t, void* stream) {
@@ -140,11 +74,12 @@ extern "C" int zs_q8_transpose(const zs_q8* q, int64_t rows, int64_t cols, const
     zs::TileArgs a{};
     ZS_Q8_TRY(check_dim(fn, "rows", rows, 0));
     ZS_Q8_TRY(check_dim(fn, "cols", cols, 1));
-    ZS_Q8_TRY(check_q8(fn, "q", q, rows, cols, false, &a.in));
-    ZS_Q8_TRY(check_q8(fn, "q_t", q_t, cols, rows, false, &a.q_t));
+    ZS_Q8_TRY(check_q8(fn, "q", q, rows, cols, false, &a.a));
+    ZS_Q8_TRY(check_q8(fn, "q_t", q_t, cols, rows, false, &a.cols_out[0]));
+    if (rows == 0) return ZS_OK;
     a.rows = rows;
     a.cols = cols;
-    return zs::launch_tiles(fn, zs::kFromQ8, a, (cudaStream_t)stream);
+    return cuda_status(fn, zs::launch_tiles<zs::kTileTurn, true>(a, (cudaStream_t)stream));
 }
 
 extern "C" int zs_q8_decode(const zs_q8* q, int64_t rows, int64_t cols, void* y, int64_t ldy, void* stream) {

@@ -360,10 +360,6 @@ __global__ void __launch_bounds__(256) k_rmsnorm_dw(const float* partials, int64
 
 // ------------------------------------------------------------------ gated activation
 
-// sigmoid(x) = 1 / (1 + exp(-x)); exp(-x) past fp32's range gives 0, as it should.  The fast
-// exponential and division are within about 1e-6 of the value, 5 orders below an e4m3 step.
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
 struct GateArgs {
     const uint16_t *gate, *up;
     int64_t ldg, ldu, rows, cols;
@@ -383,70 +379,15 @@ __global__ void __launch_bounds__(kGateThreads) k_swiglu_q8(const __grid_constan
     unpack8(wg, g);
     unpack8(wu, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = g[i] * sigmoid_f32(g[i]) * u[i];
+    for (int i = 0; i < 8; i += 2) {
+        const float2 x = make_float2(g[i], g[i + 1]);
+        const float2 y = q8_mul2(q8_mul2(x, q8_sigmoid2(x)), make_float2(u[i], u[i + 1]));
+        h[i] = y.x;
+        h[i + 1] = y.y;
+    }
     encode8(h, n, a.h, row, c);
     if (a.gate_q.codes) encode8(g, n, a.gate_q, row, c);
     if (a.up_q.codes) encode8(u, n, a.up_q, row, c);
-}
-
-struct GateBackArgs {
-    const uint16_t* dh;
-    int64_t lddh, rows, cols, tiles_c;
-    Q8 gate_q, up_q, dgate, dup, dgate_t, dup_t, h_t;
-};
-
-template <bool WIDE>
-__global__ void __launch_bounds__(kTileThreads) k_swiglu_backward_q8(const __grid_constant__ GateBackArgs a) {
-    __shared__ TileShared sh;
-    dependent_launch_prologue();
-    const TilePos t = tile_pos(blockIdx.x, a.tiles_c, a.rows, a.cols);
-    const int n = t.chunk();
-    uint4 wg[4], wu[4];
-    uint32_t wd[4][8], sg[4], su[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const int64_t r = t.r0 + t.rg * 4 + p, c = t.c0 + t.cc * 16;
-        const bool ok = t.row_ok(p);
-        wg[p] = load_codes(a.gate_q.codes + r * a.gate_q.ld + c, ok ? n : 0);
-        wu[p] = load_codes(a.up_q.codes + r * a.up_q.ld + c, ok ? n : 0);
-        load_bf16_16<WIDE>(a.dh + r * a.lddh + c, ok ? n : 0, wd[p]);
-        sg[p] = ok ? a.gate_q.scales[r * a.gate_q.lds + (t.c0 >> 7)] : 0;
-        su[p] = ok ? a.up_q.scales[r * a.up_q.lds + (t.c0 >> 7)] : 0;
-    }
-    float v[4][16], top[4];
-    auto each = [&](auto&& f) {           // v = f(gate, up, dh, sigmoid(gate))
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t g4[4] = {wg[p].x, wg[p].y, wg[p].z, wg[p].w}, u4[4] = {wu[p].x, wu[p].y, wu[p].z, wu[p].w};
-            const float s0 = q8_scale(sg[p]), s1 = q8_scale(su[p]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float g[4], u[4];
-                q8_unpack4(g4[k], s0, g);
-                q8_unpack4(u4[k], s1, u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = wd[p][k * 2 + (i >> 1)];
-                    v[p][k * 4 + i] = f(g[i], u[i], (i & 1) ? bf16_hi(w) : bf16_lo(w), sigmoid_f32(g[i]));
-                }
-            }
-        }
-        tile_row_tops(v, top);
-    };
-    if (a.dgate.codes || a.dgate_t.codes) {
-        each([](float g, float u, float d, float s) { return d * u * s * (1.f + g * (1.f - s)); });
-        if (a.dgate.codes) tile_store_rows(t, v, top, a.dgate);
-        if (a.dgate_t.codes) tile_store_columns(t, v, a.dgate_t, sh);
-    }
-    if (a.dup.codes || a.dup_t.codes) {
-        each([](float g, float, float d, float s) { return d * g * s; });
-        if (a.dup.codes) tile_store_rows(t, v, top, a.dup);
-        if (a.dup_t.codes) tile_store_columns(t, v, a.dup_t, sh);
-    }
-    if (a.h_t.codes) {
-        each([](float g, float u, float, float s) { return g * s * u; });
-        tile_store_columns(t, v, a.h_t, sh);
-    }
 }
 
 // Threads and register vectors for a row of `cols` columns: the fewest vectors per thread that keep the
@@ -613,28 +554,23 @@ extern "C" int zs_swiglu_backward_q8(const void* dh, int64_t lddh, const zs_q8* 
     static const char* fn = "zs_swiglu_backward_q8";
     zs::TraceRange trace_(fn);
     zs::clear_error();
-    zs::GateBackArgs a{};
+    zs::TileArgs a{};
     ZS_Q8_TRY(check_dim(fn, "rows", rows, 0));
     ZS_Q8_TRY(check_dim(fn, "cols", cols, 1));
     ZS_Q8_TRY(check_bf16(fn, "dh", dh, lddh, rows, cols));
-    ZS_Q8_TRY(check_q8(fn, "gate_q", gate_q, rows, cols, false, &a.gate_q));
-    ZS_Q8_TRY(check_q8(fn, "up_q", up_q, rows, cols, false, &a.up_q));
-    ZS_Q8_TRY(check_q8(fn, "dgate", dgate, rows, cols, true, &a.dgate));
-    ZS_Q8_TRY(check_q8(fn, "dup", dup, rows, cols, true, &a.dup));
-    ZS_Q8_TRY(check_q8(fn, "dgate_t", dgate_t, cols, rows, true, &a.dgate_t));
-    ZS_Q8_TRY(check_q8(fn, "dup_t", dup_t, cols, rows, true, &a.dup_t));
-    ZS_Q8_TRY(check_q8(fn, "h_t", h_t, cols, rows, true, &a.h_t));
+    ZS_Q8_TRY(check_q8(fn, "gate_q", gate_q, rows, cols, false, &a.a));
+    ZS_Q8_TRY(check_q8(fn, "up_q", up_q, rows, cols, false, &a.b));
+    ZS_Q8_TRY(check_q8(fn, "dgate", dgate, rows, cols, true, &a.rows_out[0]));
+    ZS_Q8_TRY(check_q8(fn, "dup", dup, rows, cols, true, &a.rows_out[1]));
+    ZS_Q8_TRY(check_q8(fn, "dgate_t", dgate_t, cols, rows, true, &a.cols_out[0]));
+    ZS_Q8_TRY(check_q8(fn, "dup_t", dup_t, cols, rows, true, &a.cols_out[1]));
+    ZS_Q8_TRY(check_q8(fn, "h_t", h_t, cols, rows, true, &a.cols_out[2]));
     if (!dgate && !dup && !dgate_t && !dup_t && !h_t) return fail(fn, "every output is NULL");
     if (rows == 0) return ZS_OK;
-    a.dh = (const uint16_t*)dh;
-    a.lddh = lddh;
+    a.x = (const uint16_t*)dh;
+    a.ldx = lddh;
     a.rows = rows;
     a.cols = cols;
-    a.tiles_c = (cols + 127) / 128;
-    const int64_t tiles = a.tiles_c * ((rows + 127) / 128);
-    if (tiles > 0x7fffffffLL) return fail(fn, "matrix too large for one launch");
-    const dim3 grid((unsigned)tiles), block(zs::kTileThreads);
     const cudaStream_t st = (cudaStream_t)stream;
-    return cuda_status(fn, wide(dh, lddh) ? zs::launch_kernel(zs::k_swiglu_backward_q8<true>, grid, block, 0, st, a)
-                                          : zs::launch_kernel(zs::k_swiglu_backward_q8<false>, grid, block, 0, st, a));
+    return cuda_status(fn, wide(dh, lddh) ? zs::launch_tiles<zs::kTileGate, true>(a, st) : zs::launch_tiles<zs::kTileGate, false>(a, st));
 }

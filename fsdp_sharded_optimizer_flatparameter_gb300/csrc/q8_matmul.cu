@@ -9,59 +9,11 @@
 // Roles of a CTA's warps: 0 loads tiles of codes (TMA, 128-byte swizzle) into a ring of stages; 1 issues
 // the scale copies and the products (one thread); 2 fetches scale bytes and lays them out as the scale
 // copy wants them; 3 holds the tensor memory allocation; 4-7 read the accumulator and write the result.
-#include <cuda.h>
-
-#include <atomic>
-#include <mutex>
-
-#include "q8.cuh"
+#include "q8_tma.cuh"
 
 namespace zs {
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(su32(b)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, long long limit) {
-    if (mbar_try_wait(b, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(b, parity)) {
-        if (clock64() - t0 > limit) return false;
-    }
-    return true;
-}
-
-// Tile of codes: columns x .. x + 127, rows y ..; x is a multiple of 128, so the copy starts on a
-// 16-byte boundary as it must.
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            su32(dst)),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(su32(bar))
-        : "memory");
-}
 
 // Shared-memory operand: rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
@@ -835,54 +787,10 @@ __global__ void k_q8_empty_sum(uint16_t* out, int64_t ldo, int64_t m, int64_t n)
 
 // ------------------------------------------------------------------ host
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult got;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
-            got != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (EncodeTiled)p;
-    }();
-    return fn;
-}
-
-// Tiles of box_rows rows x 128 bytes of an 8-bit matrix; what lies past its rows and columns reads as 0.
-bool make_map(CUtensorMap* map, const Q8& q, int64_t rows, int64_t cols, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)q.ld};
-    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, unit[2] = {1, 1};
-    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.codes, dims, strides, box, unit,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Raises a kernel's dynamic shared-memory limit once per device.
-cudaError_t ready_once(std::atomic<uint64_t>& ready, const void* kern, int smem) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && dev < kMaxDevices) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
-    return e;
-}
-
-// The two operands' tensor maps.  A thread that has made no CUDA call of its own yet has no current
-// context, which the driver call needs; the runtime binds the device's own on cudaSetDevice.
+// The two operands' tensor maps: boxes of 128 columns, swizzled as the products read them.
 cudaError_t make_maps(CUtensorMap* mp, CUtensorMap* mq, const Q8& p, const Q8& q, const MmArgs& a, int64_t k, int box_p, int box_q) {
-    if (!encode_tiled()) return cudaErrorNotSupported;
-    if (!make_map(mp, p, a.rows_p, k, box_p)) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaSetDevice(dev);
-        if (e != cudaSuccess) return e;
-        if (!make_map(mp, p, a.rows_p, k, box_p)) return cudaErrorInvalidValue;
-    }
-    return make_map(mq, q, a.rows_q, k, box_q) ? cudaSuccess : cudaErrorInvalidValue;
+    const cudaError_t e = make_map(mp, p.codes, false, a.rows_p, k, p.ld, box_p, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    return e != cudaSuccess ? e : make_map(mq, q.codes, false, a.rows_q, k, q.ld, box_q, 128, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int BN, int STAGES>
@@ -955,17 +863,6 @@ int pair_width(int64_t rows_p, int64_t rows_q, bool lines) {
         }
     }
     return best;
-}
-
-cudaError_t error_word(unsigned int** out) {
-    static std::atomic<unsigned int*> cached[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices && (*out = cached[dev].load(std::memory_order_acquire))) return cudaSuccess;
-    e = device_error_word(out);
-    if (e == cudaSuccess && dev < kMaxDevices) cached[dev].store(*out, std::memory_order_release);
-    return e;
 }
 
 }  // namespace

@@ -1,15 +1,24 @@
-// A 128 x 128 tile of fp32 values in the registers of one CTA, and its 8-bit forms along both directions.
+// 128 x 128 tiles in the 8-bit format, as they are and transposed: encode, transpose and the gated
+// activation's backward pass are one persistent kernel over tiles with different inputs and values.
 //
-// 256 threads; thread t (warp w, lane l) holds rows 4 * rg .. + 3 with rg = 4 * w + l / 8 and the 16
-// columns 16 * (l % 8) ..: v[p][j] is row 4 * rg + p, column 16 * (l % 8) + j.  A row's block of 128
-// columns is then eight neighbouring lanes (three shuffles for its largest magnitude, one 16-byte store
-// of codes per lane); a column's block of 128 rows is two shuffles and a maximum over the eight warps in
-// shared memory.  Four rows per thread make one 32-bit word of a column's codes, so the transpose
-// through shared memory is 16 word stores and 4 16-byte loads per thread; the word index is XORed with
-// the column chunk, which puts a warp's 32 words into 32 banks.
+// A CTA of 256 threads holds a tile as fp32 in registers; thread t (warp w, lane l) holds rows 4 * rg ..
+// 4 * rg + 3 with rg = 4 * w + l / 8, and the 16 columns 16 * (l % 8) ...  A row's block of 128 columns is
+// then eight neighbouring lanes (three shuffles for its largest magnitude, one 16-byte store of codes per
+// lane).  A column's block of 128 rows is two shuffles and a maximum over the 8 warps in shared memory; only
+// the exponent that the scale needs of it is passed on, two columns to a word.  Four rows per thread make a
+// 32-bit word of a column's codes, which pass through shared memory: a column's 128 codes are 8 chunks of 16
+// bytes, the chunk XORed with the column's 16-column group, so that a warp's stores fall into different banks.
+// What bounds these kernels next to the bytes is the shared-memory pipe (shuffles, staging) and the issue of
+// instructions, hence the wide thread tiles and the two-wide arithmetic (two rows per thread, full-width
+// maxima: 16-18 instructions per value and the pipe at 76 %, 85 us for encoding 22016 x 4096 both ways).
+//
+// The next tiles' inputs arrive by tiled copies (a ring of stages) while a tile is worked on: the kernels
+// move bytes, and a tile's loads, arithmetic and stores took their times one after another when each CTA
+// loaded into registers (one tile per CTA: 242 us for the activation's backward pass at 5003 x 5504).  bf16 inputs that such copies cannot read
+// (16-byte alignment) are loaded by the threads.
 #pragma once
 
-#include "q8.cuh"
+#include "q8_tma.cuh"
 
 namespace zs {
 
@@ -30,9 +39,9 @@ __device__ __forceinline__ TilePos tile_pos(int64_t tile, int64_t tiles_c, int64
     TilePos t;
     t.cc = threadIdx.x & 7;
     t.rg = threadIdx.x >> 3;
-    const int64_t tr = tile / tiles_c;
-    t.r0 = tr * 128;
-    t.c0 = (tile - tr * tiles_c) * 128;
+    const uint32_t tr = (uint32_t)tile / (uint32_t)tiles_c;
+    t.r0 = (int64_t)tr * 128;
+    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * 128;
     t.rows = rows - t.r0 < 128 ? (int)(rows - t.r0) : 128;
     t.cols = cols - t.c0 < 128 ? (int)(cols - t.c0) : 128;
     return t;
@@ -41,127 +50,347 @@ __device__ __forceinline__ TilePos tile_pos(int64_t tile, int64_t tiles_c, int64
 // n (0 .. 16) bytes of w at p, which is 16-byte aligned.
 __device__ __forceinline__ void store_codes(uint8_t* p, const uint4& w, int n) {
     if (n == 16) {
-        *reinterpret_cast<uint4*>(p) = w;
+        __stcs(reinterpret_cast<uint4*>(p), w);
         return;
     }
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    for (int i = 0; i < n; ++i) p[i] = (uint8_t)(x[i >> 2] >> ((i & 3) * 8));
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) p[i] = (uint8_t)(x[i >> 2] >> ((i & 3) * 8));
 }
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p, int n) {
     if (n == 16) return __ldcs(reinterpret_cast<const uint4*>(p));
     uint32_t x[4] = {0, 0, 0, 0};
-    for (int i = 0; i < n; ++i) x[i >> 2] |= (uint32_t)p[i] << ((i & 3) * 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) x[i >> 2] |= (uint32_t)p[i] << ((i & 3) * 8);
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// 16 bf16 values at p (n of them valid, the others 0) as packed words.
-template <bool WIDE>
+// 16 bf16 values at p (n of them valid, the others 0) as packed words, from any 2-byte alignment.
 __device__ __forceinline__ void load_bf16_16(const uint16_t* p, int n, uint32_t (&w)[8]) {
-    if (WIDE && n == 16) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-            w[i] = lo | (hi << 16);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+        w[i] = lo | (hi << 16);
     }
 }
 
-// Replaces infinities by NaN in this thread's values when there are any (rare: the test is one
-// comparison on the maximum that the encoding needs anyway); `top` then leaves them out.
-__device__ __forceinline__ void tile_row_tops(float (&v)[4][16], float (&top)[4]) {
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        top[p] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top[p] = q8_top(top[p], v[p][j]);
-    }
-    if (isinf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) {
+// The scale exponent of a magnitude as the upper 16 bits of a sum (q8_scale_byte's): its maximum over a block is
+// the block's, so that two columns' share a word.
+__device__ __forceinline__ uint32_t scale_keys(float a, float b) {
+    return __byte_perm(__float_as_uint(a) + 0x1fffffu, __float_as_uint(b) + 0x1fffffu, 0x7632);
+}
+__device__ __forceinline__ uint32_t key_byte(uint32_t key) {            // key: one column's 16 bits
+    const int b = (int)(key >> 7) - 8;
+    return (uint32_t)(b < 0 ? 0 : b);
+}
+
+// A thread's part of a tile's values: rows p, column pairs.
+struct TileValues {
+    float2 v[4][8];
+
+    // Largest magnitude of each row's 16 values.  Infinities become NaN, which the encoding leaves out of the
+    // scale (rare: the test is one comparison on the maximum that the encoding needs anyway).
+    __device__ __forceinline__ void find_tops(float (&top)[4]) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             top[p] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                v[p][j] = q8_no_inf(v[p][j]);
-                top[p] = q8_top(top[p], v[p][j]);
+            for (int j = 0; j < 8; ++j) top[p] = q8_top(q8_top(top[p], v[p][j].x), v[p][j].y);
+        }
+        if (isinf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                top[p] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[p][j] = make_float2(q8_no_inf(v[p][j].x), q8_no_inf(v[p][j].y));
+                    top[p] = q8_top(q8_top(top[p], v[p][j].x), v[p][j].y);
+                }
             }
         }
     }
-}
-
-// Writes the tile as it is: `top` from tile_row_tops.
-__device__ __forceinline__ void tile_store_rows(const TilePos& t, const float (&v)[4][16], const float (&top)[4],
-                                                const Q8& q) {
-    const int n = t.chunk();
+    // The tile as it is.
+    __device__ __forceinline__ void store_rows(const TilePos& t, const float (&top)[4], const Q8& q) const {
+        const int n = t.chunk();
+        const int64_t r0 = t.r0 + t.rg * 4;
+        uint8_t* codes = q.codes + r0 * q.ld + t.c0 + t.cc * 16;
+        uint8_t* scales = q.scales + r0 * q.lds + (t.c0 >> 7);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        float m = top[p];
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-        const uint32_t byte = q8_scale_byte(m);
-        const float inv = q8_inverse(byte);
-        uint4 w;
-        w.x = q8_pack4(v[p][0] * inv, v[p][1] * inv, v[p][2] * inv, v[p][3] * inv);
-        w.y = q8_pack4(v[p][4] * inv, v[p][5] * inv, v[p][6] * inv, v[p][7] * inv);
-        w.z = q8_pack4(v[p][8] * inv, v[p][9] * inv, v[p][10] * inv, v[p][11] * inv);
-        w.w = q8_pack4(v[p][12] * inv, v[p][13] * inv, v[p][14] * inv, v[p][15] * inv);
-        if (t.row_ok(p)) {
-            const int64_t r = t.r0 + t.rg * 4 + p;
-            store_codes(q.codes + r * q.ld + t.c0 + t.cc * 16, w, n);
-            if (t.cc == 0) q.scales[r * q.lds + (t.c0 >> 7)] = (uint8_t)byte;
+        for (int p = 0; p < 4; ++p) {
+            float m = top[p];
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+            const uint32_t byte = q8_scale_byte(m);
+            const float inv = q8_inverse(byte);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 a = q8_mul2(v[p][2 * k], make_float2(inv, inv)), b = q8_mul2(v[p][2 * k + 1], make_float2(inv, inv));
+                w[k] = q8_pack4(a.x, a.y, b.x, b.y);
+            }
+            if (t.row_ok(p)) {
+                store_codes(codes, make_uint4(w[0], w[1], w[2], w[3]), n);
+                if (t.cc == 0) *scales = (uint8_t)byte;
+            }
+            codes += q.ld;
+            scales += q.lds;
         }
     }
-}
-
-struct TileShared {
-    float top[8][128];       // largest magnitude of a column in a warp's 16 rows
-    float inv[128];          // 2^-e of a column's block
-    uint32_t word[128 * 32]; // a column's codes, 32 words each, word index ^ (chunk * 4)
+    // Scale keys of the columns over this warp's 16 rows, into sh[warp][column pair].
+    __device__ __forceinline__ void column_keys(uint32_t (*sh)[64]) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        uint32_t key[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = q8_top(q8_top(q8_top(fabsf(v[0][j].x), v[1][j].x), v[2][j].x), v[3][j].x);
+            const float b = q8_top(q8_top(q8_top(fabsf(v[0][j].y), v[1][j].y), v[2][j].y), v[3][j].y);
+            key[j] = scale_keys(fmaxf(a, 0.f), fmaxf(b, 0.f));
+            key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 8));
+            key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 16));
+        }
+        if (lane < 8) {
+            uint4* to = reinterpret_cast<uint4*>(&sh[warp][lane * 8]);
+            to[0] = make_uint4(key[0], key[1], key[2], key[3]);
+            to[1] = make_uint4(key[4], key[5], key[6], key[7]);
+        }
+    }
+    // Codes of the columns into word (8 chunks of 16 bytes per column), with inv[column] = 2^-e.
+    __device__ __forceinline__ void stage_columns(const TilePos& t, const float* inv, uint32_t* word) const {
+        uint32_t* to = word + t.cc * 16 * 32 + (((t.rg >> 2) ^ t.cc) << 2) + (t.rg & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 e = *reinterpret_cast<const float4*>(inv + t.cc * 16 + k * 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 s = h ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
+                float2 a[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) a[p] = q8_mul2(v[p][k * 2 + h], s);
+                to[(k * 4 + h * 2) * 32] = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
+                to[(k * 4 + h * 2 + 1) * 32] = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
+            }
+        }
+    }
 };
 
-// Writes the transposed tile: column c of the tile is row c0 + c of q.  Infinities are gone already
-// (tile_row_tops).  Every thread of the CTA calls it; `sh` may be reused at once by the next call.
-__device__ __forceinline__ void tile_store_columns(const TilePos& t, const float (&v)[4][16], const Q8& q,
-                                                   TileShared& sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Two columns' scales: the keys' maximum over the warps, the scale bytes into q, 2^-e into inv.
+__device__ __forceinline__ void column_scales(const TilePos& t, int pair, const uint32_t (*keys)[64], const Q8& q, float* inv) {
+    uint32_t m = keys[0][pair];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float m = q8_top(q8_top(q8_top(q8_top(0.f, v[0][j]), v[1][j]), v[2][j]), v[3][j]);
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-        if (lane < 8) sh.top[warp][t.cc * 16 + j] = m;
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {
-        const int c = threadIdx.x;
-        float m = sh.top[0][c];
+    for (int k = 1; k < kTileThreads / 32; ++k) m = __vmaxu2(m, keys[k][pair]);
+    const uint32_t lo = key_byte(m & 0xffffu), hi = key_byte(m >> 16);
+    *reinterpret_cast<float2*>(inv + pair * 2) = make_float2(q8_inverse(lo), q8_inverse(hi));
+    uint8_t* to = q.scales + (t.c0 + pair * 2) * q.lds + (t.r0 >> 7);
+    if (pair * 2 < t.cols) to[0] = (uint8_t)lo;
+    if (pair * 2 + 1 < t.cols) to[q.lds] = (uint8_t)hi;
+}
+
+// Staged columns to their rows of q.
+__device__ __forceinline__ void store_columns(const TilePos& t, const uint32_t* word, const Q8& q) {
+    const uint4* vec = reinterpret_cast<const uint4*>(word);
+    const int part = threadIdx.x & 7;
+    int n = t.rows - part * 16;
+    n = n < 0 ? 0 : n > 16 ? 16 : n;
+    uint8_t* to = q.codes + (t.c0 + (threadIdx.x >> 3)) * q.ld + t.r0 + part * 16;
+    const int64_t step = (kTileThreads / 8) * q.ld;
 #pragma unroll
-        for (int k = 1; k < 8; ++k) m = fmaxf(m, sh.top[k][c]);
-        const uint32_t byte = q8_scale_byte(m);
-        sh.inv[c] = q8_inverse(byte);
-        if (c < t.cols) q.scales[(t.c0 + c) * q.lds + (t.r0 >> 7)] = (uint8_t)byte;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int c = t.cc * 16 + j;
-        const float inv = sh.inv[c];
-        sh.word[c * 32 + (t.rg ^ (t.cc << 2))] = q8_pack4(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
-    }
-    __syncthreads();
-    const uint4* vec = reinterpret_cast<const uint4*>(sh.word);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = threadIdx.x + i * kTileThreads, c = k >> 3, part = k & 7;
+    for (int i = 0; i < 128 * 8 / kTileThreads; ++i, to += step) {
+        const int c = (threadIdx.x >> 3) + i * (kTileThreads / 8);
         const uint4 w = vec[c * 8 + (part ^ (c >> 4))];
-        int n = t.rows - part * 16;
-        n = n < 0 ? 0 : n > 16 ? 16 : n;
-        if (c < t.cols) store_codes(q.codes + (t.c0 + c) * q.ld + t.r0 + part * 16, w, n);
+        if (c < t.cols) store_codes(to, w, n);
     }
+}
+
+// ------------------------------------------------------------------ the kernel over tiles
+
+enum { kTileEncode = 0, kTileTurn = 1, kTileGate = 2 };
+
+struct TileArgs {
+    const uint16_t* x;       // bf16 input (kTileEncode; kTileGate: dh), ldx elements between rows
+    int64_t ldx;
+    Q8 a, b;                 // 8-bit inputs (kTileTurn: a; kTileGate: gate and up)
+    Q8 rows_out[2];          // the values as they are: encode q; gate dgate, dup
+    Q8 cols_out[3];          // transposed: encode and turn q_t; gate dgate_t, dup_t, h_t
+    int64_t rows, cols, tiles_c, tiles;
+    unsigned int* error;
+    long long wait_limit;
+};
+
+template <int KIND, bool TMA>
+struct TileShape {
+    static constexpr int kValues = KIND == kTileGate ? 3 : 1;
+    static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage: bf16 tile
+    static constexpr int kA = KIND == kTileEncode ? 0 : 128 * 128;                // and 8-bit tiles
+    static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
+    static constexpr int kStage = kX + kA + kB;
+    static constexpr int kStages = KIND == kTileTurn ? 3 : 2;
+    static constexpr int kKeys = 8 * 64 * 4;
+    static constexpr int kSmem = 128 + kStages * kStage + kValues * (128 * 128 + kKeys + 512) + 64;
+    static constexpr int kPerSm = KIND == kTileGate ? 1 : 2;
+};
+
+template <int KIND, bool TMA>
+__global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
+    k_q8_tiles(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+               const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TileArgs a) {
+    using S = TileShape<KIND, TMA>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((128 - (su32(raw) & 127)) & 127);
+    uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [kValues][128 * 32]
+    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + S::kValues * 128 * 32);    // [kValues * 8][64]
+    float* inv = reinterpret_cast<float*>(keys + S::kValues * 8);                               // [kValues][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(inv + S::kValues * 128);
+    const int lane_row = (threadIdx.x >> 3) * 4, cc = threadIdx.x & 7;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    dependent_launch_prologue();
+
+    const int64_t step = gridDim.x;
+    auto load_stage = [&](int s, int64_t tile) {                                    // thread 0
+        if constexpr (S::kStage > 0) {
+            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c;
+            const int r0 = (int)(tr * 128), c0 = (int)(((uint32_t)tile - tr * (uint32_t)a.tiles_c) * 128);
+            uint8_t* at = base + s * S::kStage;
+            mbar_expect_tx(full + s, S::kStage);
+            if constexpr (S::kX > 0) tma_load(at, &map_x, c0, r0, full + s);
+            if constexpr (S::kA > 0) tma_load(at + S::kX, &map_a, c0, r0, full + s);
+            if constexpr (S::kB > 0) tma_load(at + S::kX + S::kA, &map_b, c0, r0, full + s);
+        }
+    };
+    // scale bytes of the thread's four rows, a tile ahead of their use
+    uint32_t sa[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
+    auto load_scales = [&](int64_t tile) {
+        if constexpr (S::kA > 0) {
+            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c, blk = (uint32_t)tile - tr * (uint32_t)a.tiles_c;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int64_t r = (int64_t)tr * 128 + lane_row + p;
+                sa[p] = r < a.rows ? a.a.scales[r * a.a.lds + blk] : 0;
+                if constexpr (S::kB > 0) sb[p] = r < a.rows ? a.b.scales[r * a.b.lds + blk] : 0;
+            }
+        }
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < S::kStages; ++i)
+            if (blockIdx.x + i * step < a.tiles) load_stage(i, blockIdx.x + i * step);
+    load_scales(blockIdx.x);
+    int s = 0;
+    uint32_t parity = 0;
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += step) {
+        const TilePos t = tile_pos(tile, a.tiles_c, a.rows, a.cols);
+        bool late = false;
+        if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
+        const uint8_t* at = base + s * S::kStage;
+        TileValues v[S::kValues];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t x[8];
+            if constexpr (KIND != kTileTurn) {
+                if constexpr (TMA) {
+                    const uint4* from = reinterpret_cast<const uint4*>(at + (lane_row + p) * 256 + cc * 32);
+                    const uint4 lo = from[0], hi = from[1];
+                    x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+                    x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+                } else {
+                    load_bf16_16(a.x + (t.r0 + lane_row + p) * a.ldx + t.c0 + cc * 16, t.row_ok(p) ? t.chunk() : 0, x);
+                }
+            }
+            if constexpr (KIND == kTileEncode) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[0].v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
+            } else if constexpr (KIND == kTileTurn) {
+                const uint4 w = *reinterpret_cast<const uint4*>(at + (lane_row + p) * 128 + cc * 16);
+                const float e = q8_scale(sa[p]);
+                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[0].v[p][j] = q8_mul2(q8_unpack2(w4[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
+            } else {
+                const uint8_t* codes = at + S::kX + (lane_row + p) * 128 + cc * 16;
+                const uint4 wg = *reinterpret_cast<const uint4*>(codes), wu = *reinterpret_cast<const uint4*>(codes + S::kA);
+                const float eg = q8_scale(sa[p]), eu = q8_scale(sb[p]);
+                const uint32_t g4[4] = {wg.x, wg.y, wg.z, wg.w}, u4[4] = {wu.x, wu.y, wu.z, wu.w};
+                const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 g = q8_mul2(q8_unpack2(g4[j >> 1] >> ((j & 1) * 16)), make_float2(eg, eg));
+                    const float2 u = q8_mul2(q8_unpack2(u4[j >> 1] >> ((j & 1) * 16)), make_float2(eu, eu));
+                    const float2 d = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
+                    const float2 sig = q8_sigmoid2(g), silu = q8_mul2(g, sig);
+                    const float2 rest = q8_fma2(sig, make_float2(-1.f, -1.f), one);                  // 1 - sigmoid
+                    v[0].v[p][j] = q8_mul2(q8_mul2(d, u), q8_mul2(sig, q8_fma2(g, rest, one)));
+                    v[1].v[p][j] = q8_mul2(d, silu);
+                    v[2].v[p][j] = q8_mul2(silu, u);
+                }
+            }
+        }
+        if (tile + step < a.tiles) load_scales(tile + step);
+        float top[S::kValues][4];
+#pragma unroll
+        for (int k = 0; k < S::kValues; ++k) {
+            v[k].find_tops(top[k]);
+            if (a.cols_out[k].codes) v[k].column_keys(keys + k * 8);
+        }
+        // every thread has read the stage: its next tile may come.  A wait that ran out ends the CTA, after
+        // the copies still on their way.
+        if (__syncthreads_or(late)) {
+            if (threadIdx.x == 0) {
+                atomicCAS(a.error, 0u, ZS_DEVERR_TILE_WAIT);
+                for (int i = 0; i < S::kStages; ++i)
+                    if (tile + i * step < a.tiles)
+                        mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, a.wait_limit);
+            }
+            return;
+        }
+        if (threadIdx.x == 0 && tile + S::kStages * step < a.tiles) load_stage(s, tile + S::kStages * step);
+        if (++s == S::kStages) {
+            s = 0;
+            parity ^= 1;
+        }
+#pragma unroll
+        for (int k = 0; k < S::kValues; ++k)
+            if (a.cols_out[k].codes && (int)threadIdx.x >> 6 == k) column_scales(t, threadIdx.x & 63, keys + k * 8, a.cols_out[k], inv + k * 128);
+#pragma unroll
+        for (int k = 0; k < (S::kValues < 2 ? 1 : 2); ++k)
+            if (KIND != kTileTurn && a.rows_out[k].codes) v[k].store_rows(t, top[k], a.rows_out[k]);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < S::kValues; ++k)
+            if (a.cols_out[k].codes) v[k].stage_columns(t, inv + k * 128, word + k * 128 * 32);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < S::kValues; ++k)
+            if (a.cols_out[k].codes) store_columns(t, word + k * 128 * 32, a.cols_out[k]);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int KIND, bool TMA>
+cudaError_t launch_tiles(TileArgs& a, cudaStream_t st) {
+    using S = TileShape<KIND, TMA>;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = ready_once(ready, (const void*)k_q8_tiles<KIND, TMA>, S::kSmem);
+    if (e != cudaSuccess) return e;
+    a.tiles_c = (a.cols + 127) / 128;
+    a.tiles = a.tiles_c * ((a.rows + 127) / 128);
+    if (a.tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
+    e = error_word(&a.error);
+    CUtensorMap mx{}, ma{}, mb{};
+    if (e == cudaSuccess && S::kX > 0) e = make_map(&mx, a.x, true, a.rows, a.cols, a.ldx * 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess && S::kA > 0) e = make_map(&ma, a.a.codes, false, a.rows, a.cols, a.a.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess && S::kB > 0) e = make_map(&mb, a.b.codes, false, a.rows, a.cols, a.b.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+    const int64_t room = (int64_t)q8_host::sm_count() * S::kPerSm;
+    return launch_kernel(k_q8_tiles<KIND, TMA>, dim3((unsigned)(a.tiles < room ? a.tiles : room)), dim3(kTileThreads), S::kSmem, st, mx,
+                         ma, mb, a);
 }
 
 }  // namespace zs

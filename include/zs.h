@@ -114,6 +114,7 @@ extern "C" {
 #define ZS_DEVERR_SELFTEST      3u   /* zs_selftest_wait_timeout ran its wait out (expected)         */
 #define ZS_DEVERR_GATHER_WAIT   4u   /* a bulk-store gather gave up waiting for its tile             */
 #define ZS_DEVERR_MATMUL_WAIT   5u   /* zs_q8_matmul gave up waiting for a tile or an accumulator    */
+#define ZS_DEVERR_TILE_WAIT     6u   /* an 8-bit encode, transpose or gate backward gave up waiting  */
 
 typedef struct zs_plan_s* zs_plan_t;
 
