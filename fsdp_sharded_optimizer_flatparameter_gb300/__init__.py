@@ -650,59 +650,32 @@ __all__ = ["Plan", "ZsError", "zs_adamw_hparams", "LIB_PATH"] + EXPORTED + [
 # float8_e8m0fnu).  Both may be views (row or column ranges) of larger ones.  bf16 matrices are CUDA
 # tensors [rows, cols] whose rows are contiguous.
 
+# A small product or norm takes a few microseconds on the GPU, less than a call's checks in Python may: what
+# fits is recognised in one expression per tensor, and only what does not is looked at again for the message.
+
+try:
+    import torch as _torch
+except ImportError:            # the C ABI's host calls work without it
+    _torch = None
+
+if _torch is not None:
+    _BF16, _F32 = _torch.bfloat16, _torch.float32
+    _CODES = (_torch.float8_e4m3fn, _torch.uint8)
+    _SCALES = (_torch.float8_e8m0fnu, _torch.uint8)
+
+
 def q8_empty(rows, cols, device="cuda"):
     """An 8-bit matrix (codes, scales) of rows x cols to write into: rows of codes padded to 16 bytes."""
-    import torch
-    codes = torch.empty((rows, max(16, (cols + 15) // 16 * 16)), dtype=torch.uint8, device=device)[:, :cols]
-    scales = torch.empty((rows, (cols + ZS_Q8_BLOCK - 1) // ZS_Q8_BLOCK), dtype=torch.uint8, device=device)
-    return codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu)
+    codes = _torch.empty((rows, max(16, (cols + 15) // 16 * 16)), dtype=_torch.uint8, device=device)[:, :cols]
+    scales = _torch.empty((rows, (cols + ZS_Q8_BLOCK - 1) // ZS_Q8_BLOCK), dtype=_torch.uint8, device=device)
+    return codes.view(_torch.float8_e4m3fn), scales.view(_torch.float8_e8m0fnu)
 
 
-def _row_distance(x, rows, cols, size, what):
-    """Checks a CUDA matrix of rows x cols with contiguous rows; the elements between its rows."""
-    if not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % what)
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
-        raise ValueError("%s must be %d x %d, not %s" % (what, rows, cols, tuple(x.shape)))
-    if x.element_size() != size:
-        raise ValueError("%s must have %d-byte elements" % (what, size))
-    ld, step = x.stride()
-    if step != 1 and cols > 1:
-        raise ValueError("%s must have contiguous rows" % what)
-    if rows < 2:
-        return max(ld, cols)                 # one row: its distance is never used
-    if ld < cols:
-        raise ValueError("%s: rows overlap" % what)
-    return ld
-
-
-def _bf16(x, rows, cols, what):
-    import torch
-    if x.dtype is not torch.bfloat16:
-        raise ValueError("%s must be bfloat16" % what)
-    return x.data_ptr(), _row_distance(x, rows, cols, 2, what)
-
-
-def _vector(x, n, size, what):
-    if x is None:
-        return None
-    if not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % what)
-    if not x.is_contiguous() or x.element_size() != size or x.numel() != n:
-        raise ValueError("%s must be %d contiguous %d-byte elements" % (what, n, size))
-    return x.data_ptr()
-
-
-def _q8(q, rows, cols, what):
-    """A zs_q8 of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
-    if q is None:
-        return None
-    codes, scales = q
-    ld = _row_distance(codes, rows, cols, 1, what + " codes")
-    if rows < 2:
-        ld = (ld + 15) // 16 * 16
-    lds = _row_distance(scales, rows, (cols + ZS_Q8_BLOCK - 1) // ZS_Q8_BLOCK, 1, what + " scales")
-    return ctypes.byref(zs_q8(codes.data_ptr(), scales.data_ptr(), ld, lds))
+def _here(stream):
+    """The stream argument; by default the current stream (the tensors are on the GPU already)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _shape(x, what):
@@ -711,82 +684,132 @@ def _shape(x, what):
     return x.shape
 
 
+def _misfit(x, rows, cols, dtypes, what):
+    """What is wrong with a matrix that must be rows x cols of one of dtypes on the GPU; if nothing is, the
+    distance between its rows (that of a single row is never used)."""
+    if x.dtype not in dtypes:
+        raise ValueError("%s must be %s, not %s" % (what, " or ".join(str(d) for d in dtypes), x.dtype))
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if x.dim() != 2 or x.shape != (rows, cols):
+        raise ValueError("%s must be %d x %d, not %s" % (what, rows, cols, tuple(x.shape)))
+    ld, step = x.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError("%s must have contiguous rows" % what)
+    if rows >= 2 and ld < cols:
+        raise ValueError("%s: rows overlap" % what)
+    return ld if rows >= 2 else cols
+
+
+def _bf16(x, shape, what):
+    """Address and row distance of a bf16 matrix."""
+    if x.dtype is _BF16 and x.is_cuda and x.shape == shape:
+        ld, step = x.stride()
+        if step == 1 and ld >= shape[1]:
+            return x.data_ptr(), ld
+    return x.data_ptr(), _misfit(x, shape[0], shape[1], (_BF16,), what)
+
+
+def _vector(x, n, dtype, what):
+    if x is None:
+        return None
+    if x.dtype is dtype and x.is_cuda and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError("%s must be %d contiguous elements of %s on the GPU" % (what, n, dtype))
+
+
+def _q8(q, rows, cols, what):
+    """A zs_q8 of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
+    if q is None:
+        return None
+    codes, scales = q
+    blocks = (cols + 127) >> 7
+    ld, step = codes.stride() if codes.dim() == 2 else (0, 0)
+    if not (step == 1 and ld >= cols and ld & 15 == 0 and codes.is_cuda and codes.dtype in _CODES
+            and codes.shape == (rows, cols)):
+        ld = _misfit(codes, rows, cols, _CODES, what + " codes")
+        if rows < 2:
+            ld = max(16, (ld + 15) // 16 * 16)
+    lds, step = scales.stride() if scales.dim() == 2 else (0, 0)
+    if not (step == 1 and lds >= blocks and scales.is_cuda and scales.dtype in _SCALES and scales.shape == (rows, blocks)):
+        lds = _misfit(scales, rows, blocks, _SCALES, what + " scales")
+    return ctypes.byref(zs_q8(codes.data_ptr(), scales.data_ptr(), ld, lds))
+
+
 def zs_q8_encode(x, q=None, q_t=None, stream=None):
     """x (bf16 [rows, cols]) in 8 bits: as it is into q, transposed into q_t ([cols, rows])."""
-    rows, cols = _shape(x, "x")
-    p, ld = _bf16(x, rows, cols, "x")
-    return _check(_lib.zs_q8_encode(p, ld, rows, cols, _q8(q, rows, cols, "q"), _q8(q_t, cols, rows, "q_t"),
-                                    _stream(stream)))
+    shape = rows, cols = _shape(x, "x")
+    p, ld = _bf16(x, shape, "x")
+    return _check(_lib.zs_q8_encode(p, ld, rows, cols, _q8(q, rows, cols, "q"), _q8(q_t, cols, rows, "q_t"), _here(stream)))
 
 
 def zs_q8_decode(q, y, stream=None):
     """The values of q into y (bf16, same shape)."""
-    rows, cols = _shape(y, "y")
-    p, ld = _bf16(y, rows, cols, "y")
-    return _check(_lib.zs_q8_decode(_q8(q, rows, cols, "q"), rows, cols, p, ld, _stream(stream)))
+    shape = rows, cols = _shape(y, "y")
+    p, ld = _bf16(y, shape, "y")
+    return _check(_lib.zs_q8_decode(_q8(q, rows, cols, "q"), rows, cols, p, ld, _here(stream)))
 
 
 def zs_q8_transpose(q, q_t, stream=None):
     """q ([rows, cols]) encoded again as its transpose q_t ([cols, rows])."""
     rows, cols = _shape(q[0], "q")
-    return _check(_lib.zs_q8_transpose(_q8(q, rows, cols, "q"), rows, cols, _q8(q_t, cols, rows, "q_t"),
-                                       _stream(stream)))
+    return _check(_lib.zs_q8_transpose(_q8(q, rows, cols, "q"), rows, cols, _q8(q_t, cols, rows, "q_t"), _here(stream)))
 
 
 def zs_q8_matmul(a, b, out, scale=1.0, first=True, stream=None):
     """out (bf16 [m, n]) = (0 if first else out) + scale * a b^T for 8-bit a ([m, k]) and b ([n, k])."""
-    m, n = _shape(out, "out")
+    shape = m, n = _shape(out, "out")
     k = _shape(a[0], "a")[1]
-    p, ld = _bf16(out, m, n, "out")
-    return _check(_lib.zs_q8_matmul(_q8(a, m, k, "a"), _q8(b, n, k, "b"), m, n, k, float(scale), 1 if first else 0, p, ld,
-                                    _stream(stream)))
+    p, ld = _bf16(out, shape, "out")
+    return _check(_lib.zs_q8_matmul(_q8(a, m, k, "a"), _q8(b, n, k, "b"), m, n, k, scale, 1 if first else 0, p, ld,
+                                    _here(stream)))
 
 
 def zs_rmsnorm_q8(x, residual, weight, eps, y, s=None, rstd=None, s_q8=None, stream=None):
     """RMS norm of x + residual (residual may be None) in 8 bits into y; the sum into s (bf16) and s_q8
     (8 bits), the rows' reciprocal norms into rstd (fp32), each when given."""
-    rows, cols = _shape(x, "x")
-    px, ldx = _bf16(x, rows, cols, "x")
-    pr, ldr = (None, 0) if residual is None else _bf16(residual, rows, cols, "residual")
-    ps, lds = (None, 0) if s is None else _bf16(s, rows, cols, "s")
-    return _check(_lib.zs_rmsnorm_q8(px, ldx, pr, ldr, _vector(weight, cols, 2, "weight"), float(eps), rows, cols,
+    shape = rows, cols = _shape(x, "x")
+    px, ldx = _bf16(x, shape, "x")
+    pr, ldr = (None, 0) if residual is None else _bf16(residual, shape, "residual")
+    ps, lds = (None, 0) if s is None else _bf16(s, shape, "s")
+    return _check(_lib.zs_rmsnorm_q8(px, ldx, pr, ldr, _vector(weight, cols, _BF16, "weight"), eps, rows, cols,
                                      _q8(y, rows, cols, "y"), ps, lds, _q8(s_q8, rows, cols, "s_q8"),
-                                     _vector(rstd, rows, 4, "rstd"), _stream(stream)))
+                                     _vector(rstd, rows, _F32, "rstd"), _here(stream)))
 
 
 def zs_rmsnorm_backward(dy, s, weight, rstd, dx, dw, partials, ds=None, scale=1.0, first=True, stream=None):
     """Backward pass of zs_rmsnorm_q8.  s: the sum, a bf16 matrix or an 8-bit pair; partials: fp32 scratch
     [n, cols]; ds: gradient reaching the sum past the norm, added to dx."""
-    rows, cols = _shape(dy, "dy")
-    py, ldy = _bf16(dy, rows, cols, "dy")
+    shape = rows, cols = _shape(dy, "dy")
+    py, ldy = _bf16(dy, shape, "dy")
     if isinstance(s, tuple):
         ps, lds, qs = None, 0, _q8(s, rows, cols, "s")
     else:
-        (ps, lds), qs = _bf16(s, rows, cols, "s"), None
-    pd, ldd = (None, 0) if ds is None else _bf16(ds, rows, cols, "ds")
-    px, ldx = _bf16(dx, rows, cols, "dx")
+        (ps, lds), qs = _bf16(s, shape, "s"), None
+    pd, ldd = (None, 0) if ds is None else _bf16(ds, shape, "ds")
+    px, ldx = _bf16(dx, shape, "dx")
     n = _shape(partials, "partials")[0]
     return _check(_lib.zs_rmsnorm_backward(
-        py, ldy, ps, lds, qs, _vector(weight, cols, 2, "weight"), _vector(rstd, rows, 4, "rstd"), pd, ldd, rows, cols,
-        px, ldx, _vector(dw, cols, 2, "dw"), float(scale), 1 if first else 0, _vector(partials, n * cols, 4, "partials"),
-        n, _stream(stream)))
+        py, ldy, ps, lds, qs, _vector(weight, cols, _BF16, "weight"), _vector(rstd, rows, _F32, "rstd"), pd, ldd, rows, cols,
+        px, ldx, _vector(dw, cols, _BF16, "dw"), scale, 1 if first else 0, _vector(partials, n * cols, _F32, "partials"), n,
+        _here(stream)))
 
 
 def zs_swiglu_q8(gate, up, h, gate_q=None, up_q=None, stream=None):
     """h = gate * sigmoid(gate) * up in 8 bits; gate and up kept in 8 bits where gate_q, up_q are given."""
-    rows, cols = _shape(gate, "gate")
-    pg, ldg = _bf16(gate, rows, cols, "gate")
-    pu, ldu = _bf16(up, rows, cols, "up")
+    shape = rows, cols = _shape(gate, "gate")
+    pg, ldg = _bf16(gate, shape, "gate")
+    pu, ldu = _bf16(up, shape, "up")
     return _check(_lib.zs_swiglu_q8(pg, ldg, pu, ldu, rows, cols, _q8(h, rows, cols, "h"),
-                                    _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), _stream(stream)))
+                                    _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), _here(stream)))
 
 
 def zs_swiglu_backward_q8(dh, gate_q, up_q, dgate=None, dup=None, dgate_t=None, dup_t=None, h_t=None, stream=None):
     """Backward pass of zs_swiglu_q8 from the kept gate and up: the gradients in 8 bits as they are and
     transposed, and h recomputed and transposed, each where given."""
-    rows, cols = _shape(dh, "dh")
-    p, ld = _bf16(dh, rows, cols, "dh")
+    shape = rows, cols = _shape(dh, "dh")
+    p, ld = _bf16(dh, shape, "dh")
     return _check(_lib.zs_swiglu_backward_q8(
         p, ld, _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), rows, cols,
         _q8(dgate, rows, cols, "dgate"), _q8(dup, rows, cols, "dup"), _q8(dgate_t, cols, rows, "dgate_t"),
-        _q8(dup_t, cols, rows, "dup_t"), _q8(h_t, cols, rows, "h_t"), _stream(stream)))
+        _q8(dup_t, cols, rows, "dup_t"), _q8(h_t, cols, rows, "h_t"), _here(stream)))

@@ -1,12 +1,12 @@
 // 128 x 128 tiles in the 8-bit format, as they are and transposed: encode, transpose and the gated
 // activation's backward pass are one persistent kernel over tiles with different inputs and values.
 //
-// A CTA of 256 threads holds a tile as fp32 in registers; thread t (warp w, lane l) holds rows 4 * rg ..
-// 4 * rg + 3 with rg = 4 * w + l / 8, and the 16 columns 16 * (l % 8) ...  A row's block of 128 columns is
+// A CTA holds a tile as fp32 in registers; thread t (warp w, lane l) holds RP (4 or 2) rows from RP * rg, with
+// rg = 4 * w + l / 8, and the 16 columns 16 * (l % 8) ...  A row's block of 128 columns is
 // then eight neighbouring lanes (three shuffles for its largest magnitude, one 16-byte store of codes per
-// lane).  A column's block of 128 rows is two shuffles and a maximum over the 8 warps in shared memory; only
-// the exponent that the scale needs of it is passed on, two columns to a word.  Four rows per thread make a
-// 32-bit word of a column's codes, which pass through shared memory: a column's 128 codes are 8 chunks of 16
+// lane).  A column's block of 128 rows is two shuffles and a maximum over the warps in shared memory; only
+// the exponent that the scale needs of it is passed on, two columns to a word.  A thread's rows make a
+// word of a column's codes, which pass through shared memory: a column's 128 codes are 8 chunks of 16
 // bytes, the chunk XORed with the column's 16-column group, so that a warp's stores fall into different banks.
 // What bounds these kernels next to the bytes is the shared-memory pipe (shuffles, staging) and the issue of
 // instructions, hence the wide thread tiles and the two-wide arithmetic (two rows per thread, full-width
@@ -22,21 +22,22 @@
 
 namespace zs {
 
-constexpr int kTileThreads = 256;
 
+template <int RP>            // rows per thread
 struct TilePos {
-    int cc, rg;              // column chunk (16 columns), row group (4 rows)
+    int cc, rg;              // column chunk (16 columns), row group (RP rows)
     int64_t r0, c0;          // the tile's first row and column
     int rows, cols;          // valid rows and columns of the tile, 1 .. 128
-    __device__ __forceinline__ bool row_ok(int p) const { return rg * 4 + p < rows; }
+    __device__ __forceinline__ bool row_ok(int p) const { return rg * RP + p < rows; }
     __device__ __forceinline__ int chunk() const {            // valid columns of this thread's 16
         const int n = cols - cc * 16;
         return n < 0 ? 0 : n > 16 ? 16 : n;
     }
 };
 
-__device__ __forceinline__ TilePos tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
-    TilePos t;
+template <int RP>
+__device__ __forceinline__ TilePos<RP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
+    TilePos<RP> t;
     t.cc = threadIdx.x & 7;
     t.rg = threadIdx.x >> 3;
     const uint32_t tr = (uint32_t)tile / (uint32_t)tiles_c;
@@ -87,21 +88,25 @@ __device__ __forceinline__ uint32_t key_byte(uint32_t key) {            // key: 
 }
 
 // A thread's part of a tile's values: rows p, column pairs.
+template <int RP>
 struct TileValues {
-    float2 v[4][8];
+    float2 v[RP][8];
 
     // Largest magnitude of each row's 16 values.  Infinities become NaN, which the encoding leaves out of the
     // scale (rare: the test is one comparison on the maximum that the encoding needs anyway).
-    __device__ __forceinline__ void find_tops(float (&top)[4]) {
+    __device__ __forceinline__ void find_tops(float (&top)[RP]) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < RP; ++p) {
             top[p] = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) top[p] = q8_top(q8_top(top[p], v[p][j].x), v[p][j].y);
         }
-        if (isinf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) {
+        float most = top[0];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+        for (int p = 1; p < RP; ++p) most = fmaxf(most, top[p]);
+        if (isinf(most)) {
+#pragma unroll
+            for (int p = 0; p < RP; ++p) {
                 top[p] = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -112,13 +117,13 @@ struct TileValues {
         }
     }
     // The tile as it is.
-    __device__ __forceinline__ void store_rows(const TilePos& t, const float (&top)[4], const Q8& q) const {
+    __device__ __forceinline__ void store_rows(const TilePos<RP>& t, const float (&top)[RP], const Q8& q) const {
         const int n = t.chunk();
-        const int64_t r0 = t.r0 + t.rg * 4;
+        const int64_t r0 = t.r0 + t.rg * RP;
         uint8_t* codes = q.codes + r0 * q.ld + t.c0 + t.cc * 16;
         uint8_t* scales = q.scales + r0 * q.lds + (t.c0 >> 7);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < RP; ++p) {
             float m = top[p];
             m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
             m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
@@ -139,15 +144,19 @@ struct TileValues {
             scales += q.lds;
         }
     }
-    // Scale keys of the columns over this warp's 16 rows, into sh[warp][column pair].
+    // Scale keys of the columns over this warp's rows, into sh[warp][column pair].
     __device__ __forceinline__ void column_keys(uint32_t (*sh)[64]) const {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint32_t key[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float a = q8_top(q8_top(q8_top(fabsf(v[0][j].x), v[1][j].x), v[2][j].x), v[3][j].x);
-            const float b = q8_top(q8_top(q8_top(fabsf(v[0][j].y), v[1][j].y), v[2][j].y), v[3][j].y);
-            key[j] = scale_keys(fmaxf(a, 0.f), fmaxf(b, 0.f));
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int p = 0; p < RP; ++p) {
+                a = q8_top(a, v[p][j].x);
+                b = q8_top(b, v[p][j].y);
+            }
+            key[j] = scale_keys(a, b);
             key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 8));
             key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 16));
         }
@@ -158,29 +167,36 @@ struct TileValues {
         }
     }
     // Codes of the columns into word (8 chunks of 16 bytes per column), with inv[column] = 2^-e.
-    __device__ __forceinline__ void stage_columns(const TilePos& t, const float* inv, uint32_t* word) const {
-        uint32_t* to = word + t.cc * 16 * 32 + (((t.rg >> 2) ^ t.cc) << 2) + (t.rg & 3);
+    __device__ __forceinline__ void stage_columns(const TilePos<RP>& t, const float* inv, uint32_t* word) const {
+        uint8_t* to = reinterpret_cast<uint8_t*>(word) + t.cc * 16 * 128 + ((((t.rg * RP) >> 4) ^ t.cc) << 4) + ((t.rg * RP) & 15);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float4 e = *reinterpret_cast<const float4*>(inv + t.cc * 16 + k * 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 s = h ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
-                float2 a[4];
+                float2 a[RP];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) a[p] = q8_mul2(v[p][k * 2 + h], s);
-                to[(k * 4 + h * 2) * 32] = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
-                to[(k * 4 + h * 2 + 1) * 32] = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
+                for (int p = 0; p < RP; ++p) a[p] = q8_mul2(v[p][k * 2 + h], s);
+                uint8_t* at = to + (k * 4 + h * 2) * 128;
+                if constexpr (RP == 4) {
+                    *reinterpret_cast<uint32_t*>(at) = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
+                    *reinterpret_cast<uint32_t*>(at + 128) = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
+                } else {
+                    *reinterpret_cast<uint16_t*>(at) = (uint16_t)q8_pack2(a[0].x, a[1].x);
+                    *reinterpret_cast<uint16_t*>(at + 128) = (uint16_t)q8_pack2(a[0].y, a[1].y);
+                }
             }
         }
     }
 };
 
 // Two columns' scales: the keys' maximum over the warps, the scale bytes into q, 2^-e into inv.
-__device__ __forceinline__ void column_scales(const TilePos& t, int pair, const uint32_t (*keys)[64], const Q8& q, float* inv) {
+template <int RP>
+__device__ __forceinline__ void column_scales(const TilePos<RP>& t, int pair, const uint32_t (*keys)[64], const Q8& q, float* inv) {
     uint32_t m = keys[0][pair];
 #pragma unroll
-    for (int k = 1; k < kTileThreads / 32; ++k) m = __vmaxu2(m, keys[k][pair]);
+    for (int k = 1; k < 32 / RP; ++k) m = __vmaxu2(m, keys[k][pair]);
     const uint32_t lo = key_byte(m & 0xffffu), hi = key_byte(m >> 16);
     *reinterpret_cast<float2*>(inv + pair * 2) = make_float2(q8_inverse(lo), q8_inverse(hi));
     uint8_t* to = q.scales + (t.c0 + pair * 2) * q.lds + (t.r0 >> 7);
@@ -189,16 +205,17 @@ __device__ __forceinline__ void column_scales(const TilePos& t, int pair, const 
 }
 
 // Staged columns to their rows of q.
-__device__ __forceinline__ void store_columns(const TilePos& t, const uint32_t* word, const Q8& q) {
+template <int RP>
+__device__ __forceinline__ void store_columns(const TilePos<RP>& t, const uint32_t* word, const Q8& q) {
     const uint4* vec = reinterpret_cast<const uint4*>(word);
     const int part = threadIdx.x & 7;
     int n = t.rows - part * 16;
     n = n < 0 ? 0 : n > 16 ? 16 : n;
     uint8_t* to = q.codes + (t.c0 + (threadIdx.x >> 3)) * q.ld + t.r0 + part * 16;
-    const int64_t step = (kTileThreads / 8) * q.ld;
+    const int64_t step = (128 / RP) * q.ld;
 #pragma unroll
-    for (int i = 0; i < 128 * 8 / kTileThreads; ++i, to += step) {
-        const int c = (threadIdx.x >> 3) + i * (kTileThreads / 8);
+    for (int i = 0; i < RP; ++i, to += step) {
+        const int c = (threadIdx.x >> 3) + i * (128 / RP);
         const uint4 w = vec[c * 8 + (part ^ (c >> 4))];
         if (c < t.cols) store_codes(to, w, n);
     }
@@ -221,29 +238,34 @@ struct TileArgs {
 
 template <int KIND, bool TMA>
 struct TileShape {
+    // Rows per thread.  Two (twice the warps, half the registers) is slower for each of the three: the gate's
+    // backward pass at 5003 x 5504 takes 81 us with four and 90 with two.
+    static constexpr int kRows = 4;
+    static constexpr int kThreads = 1024 / kRows;
     static constexpr int kValues = KIND == kTileGate ? 3 : 1;
     static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage: bf16 tile
     static constexpr int kA = KIND == kTileEncode ? 0 : 128 * 128;                // and 8-bit tiles
     static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
     static constexpr int kStage = kX + kA + kB;
     static constexpr int kStages = KIND == kTileTurn ? 3 : 2;
-    static constexpr int kKeys = 8 * 64 * 4;
+    static constexpr int kKeys = (32 / kRows) * 64 * 4;
     static constexpr int kSmem = 128 + kStages * kStage + kValues * (128 * 128 + kKeys + 512) + 64;
     static constexpr int kPerSm = KIND == kTileGate ? 1 : 2;
 };
 
 template <int KIND, bool TMA>
-__global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
+__global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<KIND, TMA>::kPerSm))
     k_q8_tiles(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TileArgs a) {
     using S = TileShape<KIND, TMA>;
+    constexpr int RP = S::kRows, kWarps = S::kThreads / 32;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((128 - (su32(raw) & 127)) & 127);
     uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [kValues][128 * 32]
-    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + S::kValues * 128 * 32);    // [kValues * 8][64]
-    float* inv = reinterpret_cast<float*>(keys + S::kValues * 8);                               // [kValues][128]
+    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + S::kValues * 128 * 32);    // [kValues * warps][64]
+    float* inv = reinterpret_cast<float*>(keys + S::kValues * kWarps);                               // [kValues][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(inv + S::kValues * 128);
-    const int lane_row = (threadIdx.x >> 3) * 4, cc = threadIdx.x & 7;
+    const int lane_row = (threadIdx.x >> 3) * RP, cc = threadIdx.x & 7;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -263,13 +285,13 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
             if constexpr (S::kB > 0) tma_load(at + S::kX + S::kA, &map_b, c0, r0, full + s);
         }
     };
-    // scale bytes of the thread's four rows, a tile ahead of their use
-    uint32_t sa[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
+    // scale bytes of the thread's rows, a tile ahead of their use
+    uint32_t sa[RP] = {}, sb[RP] = {};
     auto load_scales = [&](int64_t tile) {
         if constexpr (S::kA > 0) {
             const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c, blk = (uint32_t)tile - tr * (uint32_t)a.tiles_c;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < RP; ++p) {
                 const int64_t r = (int64_t)tr * 128 + lane_row + p;
                 sa[p] = r < a.rows ? a.a.scales[r * a.a.lds + blk] : 0;
                 if constexpr (S::kB > 0) sb[p] = r < a.rows ? a.b.scales[r * a.b.lds + blk] : 0;
@@ -283,13 +305,13 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     int s = 0;
     uint32_t parity = 0;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += step) {
-        const TilePos t = tile_pos(tile, a.tiles_c, a.rows, a.cols);
+        const TilePos<RP> t = tile_pos<RP>(tile, a.tiles_c, a.rows, a.cols);
         bool late = false;
         if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
-        TileValues v[S::kValues];
+        TileValues<RP> v[S::kValues];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < RP; ++p) {
             uint32_t x[8];
             if constexpr (KIND != kTileTurn) {
                 if constexpr (TMA) {
@@ -331,11 +353,11 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
             }
         }
         if (tile + step < a.tiles) load_scales(tile + step);
-        float top[S::kValues][4];
+        float top[S::kValues][RP];
 #pragma unroll
         for (int k = 0; k < S::kValues; ++k) {
             v[k].find_tops(top[k]);
-            if (a.cols_out[k].codes) v[k].column_keys(keys + k * 8);
+            if (a.cols_out[k].codes) v[k].column_keys(keys + k * kWarps);
         }
         // every thread has read the stage: its next tile may come.  A wait that ran out ends the CTA, after
         // the copies still on their way.
@@ -355,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
         }
 #pragma unroll
         for (int k = 0; k < S::kValues; ++k)
-            if (a.cols_out[k].codes && (int)threadIdx.x >> 6 == k) column_scales(t, threadIdx.x & 63, keys + k * 8, a.cols_out[k], inv + k * 128);
+            if (a.cols_out[k].codes && (int)threadIdx.x >> 6 == k) column_scales(t, threadIdx.x & 63, keys + k * kWarps, a.cols_out[k], inv + k * 128);
 #pragma unroll
         for (int k = 0; k < (S::kValues < 2 ? 1 : 2); ++k)
             if (KIND != kTileTurn && a.rows_out[k].codes) v[k].store_rows(t, top[k], a.rows_out[k]);
@@ -389,7 +411,7 @@ cudaError_t launch_tiles(TileArgs& a, cudaStream_t st) {
     if (e == cudaSuccess && S::kB > 0) e = make_map(&mb, a.b.codes, false, a.rows, a.cols, a.b.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
     const int64_t room = (int64_t)q8_host::sm_count() * S::kPerSm;
-    return launch_kernel(k_q8_tiles<KIND, TMA>, dim3((unsigned)(a.tiles < room ? a.tiles : room)), dim3(kTileThreads), S::kSmem, st, mx,
+    return launch_kernel(k_q8_tiles<KIND, TMA>, dim3((unsigned)(a.tiles < room ? a.tiles : room)), dim3(S::kThreads), S::kSmem, st, mx,
                          ma, mb, a);
 }
 
