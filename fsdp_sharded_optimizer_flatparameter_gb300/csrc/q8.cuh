@@ -142,8 +142,8 @@ inline int check_q8(const char* fn, const char* name, const zs_q8* q, int64_t ro
     return ZS_OK;
 }
 
-// Whether 16-byte accesses of a bf16 matrix's rows are aligned.
-inline bool wide(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && (ld & 7) == 0; }
+// Whether accesses of `bytes` (16 or 32) of a bf16 matrix's rows are aligned.
+inline bool wide(const void* p, int64_t ld, int bytes = 16) { return ((uintptr_t)p & (bytes - 1)) == 0 && (ld & (bytes / 2 - 1)) == 0; }
 
 inline int sm_count() {
     static int cached[64] = {};

@@ -7,63 +7,161 @@ namespace zs {
 
 namespace {
 
-// ------------------------------------------------------------------ vectors of 8 columns
+// ------------------------------------------------------------------ vectors of 16 columns
+//
+// A thread holds 16 neighbouring columns (32 bytes of bf16, 16 codes), so eight neighbouring lanes hold a
+// block of the format.  Aligned rows move 32 bytes per access.  Rows at other addresses (an odd width, a
+// view into a flat buffer) are read as the aligned 16-byte chunks that cover a thread's columns, shifted
+// into place, and written as the aligned chunks that a thread and its right neighbour make up together;
+// element by element a row of 2047 columns took 16 accesses per thread, each touching 32 sectors.
 
-// 8 bf16 values at p, n (<= 8) of them valid, the others 0.
-template <bool WIDE>
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
-    if (n <= 0) return make_uint4(0, 0, 0, 0);
-    if (WIDE && n >= 8) return __ldcs(reinterpret_cast<const uint4*>(p));
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-        w[i] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+struct V16 {
+    uint32_t w[8];
+};
+
+// The matrix that accesses must stay in: its first and past its last byte.
+struct Span {
+    const uint8_t *lo, *hi;
+};
+__device__ __forceinline__ Span span_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t cols) {
+    return {reinterpret_cast<const uint8_t*>(p), reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols)};
 }
+
+// 16 bf16 values at p, n of them valid (n may be <= 0 or > 16), the others 0.
 template <bool WIDE>
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], int n) {
-    if (n <= 0) return;
-    const BfVec<8> v = pack(f);
-    if (WIDE && n >= 8) {
-        __stcs(reinterpret_cast<uint4*>(p), v.w);
+__device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& s) {
+    V16 v;
+    if (WIDE) {
+        if (n >= 16) {
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                           "=r"(v.w[7])
+                         : "l"(p));
+            return v;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+            v.w[i] = lo | (hi << 16);
+        }
+        return v;
+    }
+    const uint8_t* at = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)15);
+    const uint32_t off = (uint32_t)((uintptr_t)p & 15);
+    uint32_t x[13];
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (n > 0 && (c < 2 || off)) {
+            const uint8_t* a = at + c * 16;
+            if (a >= s.lo && a + 16 <= s.hi) {
+                q = *reinterpret_cast<const uint4*>(a);
+            } else {
+                uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (a + 2 * k >= s.lo && a + 2 * k < s.hi)
+                        e[k >> 1] |= (uint32_t) * reinterpret_cast<const uint16_t*>(a + 2 * k) << (16 * (k & 1));
+                q = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+        }
+        x[c * 4] = q.x; x[c * 4 + 1] = q.y; x[c * 4 + 2] = q.z; x[c * 4 + 3] = q.w;
+    }
+    x[12] = 0;
+    if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v.w[i] = (off & 2) ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
+        if (2 * i + 1 >= n) v.w[i] = 2 * i < n ? v.w[i] & 0xffffu : 0;
+    }
+    return v;
+}
+
+// 16 bf16 values to p, n of them valid.  The whole warp calls it, its lanes' columns following one another.
+template <bool WIDE>
+__device__ __forceinline__ void store16(uint16_t* p, const V16& v, int64_t n) {
+    if (WIDE) {
+        if (n >= 16) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
+                         "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+                         : "memory");
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < n) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
         return;
     }
-    const uint32_t w[4] = {v.w.x, v.w.y, v.w.z, v.w.w};
+    const int lane = threadIdx.x & 31;
+    const uint32_t off = (uint32_t)((uintptr_t)p & 15);          // the same in every lane: they are 32 bytes apart
+    const bool whole = n >= 16;
+    const bool joined = __shfl_down_sync(~0u, (int)whole, 1) && whole && lane < 31;      // writes into the next lane's columns
+    const bool covered = __shfl_up_sync(~0u, (int)joined, 1) && lane > 0;                // the lane before wrote this one's first
+    uint32_t x[13];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)(w[i >> 1] >> ((i & 1) * 16));
+    for (int i = 0; i < 8; ++i) x[i] = v.w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[8 + i] = __shfl_down_sync(~0u, v.w[i], 1);
+    x[12] = 0;
+    const int head = off ? (16 - (int)off) >> 1 : 0;             // elements before the first aligned chunk
+    const uint32_t skip = (uint32_t)head * 2;
+    if (skip & 8) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
+    }
+    if (skip & 4) {
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
+    }
+    if (skip & 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+    }
+    if (whole) {
+        *reinterpret_cast<uint4*>(p + head) = make_uint4(x[0], x[1], x[2], x[3]);
+        if (joined || head == 0) *reinterpret_cast<uint4*>(p + head + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+    const int from = whole ? (joined || head == 0 ? 16 : head + 8) : 0;      // what is left: [0, head) unless covered, [from, n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n && (i >= from || (i < head && !covered))) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
 }
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) { unpack(BfVec<8>{w}, f); }
 
-// Encodes a block of 128 columns held by 16 neighbouring lanes, 8 columns each (f, n of them valid,
-// the others 0): the whole warp calls it.
-__device__ __forceinline__ void encode8(float (&f)[8], int n, const Q8& q, int64_t row, int64_t col) {
+__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+// Encodes a block of 128 columns held by 8 neighbouring lanes, 16 columns each (f; n of them valid, the others
+// 0): the whole warp calls it.
+__device__ __forceinline__ void encode16(float2 (&f)[8], int64_t n, const Q8& q, int64_t row, int64_t col) {
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = q8_top(top, f[i]);
+    for (int i = 0; i < 8; ++i) top = q8_top(q8_top(top, f[i].x), f[i].y);
     if (isinf(top)) {
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            f[i] = q8_no_inf(f[i]);
-            top = q8_top(top, f[i]);
+            f[i] = make_float2(q8_no_inf(f[i].x), q8_no_inf(f[i].y));
+            top = q8_top(q8_top(top, f[i].x), f[i].y);
         }
     }
 #pragma unroll
-    for (int k = 1; k < 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+    for (int k = 1; k < 8; k <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
     const uint32_t byte = q8_scale_byte(top);
-    const float inv = q8_inverse(byte);
-    const uint2 w = make_uint2(q8_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                               q8_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-    if (n <= 0) return;
-    uint8_t* p = q.codes + row * q.ld + col;
-    if (n >= 8) {
-        __stcs(reinterpret_cast<uint2*>(p), w);
-    } else {
-        for (int i = 0; i < n; ++i) p[i] = (uint8_t)((i < 4 ? w.x : w.y) >> ((i & 3) * 8));
+    const float2 inv = make_float2(q8_inverse(byte), q8_inverse(byte));
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 a = q8_mul2(f[2 * k], inv), b = q8_mul2(f[2 * k + 1], inv);
+        w[k] = q8_pack4(a.x, a.y, b.x, b.y);
     }
+    if (n <= 0) return;
+    store_codes(q.codes + row * q.ld + col, make_uint4(w[0], w[1], w[2], w[3]), n < 16 ? (int)n : 16);
     if ((col & 127) == 0) q.scales[row * q.lds + (col >> 7)] = (uint8_t)byte;
 }
 
@@ -73,6 +171,7 @@ __device__ __forceinline__ float block_sum(float x, float* sh) {
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(~0u, x, k);
     const int warps = blockDim.x >> 5;
+    if (warps == 1) return x;
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
     __syncthreads();
     float sum = 0.f;
@@ -97,6 +196,7 @@ __device__ __forceinline__ float2 block_sum2(float x, float2* sh) {
         v = make_float2(s.x, (v.y + o.y) + s.y);
     }
     const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
     v = sh[0];
@@ -123,16 +223,30 @@ __device__ __forceinline__ float2 inverse_root(float2 sum, float n, float eps) {
     return make_float2(hi, fmaf(r, part, r - hi));
 }
 
-// t * r * w rounded once, and where that lands exactly on what may be the middle between two codes
-// (the low 19 bits of the mantissa are 0), moved by one bit to the side of the unrounded product.
-__device__ __forceinline__ float norm_output(float t, float2 r, float w) {
-    const float p = t * r.x, rest = fmaf(t, r.x, -p) + t * r.y;
-    const float y = fmaf(p, w, rest * w);
-    if ((__float_as_uint(y) & 0x7ffffu) == 0 && y != 0.f && isfinite(y)) {
-        const float off = fmaf(p, w, -y) + rest * w;
-        if (off != 0.f) return __uint_as_float(__float_as_uint(y) + ((off > 0.f) == (y > 0.f) ? 1 : -1));
+// t * r * w rounded once, and where that lands exactly on what may be the middle between two codes (the low 19
+// bits of the mantissa are 0), moved by one bit to the side of the unrounded product.
+__device__ __forceinline__ void norm_outputs(const float2 (&t)[8], float2 r, const V16& weight, float2 (&y)[8]) {
+    const float2 hi = make_float2(r.x, r.x), lo = make_float2(r.y, r.y), minus = make_float2(-1.f, -1.f);
+    uint32_t low = ~0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 w = pair_of(weight.w[i]);
+        const float2 p = q8_mul2(t[i], hi), rest = q8_fma2(t[i], lo, q8_fma2(t[i], hi, q8_mul2(p, minus)));
+        y[i] = q8_fma2(p, w, q8_mul2(rest, w));
+        low = min(low, min(__float_as_uint(y[i].x) << 13, __float_as_uint(y[i].y) << 13));
     }
-    return y;
+    if (low) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 w = pair_of(weight.w[i]);
+        auto nudge = [&](float t, float w, float& y) {
+            if ((__float_as_uint(y) << 13) != 0 || y == 0.f || !isfinite(y)) return;
+            const float p = t * r.x, rest = fmaf(t, r.y, fmaf(t, r.x, -p)), off = fmaf(p, w, -y) + rest * w;
+            if (off != 0.f) y = __uint_as_float(__float_as_uint(y) + ((off > 0.f) == (y > 0.f) ? 1 : -1));
+        };
+        nudge(t[i].x, w.x, y[i].x);
+        nudge(t[i].y, w.y, y[i].y);
+    }
 }
 
 // ------------------------------------------------------------------ norm, forward
@@ -146,69 +260,92 @@ struct NormArgs {
     float* rstd;
 };
 
-// One CTA per row.  NV > 0: the row's sum stays in registers, NV vectors of 8 columns per thread.
-// NV = 0, for rows longer than registers hold: the row is read a second time (from L2).
+// A CTA takes rows blockIdx.x, + gridDim.x, ...  NV > 0: a row's sum stays in registers, NV vectors of 16 columns
+// per thread, and the next row's loads are under way while a row is reduced and written.  NV = 0, for rows
+// longer than that: the row is read a second time (from L2).
 template <int NV, bool WIDE>
 __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ NormArgs a) {
-    __shared__ float2 sh[32];
+    __shared__ float2 sh[2][16];
     dependent_launch_prologue();
-    const int64_t row = blockIdx.x;
-    const uint16_t* x = a.x + row * a.ldx;
-    const uint16_t* res = a.res ? a.res + row * a.ldr : nullptr;
-    const int64_t step = (int64_t)blockDim.x * 8, col0 = (int64_t)threadIdx.x * 8;
-    auto valid = [&](int64_t c) { return (int)(a.cols - c < 8 ? a.cols - c : 8); };
-    auto sum_at = [&](int64_t c, float (&t)[8]) {
-        const int n = valid(c);
-        const uint4 wx = load8<WIDE>(x + c, n);
-        unpack8(wx, t);
-        if (res) {
-            float r[8];
-            unpack8(load8<WIDE>(res + c, n), r);
+    constexpr int N1 = NV > 0 ? NV : 1;
+    const int64_t step = (int64_t)blockDim.x * 16, col0 = (int64_t)threadIdx.x * 16;
+    const Span sx = span_of(a.x, a.ldx, a.rows, a.cols), sr = span_of(a.res, a.ldr, a.rows, a.cols);
+    const Span sw = span_of(a.weight, 0, 1, a.cols);
+    auto squares = [](const float2 (&t)[8]) {
+        float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] += r[i];
+        for (int i = 0; i < 8; ++i) q = q8_fma2(t[i], t[i], q);
+        return q.x + q.y;
+    };
+    auto sums = [](const V16& x, const V16& r, float2 (&t)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 p = pair_of(x.w[i]), q = pair_of(r.w[i]);
+            t[i] = make_float2(p.x + q.x, p.y + q.y);
         }
     };
-    auto squares = [](const float (&t)[8]) {
-        float q = 0.f;
+    auto write = [&](int64_t row, int64_t c, float2 (&t)[8], float2 r, const V16& w) {
+        const int64_t n = a.cols - c;
+        float2 y[8];
+        norm_outputs(t, r, w, y);
+        encode16(y, n, a.y, row, c);
+        if (a.s) {
+            V16 v;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(t[i], t[i], q);
-        return q;
+            for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(t[i].x, t[i].y);
+            store16<WIDE>(a.s + row * a.lds + c, v, n);
+        }
+        if (a.s_q8.codes) encode16(t, n, a.s_q8, row, c);
     };
-    auto write = [&](int64_t c, float (&t)[8], float2 r) {
-        const int n = valid(c);
-        float w[8], y[8];
-        unpack8(load8<WIDE>(a.weight + c, n), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = norm_output(t[i], r, w[i]);
-        encode8(y, n, a.y, row, c);
-        if (a.s) store8<WIDE>(a.s + row * a.lds + c, t, n);
-        if (a.s_q8.codes) encode8(t, n, a.s_q8, row, c);
-    };
-    float sq = 0.f;
+    const V16 zero = {};
+    int turn = 0;
     if constexpr (NV > 0) {
-        float t[NV][8];
+        V16 w[N1], x[N1], r[N1];
+        auto fetch = [&](int64_t row) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            sum_at(col0 + v * step, t[v]);
-            sq += squares(t[v]);
+            for (int v = 0; v < N1; ++v) {
+                const int64_t c = col0 + v * step;
+                x[v] = load16<WIDE>(a.x + row * a.ldx + c, a.cols - c, sx);
+                r[v] = a.res ? load16<WIDE>(a.res + row * a.ldr + c, a.cols - c, sr) : zero;
+            }
+        };
+        fetch(blockIdx.x);
+#pragma unroll
+        for (int v = 0; v < N1; ++v) w[v] = load16<WIDE>(a.weight + col0 + v * step, a.cols - col0 - v * step, sw);
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+            float2 t[N1][8];
+            float sq = 0.f;
+#pragma unroll
+            for (int v = 0; v < N1; ++v) {
+                sums(x[v], r[v], t[v]);
+                sq += squares(t[v]);
+            }
+            if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.eps);
+#pragma unroll
+            for (int v = 0; v < N1; ++v)
+                if (v * step < a.cols) write(row, col0 + v * step, t[v], root, w[v]);
+            if (a.rstd && threadIdx.x == 0) a.rstd[row] = root.x;
         }
-        const float2 r = inverse_root(block_sum2(sq, sh), (float)a.cols, a.eps);
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (v * step < a.cols) write(col0 + v * step, t[v], r);
-        if (a.rstd && threadIdx.x == 0) a.rstd[row] = r.x;
     } else {
-        float t[8];
-        for (int64_t c = col0; c - col0 < a.cols; c += step) {
-            sum_at(c, t);
-            sq += squares(t);
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+            float2 t[8];
+            auto sum_at = [&](int64_t c) {
+                const V16 x = load16<WIDE>(a.x + row * a.ldx + c, a.cols - c, sx);
+                sums(x, a.res ? load16<WIDE>(a.res + row * a.ldr + c, a.cols - c, sr) : zero, t);
+            };
+            float sq = 0.f;
+            for (int64_t c = col0; c - col0 < a.cols; c += step) {
+                sum_at(c);
+                sq += squares(t);
+            }
+            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.eps);
+            for (int64_t c = col0; c - col0 < a.cols; c += step) {
+                sum_at(c);
+                write(row, c, t, root, load16<WIDE>(a.weight + c, a.cols - c, sw));
+            }
+            if (a.rstd && threadIdx.x == 0) a.rstd[row] = root.x;
         }
-        const float2 r = inverse_root(block_sum2(sq, sh), (float)a.cols, a.eps);
-        for (int64_t c = col0; c - col0 < a.cols; c += step) {
-            sum_at(c, t);
-            write(c, t, r);
-        }
-        if (a.rstd && threadIdx.x == 0) a.rstd[row] = r.x;
     }
 }
 
@@ -220,138 +357,166 @@ struct NormBackArgs {
     const float* rstd;
     uint16_t* dx;
     float* partials;
+    int64_t pitch;           // floats between rows of partials: cols, or that rounded up to a multiple of 16
     int64_t lddy, lds, ldds, lddx, rows, cols;
 };
 
-// Each CTA takes rows blockIdx.x, + gridDim.x, ... and keeps its part of dw: thread t owns the columns
-// of its vectors in every row, in registers (NV > 0) or in its row of `partials` (NV = 0).
+// A CTA takes rows blockIdx.x, + gridDim.x, ... and keeps its part of dw: thread t owns the columns of its
+// vectors in every row, in registers (NV > 0) or in its row of `partials` (NV = 0).  With NV > 0 the next
+// row's loads are under way while a row is reduced and written.
 template <int NV, bool WIDE>
 __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBackArgs a) {
-    __shared__ float sh[2][32];
+    __shared__ float sh[2][16];
     dependent_launch_prologue();
     constexpr int N1 = NV > 0 ? NV : 1;
-    const int64_t step = (int64_t)blockDim.x * 8, col0 = (int64_t)threadIdx.x * 8;
-    auto valid = [&](int64_t c) { return (int)(a.cols - c < 8 ? a.cols - c : 8); };
-    // dy and the normalised sum of 8 columns
-    auto inputs = [&](int64_t row, int64_t c, float r, float (&dy)[8], float (&xh)[8]) {
-        const int n = valid(c);
-        unpack8(load8<WIDE>(a.dy + row * a.lddy + c, n), dy);
-        if (a.s_q8.codes) {
-            const uint8_t* p = a.s_q8.codes + row * a.s_q8.ld + c;
-            uint2 w = make_uint2(0, 0);
-            float q = 0.f;
-            if (n > 0) q = q8_scale(a.s_q8.scales[row * a.s_q8.lds + (c >> 7)]);
-            if (n >= 8) {
-                w = __ldcs(reinterpret_cast<const uint2*>(p));
-            } else {
-                for (int i = 0; i < n; ++i) (i < 4 ? w.x : w.y) |= (uint32_t)p[i] << ((i & 3) * 8);
-            }
-            q8_unpack4(w.x, q, xh);
-            q8_unpack4(w.y, q, xh + 4);
+    const int64_t step = (int64_t)blockDim.x * 16, col0 = (int64_t)threadIdx.x * 16;
+    const Span sy = span_of(a.dy, a.lddy, a.rows, a.cols), ss = span_of(a.s, a.lds, a.rows, a.cols);
+    const Span sd = span_of(a.ds, a.ldds, a.rows, a.cols), sw = span_of(a.weight, 0, 1, a.cols);
+    const bool kept8 = a.s_q8.codes != nullptr;
+    struct Row {
+        V16 dy, s, ds;           // s: bf16 words, or 16 codes and their scale byte in s.w[0 .. 4]
+    };
+    auto fetch = [&](int64_t row, int64_t c, Row& v) {
+        const int64_t n = a.cols - c;
+        v.dy = load16<WIDE>(a.dy + row * a.lddy + c, n, sy);
+        if (kept8) {
+            const uint4 w = load_codes(a.s_q8.codes + row * a.s_q8.ld + c, n < 0 ? 0 : n > 16 ? 16 : (int)n);
+            v.s.w[0] = w.x; v.s.w[1] = w.y; v.s.w[2] = w.z; v.s.w[3] = w.w;
+            v.s.w[4] = n > 0 ? a.s_q8.scales[row * a.s_q8.lds + (c >> 7)] : 0;
         } else {
-            unpack8(load8<WIDE>(a.s + row * a.lds + c, n), xh);
+            v.s = load16<WIDE>(a.s + row * a.lds + c, n, ss);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xh[i] *= r;
+        if (a.ds) v.ds = load16<WIDE>(a.ds + row * a.ldds + c, n, sd);
     };
-    auto weight_at = [&](int64_t c, float (&w)[8]) { unpack8(load8<WIDE>(a.weight + c, valid(c)), w); };
-    auto dot = [](const float (&dy)[8], const float (&w)[8], const float (&xh)[8]) {
-        float d = 0.f;
+    // the normalised sum
+    auto normalised = [&](const Row& v, float r, float2 (&xh)[8]) {
+        if (kept8) {
+            const float e = q8_scale(v.s.w[4]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d = fmaf(dy[i] * w[i], xh[i], d);
-        return d;
-    };
-    auto write = [&](int64_t row, int64_t c, float r, float along, const float (&dy)[8], const float (&w)[8],
-                     const float (&xh)[8]) {
-        const int n = valid(c);
-        float o[8];
+            for (int i = 0; i < 8; ++i) xh[i] = q8_mul2(q8_mul2(q8_unpack2(v.s.w[i >> 1] >> ((i & 1) * 16)), make_float2(e, e)), make_float2(r, r));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = r * (dy[i] * w[i] - xh[i] * along);
-        if (a.ds) {
-            float d[8];
-            unpack8(load8<WIDE>(a.ds + row * a.ldds + c, n), d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += d[i];
+            for (int i = 0; i < 8; ++i) xh[i] = q8_mul2(pair_of(v.s.w[i]), make_float2(r, r));
         }
-        store8<WIDE>(a.dx + row * a.lddx + c, o, n);
+    };
+    auto dot = [](const Row& v, const V16& w, const float2 (&xh)[8]) {
+        float2 d = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d = q8_fma2(q8_mul2(pair_of(v.dy.w[i]), pair_of(w.w[i])), xh[i], d);
+        return d.x + d.y;
+    };
+    auto write = [&](int64_t row, int64_t c, float r, float along, const Row& v, const V16& w, const float2 (&xh)[8]) {
+        V16 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 g = q8_mul2(pair_of(v.dy.w[i]), pair_of(w.w[i]));
+            float2 x = q8_fma2(xh[i], make_float2(-along, -along), g);
+            x = a.ds ? q8_fma2(x, make_float2(r, r), pair_of(v.ds.w[i])) : q8_mul2(x, make_float2(r, r));
+            o.w[i] = pack_bf16x2(x.x, x.y);
+        }
+        store16<WIDE>(a.dx + row * a.lddx + c, o, a.cols - c);
     };
     const float inv_cols = 1.f / (float)a.cols;
-    float* part = a.partials + (int64_t)blockIdx.x * a.cols;
-    float dw[N1][8];
-#pragma unroll
-    for (int v = 0; v < N1; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+    float* part = a.partials + (int64_t)blockIdx.x * a.pitch;
     int turn = 0;
-    bool first = true;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, first = false) {
-        const float r = a.rstd[row];
-        float d = 0.f;
-        if constexpr (NV > 0) {
-            float dy[NV][8], xh[NV][8], w[8];
+    if constexpr (NV > 0) {
+        V16 w[N1];
+        Row next[N1];
+        float2 dw[N1][8];
+        float r_next = a.rstd[blockIdx.x];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) inputs(row, col0 + v * step, r, dy[v], xh[v]);
+        for (int v = 0; v < N1; ++v) {
+            fetch(blockIdx.x, col0 + v * step, next[v]);
+            w[v] = load16<WIDE>(a.weight + col0 + v * step, a.cols - col0 - v * step, sw);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                weight_at(col0 + v * step, w);
-                d += dot(dy[v], w, xh[v]);
+            for (int i = 0; i < 8; ++i) dw[v][i] = make_float2(0.f, 0.f);
+        }
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+            Row now[N1];
+            float2 xh[N1][8];
+            const float r = r_next;
+            float d = 0.f;
+#pragma unroll
+            for (int v = 0; v < N1; ++v) {
+                now[v] = next[v];
+                normalised(now[v], r, xh[v]);
+                d += dot(now[v], w[v], xh[v]);
+            }
+            if (row + gridDim.x < a.rows) {
+                r_next = a.rstd[row + gridDim.x];
+#pragma unroll
+                for (int v = 0; v < N1; ++v) fetch(row + gridDim.x, col0 + v * step, next[v]);
             }
             const float along = block_sum(d, sh[turn]) * inv_cols;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                weight_at(col0 + v * step, w);
-                write(row, col0 + v * step, r, along, dy[v], w, xh[v]);
+            for (int v = 0; v < N1; ++v) {
+                write(row, col0 + v * step, r, along, now[v], w[v], xh[v]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dw[v][i] = fmaf(dy[v][i], xh[v][i], dw[v][i]);
-            }
-        } else {
-            float dy[8], xh[8], w[8];
-            for (int64_t c = col0; c < a.cols; c += step) {
-                inputs(row, c, r, dy, xh);
-                weight_at(c, w);
-                d += dot(dy, w, xh);
-            }
-            const float along = block_sum(d, sh[turn]) * inv_cols;
-            for (int64_t c = col0; c < a.cols; c += step) {
-                inputs(row, c, r, dy, xh);
-                weight_at(c, w);
-                write(row, c, r, along, dy, w, xh);
-                const int n = valid(c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) part[c + i] = fmaf(dy[i], xh[i], first ? 0.f : part[c + i]);
+                for (int i = 0; i < 8; ++i) dw[v][i] = q8_fma2(pair_of(now[v].dy.w[i]), xh[v][i], dw[v][i]);
             }
         }
-    }
-    if constexpr (NV > 0) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
+        for (int v = 0; v < N1; ++v) {
             const int64_t c = col0 + v * step;
-            const int n = valid(c);
+            if (c >= a.cols) continue;
+            if ((a.pitch & 15) == 0) {           // room for the last vector's columns past cols
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) part[c + i] = dw[v][i];
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<float4*>(part + c + k * 4) =
+                        make_float4(dw[v][2 * k].x, dw[v][2 * k].y, dw[v][2 * k + 1].x, dw[v][2 * k + 1].y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < a.cols) part[c + i] = (i & 1) ? dw[v][i >> 1].y : dw[v][i >> 1].x;
+            }
+        }
+    } else {
+        bool first = true;
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, first = false) {
+            const float r = a.rstd[row];
+            float d = 0.f;
+            Row v;
+            float2 xh[8];
+            for (int64_t c = col0; c - col0 < a.cols; c += step) {
+                fetch(row, c, v);
+                normalised(v, r, xh);
+                d += dot(v, load16<WIDE>(a.weight + c, a.cols - c, sw), xh);
+            }
+            const float along = block_sum(d, sh[turn]) * inv_cols;
+            for (int64_t c = col0; c - col0 < a.cols; c += step) {
+                fetch(row, c, v);
+                normalised(v, r, xh);
+                write(row, c, r, along, v, load16<WIDE>(a.weight + c, a.cols - c, sw), xh);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 d = pair_of(v.dy.w[i >> 1]);
+                    if (c + i < a.cols)
+                        part[c + i] = (i & 1) ? fmaf(d.y, xh[i >> 1].y, first ? 0.f : part[c + i]) : fmaf(d.x, xh[i >> 1].x, first ? 0.f : part[c + i]);
+                }
+            }
         }
     }
 }
 
-// dw from the partial sums: a CTA takes 32 columns, its 8 warps a share of the partials each, added in
-// index order within a warp and over the warps.
-__global__ void __launch_bounds__(256) k_rmsnorm_dw(const float* partials, int64_t count, int64_t cols, uint16_t* dw,
-                                                    float scale, int first) {
-    __shared__ float sh[8][32];
+// dw from the partial sums: a CTA takes 16 columns, 16 groups of its threads a share of the partials each, added
+// in index order within a group and then over the groups.
+__global__ void __launch_bounds__(256) k_rmsnorm_dw(const float* partials, int64_t count, int64_t pitch, int64_t cols,
+                                                    uint16_t* dw, float scale, int first) {
+    __shared__ float sh[16][16];
     dependent_launch_prologue();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + lane;
     float sum = 0.f;
-    if (c < cols)
-        for (int64_t k = warp; k < count; k += 8) sum += partials[k * cols + c];
-    sh[warp][lane] = sum;
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t k = group; k < count; k += 16) sum += partials[k * pitch + c];
+    }
+    sh[group][lane] = sum;
     __syncthreads();
-    if (warp == 0 && c < cols) {
+    if (group == 0 && c < cols) {
         float all = sh[0][lane];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) all += sh[k][lane];
+        for (int k = 1; k < 16; ++k) all += sh[k][lane];
         all *= scale;
         if (!first) all += bf16_to_f32(dw[c]);
         dw[c] = f32_to_bf16(all);
@@ -368,35 +533,32 @@ struct GateArgs {
 
 constexpr int kGateThreads = 128;
 
-// A CTA takes 1024 columns of a row, 8 per thread.
+// A CTA takes 2048 columns of a row, 16 per thread.
 template <bool WIDE>
 __global__ void __launch_bounds__(kGateThreads) k_swiglu_q8(const __grid_constant__ GateArgs a) {
     dependent_launch_prologue();
-    const int64_t row = blockIdx.x, c = ((int64_t)blockIdx.y * kGateThreads + threadIdx.x) * 8;
-    const int n = (int)(a.cols - c < 8 ? a.cols - c : 8);
-    const uint4 wg = load8<WIDE>(a.gate + row * a.ldg + c, n), wu = load8<WIDE>(a.up + row * a.ldu + c, n);
-    float g[8], u[8], h[8];
-    unpack8(wg, g);
-    unpack8(wu, u);
+    const int64_t row = blockIdx.x, c = ((int64_t)blockIdx.y * kGateThreads + threadIdx.x) * 16, n = a.cols - c;
+    const V16 wg = load16<WIDE>(a.gate + row * a.ldg + c, n, span_of(a.gate, a.ldg, a.rows, a.cols));
+    const V16 wu = load16<WIDE>(a.up + row * a.ldu + c, n, span_of(a.up, a.ldu, a.rows, a.cols));
+    float2 g[8], u[8], h[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float2 x = make_float2(g[i], g[i + 1]);
-        const float2 y = q8_mul2(q8_mul2(x, q8_sigmoid2(x)), make_float2(u[i], u[i + 1]));
-        h[i] = y.x;
-        h[i + 1] = y.y;
+    for (int i = 0; i < 8; ++i) {
+        g[i] = pair_of(wg.w[i]);
+        u[i] = pair_of(wu.w[i]);
+        h[i] = q8_mul2(q8_mul2(g[i], q8_sigmoid2(g[i])), u[i]);
     }
-    encode8(h, n, a.h, row, c);
-    if (a.gate_q.codes) encode8(g, n, a.gate_q, row, c);
-    if (a.up_q.codes) encode8(u, n, a.up_q, row, c);
+    encode16(h, n, a.h, row, c);
+    if (a.gate_q.codes) encode16(g, n, a.gate_q, row, c);
+    if (a.up_q.codes) encode16(u, n, a.up_q, row, c);
 }
 
-// Threads and register vectors for a row of `cols` columns: the fewest vectors per thread that keep the
-// CTA within `most` threads; nv = 0 when the row does not fit in registers.
-void row_shape(int64_t cols, int most, int* threads, int* nv) {
-    const int64_t vecs = (cols + 7) / 8;
-    for (int k = 1; k <= 4; k *= 2) {
+// Threads and register vectors for a row of `cols` columns: the fewest vectors per thread (at most two) that
+// keep the CTA within 512 threads; nv = 0 when the row does not fit in registers.
+void row_shape(int64_t cols, int* threads, int* nv) {
+    const int64_t vecs = (cols + 15) / 16;
+    for (int k = 1; k <= 2; ++k) {
         const int64_t need = ((vecs + k - 1) / k + 31) / 32 * 32;
-        if (need <= most) {
+        if (need <= 512) {
             *threads = (int)need;
             *nv = k;
             return;
@@ -409,12 +571,13 @@ void row_shape(int64_t cols, int most, int* threads, int* nv) {
 template <bool WIDE>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     int threads, nv;
-    row_shape(a.cols, 512, &threads, &nv);
-    const dim3 grid((unsigned)a.rows), block(threads);
+    row_shape(a.cols, &threads, &nv);
+    // as many CTAs as are resident: 768 threads per SM with two vectors and their prefetch in registers
+    const int64_t room = (int64_t)q8_host::sm_count() * (768 / threads < 1 ? 1 : 768 / threads);
+    const dim3 grid((unsigned)(a.rows < room ? a.rows : room)), block(threads);
     switch (nv) {
         case 1: return launch_kernel(k_rmsnorm_q8<1, WIDE>, grid, block, 0, st, a);
         case 2: return launch_kernel(k_rmsnorm_q8<2, WIDE>, grid, block, 0, st, a);
-        case 4: return launch_kernel(k_rmsnorm_q8<4, WIDE>, grid, block, 0, st, a);
         default: return launch_kernel(k_rmsnorm_q8<0, WIDE>, grid, block, 0, st, a);
     }
 }
@@ -422,12 +585,11 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
 template <bool WIDE>
 cudaError_t launch_norm_back(const NormBackArgs& a, int parts, cudaStream_t st) {
     int threads, nv;
-    row_shape(a.cols, 512, &threads, &nv);
+    row_shape(a.cols, &threads, &nv);
     const dim3 grid((unsigned)parts), block(threads);
     switch (nv) {
         case 1: return launch_kernel(k_rmsnorm_backward<1, WIDE>, grid, block, 0, st, a);
         case 2: return launch_kernel(k_rmsnorm_backward<2, WIDE>, grid, block, 0, st, a);
-        case 4: return launch_kernel(k_rmsnorm_backward<4, WIDE>, grid, block, 0, st, a);
         default: return launch_kernel(k_rmsnorm_backward<0, WIDE>, grid, block, 0, st, a);
     }
 }
@@ -467,7 +629,7 @@ extern "C" int zs_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, i
     a.eps = eps;
     a.s = (uint16_t*)s;
     a.rstd = rstd;
-    const bool w = wide(x, ldx) && (!residual || wide(residual, ldr)) && wide(weight, 0) && (!s || wide(s, lds));
+    const bool w = wide(x, ldx, 32) && (!residual || wide(residual, ldr, 32)) && wide(weight, 0, 32) && (!s || wide(s, lds, 32));
     const cudaStream_t st = (cudaStream_t)stream;
     return cuda_status(fn, w ? zs::launch_norm<true>(a, st) : zs::launch_norm<false>(a, st));
 }
@@ -507,17 +669,22 @@ extern "C" int zs_rmsnorm_backward(const void* dy, int64_t lddy, const void* s, 
     a.lddx = lddx;
     a.rows = rows;
     a.cols = cols;
-    const bool w = wide(dy, lddy) && (!s || wide(s, lds)) && wide(weight, 0) && (!ds || wide(ds, ldds)) && wide(dx, lddx);
+    const bool w = wide(dy, lddy, 32) && (!s || wide(s, lds, 32)) && wide(weight, 0, 32) && (!ds || wide(ds, ldds, 32)) && wide(dx, lddx, 32);
     const cudaStream_t st = (cudaStream_t)stream;
+    // rows of partial sums start at multiples of 16 floats where the scratch holds one such row, so an odd width
+    // uses a few rows of scratch less
+    a.pitch = (cols + 15) / 16 * 16;
+    if (n_partials > int64_t(1) << 30) n_partials = int64_t(1) << 30;
+    if (n_partials * cols < a.pitch) a.pitch = cols;
     int64_t parts = 2 * (int64_t)sm_count();
-    if (parts > n_partials) parts = n_partials;
+    if (parts > n_partials * cols / a.pitch) parts = n_partials * cols / a.pitch;
     if (parts > ZS_Q8_MAX_PARTIALS) parts = ZS_Q8_MAX_PARTIALS;
     if (parts > rows) parts = rows;
     if (parts > 0)
         ZS_Q8_TRY(cuda_status(fn, w ? zs::launch_norm_back<true>(a, (int)parts, st)
                                     : zs::launch_norm_back<false>(a, (int)parts, st)));
-    return cuda_status(fn, zs::launch_kernel(zs::k_rmsnorm_dw, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st,
-                                             (const float*)partials, parts, cols, (uint16_t*)dw, scale, (int)first));
+    return cuda_status(fn, zs::launch_kernel(zs::k_rmsnorm_dw, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, st,
+                                             (const float*)partials, parts, a.pitch, cols, (uint16_t*)dw, scale, (int)first));
 }
 
 extern "C" int zs_swiglu_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64_t rows, int64_t cols,
@@ -540,11 +707,11 @@ extern "C" int zs_swiglu_q8(const void* gate, int64_t ldg, const void* up, int64
     a.ldu = ldu;
     a.rows = rows;
     a.cols = cols;
-    const int64_t pieces = (cols + zs::kGateThreads * 8 - 1) / (zs::kGateThreads * 8);
+    const int64_t pieces = (cols + zs::kGateThreads * 16 - 1) / (zs::kGateThreads * 16);
     if (pieces > 65535) return fail(fn, "cols too large for one launch");
     const dim3 grid((unsigned)rows, (unsigned)pieces), block(zs::kGateThreads);
     const cudaStream_t st = (cudaStream_t)stream;
-    return cuda_status(fn, wide(gate, ldg) && wide(up, ldu) ? zs::launch_kernel(zs::k_swiglu_q8<true>, grid, block, 0, st, a)
+    return cuda_status(fn, wide(gate, ldg, 32) && wide(up, ldu, 32) ? zs::launch_kernel(zs::k_swiglu_q8<true>, grid, block, 0, st, a)
                                                             : zs::launch_kernel(zs::k_swiglu_q8<false>, grid, block, 0, st, a));
 }
 
