@@ -48,26 +48,21 @@ __device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& 
     }
     const uint8_t* at = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)15);
     const uint32_t off = (uint32_t)((uintptr_t)p & 15);
-    uint32_t x[13];
+    uint32_t x[12];
+    if (n >= 16 && at >= s.lo && at + 48 <= s.hi) {
+        const uint4* q = reinterpret_cast<const uint4*>(at);
+        const uint4 q0 = q[0], q1 = q[1], q2 = q[2];
+        x[0] = q0.x; x[1] = q0.y; x[2] = q0.z; x[3] = q0.w;
+        x[4] = q1.x; x[5] = q1.y; x[6] = q1.z; x[7] = q1.w;
+        x[8] = q2.x; x[9] = q2.y; x[10] = q2.z; x[11] = q2.w;
+    } else {                                     // the end of a row or of the matrix
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (n > 0 && (c < 2 || off)) {
-            const uint8_t* a = at + c * 16;
-            if (a >= s.lo && a + 16 <= s.hi) {
-                q = *reinterpret_cast<const uint4*>(a);
-            } else {
-                uint32_t e[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (a + 2 * k >= s.lo && a + 2 * k < s.hi)
-                        e[k >> 1] |= (uint32_t) * reinterpret_cast<const uint16_t*>(a + 2 * k) << (16 * (k & 1));
-                q = make_uint4(e[0], e[1], e[2], e[3]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+            v.w[i] = lo | (hi << 16);
         }
-        x[c * 4] = q.x; x[c * 4 + 1] = q.y; x[c * 4 + 2] = q.z; x[c * 4 + 3] = q.w;
+        return v;
     }
-    x[12] = 0;
     if (off & 8) {
 #pragma unroll
         for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
@@ -77,10 +72,7 @@ __device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& 
         for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v.w[i] = (off & 2) ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
-        if (2 * i + 1 >= n) v.w[i] = 2 * i < n ? v.w[i] & 0xffffu : 0;
-    }
+    for (int i = 0; i < 8; ++i) v.w[i] = __funnelshift_r(x[i], x[i + 1], (off & 2) * 8);
     return v;
 }
 
@@ -104,34 +96,36 @@ __device__ __forceinline__ void store16(uint16_t* p, const V16& v, int64_t n) {
     const bool whole = n >= 16;
     const bool joined = __shfl_down_sync(~0u, (int)whole, 1) && whole && lane < 31;      // writes into the next lane's columns
     const bool covered = __shfl_up_sync(~0u, (int)joined, 1) && lane > 0;                // the lane before wrote this one's first
-    uint32_t x[13];
+    uint32_t x[12];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = v.w[i];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[8 + i] = __shfl_down_sync(~0u, v.w[i], 1);
-    x[12] = 0;
     const int head = off ? (16 - (int)off) >> 1 : 0;             // elements before the first aligned chunk
-    const uint32_t skip = (uint32_t)head * 2;
-    if (skip & 8) {
+    if (head & 4) {
 #pragma unroll
         for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
     }
-    if (skip & 4) {
+    if (head & 2) {
 #pragma unroll
         for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
     }
-    if (skip & 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], (head & 1) * 16);
+    const bool second = joined || head == 0;
     if (whole) {
         *reinterpret_cast<uint4*>(p + head) = make_uint4(x[0], x[1], x[2], x[3]);
-        if (joined || head == 0) *reinterpret_cast<uint4*>(p + head + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+        if (second) *reinterpret_cast<uint4*>(p + head + 8) = make_uint4(x[4], x[5], x[6], x[7]);
     }
-    const int from = whole ? (joined || head == 0 ? 16 : head + 8) : 0;      // what is left: [0, head) unless covered, [from, n)
+    // what is left, element by element: [0, head) unless covered, and what follows the chunks written
+    uint32_t rest = whole ? (second ? 0u : 0xffffu << (head + 8)) : n > 0 ? (1u << n) - 1 : 0u;
+    if (whole && !covered) rest |= (1u << head) - 1;
+    rest &= 0xffffu;
+    if (rest) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n && (i >= from || (i < head && !covered))) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
+        for (int i = 0; i < 16; ++i)
+            if (rest >> i & 1) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
+    }
 }
 
 __device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
@@ -165,15 +159,16 @@ __device__ __forceinline__ void encode16(float2 (&f)[8], int64_t n, const Q8& q,
     if ((col & 127) == 0) q.scales[row * q.lds + (col >> 7)] = (uint8_t)byte;
 }
 
-// Sum over the CTA's threads, the same bits in every thread; `sh` holds one float per warp and is free
-// again once every thread has passed a later barrier.
-__device__ __forceinline__ float block_sum(float x, float* sh) {
+// Sum over the `threads` threads of the caller's group (whole warps; barrier `id` is the group's own), the same
+// bits in every thread; `sh` holds one float per warp and is free again once every thread of the group has
+// passed a later barrier.
+__device__ __forceinline__ float group_sum(float x, float* sh, int threads, int id) {
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(~0u, x, k);
-    const int warps = blockDim.x >> 5;
+    const int warps = threads >> 5, warp = (threadIdx.x >> 5) % warps;
     if (warps == 1) return x;
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[warp] = x;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
     float sum = 0.f;
     for (int k = 0; k < warps; ++k) sum += sh[k];
     return sum;
@@ -209,18 +204,19 @@ __device__ __forceinline__ float2 block_sum2(float x, float2* sh) {
 
 // 1 / sqrt(sum / n + eps) as an fp32 value and what rounding took from it.  An output code goes to its
 // neighbour where fp32 rounding carries a value across the middle between two codes; with the factor
-// common to a whole row in two words and one rounding per output (norm_output) that is all but gone, at
-// a few operations per row.
-__device__ __forceinline__ float2 inverse_root(float2 sum, float n, float eps) {
-    const float q = __fdiv_rn(sum.x, n);
-    const float rest = (fmaf(-q, n, sum.x) + sum.y) / n;
+// common to a whole row in two words and one rounding per output (norm_outputs) that is all but gone, at
+// a few operations per row: one Newton step on the hardware's reciprocal root, whose residual
+// 1 - (v + rest) r^2 is taken from exact products.
+__device__ __forceinline__ float2 inverse_root(float2 sum, float n, float inv_n, float eps) {
+    const float q = sum.x * inv_n;
     const float2 v = two_sum(q, eps);
-    const float root = __fsqrt_rn(v.x), r = __fdiv_rn(1.f, root);
-    // v + rest = root^2 + d and 1 / root = r (1 + e): 1 / sqrt(v + rest) = r (1 + e - d / (2 root^2))
-    const float d = (v.y + rest) - fmaf(root, root, -v.x), e = fmaf(-r, root, 1.f);
-    const float part = e - 0.5f * d * r * r, hi = fmaf(r, part, r);
+    const float rest = v.y + (fmaf(-q, n, sum.x) + sum.y) * inv_n;
+    const float r = rsqrtf(v.x);
+    const float h = v.x * r, hl = fmaf(v.x, r, -h);
+    const float off = fmaf(-h, r, 1.f) - (hl + rest * r) * r;
+    const float hi = fmaf(0.5f * r, off, r);
     if (!(isfinite(hi) && hi > 0.f)) return make_float2(r, 0.f);       // sums of 0, infinity or NaN
-    return make_float2(hi, fmaf(r, part, r - hi));
+    return make_float2(hi, fmaf(0.5f * r, off, r - hi));
 }
 
 // t * r * w rounded once, and where that lands exactly on what may be the middle between two codes (the low 19
@@ -254,7 +250,7 @@ __device__ __forceinline__ void norm_outputs(const float2 (&t)[8], float2 r, con
 struct NormArgs {
     const uint16_t *x, *res, *weight;
     int64_t ldx, ldr, lds, rows, cols;
-    float eps;
+    float eps, inv_cols;
     Q8 y, s_q8;
     uint16_t* s;
     float* rstd;
@@ -280,8 +276,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ Norm
     auto sums = [](const V16& x, const V16& r, float2 (&t)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 p = pair_of(x.w[i]), q = pair_of(r.w[i]);
-            t[i] = make_float2(p.x + q.x, p.y + q.y);
+            t[i] = q8_add2(pair_of(x.w[i]), pair_of(r.w[i]));
         }
     };
     auto write = [&](int64_t row, int64_t c, float2 (&t)[8], float2 r, const V16& w) {
@@ -321,7 +316,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ Norm
                 sq += squares(t[v]);
             }
             if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.eps);
+            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.inv_cols, a.eps);
 #pragma unroll
             for (int v = 0; v < N1; ++v)
                 if (v * step < a.cols) write(row, col0 + v * step, t[v], root, w[v]);
@@ -339,7 +334,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ Norm
                 sum_at(c);
                 sq += squares(t);
             }
-            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.eps);
+            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.inv_cols, a.eps);
             for (int64_t c = col0; c - col0 < a.cols; c += step) {
                 sum_at(c);
                 write(row, c, t, root, load16<WIDE>(a.weight + c, a.cols - c, sw));
@@ -359,27 +354,35 @@ struct NormBackArgs {
     float* partials;
     int64_t pitch;           // floats between rows of partials: cols, or that rounded up to a multiple of 16
     int64_t lddy, lds, ldds, lddx, rows, cols;
+    int threads;             // of a group
+    int parts;               // rows of partials written: the grid
 };
 
-// A CTA takes rows blockIdx.x, + gridDim.x, ... and keeps its part of dw: thread t owns the columns of its
-// vectors in every row, in registers (NV > 0) or in its row of `partials` (NV = 0).  With NV > 0 the next
-// row's loads are under way while a row is reduced and written.
-template <int NV, bool WIDE>
+// The CTA's threads are groups of `threads`, a row each at a time; a group takes every (groups of the grid)th row
+// and keeps its part of dw: a thread owns the columns of its vectors in every row, in registers (NV > 0) or
+// in the CTA's row of `partials` (NV = 0, one group).  With one vector the next row's loads are under way while a
+// row is reduced and written.  The groups' parts are added in shared memory, so that narrow rows fill the SM
+// without more rows of partials.
+template <int NV, bool WIDE, bool GROUPED, bool KEPT8>
 __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBackArgs a) {
-    __shared__ float sh[2][16];
+    __shared__ float sums[16][2][16];            // per group and turn
+    extern __shared__ float parts_sh[];          // [group][columns of its threads], with more than one group
     dependent_launch_prologue();
     constexpr int N1 = NV > 0 ? NV : 1;
-    const int64_t step = (int64_t)blockDim.x * 16, col0 = (int64_t)threadIdx.x * 16;
+    const int groups = GROUPED ? blockDim.x / a.threads : 1, group = GROUPED ? threadIdx.x / a.threads : 0;
+    const int threads = GROUPED ? a.threads : blockDim.x, tid = threadIdx.x - group * threads;
+    const int64_t step = (int64_t)threads * 16, col0 = (int64_t)tid * 16;
+    const int64_t row0 = (int64_t)blockIdx.x * groups + group, stride = (int64_t)gridDim.x * groups;
+    float (*sh)[16] = sums[group];
     const Span sy = span_of(a.dy, a.lddy, a.rows, a.cols), ss = span_of(a.s, a.lds, a.rows, a.cols);
     const Span sd = span_of(a.ds, a.ldds, a.rows, a.cols), sw = span_of(a.weight, 0, 1, a.cols);
-    const bool kept8 = a.s_q8.codes != nullptr;
     struct Row {
         V16 dy, s, ds;           // s: bf16 words, or 16 codes and their scale byte in s.w[0 .. 4]
     };
     auto fetch = [&](int64_t row, int64_t c, Row& v) {
         const int64_t n = a.cols - c;
         v.dy = load16<WIDE>(a.dy + row * a.lddy + c, n, sy);
-        if (kept8) {
+        if constexpr (KEPT8) {
             const uint4 w = load_codes(a.s_q8.codes + row * a.s_q8.ld + c, n < 0 ? 0 : n > 16 ? 16 : (int)n);
             v.s.w[0] = w.x; v.s.w[1] = w.y; v.s.w[2] = w.z; v.s.w[3] = w.w;
             v.s.w[4] = n > 0 ? a.s_q8.scales[row * a.s_q8.lds + (c >> 7)] : 0;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
     };
     // the normalised sum
     auto normalised = [&](const Row& v, float r, float2 (&xh)[8]) {
-        if (kept8) {
+        if constexpr (KEPT8) {
             const float e = q8_scale(v.s.w[4]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) xh[i] = q8_mul2(q8_mul2(q8_unpack2(v.s.w[i >> 1] >> ((i & 1) * 16)), make_float2(e, e)), make_float2(r, r));
@@ -423,15 +426,15 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
         V16 w[N1];
         Row next[N1];
         float2 dw[N1][8];
-        float r_next = a.rstd[blockIdx.x];
+        float r_next = row0 < a.rows ? a.rstd[row0] : 0.f;
 #pragma unroll
         for (int v = 0; v < N1; ++v) {
-            fetch(blockIdx.x, col0 + v * step, next[v]);
+            if (row0 < a.rows) fetch(row0, col0 + v * step, next[v]);
             w[v] = load16<WIDE>(a.weight + col0 + v * step, a.cols - col0 - v * step, sw);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[v][i] = make_float2(0.f, 0.f);
         }
-        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
             Row now[N1];
             float2 xh[N1][8];
             const float r = r_next;
@@ -442,18 +445,36 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
                 normalised(now[v], r, xh[v]);
                 d += dot(now[v], w[v], xh[v]);
             }
-            if (row + gridDim.x < a.rows) {
-                r_next = a.rstd[row + gridDim.x];
-#pragma unroll
-                for (int v = 0; v < N1; ++v) fetch(row + gridDim.x, col0 + v * step, next[v]);
+            const bool more = row + stride < a.rows;
+            if (NV == 1 && more) {               // two vectors leave no registers for the next row's
+                r_next = a.rstd[row + stride];
+                fetch(row + stride, col0, next[0]);
             }
-            const float along = block_sum(d, sh[turn]) * inv_cols;
+            const float along = group_sum(d, sh[turn], threads, group + 1) * inv_cols;
 #pragma unroll
             for (int v = 0; v < N1; ++v) {
                 write(row, col0 + v * step, r, along, now[v], w[v], xh[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dw[v][i] = q8_fma2(pair_of(now[v].dy.w[i]), xh[v][i], dw[v][i]);
             }
+            if (NV > 1 && more) {
+                r_next = a.rstd[row + stride];
+#pragma unroll
+                for (int v = 0; v < N1; ++v) fetch(row + stride, col0 + v * step, next[v]);
+            }
+        }
+        if constexpr (GROUPED) {                 // the groups' parts, in order
+            float* mine = parts_sh + (int64_t)group * step + col0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(mine + k * 4) = make_float4(dw[0][2 * k].x, dw[0][2 * k].y, dw[0][2 * k + 1].x, dw[0][2 * k + 1].y);
+            __syncthreads();
+            for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+                float all = parts_sh[c];
+                for (int g = 1; g < groups; ++g) all += parts_sh[g * step + c];
+                part[c] = all;
+            }
+            return;
         }
 #pragma unroll
         for (int v = 0; v < N1; ++v) {
@@ -472,7 +493,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
         }
     } else {
         bool first = true;
-        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, first = false) {
+        for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1, first = false) {
             const float r = a.rstd[row];
             float d = 0.f;
             Row v;
@@ -482,7 +503,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
                 normalised(v, r, xh);
                 d += dot(v, load16<WIDE>(a.weight + c, a.cols - c, sw), xh);
             }
-            const float along = block_sum(d, sh[turn]) * inv_cols;
+            const float along = group_sum(d, sh[turn], threads, group + 1) * inv_cols;
             for (int64_t c = col0; c - col0 < a.cols; c += step) {
                 fetch(row, c, v);
                 normalised(v, r, xh);
@@ -498,28 +519,43 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
     }
 }
 
-// dw from the partial sums: a CTA takes 16 columns, 16 groups of its threads a share of the partials each, added
-// in index order within a group and then over the groups.
+// dw from the partial sums: a CTA takes 16 columns, 64 groups of four threads a share of the partials each,
+// added in index order within a group and then over the groups.
 __global__ void __launch_bounds__(256) k_rmsnorm_dw(const float* partials, int64_t count, int64_t pitch, int64_t cols,
                                                     uint16_t* dw, float scale, int first) {
-    __shared__ float sh[16][16];
+    __shared__ float sh[64][17];
     dependent_launch_prologue();
-    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 16 + lane;
-    float sum = 0.f;
-    if (c < cols) {
+    const int lane = threadIdx.x & 3, group = threadIdx.x >> 2;
+    const int64_t c = (int64_t)blockIdx.x * 16 + lane * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((pitch & 15) == 0) {                     // whole vectors: a row of partials has room past cols
 #pragma unroll 8
-        for (int64_t k = group; k < count; k += 16) sum += partials[k * pitch + c];
+        for (int64_t k = group; k < count; k += 64) {
+            const float4 x = *reinterpret_cast<const float4*>(partials + k * pitch + c);
+            sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+        }
+    } else {
+        for (int64_t k = group; k < count; k += 64) {
+            const float* x = partials + k * pitch + c;
+            sum = make_float4(sum.x + (c < cols ? x[0] : 0.f), sum.y + (c + 1 < cols ? x[1] : 0.f),
+                              sum.z + (c + 2 < cols ? x[2] : 0.f), sum.w + (c + 3 < cols ? x[3] : 0.f));
+        }
     }
-    sh[group][lane] = sum;
+    sh[group][lane * 4] = sum.x;
+    sh[group][lane * 4 + 1] = sum.y;
+    sh[group][lane * 4 + 2] = sum.z;
+    sh[group][lane * 4 + 3] = sum.w;
     __syncthreads();
-    if (group == 0 && c < cols) {
-        float all = sh[0][lane];
+    // 16 threads per column add four groups each, then the 16 partial sums in a fixed tree
+    const int col = threadIdx.x >> 4, part = threadIdx.x & 15;
+    float all = (sh[part * 4][col] + sh[part * 4 + 1][col]) + (sh[part * 4 + 2][col] + sh[part * 4 + 3][col]);
 #pragma unroll
-        for (int k = 1; k < 16; ++k) all += sh[k][lane];
+    for (int k = 1; k < 16; k <<= 1) all += __shfl_xor_sync(~0u, all, k);
+    const int64_t at = (int64_t)blockIdx.x * 16 + col;
+    if (part == 0 && at < cols) {
         all *= scale;
-        if (!first) all += bf16_to_f32(dw[c]);
-        dw[c] = f32_to_bf16(all);
+        if (!first) all += bf16_to_f32(dw[at]);
+        dw[at] = f32_to_bf16(all);
     }
 }
 
@@ -552,11 +588,11 @@ __global__ void __launch_bounds__(kGateThreads) k_swiglu_q8(const __grid_constan
     if (a.up_q.codes) encode16(u, n, a.up_q, row, c);
 }
 
-// Threads and register vectors for a row of `cols` columns: the fewest vectors per thread (at most two) that
-// keep the CTA within 512 threads; nv = 0 when the row does not fit in registers.
-void row_shape(int64_t cols, int* threads, int* nv) {
+// Threads and register vectors (of 16 columns, `least` to `most` of them) for a row of `cols` columns: the fewest vectors per thread that keep the CTA within 512 threads; nv = 0 when the row does not
+// fit in registers.
+void row_shape(int64_t cols, int least, int most, int* threads, int* nv) {
     const int64_t vecs = (cols + 15) / 16;
-    for (int k = 1; k <= 2; ++k) {
+    for (int k = least; k <= most; ++k) {
         const int64_t need = ((vecs + k - 1) / k + 31) / 32 * 32;
         if (need <= 512) {
             *threads = (int)need;
@@ -571,9 +607,13 @@ void row_shape(int64_t cols, int* threads, int* nv) {
 template <bool WIDE>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     int threads, nv;
-    row_shape(a.cols, &threads, &nv);
-    // as many CTAs as are resident: 768 threads per SM with two vectors and their prefetch in registers
-    const int64_t room = (int64_t)q8_host::sm_count() * (768 / threads < 1 ? 1 : 768 / threads);
+    // Many rows: two vectors per thread, so that what a thread does once per row (the reduction, the root) is
+    // shared by 32 columns; few rows: one, for the shorter chain.
+    const int sms = q8_host::sm_count();
+    row_shape(a.cols, a.rows >= 8 * (int64_t)sms ? 2 : 1, 2, &threads, &nv);
+    // as many CTAs as are resident: 512 threads per SM with two vectors and their prefetch in registers, or 640
+    const int most = nv == 2 ? 512 : 640;
+    const int64_t room = (int64_t)sms * (most / threads < 1 ? 1 : most / threads);
     const dim3 grid((unsigned)(a.rows < room ? a.rows : room)), block(threads);
     switch (nv) {
         case 1: return launch_kernel(k_rmsnorm_q8<1, WIDE>, grid, block, 0, st, a);
@@ -582,16 +622,20 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     }
 }
 
-template <bool WIDE>
-cudaError_t launch_norm_back(const NormBackArgs& a, int parts, cudaStream_t st) {
-    int threads, nv;
-    row_shape(a.cols, &threads, &nv);
-    const dim3 grid((unsigned)parts), block(threads);
-    switch (nv) {
-        case 1: return launch_kernel(k_rmsnorm_backward<1, WIDE>, grid, block, 0, st, a);
-        case 2: return launch_kernel(k_rmsnorm_backward<2, WIDE>, grid, block, 0, st, a);
-        default: return launch_kernel(k_rmsnorm_backward<0, WIDE>, grid, block, 0, st, a);
-    }
+// Narrow rows: groups of threads in CTAs of about 512, one per SM.  Rows of 256 threads and more: a CTA each, two
+// per SM (in groups of two, 16384 x 4096 took 98 us instead of 87-90).
+template <bool WIDE, bool KEPT8>
+cudaError_t launch_norm_back(NormBackArgs& a, int64_t parts, cudaStream_t st) {
+    int nv;
+    row_shape(a.cols, 1, 1, &a.threads, &nv);             // two vectors, dw's sums and the inputs do not fit in registers
+    const int groups = nv == 1 && a.threads < 256 ? 512 / a.threads : 1;
+    const int64_t room = (groups > 1 ? 1 : 2) * (int64_t)q8_host::sm_count(), need = (a.rows + groups - 1) / groups;
+    parts = parts < room ? parts : room;
+    a.parts = (int)(parts < need ? parts : need);
+    const dim3 grid((unsigned)a.parts), block(groups * a.threads);
+    if (groups > 1) return launch_kernel(k_rmsnorm_backward<1, WIDE, true, KEPT8>, grid, block, groups * a.threads * 64, st, a);
+    if (nv == 1) return launch_kernel(k_rmsnorm_backward<1, WIDE, false, KEPT8>, grid, block, 0, st, a);
+    return launch_kernel(k_rmsnorm_backward<0, WIDE, false, KEPT8>, grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -627,6 +671,7 @@ extern "C" int zs_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, i
     a.rows = rows;
     a.cols = cols;
     a.eps = eps;
+    a.inv_cols = 1.f / (float)cols;
     a.s = (uint16_t*)s;
     a.rstd = rstd;
     const bool w = wide(x, ldx, 32) && (!residual || wide(residual, ldr, 32)) && wide(weight, 0, 32) && (!s || wide(s, lds, 32));
@@ -676,15 +721,15 @@ extern "C" int zs_rmsnorm_backward(const void* dy, int64_t lddy, const void* s, 
     a.pitch = (cols + 15) / 16 * 16;
     if (n_partials > int64_t(1) << 30) n_partials = int64_t(1) << 30;
     if (n_partials * cols < a.pitch) a.pitch = cols;
-    int64_t parts = 2 * (int64_t)sm_count();
-    if (parts > n_partials * cols / a.pitch) parts = n_partials * cols / a.pitch;
+    int64_t parts = n_partials * cols / a.pitch;
     if (parts > ZS_Q8_MAX_PARTIALS) parts = ZS_Q8_MAX_PARTIALS;
-    if (parts > rows) parts = rows;
-    if (parts > 0)
-        ZS_Q8_TRY(cuda_status(fn, w ? zs::launch_norm_back<true>(a, (int)parts, st)
-                                    : zs::launch_norm_back<false>(a, (int)parts, st)));
+    if (rows > 0) {
+        const cudaError_t e = s_q8 ? (w ? zs::launch_norm_back<true, true>(a, parts, st) : zs::launch_norm_back<false, true>(a, parts, st))
+                                   : (w ? zs::launch_norm_back<true, false>(a, parts, st) : zs::launch_norm_back<false, false>(a, parts, st));
+        ZS_Q8_TRY(cuda_status(fn, e));
+    }
     return cuda_status(fn, zs::launch_kernel(zs::k_rmsnorm_dw, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, st,
-                                             (const float*)partials, parts, a.pitch, cols, (uint16_t*)dw, scale, (int)first));
+                                             (const float*)partials, (int64_t)a.parts, a.pitch, cols, (uint16_t*)dw, scale, (int)first));
 }
 
 extern "C" int zs_swiglu_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64_t rows, int64_t cols,
