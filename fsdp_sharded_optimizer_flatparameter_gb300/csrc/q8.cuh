@@ -62,6 +62,12 @@ __device__ __forceinline__ void q8_unpack4(uint32_t four, float scale, float* f)
 
 // max(top, |x|) where x is finite or NaN (NaN never wins); an infinity shows as top = inf.
 __device__ __forceinline__ float q8_top(float top, float x) { return fmaxf(top, fabsf(x)); }
+// max(top, |x|, |y|) the same way, in one instruction.
+__device__ __forceinline__ float q8_top2(float top, float2 x) {
+    float d;
+    asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %2;\n\tabs.f32 b, %3;\n\tmax.f32 %0, %1, a, b;\n\t}" : "=f"(d) : "f"(top), "f"(x.x), "f"(x.y));
+    return d;
+}
 // The encoding's treatment of infinities: NaN in their place.
 __device__ __forceinline__ float q8_no_inf(float x) { return isinf(x) ? __uint_as_float(0x7fffffffu) : x; }
 

@@ -135,13 +135,13 @@ __device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16_
 __device__ __forceinline__ void encode16(float2 (&f)[8], int64_t n, const Q8& q, int64_t row, int64_t col) {
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = q8_top(q8_top(top, f[i].x), f[i].y);
+    for (int i = 0; i < 8; ++i) top = q8_top2(top, f[i]);
     if (isinf(top)) {
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             f[i] = make_float2(q8_no_inf(f[i].x), q8_no_inf(f[i].y));
-            top = q8_top(q8_top(top, f[i].x), f[i].y);
+            top = q8_top2(top, f[i]);
         }
     }
 #pragma unroll
@@ -359,16 +359,16 @@ struct NormBackArgs {
 };
 
 // The CTA's threads are groups of `threads`, a row each at a time; a group takes every (groups of the grid)th row
-// and keeps its part of dw: a thread owns the columns of its vectors in every row, in registers (NV > 0) or
-// in the CTA's row of `partials` (NV = 0, one group).  With one vector the next row's loads are under way while a
-// row is reduced and written.  The groups' parts are added in shared memory, so that narrow rows fill the SM
-// without more rows of partials.
-template <int NV, bool WIDE, bool GROUPED, bool KEPT8>
+// and keeps its part of dw: a thread owns its 16 columns in every row, in registers (HELD), the next row's
+// loads being under way while a row is reduced and written.  Narrow rows are GROUPED: several rows at a time in
+// a CTA, the groups' parts added in shared memory, so that they fill the SM without more rows of partials
+// (999 x 2047: 14.3 us with a group per CTA, 10.2 with four).  Rows wider than 512 threads hold are read twice
+// (from L2), dw's part in the CTA's row of `partials`.
+template <bool HELD, bool WIDE, bool GROUPED, bool KEPT8>
 __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBackArgs a) {
     __shared__ float sums[16][2][16];            // per group and turn
     extern __shared__ float parts_sh[];          // [group][columns of its threads], with more than one group
     dependent_launch_prologue();
-    constexpr int N1 = NV > 0 ? NV : 1;
     const int groups = GROUPED ? blockDim.x / a.threads : 1, group = GROUPED ? threadIdx.x / a.threads : 0;
     const int threads = GROUPED ? a.threads : blockDim.x, tid = threadIdx.x - group * threads;
     const int64_t step = (int64_t)threads * 16, col0 = (int64_t)tid * 16;
@@ -422,73 +422,49 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
     const float inv_cols = 1.f / (float)a.cols;
     float* part = a.partials + (int64_t)blockIdx.x * a.pitch;
     int turn = 0;
-    if constexpr (NV > 0) {
-        V16 w[N1];
-        Row next[N1];
-        float2 dw[N1][8];
+    if constexpr (HELD) {
+        Row next;
+        float2 dw[8];
         float r_next = row0 < a.rows ? a.rstd[row0] : 0.f;
+        if (row0 < a.rows) fetch(row0, col0, next);
+        const V16 w = load16<WIDE>(a.weight + col0, a.cols - col0, sw);
 #pragma unroll
-        for (int v = 0; v < N1; ++v) {
-            if (row0 < a.rows) fetch(row0, col0 + v * step, next[v]);
-            w[v] = load16<WIDE>(a.weight + col0 + v * step, a.cols - col0 - v * step, sw);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dw[v][i] = make_float2(0.f, 0.f);
-        }
+        for (int i = 0; i < 8; ++i) dw[i] = make_float2(0.f, 0.f);
         for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
-            Row now[N1];
-            float2 xh[N1][8];
+            const Row now = next;
+            float2 xh[8];
             const float r = r_next;
-            float d = 0.f;
-#pragma unroll
-            for (int v = 0; v < N1; ++v) {
-                now[v] = next[v];
-                normalised(now[v], r, xh[v]);
-                d += dot(now[v], w[v], xh[v]);
-            }
-            const bool more = row + stride < a.rows;
-            if (NV == 1 && more) {               // two vectors leave no registers for the next row's
+            normalised(now, r, xh);
+            const float d = dot(now, w, xh);
+            if (row + stride < a.rows) {
                 r_next = a.rstd[row + stride];
-                fetch(row + stride, col0, next[0]);
+                fetch(row + stride, col0, next);
             }
             const float along = group_sum(d, sh[turn], threads, group + 1) * inv_cols;
+            write(row, col0, r, along, now, w, xh);
 #pragma unroll
-            for (int v = 0; v < N1; ++v) {
-                write(row, col0 + v * step, r, along, now[v], w[v], xh[v]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dw[v][i] = q8_fma2(pair_of(now[v].dy.w[i]), xh[v][i], dw[v][i]);
-            }
-            if (NV > 1 && more) {
-                r_next = a.rstd[row + stride];
-#pragma unroll
-                for (int v = 0; v < N1; ++v) fetch(row + stride, col0 + v * step, next[v]);
-            }
+            for (int i = 0; i < 8; ++i) dw[i] = q8_fma2(pair_of(now.dy.w[i]), xh[i], dw[i]);
         }
         if constexpr (GROUPED) {                 // the groups' parts, in order
             float* mine = parts_sh + (int64_t)group * step + col0;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<float4*>(mine + k * 4) = make_float4(dw[0][2 * k].x, dw[0][2 * k].y, dw[0][2 * k + 1].x, dw[0][2 * k + 1].y);
+                *reinterpret_cast<float4*>(mine + k * 4) = make_float4(dw[2 * k].x, dw[2 * k].y, dw[2 * k + 1].x, dw[2 * k + 1].y);
             __syncthreads();
             for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
                 float all = parts_sh[c];
                 for (int g = 1; g < groups; ++g) all += parts_sh[g * step + c];
                 part[c] = all;
             }
-            return;
-        }
-#pragma unroll
-        for (int v = 0; v < N1; ++v) {
-            const int64_t c = col0 + v * step;
-            if (c >= a.cols) continue;
+        } else if (col0 < a.cols) {
             if ((a.pitch & 15) == 0) {           // room for the last vector's columns past cols
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    *reinterpret_cast<float4*>(part + c + k * 4) =
-                        make_float4(dw[v][2 * k].x, dw[v][2 * k].y, dw[v][2 * k + 1].x, dw[v][2 * k + 1].y);
+                    *reinterpret_cast<float4*>(part + col0 + k * 4) = make_float4(dw[2 * k].x, dw[2 * k].y, dw[2 * k + 1].x, dw[2 * k + 1].y);
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (c + i < a.cols) part[c + i] = (i & 1) ? dw[v][i >> 1].y : dw[v][i >> 1].x;
+                    if (col0 + i < a.cols) part[col0 + i] = (i & 1) ? dw[i >> 1].y : dw[i >> 1].x;
             }
         }
     } else {
@@ -633,9 +609,9 @@ cudaError_t launch_norm_back(NormBackArgs& a, int64_t parts, cudaStream_t st) {
     parts = parts < room ? parts : room;
     a.parts = (int)(parts < need ? parts : need);
     const dim3 grid((unsigned)a.parts), block(groups * a.threads);
-    if (groups > 1) return launch_kernel(k_rmsnorm_backward<1, WIDE, true, KEPT8>, grid, block, groups * a.threads * 64, st, a);
-    if (nv == 1) return launch_kernel(k_rmsnorm_backward<1, WIDE, false, KEPT8>, grid, block, 0, st, a);
-    return launch_kernel(k_rmsnorm_backward<0, WIDE, false, KEPT8>, grid, block, 0, st, a);
+    if (groups > 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, true, KEPT8>, grid, block, groups * a.threads * 64, st, a);
+    if (nv == 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, false, KEPT8>, grid, block, 0, st, a);
+    return launch_kernel(k_rmsnorm_backward<false, WIDE, false, KEPT8>, grid, block, 0, st, a);
 }
 
 }  // namespace

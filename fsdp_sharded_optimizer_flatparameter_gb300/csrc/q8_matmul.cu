@@ -804,12 +804,15 @@ cudaError_t launch_mm_split(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cuda
     if (e != cudaSuccess) return e;
     a.tiles_q = (a.rows_q + BN - 1) / BN;
     const int64_t tiles = (int64_t)((a.rows_p + 127) / 128) * a.tiles_q;
-    // Split while the CTAs still fit one per SM and keep at least five blocks each: joining the parts costs
-    // 2-4 us, which more CTAs than SMs do not earn back (1 x 22016 x 4096: 17.8 us unsplit, 22.5 and 31.7 in
-    // 2 and 8 parts; 1 x 4096 x 4096, 32 tiles: 11.4 unsplit, 6.3 in 4).
+    // Split while the CTAs still fit one per SM and keep at least five blocks each, or two per SM and ten:
+    // joining the parts costs 2-4 us, which more CTAs do not earn back (1 x 22016 x 4096, 172 tiles: 17.8 us
+    // unsplit, 22.5 and 31.7 in 2 and 8 parts; 1 x 4096 x 4096, 32 tiles: 11.4 unsplit, 6.3 in 4, 6.6 in 8;
+    // 37 x 4096 x 11008: 13.8 in 4, 12.9 in 8).
     a.split = 1;
-    while (a.split < kSplitMost && tiles * a.split * 2 <= q8_host::sm_count() && a.kblocks >= a.split * 2 * 5 &&
-           BN / (a.split * 2) >= (a.transposed ? 1 : 16))
+    const int64_t sms = q8_host::sm_count();
+    while (a.split < kSplitMost && BN / (a.split * 2) >= (a.transposed ? 1 : 16) &&
+           ((tiles * a.split * 2 <= sms && a.kblocks >= a.split * 2 * 5) ||
+            (tiles * a.split * 2 <= 2 * sms && a.kblocks >= a.split * 2 * 10)))
         a.split *= 2;
     if (tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -920,7 +923,7 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
             default: e = zs::launch_mm_pair<128>(p, q, k, g, st); break;
         }
     } else if (g.rows_q <= 16) {
-        e = zs::launch_mm_split<16, 4>(p, q, k, g, st);
+        e = zs::launch_mm_split<16, 5>(p, q, k, g, st);
     } else if (g.rows_q <= 32) {
         e = zs::launch_mm_split<32, 4>(p, q, k, g, st);
     } else if (g.rows_q <= 64) {

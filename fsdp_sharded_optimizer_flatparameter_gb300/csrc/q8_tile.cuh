@@ -99,7 +99,7 @@ struct TileValues {
         for (int p = 0; p < RP; ++p) {
             top[p] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top[p] = q8_top(q8_top(top[p], v[p][j].x), v[p][j].y);
+            for (int j = 0; j < 8; ++j) top[p] = q8_top2(top[p], v[p][j]);
         }
         float most = top[0];
 #pragma unroll
@@ -111,7 +111,7 @@ struct TileValues {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[p][j] = make_float2(q8_no_inf(v[p][j].x), q8_no_inf(v[p][j].y));
-                    top[p] = q8_top(q8_top(top[p], v[p][j].x), v[p][j].y);
+                    top[p] = q8_top2(top[p], v[p][j]);
                 }
             }
         }
@@ -152,9 +152,9 @@ struct TileValues {
         for (int j = 0; j < 8; ++j) {
             float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int p = 0; p < RP; ++p) {
-                a = q8_top(a, v[p][j].x);
-                b = q8_top(b, v[p][j].y);
+            for (int p = 0; p < RP; p += 2) {
+                a = q8_top2(a, make_float2(v[p][j].x, v[p + 1][j].x));
+                b = q8_top2(b, make_float2(v[p][j].y, v[p + 1][j].y));
             }
             key[j] = scale_keys(a, b);
             key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 8));
@@ -236,21 +236,73 @@ struct TileArgs {
     long long wait_limit;
 };
 
+// Row p of the thread's part of a tile: bf16 values as packed words, from the stage or (not TMA) from memory;
+// decoded 8-bit values of an 8-bit tile at `from`.
+template <int RP, bool TMA>
+__device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<RP>& t, const uint8_t* stage, int p, uint32_t (&x)[8]) {
+    if constexpr (TMA) {
+        const uint4* from = reinterpret_cast<const uint4*>(stage + (t.rg * RP + p) * 256 + t.cc * 32);
+        const uint4 lo = from[0], hi = from[1];
+        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    } else {
+        load_bf16_16(a.x + (t.r0 + t.rg * RP + p) * a.ldx + t.c0 + t.cc * 16, t.row_ok(p) ? t.chunk() : 0, x);
+    }
+}
+template <int RP>
+__device__ __forceinline__ void tile_codes(const uint8_t* from, int p, uint32_t byte, float2 (&v)[8]) {
+    const int rg = threadIdx.x >> 3, cc = threadIdx.x & 7;
+    const uint4 w = *reinterpret_cast<const uint4*>(from + (rg * RP + p) * 128 + cc * 16);
+    const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+    const float e = q8_scale(byte);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q8_mul2(q8_unpack2(w4[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
+}
+
+// The gated activation's backward values: 0 the gate's gradient, 1 up's, 2 the activation itself.
+template <int RP, bool TMA, int WHICH>
+__device__ __forceinline__ void gate_values(TileValues<RP>& v, const TileArgs& a, const TilePos<RP>& t, const uint8_t* stage,
+                                            const uint32_t (&sa)[RP], const uint32_t (&sb)[RP]) {
+    const uint8_t* codes = stage + (TMA ? 128 * 128 * 2 : 0);
+    const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+        uint32_t x[8] = {};
+        float2 g[8], u[8];
+        if constexpr (WHICH < 2) tile_bf16<RP, TMA>(a, t, stage, p, x);
+        tile_codes<RP>(codes, p, sa[p], g);
+        if constexpr (WHICH != 1) tile_codes<RP>(codes + 128 * 128, p, sb[p], u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 d = make_float2(bf16_lo(x[j]), bf16_hi(x[j])), sig = q8_sigmoid2(g[j]);
+            if constexpr (WHICH == 0) {
+                const float2 rest = q8_fma2(sig, make_float2(-1.f, -1.f), one);                  // 1 - sigmoid
+                v.v[p][j] = q8_mul2(q8_mul2(d, u[j]), q8_mul2(sig, q8_fma2(g[j], rest, one)));
+            } else if constexpr (WHICH == 1) {
+                v.v[p][j] = q8_mul2(d, q8_mul2(g[j], sig));
+            } else {
+                v.v[p][j] = q8_mul2(q8_mul2(g[j], sig), u[j]);
+            }
+        }
+    }
+}
+
 template <int KIND, bool TMA>
 struct TileShape {
-    // Rows per thread.  Two (twice the warps, half the registers) is slower for each of the three: the gate's
-    // backward pass at 5003 x 5504 takes 81 us with four and 90 with two.
+    // Rows per thread.  Two (twice the warps, half the registers) was slower for each of the three.
     static constexpr int kRows = 4;
     static constexpr int kThreads = 1024 / kRows;
-    static constexpr int kValues = KIND == kTileGate ? 3 : 1;
+    // The gate's three values per element are taken one after another, each computed from the tile in shared memory:
+    // all three in registers at once leave room for one CTA per SM (81 us at 5003 x 5504).
+    static constexpr int kPasses = KIND == kTileGate ? 3 : 1;
     static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage: bf16 tile
     static constexpr int kA = KIND == kTileEncode ? 0 : 128 * 128;                // and 8-bit tiles
     static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
     static constexpr int kStage = kX + kA + kB;
-    static constexpr int kStages = KIND == kTileTurn ? 3 : 2;
+    static constexpr int kStages = KIND == kTileGate ? 1 : 2;
     static constexpr int kKeys = (32 / kRows) * 64 * 4;
-    static constexpr int kSmem = 128 + kStages * kStage + kValues * (128 * 128 + kKeys + 512) + 64;
-    static constexpr int kPerSm = KIND == kTileGate ? 1 : 2;
+    static constexpr int kSmem = 128 + kStages * kStage + 128 * 128 + kKeys + 512 + 64;
+    static constexpr int kPerSm = 2;
 };
 
 template <int KIND, bool TMA>
@@ -261,11 +313,11 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     constexpr int RP = S::kRows, kWarps = S::kThreads / 32;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((128 - (su32(raw) & 127)) & 127);
-    uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [kValues][128 * 32]
-    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + S::kValues * 128 * 32);    // [kValues * warps][64]
-    float* inv = reinterpret_cast<float*>(keys + S::kValues * kWarps);                               // [kValues][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(inv + S::kValues * 128);
-    const int lane_row = (threadIdx.x >> 3) * RP, cc = threadIdx.x & 7;
+    uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [128 * 32]
+    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + 128 * 32);                 // [warps][64]
+    float* inv = reinterpret_cast<float*>(keys + kWarps);                                       // [128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(inv + 128);
+    const int lane_row = (threadIdx.x >> 3) * RP;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -309,86 +361,59 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
         bool late = false;
         if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
-        TileValues<RP> v[S::kValues];
-#pragma unroll
-        for (int p = 0; p < RP; ++p) {
-            uint32_t x[8];
-            if constexpr (KIND != kTileTurn) {
-                if constexpr (TMA) {
-                    const uint4* from = reinterpret_cast<const uint4*>(at + (lane_row + p) * 256 + cc * 32);
-                    const uint4 lo = from[0], hi = from[1];
-                    x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-                    x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+#pragma unroll 1
+        for (int pass = 0; pass < S::kPasses; ++pass) {
+            const bool rows_wanted = KIND != kTileTurn && pass < 2 && a.rows_out[pass & 1].codes;
+            const bool cols_wanted = a.cols_out[pass].codes;
+            TileValues<RP> v;
+            float top[RP];
+            if (KIND != kTileGate || rows_wanted || cols_wanted) {
+                if constexpr (KIND == kTileGate) {
+                    if (pass == 0) gate_values<RP, TMA, 0>(v, a, t, at, sa, sb);
+                    else if (pass == 1) gate_values<RP, TMA, 1>(v, a, t, at, sa, sb);
+                    else gate_values<RP, TMA, 2>(v, a, t, at, sa, sb);
                 } else {
-                    load_bf16_16(a.x + (t.r0 + lane_row + p) * a.ldx + t.c0 + cc * 16, t.row_ok(p) ? t.chunk() : 0, x);
+#pragma unroll
+                    for (int p = 0; p < RP; ++p) {
+                        if constexpr (KIND == kTileEncode) {
+                            uint32_t x[8];
+                            tile_bf16<RP, TMA>(a, t, at, p, x);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v.v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
+                        } else {
+                            tile_codes<RP>(at, p, sa[p], v.v[p]);
+                        }
+                    }
+                }
+                v.find_tops(top);
+                if (cols_wanted) v.column_keys(keys);
+            }
+            const bool last = pass == S::kPasses - 1;
+            if (last && tile + step < a.tiles) load_scales(tile + step);
+            // A wait that ran out ends the CTA, after the copies still on their way.
+            if (__syncthreads_or(late)) {
+                if (threadIdx.x == 0) {
+                    atomicCAS(a.error, 0u, ZS_DEVERR_TILE_WAIT);
+                    for (int i = 0; i < S::kStages; ++i)
+                        if (tile + i * step < a.tiles)
+                            mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, a.wait_limit);
+                }
+                return;
+            }
+            if (last) {                          // every thread has read the stage: its next tile may come
+                if (threadIdx.x == 0 && tile + S::kStages * step < a.tiles) load_stage(s, tile + S::kStages * step);
+                if (++s == S::kStages) {
+                    s = 0;
+                    parity ^= 1;
                 }
             }
-            if constexpr (KIND == kTileEncode) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[0].v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
-            } else if constexpr (KIND == kTileTurn) {
-                const uint4 w = *reinterpret_cast<const uint4*>(at + (lane_row + p) * 128 + cc * 16);
-                const float e = q8_scale(sa[p]);
-                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[0].v[p][j] = q8_mul2(q8_unpack2(w4[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
-            } else {
-                const uint8_t* codes = at + S::kX + (lane_row + p) * 128 + cc * 16;
-                const uint4 wg = *reinterpret_cast<const uint4*>(codes), wu = *reinterpret_cast<const uint4*>(codes + S::kA);
-                const float eg = q8_scale(sa[p]), eu = q8_scale(sb[p]);
-                const uint32_t g4[4] = {wg.x, wg.y, wg.z, wg.w}, u4[4] = {wu.x, wu.y, wu.z, wu.w};
-                const float2 one = make_float2(1.f, 1.f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 g = q8_mul2(q8_unpack2(g4[j >> 1] >> ((j & 1) * 16)), make_float2(eg, eg));
-                    const float2 u = q8_mul2(q8_unpack2(u4[j >> 1] >> ((j & 1) * 16)), make_float2(eu, eu));
-                    const float2 d = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
-                    const float2 sig = q8_sigmoid2(g), silu = q8_mul2(g, sig);
-                    const float2 rest = q8_fma2(sig, make_float2(-1.f, -1.f), one);                  // 1 - sigmoid
-                    v[0].v[p][j] = q8_mul2(q8_mul2(d, u), q8_mul2(sig, q8_fma2(g, rest, one)));
-                    v[1].v[p][j] = q8_mul2(d, silu);
-                    v[2].v[p][j] = q8_mul2(silu, u);
-                }
-            }
+            if (cols_wanted && threadIdx.x < 64) column_scales(t, threadIdx.x, keys, a.cols_out[pass], inv);
+            if (rows_wanted) v.store_rows(t, top, a.rows_out[pass & 1]);
+            __syncthreads();
+            if (cols_wanted) v.stage_columns(t, inv, word);
+            __syncthreads();
+            if (cols_wanted) store_columns(t, word, a.cols_out[pass]);
         }
-        if (tile + step < a.tiles) load_scales(tile + step);
-        float top[S::kValues][RP];
-#pragma unroll
-        for (int k = 0; k < S::kValues; ++k) {
-            v[k].find_tops(top[k]);
-            if (a.cols_out[k].codes) v[k].column_keys(keys + k * kWarps);
-        }
-        // every thread has read the stage: its next tile may come.  A wait that ran out ends the CTA, after
-        // the copies still on their way.
-        if (__syncthreads_or(late)) {
-            if (threadIdx.x == 0) {
-                atomicCAS(a.error, 0u, ZS_DEVERR_TILE_WAIT);
-                for (int i = 0; i < S::kStages; ++i)
-                    if (tile + i * step < a.tiles)
-                        mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, a.wait_limit);
-            }
-            return;
-        }
-        if (threadIdx.x == 0 && tile + S::kStages * step < a.tiles) load_stage(s, tile + S::kStages * step);
-        if (++s == S::kStages) {
-            s = 0;
-            parity ^= 1;
-        }
-#pragma unroll
-        for (int k = 0; k < S::kValues; ++k)
-            if (a.cols_out[k].codes && (int)threadIdx.x >> 6 == k) column_scales(t, threadIdx.x & 63, keys + k * kWarps, a.cols_out[k], inv + k * 128);
-#pragma unroll
-        for (int k = 0; k < (S::kValues < 2 ? 1 : 2); ++k)
-            if (KIND != kTileTurn && a.rows_out[k].codes) v[k].store_rows(t, top[k], a.rows_out[k]);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < S::kValues; ++k)
-            if (a.cols_out[k].codes) v[k].stage_columns(t, inv + k * 128, word + k * 128 * 32);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < S::kValues; ++k)
-            if (a.cols_out[k].codes) store_columns(t, word + k * 128 * 32, a.cols_out[k]);
     }
 }
 
