@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
 // (the tensor cores read the other half of Q from the other CTA), one thread of the leading CTA issues the
 // products for both, and each CTA keeps 128 x BN fp32 accumulators in its own tensor memory.  The pairs are
 // persistent and the accumulators doubled, so that eight warps write a tile out while the next one's
-// products run; that and the scales leave BN at 224 or less (256 columns undoubled lost about 1 us per
-// tile to the read-out).
+// products run; that and the scales leave BN at 224 or less.  Undoubled, a tile may have 256 columns: for
+// products that every pair does in one tile.
 constexpr int kPairThreads = 448;
 constexpr int kPairStages = 6;
 constexpr int kPairScaleBytes = 512 * 3;
@@ -562,9 +562,10 @@ constexpr int kPairSlots = 2;         // batches of scales in flight
 constexpr int kPairTmemScales = 12;  // columns of one group's scales
 template <int BN>
 struct PairShape {
+    static constexpr int kAccs = BN == 256 ? 1 : 2;
     static constexpr int kStageBytes = 128 * 128 + (BN / 2) * 128;
     static constexpr int kSmem = 1024 + kPairStages * kStageBytes + kPairSlots * kBatch * kPairScaleBytes + 8 * kStoreStage * 4 + 256;
-    static_assert(2 * BN + kBatch * kPairTmemScales <= 512, "tensor memory");
+    static_assert(kAccs * BN + kBatch * kPairTmemScales <= 512, "tensor memory");
     static_assert(BN % 32 == 0 && (BN / 2) % 16 == 0, "halves of whole 16-column loads");
 };
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
@@ -573,7 +574,7 @@ template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ MmArgs a) {
-    constexpr int kStageBytes = PairShape<BN>::kStageBytes;
+    constexpr int kStageBytes = PairShape<BN>::kStageBytes, kAccs = PairShape<BN>::kAccs;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (su32(raw) & 1023)) & 1023);
     uint8_t* scale_sh = base + kPairStages * kStageBytes;
@@ -614,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at, tmem_scales = tmem + 2 * BN;
+    const uint32_t tmem = *tmem_at, tmem_scales = tmem + kAccs * BN;
     const int groups = (a.kblocks + 3) / 4;
     const int tiles_p = (a.rows_p + 255) / 256;
     const int64_t tiles = (int64_t)tiles_p * a.tiles_q;
@@ -703,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (!ok) break;
             if (elect_one()) mma_commit_pair(done + acc.at);
             __syncwarp();
-            acc.next(2);
+            acc.next(kAccs);
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= 2 && warp < 6) {
@@ -746,7 +747,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         constexpr int kHalf = BN / 2;            // columns of one warp
         const int sub = warp & 3, half = (warp - 6) >> 2;
         Ring acc;
-        for (int64_t t = first_tile; t < tiles; t += step, acc.next(2)) {
+        for (int64_t t = first_tile; t < tiles; t += step, acc.next(kAccs)) {
             int p0, q0;
             place(t, p0, q0);
             if (!warp_wait(done + acc.at, acc.parity(), a.wait_limit)) {
@@ -849,17 +850,18 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
                          mq, a);
 }
 
-// The tile width with the least time in the busiest pair: rounds of tiles times the time of one block of
-// one tile, which is that of its products (1.11 ns per column) or of its loads (per row of the CTA's two
-// tiles 0.92 ns, and 1.7 where rows are not 128 bytes apart or a multiple and each touches two lines).
-int pair_width(int64_t rows_p, int64_t rows_q, bool lines) {
+// The tile width with the least time in the busiest pair: rounds of tiles times the time of one, which per block
+// of the sum is that of its products (1.11 ns per column) or of its loads (per row of the CTA's two tiles 0.92
+// ns, and 1.7 where rows are not 128 bytes apart or a multiple and each touches two lines), and about 2.5 us
+// to write a tile out, which the next tile's products hide but for the last one (and for 256 columns).
+int pair_width(int64_t rows_p, int64_t rows_q, int64_t kblocks, bool lines) {
     const int64_t pairs = q8_host::sm_count() / 2, tp = (rows_p + 255) / 256;
     int best = 224;
     double least = 1e300;
-    for (int bn : {224, 192, 160, 128}) {
+    for (int bn : {256, 224, 192, 160, 128}) {
         const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + pairs - 1) / pairs;
         const double products = 1.11 * bn, loads = (lines ? 0.92 : 1.7) * (128 + bn / 2);
-        const double cost = (double)rounds * (products > loads ? products : loads);
+        const double cost = (double)rounds * kblocks * (products > loads ? products : loads) + 2500.0 * (bn == 256 ? rounds : 1);
         if (cost < least) {
             least = cost;
             best = bn;
@@ -916,7 +918,8 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
     cudaError_t e;
     if (!swap && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
-        switch (zs::pair_width(m, n, ((qa.ld | qb.ld) & 127) == 0)) {
+        switch (zs::pair_width(m, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0)) {
+            case 256: e = zs::launch_mm_pair<256>(p, q, k, g, st); break;
             case 224: e = zs::launch_mm_pair<224>(p, q, k, g, st); break;
             case 192: e = zs::launch_mm_pair<192>(p, q, k, g, st); break;
             case 160: e = zs::launch_mm_pair<160>(p, q, k, g, st); break;
