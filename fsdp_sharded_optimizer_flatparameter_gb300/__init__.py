@@ -14,6 +14,7 @@ will touch, because the C ABI receives bare pointers and cannot.
 
 import ctypes
 import os
+import struct
 
 from ._lib import LIB_PATH, load_library
 
@@ -662,6 +663,7 @@ if _torch is not None:
     _BF16, _F32 = _torch.bfloat16, _torch.float32
     _CODES = (_torch.float8_e4m3fn, _torch.uint8)
     _SCALES = (_torch.float8_e8m0fnu, _torch.uint8)
+_PACK_Q8 = struct.Struct("@PPqq").pack     # a zs_q8 as the C compiler lays it out
 
 
 def q8_empty(rows, cols, device="cuda"):
@@ -719,21 +721,25 @@ def _vector(x, n, dtype, what):
 
 
 def _q8(q, rows, cols, what):
-    """A zs_q8 of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
+    """A zs_q8 (its bytes) of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
     if q is None:
         return None
     codes, scales = q
     blocks = (cols + 127) >> 7
-    ld, step = codes.stride() if codes.dim() == 2 else (0, 0)
-    if not (step == 1 and ld >= cols and ld & 15 == 0 and codes.is_cuda and codes.dtype in _CODES
-            and codes.shape == (rows, cols)):
-        ld = _misfit(codes, rows, cols, _CODES, what + " codes")
-        if rows < 2:
-            ld = max(16, (ld + 15) // 16 * 16)
-    lds, step = scales.stride() if scales.dim() == 2 else (0, 0)
-    if not (step == 1 and lds >= blocks and scales.is_cuda and scales.dtype in _SCALES and scales.shape == (rows, blocks)):
-        lds = _misfit(scales, rows, blocks, _SCALES, what + " scales")
-    return ctypes.byref(zs_q8(codes.data_ptr(), scales.data_ptr(), ld, lds))
+    try:
+        ld, step = codes.stride()
+        lds, step_s = scales.stride()
+        if (step == 1 and step_s == 1 and ld >= cols and lds >= blocks and not ld & 15 and codes.dtype in _CODES
+                and scales.dtype in _SCALES and codes.is_cuda and scales.is_cuda and codes.shape == (rows, cols)
+                and scales.shape == (rows, blocks)):
+            return _PACK_Q8(codes.data_ptr(), scales.data_ptr(), ld, lds)
+    except ValueError:                     # not matrices
+        pass
+    ld = _misfit(codes, rows, cols, _CODES, what + " codes")
+    lds = _misfit(scales, rows, blocks, _SCALES, what + " scales")
+    if rows < 2:
+        ld = max(16, (ld + 15) // 16 * 16)
+    return _PACK_Q8(codes.data_ptr(), scales.data_ptr(), ld, lds)
 
 
 def zs_q8_encode(x, q=None, q_t=None, stream=None):
