@@ -340,7 +340,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    dependent_launch_prologue();
+    early_launch();
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&map_p);
+        prefetch_map(&map_q);
+    }
+    // Before the allocation: CTAs of two launches on one SM are the common case here, and one that allocates
+    // while the other still runs slowed both (500 x 1000 x 5003: 14.6 us instead of 10.8).
+    wait_for_predecessor();
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_at)),
                      "r"((uint32_t)S::kTmemCols)
@@ -606,7 +613,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    dependent_launch_prologue();
+    early_launch();
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&map_p);
+        prefetch_map(&map_q);
+    }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_at)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -615,6 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    wait_for_predecessor();
     const uint32_t tmem = *tmem_at, tmem_scales = tmem + kAccs * BN;
     const int groups = (a.kblocks + 3) / 4;
     const int tiles_p = (a.rows_p + 255) / 256;
