@@ -23,28 +23,28 @@
 namespace zs {
 
 
-template <int RP>            // rows per thread
+template <int RP, int CP>    // rows and column pairs per thread; tiles have 128 rows and 16 * CP columns
 struct TilePos {
-    int cc, rg;              // column chunk (16 columns), row group (RP rows)
+    int cc, rg;              // column chunk (2 * CP columns), row group (RP rows)
     int64_t r0, c0;          // the tile's first row and column
     int rows, cols;          // valid rows and columns of the tile, 1 .. 128
     __device__ __forceinline__ bool row_ok(int p) const { return rg * RP + p < rows; }
-    __device__ __forceinline__ int chunk() const {            // valid columns of this thread's 16
-        const int n = cols - cc * 16;
-        return n < 0 ? 0 : n > 16 ? 16 : n;
+    __device__ __forceinline__ int chunk() const {            // valid columns of this thread's
+        const int n = cols - cc * 2 * CP;
+        return n < 0 ? 0 : n > 2 * CP ? 2 * CP : n;
     }
 };
 
-template <int RP>
-__device__ __forceinline__ TilePos<RP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
-    TilePos<RP> t;
+template <int RP, int CP>
+__device__ __forceinline__ TilePos<RP, CP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
+    TilePos<RP, CP> t;
     t.cc = threadIdx.x & 7;
     t.rg = threadIdx.x >> 3;
     const uint32_t tr = (uint32_t)tile / (uint32_t)tiles_c;
     t.r0 = (int64_t)tr * 128;
-    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * 128;
+    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * (16 * CP);
     t.rows = rows - t.r0 < 128 ? (int)(rows - t.r0) : 128;
-    t.cols = cols - t.c0 < 128 ? (int)(cols - t.c0) : 128;
+    t.cols = cols - t.c0 < 16 * CP ? (int)(cols - t.c0) : 16 * CP;
     return t;
 }
 
@@ -88,18 +88,18 @@ __device__ __forceinline__ uint32_t key_byte(uint32_t key) {            // key: 
 }
 
 // A thread's part of a tile's values: rows p, column pairs.
-template <int RP>
+template <int RP, int CP>
 struct TileValues {
-    float2 v[RP][8];
+    float2 v[RP][CP];
 
-    // Largest magnitude of each row's 16 values.  Infinities become NaN, which the encoding leaves out of the
+    // Largest magnitude of each row's values.  Infinities become NaN, which the encoding leaves out of the
     // scale (rare: the test is one comparison on the maximum that the encoding needs anyway).
     __device__ __forceinline__ void find_tops(float (&top)[RP]) {
 #pragma unroll
         for (int p = 0; p < RP; ++p) {
             top[p] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top[p] = q8_top2(top[p], v[p][j]);
+            for (int j = 0; j < CP; ++j) top[p] = q8_top2(top[p], v[p][j]);
         }
         float most = top[0];
 #pragma unroll
@@ -109,7 +109,7 @@ struct TileValues {
             for (int p = 0; p < RP; ++p) {
                 top[p] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < CP; ++j) {
                     v[p][j] = make_float2(q8_no_inf(v[p][j].x), q8_no_inf(v[p][j].y));
                     top[p] = q8_top2(top[p], v[p][j]);
                 }
@@ -117,7 +117,8 @@ struct TileValues {
         }
     }
     // The tile as it is.
-    __device__ __forceinline__ void store_rows(const TilePos<RP>& t, const float (&top)[RP], const Q8& q) const {
+    __device__ __forceinline__ void store_rows(const TilePos<RP, CP>& t, const float (&top)[RP], const Q8& q) const {
+        static_assert(CP == 8, "a row's block is eight lanes");
         const int n = t.chunk();
         const int64_t r0 = t.r0 + t.rg * RP;
         uint8_t* codes = q.codes + r0 * q.ld + t.c0 + t.cc * 16;
@@ -144,34 +145,50 @@ struct TileValues {
             scales += q.lds;
         }
     }
-    // Scale keys of the columns over this warp's rows, into sh[warp][column pair].
-    __device__ __forceinline__ void column_keys(uint32_t (*sh)[64]) const {
+    // Scale keys of the columns over this warp's rows, into sh[warp][column pair].  Without find_tops before it
+    // (no rows stored), infinities are found and replaced here.
+    __device__ __forceinline__ void column_keys(uint32_t (*sh)[8 * CP]) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        uint32_t key[8];
+        float2 top[CP];
+        auto tops = [&] {
+            float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float a = 0.f, b = 0.f;
+            for (int j = 0; j < CP; ++j) {
+                top[j] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int p = 0; p < RP; p += 2) {
-                a = q8_top2(a, make_float2(v[p][j].x, v[p + 1][j].x));
-                b = q8_top2(b, make_float2(v[p][j].y, v[p + 1][j].y));
+                for (int p = 0; p < RP; p += 2)
+                    top[j] = make_float2(q8_top2(top[j].x, make_float2(v[p][j].x, v[p + 1][j].x)),
+                                         q8_top2(top[j].y, make_float2(v[p][j].y, v[p + 1][j].y)));
+                most = q8_top2(most, top[j]);
             }
-            key[j] = scale_keys(a, b);
+            return most;
+        };
+        if (isinf(tops())) {
+#pragma unroll
+            for (int p = 0; p < RP; ++p)
+#pragma unroll
+                for (int j = 0; j < CP; ++j) v[p][j] = make_float2(q8_no_inf(v[p][j].x), q8_no_inf(v[p][j].y));
+            tops();
+        }
+        uint32_t key[CP];
+#pragma unroll
+        for (int j = 0; j < CP; ++j) {
+            key[j] = scale_keys(top[j].x, top[j].y);
             key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 8));
             key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 16));
         }
         if (lane < 8) {
-            uint4* to = reinterpret_cast<uint4*>(&sh[warp][lane * 8]);
-            to[0] = make_uint4(key[0], key[1], key[2], key[3]);
-            to[1] = make_uint4(key[4], key[5], key[6], key[7]);
+            uint4* to = reinterpret_cast<uint4*>(&sh[warp][lane * CP]);
+#pragma unroll
+            for (int k = 0; k < CP / 4; ++k) to[k] = make_uint4(key[4 * k], key[4 * k + 1], key[4 * k + 2], key[4 * k + 3]);
         }
     }
     // Codes of the columns into word (8 chunks of 16 bytes per column), with inv[column] = 2^-e.
-    __device__ __forceinline__ void stage_columns(const TilePos<RP>& t, const float* inv, uint32_t* word) const {
-        uint8_t* to = reinterpret_cast<uint8_t*>(word) + t.cc * 16 * 128 + ((((t.rg * RP) >> 4) ^ t.cc) << 4) + ((t.rg * RP) & 15);
+    __device__ __forceinline__ void stage_columns(const TilePos<RP, CP>& t, const float* inv, uint32_t* word) const {
+        uint8_t* to = reinterpret_cast<uint8_t*>(word) + t.cc * 2 * CP * 128 + ((((t.rg * RP) >> 4) ^ t.cc) << 4) + ((t.rg * RP) & 15);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 e = *reinterpret_cast<const float4*>(inv + t.cc * 16 + k * 4);
+        for (int k = 0; k < CP / 2; ++k) {
+            const float4 e = *reinterpret_cast<const float4*>(inv + t.cc * 2 * CP + k * 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 s = h ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
@@ -179,21 +196,17 @@ struct TileValues {
 #pragma unroll
                 for (int p = 0; p < RP; ++p) a[p] = q8_mul2(v[p][k * 2 + h], s);
                 uint8_t* at = to + (k * 4 + h * 2) * 128;
-                if constexpr (RP == 4) {
-                    *reinterpret_cast<uint32_t*>(at) = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
-                    *reinterpret_cast<uint32_t*>(at + 128) = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
-                } else {
-                    *reinterpret_cast<uint16_t*>(at) = (uint16_t)q8_pack2(a[0].x, a[1].x);
-                    *reinterpret_cast<uint16_t*>(at + 128) = (uint16_t)q8_pack2(a[0].y, a[1].y);
-                }
+                static_assert(RP == 4, "four rows make a word");
+                *reinterpret_cast<uint32_t*>(at) = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
+                *reinterpret_cast<uint32_t*>(at + 128) = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
             }
         }
     }
 };
 
 // Two columns' scales: the keys' maximum over the warps, the scale bytes into q, 2^-e into inv.
-template <int RP>
-__device__ __forceinline__ void column_scales(const TilePos<RP>& t, int pair, const uint32_t (*keys)[64], const Q8& q, float* inv) {
+template <int RP, int CP>
+__device__ __forceinline__ void column_scales(const TilePos<RP, CP>& t, int pair, const uint32_t (*keys)[8 * CP], const Q8& q, float* inv) {
     uint32_t m = keys[0][pair];
 #pragma unroll
     for (int k = 1; k < 32 / RP; ++k) m = __vmaxu2(m, keys[k][pair]);
@@ -205,8 +218,8 @@ __device__ __forceinline__ void column_scales(const TilePos<RP>& t, int pair, co
 }
 
 // Staged columns to their rows of q.
-template <int RP>
-__device__ __forceinline__ void store_columns(const TilePos<RP>& t, const uint32_t* word, const Q8& q) {
+template <int RP, int CP>
+__device__ __forceinline__ void store_columns(const TilePos<RP, CP>& t, const uint32_t* word, const Q8& q) {
     const uint4* vec = reinterpret_cast<const uint4*>(word);
     const int part = threadIdx.x & 7;
     int n = t.rows - part * 16;
@@ -214,9 +227,9 @@ __device__ __forceinline__ void store_columns(const TilePos<RP>& t, const uint32
     uint8_t* to = q.codes + (t.c0 + (threadIdx.x >> 3)) * q.ld + t.r0 + part * 16;
     const int64_t step = (128 / RP) * q.ld;
 #pragma unroll
-    for (int i = 0; i < RP; ++i, to += step) {
+    for (int i = 0; i < RP * CP / 8; ++i, to += step) {
         const int c = (threadIdx.x >> 3) + i * (128 / RP);
-        const uint4 w = vec[c * 8 + (part ^ (c >> 4))];
+        const uint4 w = vec[c * 8 + (part ^ (c / (2 * CP)))];
         if (c < t.cols) store_codes(to, w, n);
     }
 }
@@ -239,7 +252,7 @@ struct TileArgs {
 // Row p of the thread's part of a tile: bf16 values as packed words, from the stage or (not TMA) from memory;
 // decoded 8-bit values of an 8-bit tile at `from`.
 template <int RP, bool TMA>
-__device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<RP>& t, const uint8_t* stage, int p, uint32_t (&x)[8]) {
+__device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<RP, 8>& t, const uint8_t* stage, int p, uint32_t (&x)[8]) {
     if constexpr (TMA) {
         const uint4* from = reinterpret_cast<const uint4*>(stage + (t.rg * RP + p) * 256 + t.cc * 32);
         const uint4 lo = from[0], hi = from[1];
@@ -249,19 +262,26 @@ __device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<RP>& 
         load_bf16_16(a.x + (t.r0 + t.rg * RP + p) * a.ldx + t.c0 + t.cc * 16, t.row_ok(p) ? t.chunk() : 0, x);
     }
 }
-template <int RP>
-__device__ __forceinline__ void tile_codes(const uint8_t* from, int p, uint32_t byte, float2 (&v)[8]) {
+template <int RP, int CP>
+__device__ __forceinline__ void tile_codes(const uint8_t* from, int p, uint32_t byte, float2 (&v)[CP]) {
     const int rg = threadIdx.x >> 3, cc = threadIdx.x & 7;
-    const uint4 w = *reinterpret_cast<const uint4*>(from + (rg * RP + p) * 128 + cc * 16);
-    const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+    uint32_t w[CP / 2];
+    const uint8_t* at = from + (rg * RP + p) * 16 * CP + cc * 2 * CP;
+    if constexpr (CP == 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[0] = x.x; w[1] = x.y;
+    }
     const float e = q8_scale(byte);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = q8_mul2(q8_unpack2(w4[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
+    for (int j = 0; j < CP; ++j) v[j] = q8_mul2(q8_unpack2(w[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
 }
 
 // The gated activation's backward values: 0 the gate's gradient, 1 up's, 2 the activation itself.
 template <int RP, bool TMA, int WHICH>
-__device__ __forceinline__ void gate_values(TileValues<RP>& v, const TileArgs& a, const TilePos<RP>& t, const uint8_t* stage,
+__device__ __forceinline__ void gate_values(TileValues<RP, 8>& v, const TileArgs& a, const TilePos<RP, 8>& t, const uint8_t* stage,
                                             const uint32_t (&sa)[RP], const uint32_t (&sb)[RP]) {
     const uint8_t* codes = stage + (TMA ? 128 * 128 * 2 : 0);
     const float2 one = make_float2(1.f, 1.f);
@@ -270,8 +290,8 @@ __device__ __forceinline__ void gate_values(TileValues<RP>& v, const TileArgs& a
         uint32_t x[8] = {};
         float2 g[8], u[8];
         if constexpr (WHICH < 2) tile_bf16<RP, TMA>(a, t, stage, p, x);
-        tile_codes<RP>(codes, p, sa[p], g);
-        if constexpr (WHICH != 1) tile_codes<RP>(codes + 128 * 128, p, sb[p], u);
+        tile_codes<RP, 8>(codes, p, sa[p], g);
+        if constexpr (WHICH != 1) tile_codes<RP, 8>(codes + 128 * 128, p, sb[p], u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float2 d = make_float2(bf16_lo(x[j]), bf16_hi(x[j])), sig = q8_sigmoid2(g[j]);
@@ -289,20 +309,24 @@ __device__ __forceinline__ void gate_values(TileValues<RP>& v, const TileArgs& a
 
 template <int KIND, bool TMA>
 struct TileShape {
-    // Rows per thread.  Two (twice the warps, half the registers) was slower for each of the three.
+    // Rows per thread (two, with twice the warps and half the registers, was slower for each of the three) and column
+    // pairs.  The transpose needs no whole row blocks, so its tiles are half as wide and four CTAs fit an SM.
     static constexpr int kRows = 4;
     static constexpr int kThreads = 1024 / kRows;
+    static constexpr int kPairs = KIND == kTileTurn ? 4 : 8;
+    static constexpr int kCols = 16 * kPairs;
     // The gate's three values per element are taken one after another, each computed from the tile in shared memory:
-    // all three in registers at once leave room for one CTA per SM (81 us at 5003 x 5504).
+    // all three in registers at once leave room for one CTA per SM, which is no faster (81 us at 5003 x 5504), and
+    // this way only what is wanted is computed.
     static constexpr int kPasses = KIND == kTileGate ? 3 : 1;
     static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage: bf16 tile
-    static constexpr int kA = KIND == kTileEncode ? 0 : 128 * 128;                // and 8-bit tiles
+    static constexpr int kA = KIND == kTileEncode ? 0 : 128 * kCols;                // and 8-bit tiles
     static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
     static constexpr int kStage = kX + kA + kB;
     static constexpr int kStages = KIND == kTileGate ? 1 : 2;
-    static constexpr int kKeys = (32 / kRows) * 64 * 4;
-    static constexpr int kSmem = 128 + kStages * kStage + 128 * 128 + kKeys + 512 + 64;
-    static constexpr int kPerSm = 2;
+    static constexpr int kKeys = (32 / kRows) * 8 * kPairs * 4;
+    static constexpr int kSmem = 128 + kStages * kStage + 128 * kCols + kKeys + 512 + 64;
+    static constexpr int kPerSm = KIND == kTileTurn ? 4 : 2;
 };
 
 template <int KIND, bool TMA>
@@ -310,11 +334,11 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     k_q8_tiles(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TileArgs a) {
     using S = TileShape<KIND, TMA>;
-    constexpr int RP = S::kRows, kWarps = S::kThreads / 32;
+    constexpr int RP = S::kRows, CP = S::kPairs, kWarps = S::kThreads / 32;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((128 - (su32(raw) & 127)) & 127);
-    uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [128 * 32]
-    uint32_t (*keys)[64] = reinterpret_cast<uint32_t (*)[64]>(word + 128 * 32);                 // [warps][64]
+    uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [columns * 32]
+    uint32_t (*keys)[8 * CP] = reinterpret_cast<uint32_t (*)[8 * CP]>(word + S::kCols * 32);    // [warps][column pairs]
     float* inv = reinterpret_cast<float*>(keys + kWarps);                                       // [128]
     uint64_t* full = reinterpret_cast<uint64_t*>(inv + 128);
     const int lane_row = (threadIdx.x >> 3) * RP;
@@ -329,7 +353,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     auto load_stage = [&](int s, int64_t tile) {                                    // thread 0
         if constexpr (S::kStage > 0) {
             const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c;
-            const int r0 = (int)(tr * 128), c0 = (int)(((uint32_t)tile - tr * (uint32_t)a.tiles_c) * 128);
+            const int r0 = (int)(tr * 128), c0 = (int)(((uint32_t)tile - tr * (uint32_t)a.tiles_c) * S::kCols);
             uint8_t* at = base + s * S::kStage;
             mbar_expect_tx(full + s, S::kStage);
             if constexpr (S::kX > 0) tma_load(at, &map_x, c0, r0, full + s);
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     uint32_t sa[RP] = {}, sb[RP] = {};
     auto load_scales = [&](int64_t tile) {
         if constexpr (S::kA > 0) {
-            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c, blk = (uint32_t)tile - tr * (uint32_t)a.tiles_c;
+            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c, blk = ((uint32_t)tile - tr * (uint32_t)a.tiles_c) * S::kCols >> 7;
 #pragma unroll
             for (int p = 0; p < RP; ++p) {
                 const int64_t r = (int64_t)tr * 128 + lane_row + p;
@@ -357,7 +381,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     int s = 0;
     uint32_t parity = 0;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += step) {
-        const TilePos<RP> t = tile_pos<RP>(tile, a.tiles_c, a.rows, a.cols);
+        const TilePos<RP, CP> t = tile_pos<RP, CP>(tile, a.tiles_c, a.rows, a.cols);
         bool late = false;
         if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
@@ -365,7 +389,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
         for (int pass = 0; pass < S::kPasses; ++pass) {
             const bool rows_wanted = KIND != kTileTurn && pass < 2 && a.rows_out[pass & 1].codes;
             const bool cols_wanted = a.cols_out[pass].codes;
-            TileValues<RP> v;
+            TileValues<RP, CP> v;
             float top[RP];
             if (KIND != kTileGate || rows_wanted || cols_wanted) {
                 if constexpr (KIND == kTileGate) {
@@ -381,11 +405,11 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v.v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
                         } else {
-                            tile_codes<RP>(at, p, sa[p], v.v[p]);
+                            tile_codes<RP, CP>(at, p, sa[p], v.v[p]);
                         }
                     }
                 }
-                v.find_tops(top);
+                if (rows_wanted) v.find_tops(top);
                 if (cols_wanted) v.column_keys(keys);
             }
             const bool last = pass == S::kPasses - 1;
@@ -407,8 +431,9 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
                     parity ^= 1;
                 }
             }
-            if (cols_wanted && threadIdx.x < 64) column_scales(t, threadIdx.x, keys, a.cols_out[pass], inv);
-            if (rows_wanted) v.store_rows(t, top, a.rows_out[pass & 1]);
+            if (cols_wanted && threadIdx.x < 8 * CP) column_scales(t, threadIdx.x, keys, a.cols_out[pass], inv);
+            if constexpr (KIND != kTileTurn)
+                if (rows_wanted) v.store_rows(t, top, a.rows_out[pass & 1]);
             __syncthreads();
             if (cols_wanted) v.stage_columns(t, inv, word);
             __syncthreads();
@@ -425,14 +450,14 @@ cudaError_t launch_tiles(TileArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = ready_once(ready, (const void*)k_q8_tiles<KIND, TMA>, S::kSmem);
     if (e != cudaSuccess) return e;
-    a.tiles_c = (a.cols + 127) / 128;
+    a.tiles_c = (a.cols + S::kCols - 1) / S::kCols;
     a.tiles = a.tiles_c * ((a.rows + 127) / 128);
     if (a.tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
     e = error_word(&a.error);
     CUtensorMap mx{}, ma{}, mb{};
     if (e == cudaSuccess && S::kX > 0) e = make_map(&mx, a.x, true, a.rows, a.cols, a.ldx * 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess && S::kA > 0) e = make_map(&ma, a.a.codes, false, a.rows, a.cols, a.a.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess && S::kA > 0) e = make_map(&ma, a.a.codes, false, a.rows, a.cols, a.a.ld, 128, S::kCols, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess && S::kB > 0) e = make_map(&mb, a.b.codes, false, a.rows, a.cols, a.b.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
     const int64_t room = (int64_t)q8_host::sm_count() * S::kPerSm;
