@@ -1,50 +1,55 @@
-// 128 x 128 tiles in the 8-bit format, as they are and transposed: encode, transpose and the gated
-// activation's backward pass are one persistent kernel over tiles with different inputs and values.
+// Tiles of 128 rows in the 8-bit format, as they are and transposed: encode, transpose and the gated activation's
+// backward pass are one persistent kernel over tiles with different inputs and values.
 //
-// A CTA holds a tile as fp32 in registers; thread t (warp w, lane l) holds RP (4 or 2) rows from RP * rg, with
-// rg = 4 * w + l / 8, and the 16 columns 16 * (l % 8) ...  A row's block of 128 columns is
-// then eight neighbouring lanes (three shuffles for its largest magnitude, one 16-byte store of codes per
-// lane).  A column's block of 128 rows is two shuffles and a maximum over the warps in shared memory; only
-// the exponent that the scale needs of it is passed on, two columns to a word.  A thread's rows make a
-// word of a column's codes, which pass through shared memory: a column's 128 codes are 8 chunks of 16
-// bytes, the chunk XORed with the column's 16-column group, so that a warp's stores fall into different banks.
+// A CTA of 256 threads holds a tile's values as fp32 in registers; thread t (warp w, lane l) holds four rows from
+// 4 * rg, rg = 4 * w + l / 8, and the 2 * CP columns from 2 * CP * (l % 8).  With CP = 8 a row's block of 128
+// columns is eight neighbouring lanes (three shuffles for its largest magnitude, one 16-byte store of codes per
+// lane).  A column's block of 128 rows is two shuffles and a maximum over the warps in shared memory; only the
+// exponent that the scale needs of it is passed on, two columns to a word.  Four rows make a word of a column's
+// codes, which pass through shared memory: a column's 128 codes are 8 chunks of 16 bytes, the chunk XORed with
+// the column's lane, so that a warp's stores fall into different banks.
+//
 // What bounds these kernels next to the bytes is the shared-memory pipe (shuffles, staging) and the issue of
-// instructions, hence the wide thread tiles and the two-wide arithmetic (two rows per thread, full-width
-// maxima: 16-18 instructions per value and the pipe at 76 %, 85 us for encoding 22016 x 4096 both ways).
+// instructions, hence the large thread tiles and the two-wide arithmetic.  Encoding 22016 x 4096 both ways (360 MB,
+// 53 us at the copy rate): 85 us with two rows per thread, full-width maxima and 18 instructions per value, 62 us
+// with 10.7.  The transpose issues 14 per value at 65 % of the issue rate (8192 x 4096: 20 us, bytes 10), the gate's
+// backward pass 55 at 54 % (5003 x 5504: 85 us, bytes 37).
 //
-// The next tiles' inputs arrive by tiled copies (a ring of stages) while a tile is worked on: the kernels
-// move bytes, and a tile's loads, arithmetic and stores took their times one after another when each CTA
-// loaded into registers (one tile per CTA: 242 us for the activation's backward pass at 5003 x 5504).  bf16 inputs that such copies cannot read
-// (16-byte alignment) are loaded by the threads.
+// The next tiles' inputs arrive by tiled copies (a ring of stages) while a tile is worked on: with one tile per CTA
+// loaded into registers, its loads, arithmetic and stores took their times one after another (242 us for the
+// gate's backward pass).  bf16 inputs that such copies cannot read (16-byte alignment) are loaded by the threads.
 #pragma once
 
 #include "q8_tma.cuh"
 
 namespace zs {
 
+constexpr int kTileRp = 4;       // rows per thread
+constexpr int kTileLanes = 8;    // lanes per row
+constexpr int kTileThreads = 32 * kTileLanes;
 
-template <int RP, int CP>    // rows and column pairs per thread; tiles have 128 rows and 16 * CP columns
+template <int CP>            // column pairs per thread: tiles have 128 rows and 16 * CP columns
 struct TilePos {
-    int cc, rg;              // column chunk (2 * CP columns), row group (RP rows)
+    int cc, rg;              // column chunk (2 * CP columns), row group (four rows)
     int64_t r0, c0;          // the tile's first row and column
     int rows, cols;          // valid rows and columns of the tile, 1 .. 128
-    __device__ __forceinline__ bool row_ok(int p) const { return rg * RP + p < rows; }
+    __device__ __forceinline__ bool row_ok(int p) const { return rg * kTileRp + p < rows; }
     __device__ __forceinline__ int chunk() const {            // valid columns of this thread's
         const int n = cols - cc * 2 * CP;
         return n < 0 ? 0 : n > 2 * CP ? 2 * CP : n;
     }
 };
 
-template <int RP, int CP>
-__device__ __forceinline__ TilePos<RP, CP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
-    TilePos<RP, CP> t;
-    t.cc = threadIdx.x & 7;
-    t.rg = threadIdx.x >> 3;
+template <int CP>
+__device__ __forceinline__ TilePos<CP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
+    TilePos<CP> t;
+    t.cc = threadIdx.x % kTileLanes;
+    t.rg = threadIdx.x / kTileLanes;
     const uint32_t tr = (uint32_t)tile / (uint32_t)tiles_c;
     t.r0 = (int64_t)tr * 128;
-    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * (16 * CP);
+    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * (2 * CP * kTileLanes);
     t.rows = rows - t.r0 < 128 ? (int)(rows - t.r0) : 128;
-    t.cols = cols - t.c0 < 16 * CP ? (int)(cols - t.c0) : 16 * CP;
+    t.cols = cols - t.c0 < 2 * CP * kTileLanes ? (int)(cols - t.c0) : 2 * CP * kTileLanes;
     return t;
 }
 
@@ -68,10 +73,11 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p, int n) {
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// 16 bf16 values at p (n of them valid, the others 0) as packed words, from any 2-byte alignment.
-__device__ __forceinline__ void load_bf16_16(const uint16_t* p, int n, uint32_t (&w)[8]) {
+// 2 * CP bf16 values at p (n of them valid, the others 0) as packed words, from any 2-byte alignment.
+template <int CP>
+__device__ __forceinline__ void load_bf16(const uint16_t* p, int n, uint32_t (&w)[CP]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < CP; ++i) {
         const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
         w[i] = lo | (hi << 16);
     }
@@ -88,8 +94,9 @@ __device__ __forceinline__ uint32_t key_byte(uint32_t key) {            // key: 
 }
 
 // A thread's part of a tile's values: rows p, column pairs.
-template <int RP, int CP>
+template <int CP>
 struct TileValues {
+    static constexpr int RP = kTileRp;
     float2 v[RP][CP];
 
     // Largest magnitude of each row's values.  Infinities become NaN, which the encoding leaves out of the
@@ -117,23 +124,22 @@ struct TileValues {
         }
     }
     // The tile as it is.
-    __device__ __forceinline__ void store_rows(const TilePos<RP, CP>& t, const float (&top)[RP], const Q8& q) const {
-        static_assert(CP == 8, "a row's block is eight lanes");
+    __device__ __forceinline__ void store_rows(const TilePos<CP>& t, const float (&top)[RP], const Q8& q) const {
+        static_assert(2 * CP * kTileLanes == 128, "a row of the tile is a block");
         const int n = t.chunk();
         const int64_t r0 = t.r0 + t.rg * RP;
-        uint8_t* codes = q.codes + r0 * q.ld + t.c0 + t.cc * 16;
+        uint8_t* codes = q.codes + r0 * q.ld + t.c0 + t.cc * 2 * CP;
         uint8_t* scales = q.scales + r0 * q.lds + (t.c0 >> 7);
 #pragma unroll
         for (int p = 0; p < RP; ++p) {
             float m = top[p];
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+#pragma unroll
+            for (int k = 1; k < kTileLanes; k <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
             const uint32_t byte = q8_scale_byte(m);
             const float inv = q8_inverse(byte);
-            uint32_t w[4];
+            uint32_t w[CP / 2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < CP / 2; ++k) {
                 const float2 a = q8_mul2(v[p][2 * k], make_float2(inv, inv)), b = q8_mul2(v[p][2 * k + 1], make_float2(inv, inv));
                 w[k] = q8_pack4(a.x, a.y, b.x, b.y);
             }
@@ -147,7 +153,7 @@ struct TileValues {
     }
     // Scale keys of the columns over this warp's rows, into sh[warp][column pair].  Without find_tops before it
     // (no rows stored), infinities are found and replaced here.
-    __device__ __forceinline__ void column_keys(uint32_t (*sh)[8 * CP]) {
+    __device__ __forceinline__ void column_keys(uint32_t (*sh)[CP * kTileLanes]) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         float2 top[CP];
         auto tops = [&] {
@@ -174,18 +180,19 @@ struct TileValues {
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
             key[j] = scale_keys(top[j].x, top[j].y);
-            key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 8));
-            key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], 16));
+#pragma unroll
+            for (int k = kTileLanes; k < 32; k <<= 1) key[j] = __vmaxu2(key[j], __shfl_xor_sync(~0u, key[j], k));
         }
-        if (lane < 8) {
+        if (lane < kTileLanes) {
             uint4* to = reinterpret_cast<uint4*>(&sh[warp][lane * CP]);
 #pragma unroll
             for (int k = 0; k < CP / 4; ++k) to[k] = make_uint4(key[4 * k], key[4 * k + 1], key[4 * k + 2], key[4 * k + 3]);
         }
     }
-    // Codes of the columns into word (8 chunks of 16 bytes per column), with inv[column] = 2^-e.
-    __device__ __forceinline__ void stage_columns(const TilePos<RP, CP>& t, const float* inv, uint32_t* word) const {
-        uint8_t* to = reinterpret_cast<uint8_t*>(word) + t.cc * 2 * CP * 128 + ((((t.rg * RP) >> 4) ^ t.cc) << 4) + ((t.rg * RP) & 15);
+    // Codes of the columns into word (8 chunks of 16 bytes per column), with inv[column] = 2^-e.  The chunk is XORed
+    // with the column chunk, so that a warp's words fall into different banks.
+    __device__ __forceinline__ void stage_columns(const TilePos<CP>& t, const float* inv, uint32_t* word) const {
+        uint32_t* to = word + t.cc * 2 * CP * 32 + (((t.rg >> 2) ^ t.cc) << 2) + (t.rg & 3);
 #pragma unroll
         for (int k = 0; k < CP / 2; ++k) {
             const float4 e = *reinterpret_cast<const float4*>(inv + t.cc * 2 * CP + k * 4);
@@ -195,21 +202,19 @@ struct TileValues {
                 float2 a[RP];
 #pragma unroll
                 for (int p = 0; p < RP; ++p) a[p] = q8_mul2(v[p][k * 2 + h], s);
-                uint8_t* at = to + (k * 4 + h * 2) * 128;
-                static_assert(RP == 4, "four rows make a word");
-                *reinterpret_cast<uint32_t*>(at) = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
-                *reinterpret_cast<uint32_t*>(at + 128) = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
+                to[(k * 4 + h * 2) * 32] = q8_pack4(a[0].x, a[1].x, a[2].x, a[3].x);
+                to[(k * 4 + h * 2 + 1) * 32] = q8_pack4(a[0].y, a[1].y, a[2].y, a[3].y);
             }
         }
     }
 };
 
 // Two columns' scales: the keys' maximum over the warps, the scale bytes into q, 2^-e into inv.
-template <int RP, int CP>
-__device__ __forceinline__ void column_scales(const TilePos<RP, CP>& t, int pair, const uint32_t (*keys)[8 * CP], const Q8& q, float* inv) {
+template <int CP>
+__device__ __forceinline__ void column_scales(const TilePos<CP>& t, int pair, const uint32_t (*keys)[CP * kTileLanes], const Q8& q, float* inv) {
     uint32_t m = keys[0][pair];
 #pragma unroll
-    for (int k = 1; k < 32 / RP; ++k) m = __vmaxu2(m, keys[k][pair]);
+    for (int k = 1; k < kTileLanes; ++k) m = __vmaxu2(m, keys[k][pair]);
     const uint32_t lo = key_byte(m & 0xffffu), hi = key_byte(m >> 16);
     *reinterpret_cast<float2*>(inv + pair * 2) = make_float2(q8_inverse(lo), q8_inverse(hi));
     uint8_t* to = q.scales + (t.c0 + pair * 2) * q.lds + (t.r0 >> 7);
@@ -218,17 +223,17 @@ __device__ __forceinline__ void column_scales(const TilePos<RP, CP>& t, int pair
 }
 
 // Staged columns to their rows of q.
-template <int RP, int CP>
-__device__ __forceinline__ void store_columns(const TilePos<RP, CP>& t, const uint32_t* word, const Q8& q) {
+template <int CP>
+__device__ __forceinline__ void store_columns(const TilePos<CP>& t, const uint32_t* word, const Q8& q) {
     const uint4* vec = reinterpret_cast<const uint4*>(word);
     const int part = threadIdx.x & 7;
     int n = t.rows - part * 16;
     n = n < 0 ? 0 : n > 16 ? 16 : n;
     uint8_t* to = q.codes + (t.c0 + (threadIdx.x >> 3)) * q.ld + t.r0 + part * 16;
-    const int64_t step = (128 / RP) * q.ld;
+    const int64_t step = 4 * kTileLanes * q.ld;
 #pragma unroll
-    for (int i = 0; i < RP * CP / 8; ++i, to += step) {
-        const int c = (threadIdx.x >> 3) + i * (128 / RP);
+    for (int i = 0; i < CP / 2; ++i, to += step) {
+        const int c = (threadIdx.x >> 3) + i * 4 * kTileLanes;
         const uint4 w = vec[c * 8 + (part ^ (c / (2 * CP)))];
         if (c < t.cols) store_codes(to, w, n);
     }
@@ -251,22 +256,23 @@ struct TileArgs {
 
 // Row p of the thread's part of a tile: bf16 values as packed words, from the stage or (not TMA) from memory;
 // decoded 8-bit values of an 8-bit tile at `from`.
-template <int RP, bool TMA>
-__device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<RP, 8>& t, const uint8_t* stage, int p, uint32_t (&x)[8]) {
+template <bool TMA, int CP>
+__device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<CP>& t, const uint8_t* stage, int p, uint32_t (&x)[CP]) {
     if constexpr (TMA) {
-        const uint4* from = reinterpret_cast<const uint4*>(stage + (t.rg * RP + p) * 256 + t.cc * 32);
-        const uint4 lo = from[0], hi = from[1];
-        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+        const uint4* from = reinterpret_cast<const uint4*>(stage + (t.rg * kTileRp + p) * 4 * CP * kTileLanes + t.cc * 4 * CP);
+#pragma unroll
+        for (int k = 0; k < CP / 4; ++k) {
+            const uint4 w = from[k];
+            x[4 * k] = w.x; x[4 * k + 1] = w.y; x[4 * k + 2] = w.z; x[4 * k + 3] = w.w;
+        }
     } else {
-        load_bf16_16(a.x + (t.r0 + t.rg * RP + p) * a.ldx + t.c0 + t.cc * 16, t.row_ok(p) ? t.chunk() : 0, x);
+        load_bf16<CP>(a.x + (t.r0 + t.rg * kTileRp + p) * a.ldx + t.c0 + t.cc * 2 * CP, t.row_ok(p) ? t.chunk() : 0, x);
     }
 }
-template <int RP, int CP>
-__device__ __forceinline__ void tile_codes(const uint8_t* from, int p, uint32_t byte, float2 (&v)[CP]) {
-    const int rg = threadIdx.x >> 3, cc = threadIdx.x & 7;
+template <int CP>
+__device__ __forceinline__ void tile_codes(const TilePos<CP>& t, const uint8_t* from, int p, uint32_t byte, float2 (&v)[CP]) {
     uint32_t w[CP / 2];
-    const uint8_t* at = from + (rg * RP + p) * 16 * CP + cc * 2 * CP;
+    const uint8_t* at = from + (t.rg * kTileRp + p) * 2 * CP * kTileLanes + t.cc * 2 * CP;
     if constexpr (CP == 8) {
         const uint4 x = *reinterpret_cast<const uint4*>(at);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
@@ -280,20 +286,20 @@ __device__ __forceinline__ void tile_codes(const uint8_t* from, int p, uint32_t 
 }
 
 // The gated activation's backward values: 0 the gate's gradient, 1 up's, 2 the activation itself.
-template <int RP, bool TMA, int WHICH>
-__device__ __forceinline__ void gate_values(TileValues<RP, 8>& v, const TileArgs& a, const TilePos<RP, 8>& t, const uint8_t* stage,
-                                            const uint32_t (&sa)[RP], const uint32_t (&sb)[RP]) {
+template <int WHICH, bool TMA, int CP>
+__device__ __forceinline__ void gate_values(TileValues<CP>& v, const TileArgs& a, const TilePos<CP>& t, const uint8_t* stage,
+                                            const uint32_t (&sa)[kTileRp], const uint32_t (&sb)[kTileRp]) {
     const uint8_t* codes = stage + (TMA ? 128 * 128 * 2 : 0);
     const float2 one = make_float2(1.f, 1.f);
 #pragma unroll
-    for (int p = 0; p < RP; ++p) {
-        uint32_t x[8] = {};
-        float2 g[8], u[8];
-        if constexpr (WHICH < 2) tile_bf16<RP, TMA>(a, t, stage, p, x);
-        tile_codes<RP, 8>(codes, p, sa[p], g);
-        if constexpr (WHICH != 1) tile_codes<RP, 8>(codes + 128 * 128, p, sb[p], u);
+    for (int p = 0; p < kTileRp; ++p) {
+        uint32_t x[CP] = {};
+        float2 g[CP], u[CP];
+        if constexpr (WHICH < 2) tile_bf16<TMA>(a, t, stage, p, x);
+        tile_codes(t, codes, p, sa[p], g);
+        if constexpr (WHICH != 1) tile_codes(t, codes + 128 * 128, p, sb[p], u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < CP; ++j) {
             const float2 d = make_float2(bf16_lo(x[j]), bf16_hi(x[j])), sig = q8_sigmoid2(g[j]);
             if constexpr (WHICH == 0) {
                 const float2 rest = q8_fma2(sig, make_float2(-1.f, -1.f), one);                  // 1 - sigmoid
@@ -309,12 +315,11 @@ __device__ __forceinline__ void gate_values(TileValues<RP, 8>& v, const TileArgs
 
 template <int KIND, bool TMA>
 struct TileShape {
-    // Rows per thread (two, with twice the warps and half the registers, was slower for each of the three) and column
-    // pairs.  The transpose needs no whole row blocks, so its tiles are half as wide and four CTAs fit an SM.
-    static constexpr int kRows = 4;
-    static constexpr int kThreads = 1024 / kRows;
+    // Column pairs per thread and lanes per row.  The transpose needs no whole row blocks, so its tiles are half as wide
+    // and four CTAs fit an SM.  The others do best with large threads: the gate's backward pass at 5003 x 5504
+    // takes 85 us so and 108 with 16 lanes of half the columns.
     static constexpr int kPairs = KIND == kTileTurn ? 4 : 8;
-    static constexpr int kCols = 16 * kPairs;
+    static constexpr int kCols = 2 * kPairs * kTileLanes;
     // The gate's three values per element are taken one after another, each computed from the tile in shared memory:
     // all three in registers at once leave room for one CTA per SM, which is no faster (81 us at 5003 x 5504), and
     // this way only what is wanted is computed.
@@ -324,24 +329,24 @@ struct TileShape {
     static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
     static constexpr int kStage = kX + kA + kB;
     static constexpr int kStages = KIND == kTileGate ? 1 : 2;
-    static constexpr int kKeys = (32 / kRows) * 8 * kPairs * 4;
+    static constexpr int kKeys = kTileLanes * kPairs * kTileLanes * 4;
     static constexpr int kSmem = 128 + kStages * kStage + 128 * kCols + kKeys + 512 + 64;
     static constexpr int kPerSm = KIND == kTileTurn ? 4 : 2;
 };
 
 template <int KIND, bool TMA>
-__global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<KIND, TMA>::kPerSm))
+__global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     k_q8_tiles(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TileArgs a) {
     using S = TileShape<KIND, TMA>;
-    constexpr int RP = S::kRows, CP = S::kPairs, kWarps = S::kThreads / 32;
+    constexpr int RP = kTileRp, CP = S::kPairs;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((128 - (su32(raw) & 127)) & 127);
     uint32_t* word = reinterpret_cast<uint32_t*>(base + S::kStages * S::kStage);                // [columns * 32]
-    uint32_t (*keys)[8 * CP] = reinterpret_cast<uint32_t (*)[8 * CP]>(word + S::kCols * 32);    // [warps][column pairs]
-    float* inv = reinterpret_cast<float*>(keys + kWarps);                                       // [128]
+    uint32_t (*keys)[CP * kTileLanes] = reinterpret_cast<uint32_t (*)[CP * kTileLanes]>(word + S::kCols * 32);    // [warps][column pairs]
+    float* inv = reinterpret_cast<float*>(keys + kTileLanes);                                       // [128]
     uint64_t* full = reinterpret_cast<uint64_t*>(inv + 128);
-    const int lane_row = (threadIdx.x >> 3) * RP;
+    const int lane_row = threadIdx.x / kTileLanes * RP;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
     int s = 0;
     uint32_t parity = 0;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += step) {
-        const TilePos<RP, CP> t = tile_pos<RP, CP>(tile, a.tiles_c, a.rows, a.cols);
+        const TilePos<CP> t = tile_pos<CP>(tile, a.tiles_c, a.rows, a.cols);
         bool late = false;
         if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
@@ -389,23 +394,23 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
         for (int pass = 0; pass < S::kPasses; ++pass) {
             const bool rows_wanted = KIND != kTileTurn && pass < 2 && a.rows_out[pass & 1].codes;
             const bool cols_wanted = a.cols_out[pass].codes;
-            TileValues<RP, CP> v;
+            TileValues<CP> v;
             float top[RP];
             if (KIND != kTileGate || rows_wanted || cols_wanted) {
                 if constexpr (KIND == kTileGate) {
-                    if (pass == 0) gate_values<RP, TMA, 0>(v, a, t, at, sa, sb);
-                    else if (pass == 1) gate_values<RP, TMA, 1>(v, a, t, at, sa, sb);
-                    else gate_values<RP, TMA, 2>(v, a, t, at, sa, sb);
+                    if (pass == 0) gate_values<0, TMA>(v, a, t, at, sa, sb);
+                    else if (pass == 1) gate_values<1, TMA>(v, a, t, at, sa, sb);
+                    else gate_values<2, TMA>(v, a, t, at, sa, sb);
                 } else {
 #pragma unroll
                     for (int p = 0; p < RP; ++p) {
                         if constexpr (KIND == kTileEncode) {
-                            uint32_t x[8];
-                            tile_bf16<RP, TMA>(a, t, at, p, x);
+                            uint32_t x[CP];
+                            tile_bf16<TMA>(a, t, at, p, x);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) v.v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
+                            for (int j = 0; j < CP; ++j) v.v[p][j] = make_float2(bf16_lo(x[j]), bf16_hi(x[j]));
                         } else {
-                            tile_codes<RP, CP>(at, p, sa[p], v.v[p]);
+                            tile_codes(t, at, p, sa[p], v.v[p]);
                         }
                     }
                 }
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__((TileShape<KIND, TMA>::kThreads), (TileShape<K
                     parity ^= 1;
                 }
             }
-            if (cols_wanted && threadIdx.x < 8 * CP) column_scales(t, threadIdx.x, keys, a.cols_out[pass], inv);
+            if (cols_wanted && threadIdx.x < CP * kTileLanes) column_scales(t, threadIdx.x, keys, a.cols_out[pass], inv);
             if constexpr (KIND != kTileTurn)
                 if (rows_wanted) v.store_rows(t, top, a.rows_out[pass & 1]);
             __syncthreads();
@@ -461,7 +466,7 @@ cudaError_t launch_tiles(TileArgs& a, cudaStream_t st) {
     if (e == cudaSuccess && S::kB > 0) e = make_map(&mb, a.b.codes, false, a.rows, a.cols, a.b.ld, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
     const int64_t room = (int64_t)q8_host::sm_count() * S::kPerSm;
-    return launch_kernel(k_q8_tiles<KIND, TMA>, dim3((unsigned)(a.tiles < room ? a.tiles : room)), dim3(S::kThreads), S::kSmem, st, mx,
+    return launch_kernel(k_q8_tiles<KIND, TMA>, dim3((unsigned)(a.tiles < room ? a.tiles : room)), dim3(kTileThreads), S::kSmem, st, mx,
                          ma, mb, a);
 }
 

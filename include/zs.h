@@ -624,7 +624,9 @@ int zs_zero3_step(zs_plan_t plan, void* shards, float* master, float* m, float* 
  *              codes 16-byte aligned (so a matrix may be a column range of a
  *              larger one that starts at a multiple of 16).
  *   ld_scales  bytes between rows of scales, >= ceil(cols / ZS_Q8_BLOCK).
- * Only the rows x cols codes and their scales are read or written.
+ * Only the rows x cols codes and their scales are written.  Bytes between the
+ * first and the last of a matrix that are not its own (a row distance larger
+ * than the row) may be read along with it and do not matter.
  *
  * bf16 matrices are given by a 2-byte aligned pointer and the elements between
  * rows (>= cols): views into flat parameter and gradient buffers at any
