@@ -60,6 +60,46 @@ def test_decode_and_transpose_are_exact(rows, cols, layout):
     qt.assert_untouched_outside()
 
 
+@pytest.mark.parametrize("spread", [0, 3, 15, 16, 40, 120])
+@pytest.mark.parametrize("rows,cols", [(128, 64), (300, 200), (77, 130)])
+def test_transpose_of_rows_with_far_scales(spread, rows, cols):
+    """Scales of neighbouring rows up to 2^120 apart, columns of every size, rows and columns of zeros, NaN codes
+    and NaN scales: the transpose is exact whichever way a tile takes."""
+    rng = np.random.default_rng(spread * 100 + rows)
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-spread, spread + 1, (rows, 1)))
+    x *= np.exp2(rng.integers(-spread // 2, 1, (1, cols)))
+    x[rng.integers(0, rows, 5)] = 0.0
+    x[:, rng.integers(0, cols, 5)] = 0.0
+    x[rows // 2:rows // 2 + 20, :] *= np.exp2(-spread)                  # warps of rows far below the others
+    codes, scales = q8.encode(x)
+    codes[rows // 3, cols // 2] = 0x7f
+    codes[0, :3] = 0x80                                                # negative zeros
+    if spread == 40:
+        scales[rows // 4, 0] = 255
+    q = Q8Matrix(rows, cols).fill(codes, scales)
+    qt = Q8Matrix(cols, rows)
+    zs.zs_q8_transpose(q.pair, qt.pair)
+    want = q8.encode(q8.decode(codes, scales).T)
+    got = qt.numpy()
+    assert np.array_equal(got[1], want[1])
+    a, b = q8.VALUES[got[0]], q8.VALUES[want[0]]
+    assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(a[~np.isnan(a)], b[~np.isnan(b)])
+    qt.assert_untouched_outside()
+
+
+def test_transpose_near_the_ends_of_the_scales():
+    """Scale bytes 0 to 254: values down to 2^-136 and up to 448 * 2^119 (beyond, fp32 would overflow)."""
+    for low, high in ((0, 12), (0, 40), (100, 140), (230, 246), (236, 247)):
+        rng = np.random.default_rng(low + high)
+        codes = rng.integers(0, 127, (130, 70)).astype(np.uint8) | (rng.integers(0, 2, (130, 70)) << 7).astype(np.uint8)
+        scales = rng.integers(low, high, (130, 1)).astype(np.uint8)
+        q, qt = Q8Matrix(130, 70).fill(codes, scales), Q8Matrix(70, 130)
+        zs.zs_q8_transpose(q.pair, qt.pair)
+        want = q8.encode(q8.decode(codes, scales).T)
+        assert np.array_equal(qt.numpy()[1], want[1])
+        assert np.array_equal(q8.VALUES[qt.numpy()[0]], q8.VALUES[want[0]])
+
+
 def test_encode_values_at_the_edges():
     """Zeros, the smallest and largest bf16 values, ties, infinities and NaN, each in a block of its own."""
     rows = np.zeros((10, 256))
