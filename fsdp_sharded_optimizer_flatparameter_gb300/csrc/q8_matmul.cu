@@ -506,11 +506,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                 const int c = c0 + (i >> 5), r = (i & 31) * 4;
                 const int64_t p = (int64_t)p0 + r;
                 if (c >= n || p >= a.rows_p) continue;
+                // every part's load under way before the first is added
+                float4 x[kSplitMost];
+#pragma unroll
+                for (int k = 0; k < kSplitMost; ++k)
+                    if (k < split) x[k] = cluster_ld4(at_rank(base + (c * 128 + r) * 4, k));
                 float v[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int k = 0; k < split; ++k) {
-                    const float4 x = cluster_ld4(at_rank(base + (c * 128 + r) * 4, k));
-                    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                }
+#pragma unroll
+                for (int k = 0; k < kSplitMost; ++k)
+                    if (k < split) {
+                        v[0] += x[k].x; v[1] += x[k].y; v[2] += x[k].z; v[3] += x[k].w;
+                    }
                 uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = v[j] * a.scale;
@@ -532,13 +538,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                     float f[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) f[j] = 0.f;
-                    for (int k = 0; k < split; ++k) {
-                        const uint32_t at = at_rank(base + (c * 128 + r0 + lane) * 4, k);
-                        float x[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = cluster_ld(at + j * 512);
+                    for (int k = 0; k < kSplitMost; k += 2) {        // two parts' loads under way at a time
+                        if (k >= split) break;
+                        float x[2][16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] += x[j];
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t at = at_rank(base + (c * 128 + r0 + lane) * 4, k + i);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[i][j] = cluster_ld(at + j * 512);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) f[j] += x[i][j];
                     }
                     store_rows16(a.out + p * a.ldo + q0 + c, a.ldo, f, rows, n - c, a.align, a.scale, a.first,
                                  store_sh + (warp - 6) * kStoreStage);
