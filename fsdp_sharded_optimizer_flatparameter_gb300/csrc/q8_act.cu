@@ -245,6 +245,29 @@ __device__ __forceinline__ void norm_outputs(const float2 (&t)[8], float2 r, con
     }
 }
 
+// ------------------------------------------------------------------ rows through shared memory
+
+constexpr int kRowStages = 4;
+constexpr int kRowSmem = kRowStages * 8192 * 6;      // the widest row of 512 threads, three bf16 matrices
+constexpr long long kRowWait = 4000000000LL;         // ~2 s at the 2.07 GHz maximum SM clock
+
+// bytes (a multiple of 16) from src to dst, both 16-byte aligned, counted on bar.
+__device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)), "l"(src),
+                 "r"(bytes), "r"(su32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ V16 row16(const uint8_t* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    return V16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+// After a wait ran out: one thread lets the copies on their way land, so that the CTA may exit.
+__device__ __forceinline__ void drain_rows(uint64_t* full, int at, uint32_t parity, int64_t left, unsigned int* error) {
+    atomicCAS(error, 0u, ZS_DEVERR_TILE_WAIT);
+    for (int i = 0; i < kRowStages && i < left; ++i)
+        mbar_wait(full + (at + i) % kRowStages, at + i >= kRowStages ? parity ^ 1 : parity, kRowWait);
+}
+
 // ------------------------------------------------------------------ norm, forward
 
 struct NormArgs {
@@ -258,7 +281,8 @@ struct NormArgs {
 
 // A CTA takes rows blockIdx.x, + gridDim.x, ...  NV > 0: a row's sum stays in registers, NV vectors of 16 columns
 // per thread, and the next row's loads are under way while a row is reduced and written.  NV = 0, for rows
-// longer than that: the row is read a second time (from L2).
+// longer than that: the row is read a second time (from L2).  Rows brought by bulk copies through shared memory, two
+// to four stages of them, took the same time (16384 x 4096: 91-93 us, and 92-95 with 640 to 1024 threads per SM).
 template <int NV, bool WIDE>
 __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ NormArgs a) {
     __shared__ float2 sh[2][16];
@@ -356,18 +380,19 @@ struct NormBackArgs {
     int64_t lddy, lds, ldds, lddx, rows, cols;
     int threads;             // of a group
     int parts;               // rows of partials written: the grid
+    unsigned int* error;
 };
 
 // The CTA's threads are groups of `threads`, a row each at a time; a group takes every (groups of the grid)th row
-// and keeps its part of dw: a thread owns its 16 columns in every row, in registers (HELD), the next row's
-// loads being under way while a row is reduced and written.  Narrow rows are GROUPED: several rows at a time in
-// a CTA, the groups' parts added in shared memory, so that they fill the SM without more rows of partials
-// (999 x 2047: 14.3 us with a group per CTA, 10.2 with four).  Rows wider than 512 threads hold are read twice
-// (from L2), dw's part in the CTA's row of `partials`.
-template <bool HELD, bool WIDE, bool GROUPED, bool KEPT8>
+// and keeps its part of dw: a thread owns its 16 columns in every row, in registers (HELD), the loads of the next
+// row, or the next four (RING), being under way while a row is reduced and written.  Narrow rows are GROUPED: several
+// rows at a time in a CTA, the groups' parts added in shared memory, so that they fill the SM without more rows of
+// partials (999 x 2047: 14.3 us with a group per CTA, 9.9 with four).  Rows wider than 512 threads hold are read
+// twice (from L2), dw's part in the CTA's row of `partials`.
+template <bool HELD, bool WIDE, bool GROUPED, bool KEPT8, bool RING>
 __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBackArgs a) {
     __shared__ float sums[16][2][16];            // per group and turn
-    extern __shared__ float parts_sh[];          // [group][columns of its threads], with more than one group
+    extern __shared__ __align__(16) float parts_sh[];    // [group][columns of its threads], or the RING's stages
     dependent_launch_prologue();
     const int groups = GROUPED ? blockDim.x / a.threads : 1, group = GROUPED ? threadIdx.x / a.threads : 0;
     const int threads = GROUPED ? a.threads : blockDim.x, tid = threadIdx.x - group * threads;
@@ -423,24 +448,79 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
     float* part = a.partials + (int64_t)blockIdx.x * a.pitch;
     int turn = 0;
     if constexpr (HELD) {
-        Row next;
+        Row next = {};
         float2 dw[8];
-        float r_next = row0 < a.rows ? a.rstd[row0] : 0.f;
-        if (row0 < a.rows) fetch(row0, col0, next);
+        float r_next = 0.f;
         const V16 w = load16<WIDE>(a.weight + col0, a.cols - col0, sw);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[i] = make_float2(0.f, 0.f);
+
+        // RING, with one group: the CTA's rows in stages of dy, s (or its codes) and ds; thread 0 issues the copies.
+        __shared__ uint64_t full[kRowStages];
+        __shared__ int gave_up[2];
+        const uint32_t bytes = (uint32_t)a.cols * 2, kept = KEPT8 ? bytes / 2 : bytes, stage = bytes + kept + (a.ds ? bytes : 0);
+        uint8_t* ring = reinterpret_cast<uint8_t*>(parts_sh);
+        const bool in = col0 < a.cols;
+        auto copy = [&](int64_t row, int at) {
+            uint8_t* to = ring + at * stage;
+            mbar_expect_tx(full + at, stage);
+            bulk_row(to, a.dy + row * a.lddy, bytes, full + at);
+            bulk_row(to + bytes, KEPT8 ? (const void*)(a.s_q8.codes + row * a.s_q8.ld) : (const void*)(a.s + row * a.lds), kept, full + at);
+            if (a.ds) bulk_row(to + bytes + kept, a.ds + row * a.ldds, bytes, full + at);
+        };
+        auto begin = [&](int64_t row) {          // what a row's turn needs besides its stage, or all of the row
+            r_next = a.rstd[row];
+            if constexpr (!RING) fetch(row, col0, next);
+            else if (KEPT8 && in) next.s.w[4] = a.s_q8.scales[row * a.s_q8.lds + (col0 >> 7)];
+        };
+        if constexpr (RING) {
+            if (tid == 0) {
+                for (int i = 0; i < kRowStages; ++i) mbar_init(full + i, 1);
+                gave_up[0] = gave_up[1] = 0;
+                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            }
+            __syncthreads();
+            if (tid == 0)
+#pragma unroll 1                                 // unrolled, 16384 x 4096 took 85 us instead of 76
+                for (int i = 0; i < kRowStages && row0 + i * stride < a.rows; ++i) copy(row0 + i * stride, i);
+        }
+        if (row0 < a.rows) begin(row0);
+        int at = 0;
+        uint32_t parity = 0;
         for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
+            if constexpr (RING) {
+                if (!mbar_wait(full + at, parity, kRowWait)) gave_up[turn] = 1;
+                const uint8_t* from = ring + at * stage;
+                if (in) {
+                    next.dy = row16(from + col0 * 2);
+                    if constexpr (KEPT8) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(from + bytes + col0);
+                        next.s.w[0] = q.x, next.s.w[1] = q.y, next.s.w[2] = q.z, next.s.w[3] = q.w;
+                    } else {
+                        next.s = row16(from + bytes + col0 * 2);
+                    }
+                    if (a.ds) next.ds = row16(from + bytes + kept + col0 * 2);
+                }
+            }
             const Row now = next;
             float2 xh[8];
             const float r = r_next;
             normalised(now, r, xh);
             const float d = dot(now, w, xh);
-            if (row + stride < a.rows) {
-                r_next = a.rstd[row + stride];
-                fetch(row + stride, col0, next);
-            }
+            if (row + stride < a.rows) begin(row + stride);
             const float along = group_sum(d, sh[turn], threads, group + 1) * inv_cols;
+            if constexpr (RING) {
+                // the whole CTA has read the stage, and knows who gave up (the next row's flag is another)
+                if (gave_up[turn]) {
+                    if (tid == 0) drain_rows(full, at, parity, (a.rows - row + stride - 1) / stride, a.error);
+                    break;
+                }
+                if (tid == 0 && row + kRowStages * stride < a.rows) copy(row + kRowStages * stride, at);
+                if (++at == kRowStages) {
+                    at = 0;
+                    parity ^= 1;
+                }
+            }
             write(row, col0, r, along, now, w, xh);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[i] = q8_fma2(pair_of(now.dy.w[i]), xh[i], dw[i]);
@@ -564,8 +644,8 @@ __global__ void __launch_bounds__(kGateMost) k_swiglu_q8(const __grid_constant__
     if (a.up_q.codes) encode16(u, n, a.up_q, row, c);
 }
 
-// Threads and register vectors (of 16 columns, `least` to `most` of them) for a row of `cols` columns: the fewest vectors per thread that keep the CTA within 512 threads; nv = 0 when the row does not
-// fit in registers.
+// Threads and register vectors (of 16 columns, `least` to `most` of them) for a row of `cols` columns: the fewest
+// vectors per thread that keep the CTA within 512 threads; nv = 0 when the row does not fit in registers.
 void row_shape(int64_t cols, int least, int most, int* threads, int* nv) {
     const int64_t vecs = (cols + 15) / 16;
     for (int k = least; k <= most; ++k) {
@@ -583,13 +663,15 @@ void row_shape(int64_t cols, int least, int most, int* threads, int* nv) {
 template <bool WIDE>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     int threads, nv;
-    // Many rows: two vectors per thread, so that what a thread does once per row (the reduction, the root) is
-    // shared by 32 columns; few rows: one, for the shorter chain.
+    // As many CTAs as are resident: 640 threads per SM, or 512 with two vectors in their registers.  One vector per
+    // thread, except where its CTAs of 256 threads and more fill 512 threads of an SM only and not all rows are
+    // resident at once: then two, which share what a thread does once per row (16384 x 4096: 93 us with two, 109 with
+    // one; 16384 x 2560: 77 and 61; 300 x 4096: 4.4 and 3.3; 4096 x 512: 6.5 and 5.9).
     const int sms = q8_host::sm_count();
-    row_shape(a.cols, a.rows >= 8 * (int64_t)sms ? 2 : 1, 2, &threads, &nv);
-    // as many CTAs as are resident: 512 threads per SM with two vectors and their prefetch in registers, or 640
-    const int most = nv == 2 ? 512 : 640;
-    const int64_t room = (int64_t)sms * (most / threads < 1 ? 1 : most / threads);
+    auto ctas = [&] { return sms * std::max(1, (nv == 2 ? 512 : 640) / threads); };
+    row_shape(a.cols, 1, 2, &threads, &nv);
+    if (nv == 1 && threads >= 256 && a.rows > ctas()) row_shape(a.cols, 2, 2, &threads, &nv);
+    const int64_t room = ctas();
     const dim3 grid((unsigned)(a.rows < room ? a.rows : room)), block(threads);
     switch (nv) {
         case 1: return launch_kernel(k_rmsnorm_q8<1, WIDE>, grid, block, 0, st, a);
@@ -598,20 +680,37 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     }
 }
 
-// Narrow rows: groups of threads in CTAs of about 512, one per SM.  Rows of 256 threads and more: a CTA each, two
-// per SM (in groups of two, 16384 x 4096 took 98 us instead of 87-90).
+// Narrow rows: groups of threads in CTAs of about 512, one per SM.  Rows of 256 threads and more: a CTA each, as many
+// as are resident (16384 x 4096 in groups of two took 98 us instead of 87-90; 512 x 8192 with two CTAs of 512 threads
+// to an SM, which take turns, 15.3 instead of 11.5).
 template <bool WIDE, bool KEPT8>
 cudaError_t launch_norm_back(NormBackArgs& a, int64_t parts, cudaStream_t st) {
     int nv;
     row_shape(a.cols, 1, 1, &a.threads, &nv);             // two vectors, dw's sums and the inputs do not fit in registers
     const int groups = nv == 1 && a.threads < 256 ? 512 / a.threads : 1;
-    const int64_t room = (groups > 1 ? 1 : 2) * (int64_t)q8_host::sm_count(), need = (a.rows + groups - 1) / groups;
+    // a row read twice: more CTAs than are resident, which even out (4096 x 9000: 505 us, 528 with one per SM)
+    const int per_sm = groups > 1 || (nv == 1 && a.threads > 256) ? 1 : 2;
+    const int64_t room = per_sm * (int64_t)q8_host::sm_count(), need = (a.rows + groups - 1) / groups;
     parts = parts < room ? parts : room;
     a.parts = (int)(parts < need ? parts : need);
     const dim3 grid((unsigned)a.parts), block(groups * a.threads);
-    if (groups > 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, true, KEPT8>, grid, block, groups * a.threads * 64, st, a);
-    if (nv == 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, false, KEPT8>, grid, block, 0, st, a);
-    return launch_kernel(k_rmsnorm_backward<false, WIDE, false, KEPT8>, grid, block, 0, st, a);
+    // Rows of a CTA each, of a multiple of 16 columns, aligned, and many per CTA: through a ring in shared memory.
+    // Registers hold no more than the next row, too few bytes in flight (16384 x 4096 with kept codes: 76 us, and 85
+    // without the ring; 16384 x 8192: 154 and 180).  With 13 rows per CTA both take the same time, with fewer and with
+    // groups the ring is up to 10 % slower.
+    if constexpr (WIDE) {
+        if (nv == 1 && groups == 1 && (a.cols & 15) == 0 && a.rows >= 16 * (int64_t)a.parts) {
+            static std::atomic<uint64_t> ready{0};
+            const size_t smem = kRowStages * (size_t)a.cols * ((KEPT8 ? 3 : 4) + (a.ds ? 2 : 0));
+            cudaError_t e = error_word(&a.error);
+            if (e == cudaSuccess) e = ready_once(ready, (const void*)k_rmsnorm_backward<true, true, false, KEPT8, true>, kRowSmem);
+            if (e != cudaSuccess) return e;
+            return launch_kernel(k_rmsnorm_backward<true, true, false, KEPT8, true>, grid, block, smem, st, a);
+        }
+    }
+    if (groups > 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, true, KEPT8, false>, grid, block, groups * a.threads * 64, st, a);
+    if (nv == 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, false, KEPT8, false>, grid, block, 0, st, a);
+    return launch_kernel(k_rmsnorm_backward<false, WIDE, false, KEPT8, false>, grid, block, 0, st, a);
 }
 
 }  // namespace

@@ -244,6 +244,19 @@ def test_norm_backward(rows, cols, layout, kept):
     check_close(to64(dy.t), want_dx - dsv, U16 * np.abs(want_dx - dsv) + dx_bound - U16 * np.abs(want_dx), "dx in place")
 
 
+@pytest.mark.parametrize("rows,cols", [(650, 4096), (999, 6160), (6001, 4080)])
+@pytest.mark.parametrize("layout", [LAYOUTS[0], dict(lead=16, pad=16)])
+@pytest.mark.parametrize("kept", ["bf16", "q8"])
+def test_norm_backward_of_many_rows_per_part(rows, cols, layout, kept):
+    test_norm_backward(rows, cols, layout, kept)
+
+
+@pytest.mark.parametrize("rows,cols", [(305, 4096), (2000, 4090), (400, 8192), (1300, 528)])
+@pytest.mark.parametrize("layout", [LAYOUTS[0], LAYOUTS[3]])
+def test_norm_of_more_rows_than_are_resident(rows, cols, layout):
+    test_norm(rows, cols, layout, True)
+
+
 def test_norm_backward_without_rows_writes_the_empty_sum():
     cols = 100
     z = torch.empty(0, cols, dtype=torch.bfloat16, device="cuda")
