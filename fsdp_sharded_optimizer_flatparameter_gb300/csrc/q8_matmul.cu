@@ -6,9 +6,9 @@
 // four blocks (the instruction descriptor's scale id picks the byte), so scales are fetched once per
 // 512 columns.
 //
-// Roles of a CTA's warps: 0 loads tiles of codes (TMA, 128-byte swizzle) into a ring of stages; 1 issues
-// the scale copies and the products (one thread); 2 fetches scale bytes and lays them out as the scale
-// copy wants them; 3 holds the tensor memory allocation; 4-7 read the accumulator and write the result.
+// Roles of a CTA's warps: 0 loads tiles of codes (TMA, 128-byte swizzle) into a ring of stages; 1 issues the
+// scale copies and the products; 2-5 fetch scale bytes and lay them out as the scale copy wants them (2 also
+// holds the tensor memory allocation); the others, four or eight, read the accumulator and write the result.
 #include "q8_tma.cuh"
 
 namespace zs {
@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
         const uint64_t desc0 = operand_desc(su32(base)), sdesc0 = scales_desc(su32(scale_sh));
         bool ok = true;
         Ring ring, slots;
+        // A group's scales overwrite those of four groups before: the products that read these are 13 blocks back
+        // or more, and complete, since the ring's stages have been loaded again since.
         for (int kb = 0; kb < kbs; ++kb) {
             const int in = (kb >> 2) & (kBatch - 1);
             const uint32_t sfa = tmem_scales + in * S::kScaleCols;
@@ -528,6 +530,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                         if (p + j < a.rows_p) o[j] = f32_to_bf16(a.first ? v[j] : v[j] + bf16_to_f32(o[j]));
                 }
             }
+        } else if (ok && share < 16) {
+            for (int i = threadIdx.x; i < share * 128; i += kSplitThreads) {
+                const int c = c0 + i % share, r = i / share;
+                const int64_t p = (int64_t)p0 + r;
+                if (c >= n || p >= a.rows_p) continue;
+                float x[kSplitMost], v = 0.f;
+#pragma unroll
+                for (int k = 0; k < kSplitMost; ++k)
+                    if (k < split) x[k] = cluster_ld(at_rank(base + (c * 128 + r) * 4, k));
+#pragma unroll
+                for (int k = 0; k < kSplitMost; ++k)
+                    if (k < split) v += x[k];
+                uint16_t* o = a.out + p * a.ldo + q0 + c;
+                *o = f32_to_bf16(fmaf(v, a.scale, a.first ? 0.f : bf16_to_f32(*o)));
+            }
         } else if (ok) {
             // 16 columns of a row per thread; the four warps that own staging memory
             if (warp >= 6) {
@@ -580,12 +597,13 @@ constexpr int kPairStages = 6;
 constexpr int kPairScaleBytes = 512 * 3;
 constexpr int kPairSlots = 2;         // batches of scales in flight
 constexpr int kPairTmemScales = 12;  // columns of one group's scales
+constexpr int kScaleSets = 4;        // groups with columns of their own
 template <int BN>
 struct PairShape {
     static constexpr int kAccs = BN == 256 ? 1 : 2;
     static constexpr int kStageBytes = 128 * 128 + (BN / 2) * 128;
     static constexpr int kSmem = 1024 + kPairStages * kStageBytes + kPairSlots * kBatch * kPairScaleBytes + 8 * kStoreStage * 4 + 256;
-    static_assert(kAccs * BN + kBatch * kPairTmemScales <= 512, "tensor memory");
+    static_assert(kAccs * BN + kScaleSets * kPairTmemScales <= 512, "tensor memory");
     static_assert(BN % 32 == 0 && (BN / 2) % 16 == 0, "halves of whole 16-column loads");
 };
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
@@ -690,15 +708,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t desc0 = operand_desc(su32(base));
         const uint64_t sdesc0 = scales_desc(su32(scale_sh));
         bool ok = true;
-        Ring ring, slots, acc;
+        Ring ring, slots, acc, set;
+        uint32_t sfa = tmem_scales;
+        // A group's scales overwrite those of four groups before, whose products are complete: within a tile and into
+        // the next they are nine blocks back or more, and the ring's six stages have been loaded again since; those
+        // of the tile before that have been read out.
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
             if (acc.round > 0 && !(ok = warp_wait_cluster(acc_free + acc.at, acc.parity() ^ 1, a.wait_limit))) break;
             tc_fence_after();
             const uint32_t sums = tmem + acc.at * BN;
             for (int kb = 0; kb < a.kblocks; ++kb) {
-                const int in = (kb >> 2) & (kBatch - 1);             // group of the batch
-                const uint32_t sfa = tmem_scales + in * kPairTmemScales;
                 if ((kb & 3) == 0) {
+                    const int in = (kb >> 2) & (kBatch - 1);         // group of the batch
+                    sfa = tmem_scales + set.at * kPairTmemScales;
+                    set.next(kScaleSets);
                     if (in == 0) {
                         if (!(ok = warp_wait_cluster(sfull + slots.at, slots.parity(), a.wait_limit))) break;
                         tc_fence_after();
@@ -836,7 +859,7 @@ cudaError_t launch_mm_split(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cuda
     // 37 x 4096 x 11008: 13.8 in 4, 12.9 in 8).
     a.split = 1;
     const int64_t sms = q8_host::sm_count();
-    while (a.split < kSplitMost && BN / (a.split * 2) >= (a.transposed ? 1 : 16) &&
+    while (a.split < kSplitMost &&
            ((tiles * a.split * 2 <= sms && a.kblocks >= a.split * 2 * 5) ||
             (tiles * a.split * 2 <= 2 * sms && a.kblocks >= a.split * 2 * 10)))
         a.split *= 2;
@@ -941,8 +964,10 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     g.first = first != 0;
     g.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
+    // Up to 64 rows of b as well: the small kernel's narrow tiles (8192 x 8 x 4096: 10.6 us, and 13.3 in pairs of CTAs;
+    // 8192 x 64 x 4096: 11.8 and 13.0; 50000 x 64 x 2048: 22.8 and 22.1).
     cudaError_t e;
-    if (!swap && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
+    if (!swap && n > 64 && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
         switch (zs::pair_width(m, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0)) {
             case 256: e = zs::launch_mm_pair<256>(p, q, k, g, st); break;
             case 224: e = zs::launch_mm_pair<224>(p, q, k, g, st); break;

@@ -392,6 +392,31 @@ def test_product_scales_differ_between_blocks():
     check_close(to64(few), want[:9], _product_bound(av[:9], bv, want[:9], k), "few rows")
 
 
+@pytest.mark.parametrize("m,n,k", [(200, 7, 5000), (70, 16, 11000), (513, 33, 3000), (9000, 20, 700), (6400, 50, 130)])
+def test_product_of_few_rows_of_b(m, n, k):
+    test_product(m, n, k)
+
+
+@pytest.mark.parametrize("k", [100, 300, 640, 1100])
+def test_product_of_many_tiles_with_scales_of_their_own(k):
+    # tiles of one group of scales and of a few, every block with its own: each tile's products read their own scales
+    rng = np.random.default_rng(k)
+    m, n, nb = 3500, 2900, -(-k // 128)
+
+    def operand(rows):
+        codes = rng.integers(0, 0x50, (rows, k)).astype(np.uint8)
+        scales = rng.integers(117, 138, (rows, nb)).astype(np.uint8)
+        return Q8Matrix(rows, k).fill(codes, scales), q8.decode(codes, scales)
+
+    a, av = operand(m)
+    b, bv = operand(n)
+    out = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        zs.zs_q8_matmul(a.pair, b.pair, out)
+    want = av @ bv.T
+    check_close(to64(out), want, _product_bound(av, bv, want, k), "out")
+
+
 def test_product_reads_nothing_outside_its_matrices():
     """NaN codes and NaN scales around the operands do not reach the result."""
     rng = np.random.default_rng(12)
