@@ -13,7 +13,8 @@ namespace {
 // block of the format.  Aligned rows move 32 bytes per access.  Rows at other addresses (an odd width, a
 // view into a flat buffer) are read as the aligned 16-byte chunks that cover a thread's columns, shifted
 // into place, and written as the aligned chunks that a thread and its right neighbour make up together;
-// element by element a row of 2047 columns took 16 accesses per thread, each touching 32 sectors.
+// element by element a row of 2047 columns took 16 accesses per thread, each touching 32 sectors.  Where rows are
+// read ahead, the chunks go through shared memory (fetch16, take16).
 
 struct V16 {
     uint32_t w[8];
@@ -26,6 +27,30 @@ struct Span {
 __device__ __forceinline__ Span span_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t cols) {
     return {reinterpret_cast<const uint8_t*>(p), reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols)};
 }
+
+// The 32 bytes that begin `off` (even, < 16) bytes into x.
+__device__ __forceinline__ V16 shifted(uint32_t (&x)[12], uint32_t off) {
+    if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
+    }
+    V16 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = __funnelshift_r(x[i], x[i + 1], (off & 2) * 8);
+    return v;
+}
+
+// Copies `bytes` <= 16 from src to dst, both 16-byte aligned, and zeros up to 16.
+__device__ __forceinline__ void async16(uint8_t* dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest group have landed.
+__device__ __forceinline__ void async_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // 16 bf16 values at p, n of them valid (n may be <= 0 or > 16), the others 0.
 template <bool WIDE>
@@ -63,18 +88,42 @@ __device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& 
         }
         return v;
     }
-    if (off & 8) {
+    return shifted(x, off);
+}
+
+// The same in two steps, for rows that are read ahead: the chunks are copied to 48 bytes of shared memory of the
+// thread's own, and shifted when the row's turn comes.  (Loaded into registers they are shifted, and so waited for, at
+// once: 16384 x 2047 took 107 us forward and 108 backward, 88 and 75 this way.)  The caller commits and waits.
+__device__ __forceinline__ void fetch16(uint8_t* slot, const uint16_t* p, int64_t n, const Span& s) {
+    const uint8_t* at = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)15);
+    const int end = n <= 0 ? 0 : (int)((uintptr_t)p & 15) + 2 * (n < 16 ? (int)n : 16);       // of the bytes wanted
 #pragma unroll
-        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
+    for (int i = 0; i < 3; ++i, at += 16) {
+        if (16 * i >= end) break;
+        if (at >= s.lo) {
+            async16(slot + 16 * i, at, s.hi - at < 16 ? (int)(s.hi - at) : 16);
+        } else {                                 // the matrix starts inside this chunk
+            for (int k = 0; k < 16; k += 2)
+                if (at + k >= s.lo && at + k < s.hi) *reinterpret_cast<uint16_t*>(slot + k) = *reinterpret_cast<const uint16_t*>(at + k);
+        }
     }
-    if (off & 4) {
+}
+__device__ __forceinline__ V16 take16(const uint8_t* slot, const uint16_t* p, int64_t n) {
+    uint32_t x[12];
 #pragma unroll
-        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
+    for (int i = 0; i < 3; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(slot)[i];
+        x[4 * i] = q.x; x[4 * i + 1] = q.y; x[4 * i + 2] = q.z; x[4 * i + 3] = q.w;
     }
+    V16 v = shifted(x, (uint32_t)((uintptr_t)p & 15));
+    if (n < 16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v.w[i] = __funnelshift_r(x[i], x[i + 1], (off & 2) * 8);
+        for (int i = 0; i < 8; ++i) v.w[i] &= 2 * i + 1 < n ? ~0u : 2 * i < n ? 0xffffu : 0u;
+    }
     return v;
 }
+constexpr int kSlot = 48;
+constexpr int kSlotStages = 2;       // rows under way
 
 // 16 bf16 values to p, n of them valid.  The whole warp calls it, its lanes' columns following one another.
 template <bool WIDE>
@@ -117,14 +166,26 @@ __device__ __forceinline__ void store16(uint16_t* p, const V16& v, int64_t n) {
         *reinterpret_cast<uint4*>(p + head) = make_uint4(x[0], x[1], x[2], x[3]);
         if (second) *reinterpret_cast<uint4*>(p + head + 8) = make_uint4(x[4], x[5], x[6], x[7]);
     }
-    // what is left, element by element: [0, head) unless covered, and what follows the chunks written
-    uint32_t rest = whole ? (second ? 0u : 0xffffu << (head + 8)) : n > 0 ? (1u << n) - 1 : 0u;
-    if (whole && !covered) rest |= (1u << head) - 1;
-    rest &= 0xffffu;
-    if (rest) {
+    // what is left: the elements before the first chunk and after the last, or all of a row's last few
+    if (whole) {
+        if (!covered && head) {
+            const uint32_t sh = (head & 1) * 16;
+            const uint32_t y[3] = {__funnelshift_r(v.w[0], v.w[1], sh), __funnelshift_r(v.w[1], v.w[2], sh), __funnelshift_r(v.w[2], v.w[3], sh)};
+            if (head & 1) p[0] = (uint16_t)v.w[0];
+            if (head & 2) *reinterpret_cast<uint32_t*>(p + (head & 1)) = y[0];
+            if (head & 4) *reinterpret_cast<uint2*>(p + (head & 3)) = (head & 2) ? make_uint2(y[1], y[2]) : make_uint2(y[0], y[1]);
+        }
+        if (!second) {
+            const int left = 8 - head;
+            uint16_t* o = p + head + 8;
+            if (left & 4) *reinterpret_cast<uint2*>(o) = make_uint2(x[4], x[5]);
+            if (left & 2) *reinterpret_cast<uint32_t*>(o + (left & 4)) = (left & 4) ? x[6] : x[4];
+            if (left & 1) o[left - 1] = (uint16_t)((left & 4) ? (left & 2 ? x[7] : x[6]) : (left & 2 ? x[5] : x[4]));
+        }
+    } else if (n > 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (rest >> i & 1) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
+            if (i < n) p[i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
     }
 }
 
@@ -320,18 +381,42 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ Norm
     int turn = 0;
     if constexpr (NV > 0) {
         V16 w[N1], x[N1], r[N1];
+        extern __shared__ __align__(16) uint8_t slots[];         // [stage][x, res][v][thread], unless WIDE
+        auto slot = [&](int at, int m, int v) { return slots + ((int64_t)((at * 2 + m) * N1 + v) * blockDim.x + threadIdx.x) * kSlot; };
         auto fetch = [&](int64_t row) {
 #pragma unroll
             for (int v = 0; v < N1; ++v) {
-                const int64_t c = col0 + v * step;
-                x[v] = load16<WIDE>(a.x + row * a.ldx + c, a.cols - c, sx);
-                r[v] = a.res ? load16<WIDE>(a.res + row * a.ldr + c, a.cols - c, sr) : zero;
+                const int64_t c = col0 + v * step, n = a.cols - c;
+                x[v] = load16<WIDE>(a.x + row * a.ldx + c, n, sx);
+                r[v] = a.res ? load16<WIDE>(a.res + row * a.ldr + c, n, sr) : zero;
             }
         };
+        auto ahead = [&](int64_t row, int at) {
+            if (row < a.rows) {
+#pragma unroll
+                for (int v = 0; v < N1; ++v) {
+                    const int64_t c = col0 + v * step, n = a.cols - c;
+                    fetch16(slot(at, 0, v), a.x + row * a.ldx + c, n, sx);
+                    if (a.res) fetch16(slot(at, 1, v), a.res + row * a.ldr + c, n, sr);
+                }
+            }
+            async_commit();
+        };
+        // unless WIDE, only the first row comes without the slots (512 x 999: 5.3 us, 6.5 through them)
+        if constexpr (!WIDE) ahead(blockIdx.x + (int64_t)gridDim.x, 1);
         fetch(blockIdx.x);
 #pragma unroll
         for (int v = 0; v < N1; ++v) w[v] = load16<WIDE>(a.weight + col0 + v * step, a.cols - col0 - v * step, sw);
         for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+            if (!WIDE && row != blockIdx.x) {
+                async_wait_older();
+#pragma unroll
+                for (int v = 0; v < N1; ++v) {
+                    const int64_t c = col0 + v * step, n = a.cols - c;
+                    x[v] = take16(slot(turn, 0, v), a.x + row * a.ldx + c, n);
+                    r[v] = a.res ? take16(slot(turn, 1, v), a.res + row * a.ldr + c, n) : zero;
+                }
+            }
             float2 t[N1][8];
             float sq = 0.f;
 #pragma unroll
@@ -339,8 +424,10 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(const __grid_constant__ Norm
                 sums(x[v], r[v], t[v]);
                 sq += squares(t[v]);
             }
-            if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-            const float2 root = inverse_root(block_sum2(sq, sh[turn]), (float)a.cols, a.inv_cols, a.eps);
+            if (WIDE && row + gridDim.x < a.rows) fetch(row + gridDim.x);
+            const float2 sum = block_sum2(sq, sh[turn]);
+            if constexpr (!WIDE) ahead(row + 2 * (int64_t)gridDim.x, turn);      // sq has taken all that the slots held
+            const float2 root = inverse_root(sum, (float)a.cols, a.inv_cols, a.eps);
 #pragma unroll
             for (int v = 0; v < N1; ++v)
                 if (v * step < a.cols) write(row, col0 + v * step, t[v], root, w[v]);
@@ -387,12 +474,12 @@ struct NormBackArgs {
 // and keeps its part of dw: a thread owns its 16 columns in every row, in registers (HELD), the loads of the next
 // row, or the next four (RING), being under way while a row is reduced and written.  Narrow rows are GROUPED: several
 // rows at a time in a CTA, the groups' parts added in shared memory, so that they fill the SM without more rows of
-// partials (999 x 2047: 14.3 us with a group per CTA, 9.9 with four).  Rows wider than 512 threads hold are read
+// partials (999 x 2047: 14.3 us with a group per CTA, 10 with four).  Rows wider than 512 threads hold are read
 // twice (from L2), dw's part in the CTA's row of `partials`.
 template <bool HELD, bool WIDE, bool GROUPED, bool KEPT8, bool RING>
 __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBackArgs a) {
     __shared__ float sums[16][2][16];            // per group and turn
-    extern __shared__ __align__(16) float parts_sh[];    // [group][columns of its threads], or the RING's stages
+    extern __shared__ __align__(16) float parts_sh[];    // [group][columns of its threads]; the RING's stages or the slots
     dependent_launch_prologue();
     const int groups = GROUPED ? blockDim.x / a.threads : 1, group = GROUPED ? threadIdx.x / a.threads : 0;
     const int threads = GROUPED ? a.threads : blockDim.x, tid = threadIdx.x - group * threads;
@@ -468,9 +555,27 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
             bulk_row(to + bytes, KEPT8 ? (const void*)(a.s_q8.codes + row * a.s_q8.ld) : (const void*)(a.s + row * a.lds), kept, full + at);
             if (a.ds) bulk_row(to + bytes + kept, a.ds + row * a.ldds, bytes, full + at);
         };
-        auto begin = [&](int64_t row) {          // what a row's turn needs besides its stage, or all of the row
+        // Unless WIDE: [stage][dy, s, ds][thread]
+        constexpr int kKept = KEPT8 ? 16 : kSlot, kSlots = 2 * kSlot + kKept;
+        uint8_t* slots = reinterpret_cast<uint8_t*>(parts_sh) + (GROUPED ? blockDim.x * 64 : 0);
+        auto slot = [&](int st, int before, int size) { return slots + (st * kSlots + before) * (int)blockDim.x + (int)threadIdx.x * size; };
+        auto ahead = [&](int64_t row, int st) {
+            const int64_t n = a.cols - col0;
+            if (row < a.rows) {
+                fetch16(slot(st, 0, kSlot), a.dy + row * a.lddy + col0, n, sy);
+                if constexpr (!KEPT8) fetch16(slot(st, 2 * kSlot, kKept), a.s + row * a.lds + col0, n, ss);
+                else if (n > 0) async16(slot(st, 2 * kSlot, kKept), a.s_q8.codes + row * a.s_q8.ld + col0, n < 16 ? (int)n : 16);
+                if (a.ds) fetch16(slot(st, kSlot, kSlot), a.ds + row * a.ldds + col0, n, sd);
+            }
+            async_commit();
+        };
+        if constexpr (!WIDE) {
+            ahead(row0, 0);
+            ahead(row0 + stride, 1);
+        }
+        auto begin = [&](int64_t row) {          // what a row's turn needs besides its stage or slots, or all of the row
             r_next = a.rstd[row];
-            if constexpr (!RING) fetch(row, col0, next);
+            if constexpr (WIDE && !RING) fetch(row, col0, next);
             else if (KEPT8 && in) next.s.w[4] = a.s_q8.scales[row * a.s_q8.lds + (col0 >> 7)];
         };
         if constexpr (RING) {
@@ -502,6 +607,18 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
                     if (a.ds) next.ds = row16(from + bytes + kept + col0 * 2);
                 }
             }
+            if constexpr (!WIDE) {
+                async_wait_older();
+                const int64_t n = a.cols - col0;
+                next.dy = take16(slot(turn, 0, kSlot), a.dy + row * a.lddy + col0, n);
+                if constexpr (KEPT8) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(slot(turn, 2 * kSlot, kKept));
+                    next.s.w[0] = in ? q.x : 0, next.s.w[1] = in ? q.y : 0, next.s.w[2] = in ? q.z : 0, next.s.w[3] = in ? q.w : 0;
+                } else {
+                    next.s = take16(slot(turn, 2 * kSlot, kKept), a.s + row * a.lds + col0, n);
+                }
+                if (a.ds) next.ds = take16(slot(turn, kSlot, kSlot), a.ds + row * a.ldds + col0, n);
+            }
             const Row now = next;
             float2 xh[8];
             const float r = r_next;
@@ -509,6 +626,10 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
             const float d = dot(now, w, xh);
             if (row + stride < a.rows) begin(row + stride);
             const float along = group_sum(d, sh[turn], threads, group + 1) * inv_cols;
+            if constexpr (!WIDE) {
+                if (threads == 32) __syncwarp();
+                ahead(row + 2 * stride, turn);
+            }
             if constexpr (RING) {
                 // the whole CTA has read the stage, and knows who gave up (the next row's flag is another)
                 if (gave_up[turn]) {
@@ -673,9 +794,16 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     if (nv == 1 && threads >= 256 && a.rows > ctas()) row_shape(a.cols, 2, 2, &threads, &nv);
     const int64_t room = ctas();
     const dim3 grid((unsigned)(a.rows < room ? a.rows : room)), block(threads);
+    const size_t smem = WIDE ? 0 : (size_t)kSlotStages * 2 * nv * threads * kSlot;
+    static std::atomic<uint64_t> ready[2];
+    if (!WIDE && nv > 0) {
+        const cudaError_t e = ready_once(ready[nv - 1], nv == 1 ? (const void*)k_rmsnorm_q8<1, WIDE> : (const void*)k_rmsnorm_q8<2, WIDE>,
+                                         kSlotStages * 2 * 512 * kSlot * nv);
+        if (e != cudaSuccess) return e;
+    }
     switch (nv) {
-        case 1: return launch_kernel(k_rmsnorm_q8<1, WIDE>, grid, block, 0, st, a);
-        case 2: return launch_kernel(k_rmsnorm_q8<2, WIDE>, grid, block, 0, st, a);
+        case 1: return launch_kernel(k_rmsnorm_q8<1, WIDE>, grid, block, smem, st, a);
+        case 2: return launch_kernel(k_rmsnorm_q8<2, WIDE>, grid, block, smem, st, a);
         default: return launch_kernel(k_rmsnorm_q8<0, WIDE>, grid, block, 0, st, a);
     }
 }
@@ -708,8 +836,15 @@ cudaError_t launch_norm_back(NormBackArgs& a, int64_t parts, cudaStream_t st) {
             return launch_kernel(k_rmsnorm_backward<true, true, false, KEPT8, true>, grid, block, smem, st, a);
         }
     }
-    if (groups > 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, true, KEPT8, false>, grid, block, groups * a.threads * 64, st, a);
-    if (nv == 1) return launch_kernel(k_rmsnorm_backward<true, WIDE, false, KEPT8, false>, grid, block, 0, st, a);
+    const size_t smem = (groups > 1 ? groups * a.threads * 64 : 0) +
+                        (WIDE ? 0 : (size_t)kSlotStages * groups * a.threads * (2 * kSlot + (KEPT8 ? 16 : kSlot)));
+    if (nv == 1) {
+        auto* kern = groups > 1 ? k_rmsnorm_backward<true, WIDE, true, KEPT8, false> : k_rmsnorm_backward<true, WIDE, false, KEPT8, false>;
+        static std::atomic<uint64_t> ready[2];
+        const cudaError_t e = ready_once(ready[groups > 1], (const void*)kern, 512 * (64 + kSlotStages * 3 * kSlot));
+        if (e != cudaSuccess) return e;
+        return launch_kernel(kern, grid, block, smem, st, a);
+    }
     return launch_kernel(k_rmsnorm_backward<false, WIDE, false, KEPT8, false>, grid, block, 0, st, a);
 }
 
