@@ -397,6 +397,12 @@ def test_product_of_few_rows_of_b(m, n, k):
     test_product(m, n, k)
 
 
+@pytest.mark.parametrize("m,n,k", [(2600, 1500, 1100), (2561, 1537, 77), (5000, 700, 1300), (3001, 2045, 500), (2600, 1500, 1024)])
+def test_product_of_large_tiles(m, n, k):
+    # odd counts of 256-row tiles, the last one nearly empty; rows of codes that cross 128-byte lines and not
+    test_product(m, n, k)
+
+
 @pytest.mark.parametrize("k", [100, 300, 640, 1100])
 def test_product_of_many_tiles_with_scales_of_their_own(k):
     # tiles of one group of scales and of a few, every block with its own: each tile's products read their own scales
