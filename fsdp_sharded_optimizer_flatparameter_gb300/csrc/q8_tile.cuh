@@ -11,7 +11,7 @@
 //
 // What bounds these kernels next to the bytes is the shared-memory pipe (shuffles, staging) and the issue of
 // instructions, hence the large thread tiles and the two-wide arithmetic.  Encoding 22016 x 4096 both ways (360 MB,
-// 53 us at the copy rate): 85 us with two rows per thread, full-width maxima and 18 instructions per value, 62 us
+// 53 us at the copy rate): 85 us with two rows per thread, full-width maxima and 18 instructions per value, 62-63 us
 // with 10.7.  The transpose issues 14 per value at 65 % of the issue rate (8192 x 4096: 20 us, bytes 10), the gate's
 // backward pass 55 at 54 % (5003 x 5504: 85 us, bytes 37).
 //
@@ -40,14 +40,28 @@ struct TilePos {
     }
 };
 
+// A tile's row and column among the tiles.  A CTA goes from tile to tile in steps of the grid without dividing (with
+// three divisions per tile: transpose of 8192 x 4096 20.8 us instead of 19.9, 3001 x 2047 encoded 13.9 and 13.6;
+// encoding 22016 x 4096 62.0 and 63.3).
+struct TileAt {
+    uint32_t r, c;
+    __device__ __forceinline__ void next(const TileAt& step, uint32_t tiles_c) {
+        r += step.r;
+        c += step.c;
+        if (c >= tiles_c) {
+            c -= tiles_c;
+            ++r;
+        }
+    }
+};
+
 template <int CP>
-__device__ __forceinline__ TilePos<CP> tile_pos(int64_t tile, int64_t tiles_c, int64_t rows, int64_t cols) {
+__device__ __forceinline__ TilePos<CP> tile_pos(const TileAt& at, int64_t rows, int64_t cols) {
     TilePos<CP> t;
     t.cc = threadIdx.x % kTileLanes;
     t.rg = threadIdx.x / kTileLanes;
-    const uint32_t tr = (uint32_t)tile / (uint32_t)tiles_c;
-    t.r0 = (int64_t)tr * 128;
-    t.c0 = (int64_t)((uint32_t)tile - tr * (uint32_t)tiles_c) * (2 * CP * kTileLanes);
+    t.r0 = (int64_t)at.r * 128;
+    t.c0 = (int64_t)at.c * (2 * CP * kTileLanes);
     t.rows = rows - t.r0 < 128 ? (int)(rows - t.r0) : 128;
     t.cols = cols - t.c0 < 2 * CP * kTileLanes ? (int)(cols - t.c0) : 2 * CP * kTileLanes;
     return t;
@@ -354,11 +368,11 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     __syncthreads();
     dependent_launch_prologue();
 
-    const int64_t step = gridDim.x;
-    auto load_stage = [&](int s, int64_t tile) {                                    // thread 0
+    const uint32_t tiles_c = (uint32_t)a.tiles_c, tiles = (uint32_t)a.tiles, grid = gridDim.x;
+    const TileAt step = {grid / tiles_c, grid % tiles_c};
+    auto load_stage = [&](int s, const TileAt& tile) {                              // thread 0
         if constexpr (S::kStage > 0) {
-            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c;
-            const int r0 = (int)(tr * 128), c0 = (int)(((uint32_t)tile - tr * (uint32_t)a.tiles_c) * S::kCols);
+            const int r0 = (int)(tile.r * 128), c0 = (int)(tile.c * S::kCols);
             uint8_t* at = base + s * S::kStage;
             mbar_expect_tx(full + s, S::kStage);
             if constexpr (S::kX > 0) tma_load(at, &map_x, c0, r0, full + s);
@@ -368,25 +382,30 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     };
     // scale bytes of the thread's rows, a tile ahead of their use
     uint32_t sa[RP] = {}, sb[RP] = {};
-    auto load_scales = [&](int64_t tile) {
+    auto load_scales = [&](const TileAt& tile) {
         if constexpr (S::kA > 0) {
-            const uint32_t tr = (uint32_t)tile / (uint32_t)a.tiles_c, blk = ((uint32_t)tile - tr * (uint32_t)a.tiles_c) * S::kCols >> 7;
+            const uint32_t blk = tile.c * S::kCols >> 7;
+            const int64_t r = (int64_t)tile.r * 128 + lane_row;
+            const uint8_t *pa = a.a.scales + r * a.a.lds + blk, *pb = a.b.scales + r * a.b.lds + blk;
 #pragma unroll
-            for (int p = 0; p < RP; ++p) {
-                const int64_t r = (int64_t)tr * 128 + lane_row + p;
-                sa[p] = r < a.rows ? a.a.scales[r * a.a.lds + blk] : 0;
-                if constexpr (S::kB > 0) sb[p] = r < a.rows ? a.b.scales[r * a.b.lds + blk] : 0;
+            for (int p = 0; p < RP; ++p, pa += a.a.lds, pb += a.b.lds) {
+                sa[p] = r + p < a.rows ? *pa : 0;
+                if constexpr (S::kB > 0) sb[p] = r + p < a.rows ? *pb : 0;
             }
         }
     };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < S::kStages; ++i)
-            if (blockIdx.x + i * step < a.tiles) load_stage(i, blockIdx.x + i * step);
-    load_scales(blockIdx.x);
+    // the tile at work (then the next), and the one whose copies are issued next
+    TileAt now = {blockIdx.x / tiles_c, blockIdx.x % tiles_c}, ahead = now;
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+        if (threadIdx.x == 0 && blockIdx.x + i * (int64_t)grid < tiles) load_stage(i, ahead);
+        ahead.next(step, tiles_c);
+    }
+    load_scales(now);
     int s = 0;
     uint32_t parity = 0;
-    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += step) {
-        const TilePos<CP> t = tile_pos<CP>(tile, a.tiles_c, a.rows, a.cols);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += grid) {
+        const TilePos<CP> t = tile_pos<CP>(now, a.rows, a.cols);
         bool late = false;
         if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
@@ -418,19 +437,23 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
                 if (cols_wanted) v.column_keys(keys);
             }
             const bool last = pass == S::kPasses - 1;
-            if (last && tile + step < a.tiles) load_scales(tile + step);
+            if (last) {
+                now.next(step, tiles_c);
+                if (tile + grid < tiles) load_scales(now);
+            }
             // A wait that ran out ends the CTA, after the copies still on their way.
             if (__syncthreads_or(late)) {
                 if (threadIdx.x == 0) {
                     atomicCAS(a.error, 0u, ZS_DEVERR_TILE_WAIT);
                     for (int i = 0; i < S::kStages; ++i)
-                        if (tile + i * step < a.tiles)
+                        if (tile + i * (int64_t)grid < tiles)
                             mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, a.wait_limit);
                 }
                 return;
             }
             if (last) {                          // every thread has read the stage: its next tile may come
-                if (threadIdx.x == 0 && tile + S::kStages * step < a.tiles) load_stage(s, tile + S::kStages * step);
+                if (threadIdx.x == 0 && tile + S::kStages * (int64_t)grid < tiles) load_stage(s, ahead);
+                ahead.next(step, tiles_c);
                 if (++s == S::kStages) {
                     s = 0;
                     parity ^= 1;
