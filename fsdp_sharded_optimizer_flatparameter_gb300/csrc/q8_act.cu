@@ -16,42 +16,6 @@ namespace {
 // element by element a row of 2047 columns took 16 accesses per thread, each touching 32 sectors.  Where rows are
 // read ahead, the chunks go through shared memory (fetch16, take16).
 
-struct V16 {
-    uint32_t w[8];
-};
-
-// The matrix that accesses must stay in: its first and past its last byte.
-struct Span {
-    const uint8_t *lo, *hi;
-};
-__device__ __forceinline__ Span span_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t cols) {
-    return {reinterpret_cast<const uint8_t*>(p), reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols)};
-}
-
-// The 32 bytes that begin `off` (even, < 16) bytes into x.
-__device__ __forceinline__ V16 shifted(uint32_t (&x)[12], uint32_t off) {
-    if (off & 8) {
-#pragma unroll
-        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
-    }
-    if (off & 4) {
-#pragma unroll
-        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
-    }
-    V16 v;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.w[i] = __funnelshift_r(x[i], x[i + 1], (off & 2) * 8);
-    return v;
-}
-
-// Copies `bytes` <= 16 from src to dst, both 16-byte aligned, and zeros up to 16.
-__device__ __forceinline__ void async16(uint8_t* dst, const uint8_t* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest group have landed.
-__device__ __forceinline__ void async_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
 // 16 bf16 values at p, n of them valid (n may be <= 0 or > 16), the others 0.
 template <bool WIDE>
 __device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& s) {
@@ -91,38 +55,6 @@ __device__ __forceinline__ V16 load16(const uint16_t* p, int64_t n, const Span& 
     return shifted(x, off);
 }
 
-// The same in two steps, for rows that are read ahead: the chunks are copied to 48 bytes of shared memory of the
-// thread's own, and shifted when the row's turn comes.  (Loaded into registers they are shifted, and so waited for, at
-// once: 16384 x 2047 took 107 us forward and 108 backward, 88 and 75 this way.)  The caller commits and waits.
-__device__ __forceinline__ void fetch16(uint8_t* slot, const uint16_t* p, int64_t n, const Span& s) {
-    const uint8_t* at = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)15);
-    const int end = n <= 0 ? 0 : (int)((uintptr_t)p & 15) + 2 * (n < 16 ? (int)n : 16);       // of the bytes wanted
-#pragma unroll
-    for (int i = 0; i < 3; ++i, at += 16) {
-        if (16 * i >= end) break;
-        if (at >= s.lo) {
-            async16(slot + 16 * i, at, s.hi - at < 16 ? (int)(s.hi - at) : 16);
-        } else {                                 // the matrix starts inside this chunk
-            for (int k = 0; k < 16; k += 2)
-                if (at + k >= s.lo && at + k < s.hi) *reinterpret_cast<uint16_t*>(slot + k) = *reinterpret_cast<const uint16_t*>(at + k);
-        }
-    }
-}
-__device__ __forceinline__ V16 take16(const uint8_t* slot, const uint16_t* p, int64_t n) {
-    uint32_t x[12];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const uint4 q = reinterpret_cast<const uint4*>(slot)[i];
-        x[4 * i] = q.x; x[4 * i + 1] = q.y; x[4 * i + 2] = q.z; x[4 * i + 3] = q.w;
-    }
-    V16 v = shifted(x, (uint32_t)((uintptr_t)p & 15));
-    if (n < 16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v.w[i] &= 2 * i + 1 < n ? ~0u : 2 * i < n ? 0xffffu : 0u;
-    }
-    return v;
-}
-constexpr int kSlot = 48;
 constexpr int kSlotStages = 2;       // rows under way
 
 // 16 bf16 values to p, n of them valid.  The whole warp calls it, its lanes' columns following one another.

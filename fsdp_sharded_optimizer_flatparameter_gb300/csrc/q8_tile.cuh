@@ -17,7 +17,8 @@
 //
 // The next tiles' inputs arrive by tiled copies (a ring of stages) while a tile is worked on: with one tile per CTA
 // loaded into registers, its loads, arithmetic and stores took their times one after another (242 us for the
-// gate's backward pass).  bf16 inputs that such copies cannot read (16-byte alignment) are loaded by the threads.
+// gate's backward pass).  bf16 inputs that such copies cannot read (16-byte alignment) are copied by the threads, each
+// what it needs, a tile ahead (22016 x 4096 one element off, both ways: 86 us; loaded element by element 143).
 #pragma once
 
 #include "q8_tma.cuh"
@@ -67,6 +68,81 @@ __device__ __forceinline__ TilePos<CP> tile_pos(const TileAt& at, int64_t rows, 
     return t;
 }
 
+// ------------------------------------------------------------------ 16 values at any address
+
+struct V16 {
+    uint32_t w[8];
+};
+
+// The matrix that accesses must stay in: its first and past its last byte.
+struct Span {
+    const uint8_t *lo, *hi;
+};
+__device__ __forceinline__ Span span_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t cols) {
+    return {reinterpret_cast<const uint8_t*>(p), reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols)};
+}
+
+// The 32 bytes that begin `off` (even, < 16) bytes into x.
+__device__ __forceinline__ V16 shifted(uint32_t (&x)[12], uint32_t off) {
+    if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) x[i] = x[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = x[i + 1];
+    }
+    V16 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = __funnelshift_r(x[i], x[i + 1], (off & 2) * 8);
+    return v;
+}
+
+// Copies `bytes` <= 16 from src to dst, both 16-byte aligned, and zeros up to 16.
+__device__ __forceinline__ void async16(uint8_t* dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// All but the newest group have landed.
+__device__ __forceinline__ void async_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// 16 bf16 values at p, read ahead of their use: the aligned 16-byte chunks that cover the n valid ones are copied to 48
+// bytes of shared memory of the thread's own (fetch16), and shifted into place when their turn comes, the others 0
+// (take16).  The caller commits and waits.  Loaded into registers they are shifted, and so waited for, at once: the
+// norm of 16384 x 2047 took 107 us forward and 108 backward, 88 and 75 this way.
+__device__ __forceinline__ void fetch16(uint8_t* slot, const uint16_t* p, int64_t n, const Span& s) {
+    const uint8_t* at = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)15);
+    const int end = n <= 0 ? 0 : (int)((uintptr_t)p & 15) + 2 * (n < 16 ? (int)n : 16);       // of the bytes wanted
+#pragma unroll
+    for (int i = 0; i < 3; ++i, at += 16) {
+        if (16 * i >= end) break;
+        if (at >= s.lo) {
+            async16(slot + 16 * i, at, s.hi - at < 16 ? (int)(s.hi - at) : 16);
+        } else {                                 // the matrix starts inside this chunk
+            for (int k = 0; k < 16; k += 2)
+                if (at + k >= s.lo && at + k < s.hi) *reinterpret_cast<uint16_t*>(slot + k) = *reinterpret_cast<const uint16_t*>(at + k);
+        }
+    }
+}
+__device__ __forceinline__ V16 take16(const uint8_t* slot, const uint16_t* p, int64_t n) {
+    uint32_t x[12];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(slot)[i];
+        x[4 * i] = q.x; x[4 * i + 1] = q.y; x[4 * i + 2] = q.z; x[4 * i + 3] = q.w;
+    }
+    V16 v = shifted(x, (uint32_t)((uintptr_t)p & 15));
+    if (n < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.w[i] &= 2 * i + 1 < n ? ~0u : 2 * i < n ? 0xffffu : 0u;
+    }
+    return v;
+}
+constexpr int kSlot = 48;
+
+// ------------------------------------------------------------------ tiles in registers
+
 // n (0 .. 16) bytes of w at p, which is 16-byte aligned.
 __device__ __forceinline__ void store_codes(uint8_t* p, const uint4& w, int n) {
     if (n == 16) {
@@ -85,16 +161,6 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p, int n) {
     for (int i = 0; i < 16; ++i)
         if (i < n) x[i >> 2] |= (uint32_t)p[i] << ((i & 3) * 8);
     return make_uint4(x[0], x[1], x[2], x[3]);
-}
-
-// 2 * CP bf16 values at p (n of them valid, the others 0) as packed words, from any 2-byte alignment.
-template <int CP>
-__device__ __forceinline__ void load_bf16(const uint16_t* p, int n, uint32_t (&w)[CP]) {
-#pragma unroll
-    for (int i = 0; i < CP; ++i) {
-        const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-        w[i] = lo | (hi << 16);
-    }
 }
 
 // The scale exponent of a magnitude as the upper 16 bits of a sum (q8_scale_byte's): its maximum over a block is
@@ -268,7 +334,15 @@ struct TileArgs {
     long long wait_limit;
 };
 
-// Row p of the thread's part of a tile: bf16 values as packed words, from the stage or (not TMA) from memory;
+// Not TMA: the thread's slot for row p, and where the row's values are.
+__device__ __forceinline__ uint8_t* tile_slot(const uint8_t* stage, int p) {
+    return const_cast<uint8_t*>(stage) + (p * kTileThreads + threadIdx.x) * kSlot;
+}
+template <int CP>
+__device__ __forceinline__ const uint16_t* tile_x(const TileArgs& a, const TilePos<CP>& t, int p) {
+    return a.x + (t.r0 + t.rg * kTileRp + p) * a.ldx + t.c0 + t.cc * 2 * CP;
+}
+// Row p of the thread's part of a tile: bf16 values as packed words, from the stage or (not TMA) the thread's slots;
 // decoded 8-bit values of an 8-bit tile at `from`.
 template <bool TMA, int CP>
 __device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<CP>& t, const uint8_t* stage, int p, uint32_t (&x)[CP]) {
@@ -280,7 +354,10 @@ __device__ __forceinline__ void tile_bf16(const TileArgs& a, const TilePos<CP>& 
             x[4 * k] = w.x; x[4 * k + 1] = w.y; x[4 * k + 2] = w.z; x[4 * k + 3] = w.w;
         }
     } else {
-        load_bf16<CP>(a.x + (t.r0 + t.rg * kTileRp + p) * a.ldx + t.c0 + t.cc * 2 * CP, t.row_ok(p) ? t.chunk() : 0, x);
+        static_assert(CP == 8, "16 columns");
+        const V16 v = take16(tile_slot(stage, p), tile_x(a, t, p), t.row_ok(p) ? t.chunk() : 0);
+#pragma unroll
+        for (int j = 0; j < CP; ++j) x[j] = v.w[j];
     }
 }
 template <int CP>
@@ -299,11 +376,34 @@ __device__ __forceinline__ void tile_codes(const TilePos<CP>& t, const uint8_t* 
     for (int j = 0; j < CP; ++j) v[j] = q8_mul2(q8_unpack2(w[j >> 1] >> ((j & 1) * 16)), make_float2(e, e));
 }
 
+template <int KIND, bool TMA>
+struct TileShape {
+    // Column pairs per thread and lanes per row.  The transpose needs no whole row blocks, so its tiles are half as wide
+    // and four CTAs fit an SM.  The others do best with large threads: the gate's backward pass at 5003 x 5504
+    // takes 85 us so and 108 with 16 lanes of half the columns.
+    static constexpr int kPairs = KIND == kTileTurn ? 4 : 8;
+    static constexpr int kCols = 2 * kPairs * kTileLanes;
+    // The gate's three values per element are taken one after another, each computed from the tile in shared memory:
+    // all three in registers at once leave room for one CTA per SM, which is no faster (81 us at 5003 x 5504), and
+    // this way only what is wanted is computed.
+    static constexpr int kPasses = KIND == kTileGate ? 3 : 1;
+    static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage's copies: bf16 tile
+    static constexpr int kA = KIND == kTileEncode ? 0 : 128 * kCols;                // and 8-bit tiles
+    static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
+    static constexpr int kLoads = kX + kA + kB;
+    static constexpr int kBf16 = KIND == kTileTurn ? 0 : TMA ? kX : kTileThreads * kTileRp * kSlot;    // of the bf16 tile or the slots
+    static constexpr int kStage = kBf16 + kA + kB;
+    static constexpr int kStages = KIND == kTileGate || (KIND == kTileEncode && !TMA) ? 1 : 2;
+    static constexpr int kKeys = kTileLanes * kPairs * kTileLanes * 4;
+    static constexpr int kSmem = 128 + kStages * kStage + 128 * kCols + kKeys + 512 + 64;
+    static constexpr int kPerSm = KIND == kTileTurn ? 4 : 2;
+};
+
 // The gated activation's backward values: 0 the gate's gradient, 1 up's, 2 the activation itself.
 template <int WHICH, bool TMA, int CP>
 __device__ __forceinline__ void gate_values(TileValues<CP>& v, const TileArgs& a, const TilePos<CP>& t, const uint8_t* stage,
                                             const uint32_t (&sa)[kTileRp], const uint32_t (&sb)[kTileRp]) {
-    const uint8_t* codes = stage + (TMA ? 128 * 128 * 2 : 0);
+    const uint8_t* codes = stage + TileShape<kTileGate, TMA>::kBf16;
     const float2 one = make_float2(1.f, 1.f);
 #pragma unroll
     for (int p = 0; p < kTileRp; ++p) {
@@ -328,27 +428,6 @@ __device__ __forceinline__ void gate_values(TileValues<CP>& v, const TileArgs& a
 }
 
 template <int KIND, bool TMA>
-struct TileShape {
-    // Column pairs per thread and lanes per row.  The transpose needs no whole row blocks, so its tiles are half as wide
-    // and four CTAs fit an SM.  The others do best with large threads: the gate's backward pass at 5003 x 5504
-    // takes 85 us so and 108 with 16 lanes of half the columns.
-    static constexpr int kPairs = KIND == kTileTurn ? 4 : 8;
-    static constexpr int kCols = 2 * kPairs * kTileLanes;
-    // The gate's three values per element are taken one after another, each computed from the tile in shared memory:
-    // all three in registers at once leave room for one CTA per SM, which is no faster (81 us at 5003 x 5504), and
-    // this way only what is wanted is computed.
-    static constexpr int kPasses = KIND == kTileGate ? 3 : 1;
-    static constexpr int kX = KIND == kTileTurn || !TMA ? 0 : 128 * 128 * 2;      // bytes of a stage: bf16 tile
-    static constexpr int kA = KIND == kTileEncode ? 0 : 128 * kCols;                // and 8-bit tiles
-    static constexpr int kB = KIND == kTileGate ? 128 * 128 : 0;
-    static constexpr int kStage = kX + kA + kB;
-    static constexpr int kStages = KIND == kTileGate ? 1 : 2;
-    static constexpr int kKeys = kTileLanes * kPairs * kTileLanes * 4;
-    static constexpr int kSmem = 128 + kStages * kStage + 128 * kCols + kKeys + 512 + 64;
-    static constexpr int kPerSm = KIND == kTileTurn ? 4 : 2;
-};
-
-template <int KIND, bool TMA>
 __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     k_q8_tiles(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TileArgs a) {
@@ -371,13 +450,13 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
     const uint32_t tiles_c = (uint32_t)a.tiles_c, tiles = (uint32_t)a.tiles, grid = gridDim.x;
     const TileAt step = {grid / tiles_c, grid % tiles_c};
     auto load_stage = [&](int s, const TileAt& tile) {                              // thread 0
-        if constexpr (S::kStage > 0) {
+        if constexpr (S::kLoads > 0) {
             const int r0 = (int)(tile.r * 128), c0 = (int)(tile.c * S::kCols);
             uint8_t* at = base + s * S::kStage;
-            mbar_expect_tx(full + s, S::kStage);
+            mbar_expect_tx(full + s, S::kLoads);
             if constexpr (S::kX > 0) tma_load(at, &map_x, c0, r0, full + s);
-            if constexpr (S::kA > 0) tma_load(at + S::kX, &map_a, c0, r0, full + s);
-            if constexpr (S::kB > 0) tma_load(at + S::kX + S::kA, &map_b, c0, r0, full + s);
+            if constexpr (S::kA > 0) tma_load(at + S::kBf16, &map_a, c0, r0, full + s);
+            if constexpr (S::kB > 0) tma_load(at + S::kBf16 + S::kA, &map_b, c0, r0, full + s);
         }
     };
     // scale bytes of the thread's rows, a tile ahead of their use
@@ -394,6 +473,15 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
             }
         }
     };
+    // not TMA: the thread's bf16 values of a tile, under way while the tile before is worked on
+    constexpr bool kSlots = KIND != kTileTurn && !TMA;
+    const Span sx = span_of(a.x, a.ldx, a.rows, a.cols);
+    auto fetch_x = [&](const TileAt& tile) {
+        const TilePos<CP> t = tile_pos<CP>(tile, a.rows, a.cols);
+#pragma unroll
+        for (int p = 0; p < RP; ++p) fetch16(tile_slot(base, p), tile_x(a, t, p), t.row_ok(p) ? t.chunk() : 0, sx);
+        async_commit();
+    };
     // the tile at work (then the next), and the one whose copies are issued next
     TileAt now = {blockIdx.x / tiles_c, blockIdx.x % tiles_c}, ahead = now;
 #pragma unroll
@@ -402,12 +490,14 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
         ahead.next(step, tiles_c);
     }
     load_scales(now);
+    if constexpr (kSlots) fetch_x(now);
     int s = 0;
     uint32_t parity = 0;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += grid) {
         const TilePos<CP> t = tile_pos<CP>(now, a.rows, a.cols);
         bool late = false;
-        if constexpr (S::kStage > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
+        if constexpr (kSlots) async_wait_all();
+        if constexpr (S::kLoads > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
 #pragma unroll 1
         for (int pass = 0; pass < S::kPasses; ++pass) {
@@ -439,7 +529,10 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
             const bool last = pass == S::kPasses - 1;
             if (last) {
                 now.next(step, tiles_c);
-                if (tile + grid < tiles) load_scales(now);
+                if (tile + grid < tiles) {
+                    load_scales(now);
+                    if constexpr (kSlots) fetch_x(now);
+                }
             }
             // A wait that ran out ends the CTA, after the copies still on their way.
             if (__syncthreads_or(late)) {
