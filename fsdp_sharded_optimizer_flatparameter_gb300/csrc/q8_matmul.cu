@@ -155,7 +155,9 @@ __device__ __forceinline__ void tmem_load16(uint32_t tmem, float (&f)[16]) {
 // `rows` and `n` are what is valid of them (the same in every lane).  With `align` 32 or 16, rows start at
 // multiples of that many bytes and a lane stores its own segment (a full sector at 32).  Otherwise the
 // values go through 2 KB of the warp's shared memory, so that neighbouring lanes store neighbouring
-// columns: one 2-byte store per lane and row cost 15 of 27 us for 160 x 339 x 4096.
+// columns: one 2-byte store per lane and row cost 15 of 27 us for 160 x 339 x 4096.  What the rows hold (not
+// `first`) is read at once before anything is stored (11008 x 4096 x 2048 at an odd element: 144 us, and 539 with
+// each value read and stored in turn).  Reading pieces ahead, or asking lines into L2 a tile ahead, gains nothing.
 __device__ __forceinline__ void store_rows16(uint16_t* out, int64_t ldo, const float (&f)[16], int rows, int n, int align,
                                              float scale, int first, float* stage) {
     const int lane = threadIdx.x & 31;
@@ -182,17 +184,24 @@ __device__ __forceinline__ void store_rows16(uint16_t* out, int64_t ldo, const f
         }
         return;
     }
+    const int c = lane & 15;
+    uint16_t* o = out + (lane >> 4) * ldo + c;
+    uint32_t was[8] = {0, 0, 0, 0, 0, 0, 0, 0};      // rows lane / 16 + 4 i and + 4 i + 2
+    if (!first) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 2 * i + (lane >> 4) < rows && c < n ? o[2 * i * ldo] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) was[i] = x[2 * i] | (x[2 * i + 1] << 16);
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) stage[lane * 16 + (j ^ (lane & 15))] = f[j];
     __syncwarp();
-    const int c = lane & 15;
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int r = 2 * i + (lane >> 4);
-        if (r < rows && c < n) {
-            uint16_t* o = out + r * ldo + c;
-            o[0] = f32_to_bf16(fmaf(stage[r * 16 + (c ^ (r & 15))], scale, first ? 0.f : bf16_to_f32(o[0])));
-        }
+        const float x = (i & 1) ? bf16_hi(was[i >> 1]) : bf16_lo(was[i >> 1]);
+        if (r < rows && c < n) o[2 * i * ldo] = f32_to_bf16(fmaf(stage[r * 16 + (c ^ (r & 15))], scale, x));
     }
     __syncwarp();
 }
@@ -479,10 +488,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                     tmem_load16(from + c, f);
                     if (a.transposed) {
                         uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p + lane;
+                        uint16_t was[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) was[j] = !a.first && c + j < n && lane < rows ? o[j * a.ldo] : 0;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (c + j < n && lane < rows)
-                                o[j * a.ldo] = f32_to_bf16(fmaf(f[j], a.scale, a.first ? 0.f : bf16_to_f32(o[j * a.ldo])));
+                            if (c + j < n && lane < rows) o[j * a.ldo] = f32_to_bf16(fmaf(f[j], a.scale, bf16_to_f32(was[j])));
                     } else {
                         store_rows16(a.out + p * a.ldo + q0 + c, a.ldo, f, rows, n - c, a.align, a.scale, a.first,
                                      store_sh + sub * kStoreStage);
@@ -529,14 +540,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                         v[0] += x[k].x; v[1] += x[k].y; v[2] += x[k].z; v[3] += x[k].w;
                     }
                 uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p;
+                uint16_t was[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = v[j] * a.scale;
-                if (a.first && ((uintptr_t)o & 7) == 0 && p + 4 <= a.rows_p) {
+                for (int j = 0; j < 4; ++j) was[j] = !a.first && p + j < a.rows_p ? o[j] : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], a.scale, bf16_to_f32(was[j]));
+                if (((uintptr_t)o & 7) == 0 && p + 4 <= a.rows_p) {
                     *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (p + j < a.rows_p) o[j] = f32_to_bf16(a.first ? v[j] : v[j] + bf16_to_f32(o[j]));
+                        if (p + j < a.rows_p) o[j] = f32_to_bf16(v[j]);
                 }
             }
         } else if (ok && share < 16) {
@@ -830,7 +844,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int qh = q0 + half * kHalf;
             uint16_t* o = a.out + p * a.ldo + qh;
             const uint32_t from = tmem + acc.at * BN + half * kHalf + ((uint32_t)(sub * 32) << 16);
-#pragma unroll 2
+#pragma unroll 1
             for (int c = 0; c < kHalf; c += 16) {
                 float f[16];
                 tmem_load16(from + c, f);
