@@ -488,12 +488,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                     tmem_load16(from + c, f);
                     if (a.transposed) {
                         uint16_t* o = a.out + (int64_t)(q0 + c) * a.ldo + p + lane;
-                        uint16_t was[16];
+                        if (!a.first) {
+                            uint16_t was[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) was[j] = !a.first && c + j < n && lane < rows ? o[j * a.ldo] : 0;
+                            for (int j = 0; j < 16; ++j) was[j] = c + j < n && lane < rows ? o[j * a.ldo] : 0;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) f[j] = fmaf(f[j], a.scale, bf16_to_f32(was[j]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) f[j] *= a.scale;
+                        }
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (c + j < n && lane < rows) o[j * a.ldo] = f32_to_bf16(fmaf(f[j], a.scale, bf16_to_f32(was[j])));
+                            if (c + j < n && lane < rows) o[j * a.ldo] = f32_to_bf16(f[j]);
                     } else {
                         store_rows16(a.out + p * a.ldo + q0 + c, a.ldo, f, rows, n - c, a.align, a.scale, a.first,
                                      store_sh + sub * kStoreStage);
