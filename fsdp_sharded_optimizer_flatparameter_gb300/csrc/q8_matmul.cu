@@ -108,15 +108,6 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
         "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-// The same into every CTA of `mask`, at this offset; the bytes count on the barrier of bar's offset in the even CTA of
-// each receiver's pair (bar itself lies in an even CTA).
-__device__ __forceinline__ void tma_load_pairs(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-        "[%4], %5;" ::"r"(su32(dst)),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar), "h"(mask)
-        : "memory");
-}
 // Into both CTAs' tensor memory, each from its own shared memory.
 __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t tmem, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
@@ -622,11 +613,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
 // persistent and the accumulators doubled, so that eight warps write a tile out while the next one's
 // products run; that and the scales leave BN at 224 or less.  Undoubled, a tile may have 256 columns: for
 // products that every pair does in one tile.
-//
-// With PAIRS = 2 a cluster's two pairs take 256 P rows each against the same Q rows: each loads half of what
-// both read and multicasts it, so a CTA asks for 128 + BN / 4 rows per block instead of 128 + BN / 2.  That pays
-// where the loads take the time (11008 x 2048 x 5003: 97 us in single pairs, 81 in twos); clusters of four run on
-// 144 of the 152 SMs.
 constexpr int kPairThreads = 448;
 constexpr int kPairStages = 6;
 constexpr int kPairScaleBytes = 512 * 3;
@@ -643,7 +629,7 @@ struct PairShape {
 };
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
 
-template <int BN, int PAIRS>
+template <int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ MmArgs a) {
@@ -661,13 +647,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 2);
     uint32_t* gave_up = tmem_at + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t in_cluster = cluster_rank(), rank = in_cluster & 1, lead = in_cluster & ~1u;
-    const uint16_t pair_mask = (uint16_t)(3 << lead), all_mask = (uint16_t)((1 << 2 * PAIRS) - 1);
+    const uint32_t rank = cluster_rank();        // CTA 0 of the pair leads
+    constexpr uint16_t kBoth = 3;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPairStages; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, PAIRS);         // the products of every pair that this CTA's copies reach
+            mbar_init(empty + i, 1);
         }
         for (int i = 0; i < kPairSlots; ++i) {
             mbar_init(sfull + i, 8);             // the four scale warps of both CTAs
@@ -696,16 +682,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     wait_for_predecessor();
     const uint32_t tmem = *tmem_at, tmem_scales = tmem + kAccs * BN;
     const int groups = (a.kblocks + 3) / 4;
-    constexpr int kRows = 256 * PAIRS, kGroup = kPairGroup / PAIRS;
-    const int tiles_p = (int)(((int64_t)a.rows_p + kRows - 1) / kRows);
+    const int tiles_p = (int)(((int64_t)a.rows_p + 255) / 256);
     const int64_t tiles = (int64_t)tiles_p * a.tiles_q;
-    const int64_t first_tile = blockIdx.x / (2 * PAIRS), step = gridDim.x / (2 * PAIRS);
-    // the cluster's tile t: kGroup P tiles at a time, within them Q tile by Q tile
+    const int64_t first_tile = blockIdx.x / 2, step = gridDim.x / 2;
+    // the pair's tile t: kPairGroup P tiles at a time, within them Q tile by Q tile
     auto place = [&](int64_t t, int& p0, int& q0) {
-        const int64_t per = (int64_t)kGroup * a.tiles_q;
+        const int64_t per = (int64_t)kPairGroup * a.tiles_q;
         const int g = (int)(t / per), in = (int)(t - g * per);
-        const int width = tiles_p - g * kGroup < kGroup ? tiles_p - g * kGroup : kGroup;
-        p0 = (g * kGroup + in % width) * kRows + (int)lead * 128;
+        const int width = tiles_p - g * kPairGroup < kPairGroup ? tiles_p - g * kPairGroup : kPairGroup;
+        p0 = (g * kPairGroup + in % width) * 256;
         q0 = (in / width) * BN;
     };
     auto fail = [&] {
@@ -716,7 +701,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 0) {
         Ring ring;
         bool ok = true;
-        const uint32_t full0 = at_rank(full, lead);
+        const uint32_t full0 = at_rank(full, 0);
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
             int p0, q0;
             place(t, p0, q0);
@@ -726,13 +711,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kStageBytes);
                     tma_load_pair(at, &map_p, kb * 128, p0 + (int)rank * 128, full0 + ring.at * 8);
-                    if constexpr (PAIRS == 1) {
-                        tma_load_pair(at + 128 * 128, &map_q, kb * 128, q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
-                    } else {                     // this pair's share of the half that the same CTA of every pair reads
-                        const int share = (int)(lead / 2) * (BN / 2 / PAIRS);
-                        tma_load_pairs(at + 128 * 128 + share * 128, &map_q, kb * 128, q0 + (int)rank * (BN / 2) + share,
-                                       full0 + ring.at * 8, (uint16_t)(5 << rank));
-                    }
+                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
                 }
                 __syncwarp();
                 ring.next(kPairStages);
@@ -775,7 +754,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tmem_copy_scales_pair(sfa, from);
                         tmem_copy_scales_pair(sfa + 4, from + (512 >> 4));
                         tmem_copy_scales_pair(sfa + 8, from + (1024 >> 4));
-                        if (last) mma_commit_pair(sempty + slots.at, pair_mask);
+                        if (last) mma_commit_pair(sempty + slots.at, kBoth);
                     }
                     __syncwarp();
                     if (last) slots.next(kPairSlots);
@@ -787,13 +766,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_scaled_pair(sums, da + 2 * k, db + 2 * k, id, sfa, sfa + 4, kb > 0 || k > 0);
-                    mma_commit_pair(empty + ring.at, all_mask);
+                    mma_commit_pair(empty + ring.at, kBoth);
                 }
                 __syncwarp();
                 ring.next(kPairStages);
             }
             if (!ok) break;
-            if (elect_one()) mma_commit_pair(done + acc.at, pair_mask);
+            if (elect_one()) mma_commit_pair(done + acc.at, kBoth);
             __syncwarp();
             acc.next(kAccs);
         }
@@ -827,7 +806,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 // 2,048 columns.  (One group at a time: 383 us for 8192^3 against 297 with no scales at all.)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(at_rank(sfull + slots.at, lead));
+                if (lane == 0) mbar_arrive_cluster(at_rank(sfull + slots.at, 0));
                 slots.next(kPairSlots);
 #pragma unroll
                 for (int c = 0; c < 3; ++c) row[c].advance();
@@ -860,7 +839,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(at_rank(acc_free + acc.at, lead));
+            if (lane == 0) mbar_arrive_cluster(at_rank(acc_free + acc.at, 0));
         }
     }
     __syncthreads();
@@ -925,50 +904,23 @@ cudaError_t launch_mm_split(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cuda
     return e;
 }
 
-// Clusters of `pairs` CTA pairs that are resident at once.  Pairs fill the GPU; clusters of four CTAs need four SMs of
-// one group of them, and leave some groups' last SMs idle (36 clusters on 152 SMs).
-int64_t clusters(int pairs) {
-    if (pairs == 1) return q8_host::sm_count() / 2;
-    static std::atomic<int> cached[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 0;
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    const auto kern = k_q8_matmul_pair<256, 2>;
-    static std::atomic<uint64_t> ready{0};
-    if (ready_once(ready, (const void*)kern, PairShape<256>::kSmem) != cudaSuccess) return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * 64);
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = PairShape<256>::kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 4;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, (const void*)kern, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    cached[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
+// CTA pairs that are resident at once.
+int64_t resident_pairs() { return q8_host::sm_count() / 2; }
 
-template <int BN, int PAIRS>
+template <int BN>
 cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
     constexpr int smem = PairShape<BN>::kSmem;
-    const auto kern = k_q8_matmul_pair<BN, PAIRS>;
+    const auto kern = k_q8_matmul_pair<BN>;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = ready_once(ready, (const void*)kern, smem);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq;
-    e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2 / PAIRS);
+    e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2);
     if (e != cudaSuccess) return e;
     a.tiles_q = (a.rows_q + BN - 1) / BN;
-    const int64_t tiles = ((int64_t)a.rows_p + 256 * PAIRS - 1) / (256 * PAIRS) * a.tiles_q, room = clusters(PAIRS);
+    const int64_t tiles = ((int64_t)a.rows_p + 255) / 256 * a.tiles_q, room = resident_pairs();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * PAIRS * (tiles < room ? tiles : room)));
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < room ? tiles : room)));
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -976,7 +928,7 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = dependent_launch() ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2 * PAIRS;
+    attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -985,30 +937,22 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
     return e;
 }
 
-// The tile width, and pairs per cluster, with the least time in the busiest cluster: rounds of tiles times the time of
-// one.  Measured per block of the sum, one to three rounds of 4096 to 16384 columns, ns for tiles of 128 / 160 / 192 /
-// 224 / 256 columns: 243 251 266 284 302; where rows of codes are not 128 bytes apart, or a multiple, and each row of a
-// box touches two lines, 296 322 349 370 395, and 300 319 328 for the last three in clusters of two pairs, whose CTAs
-// ask for fewer rows (aligned, they take what single pairs take, on fewer SMs).  Writing a tile out, 2.5 us, is
-// hidden by the next tile's products but for the last one (and for 256 columns).
-struct PairChoice {
-    int bn, pairs;
-};
-PairChoice pair_choice(int64_t rows_p, int64_t rows_q, int64_t kblocks, bool lines) {
-    PairChoice best = {224, 1};
+// The tile width with the least time in the busiest pair: rounds of tiles times the time of one.  Measured per block of
+// the sum, one to three rounds of 4096 to 16384 columns, ns for tiles of 128 / 160 / 192 / 224 / 256 columns: 243 251
+// 266 284 302; where rows of codes are not 128 bytes apart, or a multiple, and each row of a box touches two lines,
+// 296 322 349 370 395.  Writing a tile out, 2.5 us, is hidden by the next tile's products but for the last one (and
+// for 256 columns).
+int pair_width(int64_t rows_p, int64_t rows_q, int64_t kblocks, bool lines) {
+    int best = 224;
     double least = 1e300;
-    for (int pairs : {1, 2}) {
-        const int64_t room = clusters(pairs), tp = (rows_p + 256 * pairs - 1) / (256 * pairs);
-        if (room == 0) continue;
-        for (int bn : {256, 224, 192, 160, 128}) {
-            if (pairs == 2 && bn < 192) break;
-            const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + room - 1) / room;
-            const double block = lines ? 180 + 0.48 * bn : pairs == 1 ? 200 + 0.765 * bn : 215 + 0.45 * bn;
-            const double cost = (double)rounds * kblocks * block + 2500.0 * (bn == 256 ? rounds : 1);
-            if (cost < least) {
-                least = cost;
-                best = {bn, pairs};
-            }
+    const int64_t room = resident_pairs(), tp = (rows_p + 255) / 256;
+    for (int bn : {256, 224, 192, 160, 128}) {
+        const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + room - 1) / room;
+        const double block = lines ? 180 + 0.48 * bn : 200 + 0.765 * bn;
+        const double cost = (double)rounds * kblocks * block + 2500.0 * (bn == 256 ? rounds : 1);
+        if (cost < least) {
+            least = cost;
+            best = bn;
         }
     }
     return best;
@@ -1064,16 +1008,12 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     // 8192 x 64 x 4096: 11.8 and 13.0; 50000 x 64 x 2048: 22.8 and 22.1).
     cudaError_t e;
     if (!swap && n > 64 && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
-        const zs::PairChoice c = zs::pair_choice(m, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0);
-        switch (c.bn * c.pairs) {
-            case 256: e = zs::launch_mm_pair<256, 1>(p, q, k, g, st); break;
-            case 224: e = zs::launch_mm_pair<224, 1>(p, q, k, g, st); break;
-            case 192: e = zs::launch_mm_pair<192, 1>(p, q, k, g, st); break;
-            case 160: e = zs::launch_mm_pair<160, 1>(p, q, k, g, st); break;
-            case 512: e = zs::launch_mm_pair<256, 2>(p, q, k, g, st); break;
-            case 448: e = zs::launch_mm_pair<224, 2>(p, q, k, g, st); break;
-            case 384: e = zs::launch_mm_pair<192, 2>(p, q, k, g, st); break;
-            default: e = zs::launch_mm_pair<128, 1>(p, q, k, g, st); break;
+        switch (zs::pair_width(m, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0)) {
+            case 256: e = zs::launch_mm_pair<256>(p, q, k, g, st); break;
+            case 224: e = zs::launch_mm_pair<224>(p, q, k, g, st); break;
+            case 192: e = zs::launch_mm_pair<192>(p, q, k, g, st); break;
+            case 160: e = zs::launch_mm_pair<160>(p, q, k, g, st); break;
+            default: e = zs::launch_mm_pair<128>(p, q, k, g, st); break;
         }
     } else if (g.rows_q <= 16) {
         e = zs::launch_mm_split<16, 5>(p, q, k, g, st);
