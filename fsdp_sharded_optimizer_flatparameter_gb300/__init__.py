@@ -112,6 +112,7 @@ _sig("zs_set_fused_variant", [c_i32])
 _sig("zs_set_dependent_launch", [c_i32])
 _sig("zs_device_status", [ctypes.POINTER(ctypes.c_uint32), c_i32])
 _sig("zs_selftest_wait_timeout", [c_i64, c_vp])
+_sig("zs_set_q8_wait_limit", [c_i64])
 _sig("zs_q8_encode", [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp])
 _sig("zs_q8_decode", [c_vp, c_i64, c_i64, c_vp, c_i64, c_vp])
 _sig("zs_q8_transpose", [c_vp, c_i64, c_i64, c_vp, c_vp])
@@ -134,6 +135,7 @@ EXPORTED = [
     "zs_fsdp2_chunk_cat", "zs_fsdp2_copy_out", "zs_fused_step_buckets", "zs_set_dependent_launch",
     "zs_rank_shard_step", "zs_fused_step_accumulate", "zs_q8_encode", "zs_q8_decode", "zs_q8_transpose",
     "zs_q8_matmul", "zs_rmsnorm_q8", "zs_rmsnorm_backward", "zs_swiglu_q8", "zs_swiglu_backward_q8",
+    "zs_set_q8_wait_limit",
 ]
 
 
@@ -638,6 +640,11 @@ def zs_device_status(clear=False):
 
 def zs_selftest_wait_timeout(limit_cycles, stream=None):
     return _check(_lib.zs_selftest_wait_timeout(int(limit_cycles), _stream(stream)))
+
+
+def zs_set_q8_wait_limit(limit_cycles=4 * 10 ** 9):
+    """What a wait inside the 8-bit product's kernels may take, in SM cycles."""
+    return _check(_lib.zs_set_q8_wait_limit(int(limit_cycles)))
 
 
 __all__ = ["Plan", "ZsError", "zs_adamw_hparams", "LIB_PATH"] + EXPORTED + [

@@ -46,6 +46,13 @@ __global__ void __launch_bounds__(256) k_q8_decode(const __grid_constant__ Decod
 
 using namespace zs::q8_host;
 
+extern "C" int zs_set_q8_wait_limit(int64_t limit_cycles) {
+    zs::clear_error();
+    if (limit_cycles < 0 || limit_cycles > (int64_t(1) << 32)) return fail("zs_set_q8_wait_limit", "limit_cycles out of range");
+    zs::wait_limit().store((long long)limit_cycles, std::memory_order_relaxed);
+    return ZS_OK;
+}
+
 extern "C" int zs_q8_encode(const void* x, int64_t ldx, int64_t rows, int64_t cols, const zs_q8* q, const zs_q8* q_t,
                             void* stream) {
     static const char* fn = "zs_q8_encode";

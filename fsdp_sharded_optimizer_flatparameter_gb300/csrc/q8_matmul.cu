@@ -69,6 +69,14 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
     return a;
 }
+__device__ __forceinline__ void cluster_st(uint32_t at, uint32_t x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t at) {
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -96,6 +104,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* b, uint32_t parity, 
 // A whole warp waits, and agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, long long limit) {
     return __all_sync(~0u, mbar_wait(b, parity, limit));
+}
+__device__ __forceinline__ bool warp_wait_or_look(uint64_t* b, uint32_t parity, long long limit) {
+    return __all_sync(~0u, mbar_wait_or_look(b, parity, limit));
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* b, uint32_t parity, long long limit) {
     return __all_sync(~0u, mbar_wait_cluster(b, parity, limit));
@@ -202,6 +213,7 @@ constexpr int kStoreStage = 32 * 16;             // floats of shared memory per 
 struct Ring {
     int at = 0;
     uint32_t round = 0;
+    __device__ __forceinline__ uint32_t count(int stages) const { return round * stages + at; }
     __device__ __forceinline__ uint32_t parity() const { return round & 1; }
     __device__ __forceinline__ void next(int stages) {
         if (++at == stages) {
@@ -332,7 +344,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
     uint64_t* sfull = empty + STAGES;
     uint64_t* sempty = sfull + 2;
     uint64_t* done = sempty + 2;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* settled = done + 1;                // all that the products' warp issued is complete
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(settled + 1);
     uint32_t* gave_up = tmem_at + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -346,6 +359,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
             mbar_init(sempty + i, 1);
         }
         mbar_init(done, 1);
+        mbar_init(settled, 1);
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
         Ring ring;
         bool ok = true;
         for (int kb = 0; kb < kbs; ++kb) {
-            if (ring.round > 0 && !(ok = warp_wait(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
+            if (ring.round > 0 && !(ok = warp_wait_or_look(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
             uint8_t* at = base + ring.at * S::kStageBytes;
             if (elect_one()) {
                 mbar_expect_tx(full + ring.at, S::kStageBytes);
@@ -391,11 +405,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
             ring.next(STAGES);
         }
         if (!ok && lane == 0) fail();
-        const bool wrapped = ring.round > 0;     // let every copy land before the CTA may go on
-        for (int k = 0; k < STAGES; ++k) {
-            if (k < ring.at) warp_wait(full + k, ring.parity(), a.wait_limit);
-            else if (wrapped) warp_wait(full + k, ring.parity() ^ 1, a.wait_limit);
-        }
+        ring_settled(full, STAGES, ring.count(STAGES));      // no copy is under way when the CTA goes on
     } else if (warp == 1) {
         const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
         const uint64_t desc0 = operand_desc(su32(base)), sdesc0 = scales_desc(su32(scale_sh));
@@ -434,8 +444,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
             ring.next(STAGES);
         }
         if (!ok && lane == 0) fail();
-        if (ok && elect_one()) mma_commit(done);
+        if (elect_one()) {
+            if (ok) mma_commit(done);
+            mma_commit(settled);
+        }
         __syncwarp();
+        // and neither a product nor an arrival
+        ring_settled(empty, STAGES, ring.count(STAGES));
+        ring_settled(sempty, 2, slots.count(2));
+        ring_settled(done, 1, ok);
+        ring_settled(settled, 1, 1);
     } else if (warp < 6) {
         // thread r of 128: P row r and Q row r of the tile (see the scale copy's layout below)
         Ring slots;
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
         row[0].start(a.sp, a.ldsp, (int64_t)p0 + r, a.rows_p, kb0, kbs, a.kblocks);
         row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, r < BN ? a.rows_q : 0, kb0, kbs, a.kblocks);
         for (int g = 0; g < groups; g += kBatch) {
-            if (slots.round > 0 && !(ok = warp_wait(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
+            if (slots.round > 0 && !(ok = warp_wait_or_look(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t w[kBatch];
@@ -466,7 +484,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
     } else {
         const int sub = warp & 3;
         const uint32_t from = tmem + ((uint32_t)(sub * 32) << 16);
-        if (!warp_wait(done, 0, a.wait_limit)) {
+        if (!warp_wait_or_look(done, 0, a.wait_limit)) {
             if (lane == 0) fail();
         } else {
             tc_fence_after();
@@ -515,8 +533,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
         cluster_sync();
         bool ok = true;
         for (int k = 0; k < split; ++k) {
-            uint32_t bad;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad) : "r"(at_rank(gave_up, k)));
+            const uint32_t bad = cluster_ld_u32(at_rank(gave_up, k));        // all under way before the first is looked at
             ok = ok && bad == 0;
         }
         const int share = BN / split, c0 = rank * share, n = a.rows_q - q0;
@@ -596,6 +613,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_q8_matmul_split(const __gr
                 }
             }
         }
+        __syncwarp();
         cluster_sync();                          // no CTA leaves while another reads its part
     }
     __syncthreads();
@@ -629,6 +647,16 @@ struct PairShape {
 };
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
 
+// What the barriers of a pair's CTA have been or will be sent by copies and products, each to its ring in turn.  A CTA
+// leaves only when all of it has arrived, after a wait that ran out as after the last tile: nothing may be under way
+// when its shared and tensor memory go.
+struct Sent {
+    uint32_t loads;          // blocks that this CTA asked for
+    uint32_t products;       // blocks multiplied
+    uint32_t scales;         // batches of scales copied to tensor memory
+    uint32_t sums;           // accumulators completed
+};
+
 template <int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
@@ -644,8 +672,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint64_t* sempty = sfull + kPairSlots;       // each CTA: they are copied out
     uint64_t* done = sempty + kPairSlots;        // each CTA: an accumulator is complete
     uint64_t* acc_free = done + 2;               // leader: both CTAs have read it
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 2);
-    uint32_t* gave_up = tmem_at + 1;
+    uint64_t* settled = acc_free + 2;            // each CTA: all that the products' warp issued is complete
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(settled + 1);
+    uint32_t* gave_up = tmem_at + 1;             // set in both CTAs
+    Sent* sent = reinterpret_cast<Sent*>(gave_up + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();        // CTA 0 of the pair leads
     constexpr uint16_t kBoth = 3;
@@ -663,6 +693,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(done + i, 1);
             mbar_init(acc_free + i, 16);         // the eight reading warps of both CTAs
         }
+        mbar_init(settled, 1);
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -694,7 +725,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         q0 = (in / width) * BN;
     };
     auto fail = [&] {
-        atomicExch(gave_up, 1u);
+        cluster_st(at_rank(gave_up, 0), 1);
+        cluster_st(at_rank(gave_up, 1), 1);
         atomicCAS(a.error, 0u, ZS_DEVERR_MATMUL_WAIT);
     };
 
@@ -706,7 +738,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int p0, q0;
             place(t, p0, q0);
             for (int kb = 0; kb < a.kblocks; ++kb) {
-                if (ring.round > 0 && !(ok = warp_wait(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
+                if (ring.round > 0 && !(ok = warp_wait_or_look(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
                 uint8_t* at = base + ring.at * kStageBytes;
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kStageBytes);
@@ -717,14 +749,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ring.next(kPairStages);
             }
         }
+        if (lane == 0) sent->loads = ring.count(kPairStages);
         if (!ok && lane == 0) fail();
-        if (rank == 0) {                         // let every copy land before the CTAs may exit
-            const bool wrapped = ring.round > 0;
-            for (int k = 0; k < kPairStages; ++k) {
-                if (k < ring.at) mbar_wait(full + k, ring.parity(), a.wait_limit);
-                else if (wrapped) mbar_wait(full + k, ring.parity() ^ 1, a.wait_limit);
-            }
-        }
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
         const uint64_t desc0 = operand_desc(su32(base));
@@ -776,6 +802,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             acc.next(kAccs);
         }
+        if (elect_one()) mma_commit_pair(settled, kBoth);
+        __syncwarp();
+        if (lane < 2) {
+            cluster_st(at_rank(&sent->products, lane), ring.count(kPairStages));
+            cluster_st(at_rank(&sent->scales, lane), slots.count(kPairSlots));
+            cluster_st(at_rank(&sent->sums, lane), acc.count(kAccs));
+        }
         if (!ok && lane == 0) fail();
     } else if (warp >= 2 && warp < 6) {
         // thread r of 128: P row r, Q rows r and 128 + r of the tile; the scale copy wants row r's word at
@@ -792,7 +825,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, a.rows_q, 0, a.kblocks, a.kblocks);
             row[2].start(a.sq, a.ldsq, (int64_t)q0 + 128 + r, BN > 128 + r ? a.rows_q : 0, 0, a.kblocks, a.kblocks);
             for (int g = 0; g < groups; g += kBatch) {
-                if (slots.round > 0 && !(ok = warp_wait(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
+                if (slots.round > 0 && !(ok = warp_wait_or_look(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
                     uint32_t w[kBatch];
@@ -820,7 +853,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int64_t t = first_tile; t < tiles; t += step, acc.next(kAccs)) {
             int p0, q0;
             place(t, p0, q0);
-            if (!warp_wait(done + acc.at, acc.parity(), a.wait_limit)) {
+            if (!warp_wait_or_look(done + acc.at, acc.parity(), a.wait_limit)) {
                 if (lane == 0) fail();
                 break;
             }
@@ -843,7 +876,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     }
     __syncthreads();
-    cluster_sync();
+    cluster_sync();                              // nobody issues anything any more, and what was issued is known
+    const bool bad = *gave_up != 0;
+    if (warp == 0) {
+        // Both CTAs' copies count on the leader's barriers, each phase of which wants a block of both.  CTAs that gave
+        // up may have asked for different numbers of blocks (six apart at most: a stage is loaded again only when the
+        // products have read it, which takes both): the leader makes the phases whole, and waits for them.
+        if (bad && rank == 0) {
+            const uint32_t mine = sent->loads, other = cluster_ld_u32(at_rank(&sent->loads, 1));
+            if (lane == 0) {
+                for (uint32_t j = other; j < mine; ++j) mbar_complete_tx(full + j % kPairStages, kStageBytes);
+                for (uint32_t j = mine; j < other; ++j) mbar_expect_tx(full + j % kPairStages, kStageBytes);
+            }
+            __syncwarp();
+            ring_settled(full, kPairStages, mine > other ? mine : other);
+        }
+        ring_settled(empty, kPairStages, sent->products);
+        ring_settled(sempty, kPairSlots, sent->scales);
+        ring_settled(done, kAccs, sent->sums);
+        ring_settled(settled, 1, 1);
+    }
+    if (bad) {                                   // in both CTAs: the other's copies are counted here, tensor memory is both's
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 2) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
@@ -1002,7 +1058,7 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     g.align = ((uintptr_t)out & 31) == 0 && (ldo & 15) == 0 ? 32 : wide(out, ldo) ? 16 : 0;
     g.scale = scale;
     g.first = first != 0;
-    g.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
+    g.wait_limit = zs::wait_limit().load(std::memory_order_relaxed);
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
     // Up to 64 rows of b as well: the small kernel's narrow tiles (8192 x 8 x 4096: 10.6 us, and 13.3 in pairs of CTAs;
     // 8192 x 64 x 4096: 11.8 and 13.0; 50000 x 64 x 2048: 22.8 and 22.1).

@@ -19,6 +19,10 @@ __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
 }
+// Counts bytes as landed that a copy never issued would have brought.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
 }
@@ -40,6 +44,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, long lon
         if (clock64() - t0 > limit) return false;
     }
     return true;
+}
+
+// The same, which looks once with a limit of 0 (try_wait itself may wait).  The waits of the products' warp, which is short
+// of issue slots, do without that test (8192 x 22016 x 4096: 511 us with it, 496 without).
+__device__ __forceinline__ bool mbar_wait_or_look(uint64_t* b, uint32_t parity, long long limit) {
+    if (limit != 0) return mbar_wait(b, parity, limit);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(su32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// What a wait may take (zs_set_q8_wait_limit changes it), and a wait for what is under way already, which a kernel that
+// gave up makes before its shared memory goes: ~2 s at the 2.07 GHz maximum SM clock.
+constexpr long long kWaitLimit = 4000000000LL, kDrainLimit = 4000000000LL;
+
+// A whole warp, lane k for barrier k: waits for the last of the `count` events that came to a ring of barriers in turn.
+__device__ __forceinline__ void ring_settled(uint64_t* ring, uint32_t stages, uint32_t count) {
+    const uint32_t lane = threadIdx.x & 31;
+    if (lane < stages && lane < count) mbar_wait(ring + lane, ((count - 1 - lane) / stages) & 1, kDrainLimit);
+    __syncwarp();
 }
 
 // A map's box at column x and row y; x is a multiple of 128 elements here, so that the copy starts on a
@@ -109,6 +139,12 @@ inline cudaError_t ready_once(std::atomic<uint64_t>& ready, const void* kern, in
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess && dev < kMaxDevices) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     return e;
+}
+
+// Cycles that a wait of the 8-bit kernels may take.
+inline std::atomic<long long>& wait_limit() {
+    static std::atomic<long long> cycles{kWaitLimit};
+    return cycles;
 }
 
 // The current device's status word (zs_device_status).

@@ -256,6 +256,13 @@ int zs_device_status(uint32_t* code, int32_t clear);
  * Errors: ZS_ERR_INVALID for a limit out of range; ZS_ERR_CUDA. */
 int zs_selftest_wait_timeout(int64_t limit_cycles, void* stream);
 
+/* What a wait of zs_q8_matmul's kernels may take, in SM cycles (0 .. 2^32; the
+ * default is 4 * 10^9, about 2 s), for calls of the whole process from now on.
+ * With 0 a wait looks once and gives up, which is how a test sees it: the call
+ * records its ZS_DEVERR_* code, lets everything under way arrive, and returns
+ * with its outputs unspecified.  Errors: ZS_ERR_INVALID for a limit out of range. */
+int zs_set_q8_wait_limit(int64_t limit_cycles);
+
 /* ------------------------------------------------------------------ device operations */
 
 /* Gradient accumulation without synchronisation ("Infra: Data Parallel",
