@@ -643,7 +643,7 @@ def zs_selftest_wait_timeout(limit_cycles, stream=None):
 
 
 def zs_set_q8_wait_limit(limit_cycles=4 * 10 ** 9):
-    """What a wait inside the 8-bit product's kernels may take, in SM cycles."""
+    """What a wait inside the 8-bit operators' kernels may take, in SM cycles."""
     return _check(_lib.zs_set_q8_wait_limit(int(limit_cycles)))
 
 

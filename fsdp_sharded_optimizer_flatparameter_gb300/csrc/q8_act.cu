@@ -242,7 +242,6 @@ __device__ __forceinline__ void norm_outputs(const float2 (&t)[8], float2 r, con
 
 constexpr int kRowStages = 4;
 constexpr int kRowSmem = kRowStages * 8192 * 6;      // the widest row of 512 threads, three bf16 matrices
-constexpr long long kRowWait = 4000000000LL;         // ~2 s at the 2.07 GHz maximum SM clock
 
 // bytes (a multiple of 16) from src to dst, both 16-byte aligned, counted on bar.
 __device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -258,7 +257,7 @@ __device__ __forceinline__ V16 row16(const uint8_t* p) {
 __device__ __forceinline__ void drain_rows(uint64_t* full, int at, uint32_t parity, int64_t left, unsigned int* error) {
     atomicCAS(error, 0u, ZS_DEVERR_TILE_WAIT);
     for (int i = 0; i < kRowStages && i < left; ++i)
-        mbar_wait(full + (at + i) % kRowStages, at + i >= kRowStages ? parity ^ 1 : parity, kRowWait);
+        mbar_wait(full + (at + i) % kRowStages, at + i >= kRowStages ? parity ^ 1 : parity, kDrainLimit);
 }
 
 // ------------------------------------------------------------------ norm, forward
@@ -400,6 +399,7 @@ struct NormBackArgs {
     int threads;             // of a group
     int parts;               // rows of partials written: the grid
     unsigned int* error;
+    long long wait_limit;
 };
 
 // The CTA's threads are groups of `threads`, a row each at a time; a group takes every (groups of the grid)th row
@@ -517,16 +517,19 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
                 asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             }
             __syncthreads();
-            if (tid == 0)
+            if (tid == 0) {
 #pragma unroll 1                                 // unrolled, 16384 x 4096 took 85 us instead of 76
                 for (int i = 0; i < kRowStages && row0 + i * stride < a.rows; ++i) copy(row0 + i * stride, i);
+                // a limit of 0: the look is here, before the loop, where it costs 6 of 83 us
+                if (a.wait_limit == 0) gave_up[0] = !mbar_wait_or_look(full, 0, 0);
+            }
         }
         if (row0 < a.rows) begin(row0);
         int at = 0;
         uint32_t parity = 0;
         for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
             if constexpr (RING) {
-                if (!mbar_wait(full + at, parity, kRowWait)) gave_up[turn] = 1;
+                if (!mbar_wait(full + at, parity, a.wait_limit)) gave_up[turn] = 1;
                 const uint8_t* from = ring + at * stage;
                 if (in) {
                     next.dy = row16(from + col0 * 2);
@@ -763,6 +766,7 @@ cudaError_t launch_norm_back(NormBackArgs& a, int64_t parts, cudaStream_t st) {
             static std::atomic<uint64_t> ready{0};
             const size_t smem = kRowStages * (size_t)a.cols * ((KEPT8 ? 3 : 4) + (a.ds ? 2 : 0));
             cudaError_t e = error_word(&a.error);
+            a.wait_limit = wait_limit().load(std::memory_order_relaxed);
             if (e == cudaSuccess) e = ready_once(ready, (const void*)k_rmsnorm_backward<true, true, false, KEPT8, true>, kRowSmem);
             if (e != cudaSuccess) return e;
             return launch_kernel(k_rmsnorm_backward<true, true, false, KEPT8, true>, grid, block, smem, st, a);

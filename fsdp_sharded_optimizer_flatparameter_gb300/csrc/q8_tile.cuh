@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
         const TilePos<CP> t = tile_pos<CP>(now, a.rows, a.cols);
         bool late = false;
         if constexpr (kSlots) async_wait_all();
-        if constexpr (S::kLoads > 0) late = !mbar_wait(full + s, parity, a.wait_limit);
+        if constexpr (S::kLoads > 0) late = !mbar_wait_or_look(full + s, parity, a.wait_limit);
         const uint8_t* at = base + s * S::kStage;
 #pragma unroll 1
         for (int pass = 0; pass < S::kPasses; ++pass) {
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kTileThreads, (TileShape<KIND, TMA>::kPerSm))
                     atomicCAS(a.error, 0u, ZS_DEVERR_TILE_WAIT);
                     for (int i = 0; i < S::kStages; ++i)
                         if (tile + i * (int64_t)grid < tiles)
-                            mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, a.wait_limit);
+                            mbar_wait(full + (s + i) % S::kStages, s + i >= S::kStages ? parity ^ 1 : parity, kDrainLimit);
                 }
                 return;
             }
@@ -574,7 +574,7 @@ cudaError_t launch_tiles(TileArgs& a, cudaStream_t st) {
     a.tiles_c = (a.cols + S::kCols - 1) / S::kCols;
     a.tiles = a.tiles_c * ((a.rows + 127) / 128);
     if (a.tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    a.wait_limit = 4000000000LL;                     // ~2 s at the 2.07 GHz maximum SM clock
+    a.wait_limit = wait_limit().load(std::memory_order_relaxed);
     e = error_word(&a.error);
     CUtensorMap mx{}, ma{}, mb{};
     if (e == cudaSuccess && S::kX > 0) e = make_map(&mx, a.x, true, a.rows, a.cols, a.ldx * 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);

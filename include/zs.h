@@ -114,7 +114,7 @@ extern "C" {
 #define ZS_DEVERR_SELFTEST      3u   /* zs_selftest_wait_timeout ran its wait out (expected)         */
 #define ZS_DEVERR_GATHER_WAIT   4u   /* a bulk-store gather gave up waiting for its tile             */
 #define ZS_DEVERR_MATMUL_WAIT   5u   /* zs_q8_matmul gave up waiting for a tile or an accumulator    */
-#define ZS_DEVERR_TILE_WAIT     6u   /* an 8-bit encode, transpose or gate backward gave up waiting  */
+#define ZS_DEVERR_TILE_WAIT     6u   /* an 8-bit encode, transpose, gate or norm backward gave up    */
 
 typedef struct zs_plan_s* zs_plan_t;
 
@@ -256,7 +256,7 @@ int zs_device_status(uint32_t* code, int32_t clear);
  * Errors: ZS_ERR_INVALID for a limit out of range; ZS_ERR_CUDA. */
 int zs_selftest_wait_timeout(int64_t limit_cycles, void* stream);
 
-/* What a wait of zs_q8_matmul's kernels may take, in SM cycles (0 .. 2^32; the
+/* What a wait of the 8-bit operators' kernels may take, in SM cycles (0 .. 2^32; the
  * default is 4 * 10^9, about 2 s), for calls of the whole process from now on.
  * With 0 a wait looks once and gives up, which is how a test sees it: the call
  * records its ZS_DEVERR_* code, lets everything under way arrive, and returns
