@@ -656,7 +656,7 @@ __all__ = ["Plan", "ZsError", "zs_adamw_hparams", "LIB_PATH"] + EXPORTED + [
 # An 8-bit matrix is a pair (codes, scales): codes a CUDA tensor [rows, cols] of one byte per value
 # (uint8 or float8_e4m3fn), rows 16 bytes apart or a multiple; scales [rows, ceil(cols / 128)] (uint8 or
 # float8_e8m0fnu).  Both may be views (row or column ranges) of larger ones.  bf16 matrices are CUDA
-# tensors [rows, cols] whose rows are contiguous.
+# tensors [rows, cols] whose rows are contiguous.  All of a call's tensors are on the current device.
 
 # A small product or norm takes a few microseconds on the GPU, less than a call's checks in Python may: what
 # fits is recognised in one expression per tensor, and only what does not is looked at again for the message.
@@ -680,10 +680,18 @@ def q8_empty(rows, cols, device="cuda"):
     return codes.view(_torch.float8_e4m3fn), scales.view(_torch.float8_e8m0fnu)
 
 
-def _here(stream):
-    """The stream argument; by default the current stream (the tensors are on the GPU already)."""
+def _device():
+    """The current device's index: kernels are launched on it, and read and write its own memory only."""
+    try:
+        return _torch._C._cuda_getDevice()
+    except RuntimeError:                   # no GPU: no tensor is on one
+        return None
+
+
+def _here(stream, dev):
+    """The stream argument; by default the current stream of device `dev` (the tensors are on it already)."""
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        return _torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -693,13 +701,20 @@ def _shape(x, what):
     return x.shape
 
 
-def _misfit(x, rows, cols, dtypes, what):
-    """What is wrong with a matrix that must be rows x cols of one of dtypes on the GPU; if nothing is, the
+def _elsewhere(x, dev, what):
+    """What is wrong with the place of a tensor that must be on device `dev`, if anything."""
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if x.get_device() != dev:
+        raise ValueError("%s is on cuda:%d and the current device is cuda:%s" % (what, x.get_device(), dev))
+
+
+def _misfit(x, rows, cols, dtypes, what, dev):
+    """What is wrong with a matrix that must be rows x cols of one of dtypes on device `dev`; if nothing is, the
     distance between its rows (that of a single row is never used)."""
     if x.dtype not in dtypes:
         raise ValueError("%s must be %s, not %s" % (what, " or ".join(str(d) for d in dtypes), x.dtype))
-    if not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % what)
+    _elsewhere(x, dev, what)
     if x.dim() != 2 or x.shape != (rows, cols):
         raise ValueError("%s must be %d x %d, not %s" % (what, rows, cols, tuple(x.shape)))
     ld, step = x.stride()
@@ -710,24 +725,25 @@ def _misfit(x, rows, cols, dtypes, what):
     return ld if rows >= 2 else cols
 
 
-def _bf16(x, shape, what):
+def _bf16(x, shape, what, dev):
     """Address and row distance of a bf16 matrix."""
-    if x.dtype is _BF16 and x.is_cuda and x.shape == shape:
+    if x.dtype is _BF16 and x.get_device() == dev and x.shape == shape:
         ld, step = x.stride()
         if step == 1 and ld >= shape[1]:
             return x.data_ptr(), ld
-    return x.data_ptr(), _misfit(x, shape[0], shape[1], (_BF16,), what)
+    return x.data_ptr(), _misfit(x, shape[0], shape[1], (_BF16,), what, dev)
 
 
-def _vector(x, n, dtype, what):
+def _vector(x, n, dtype, what, dev):
     if x is None:
         return None
-    if x.dtype is dtype and x.is_cuda and x.numel() == n and x.is_contiguous():
+    if x.dtype is dtype and x.get_device() == dev and x.numel() == n and x.is_contiguous():
         return x.data_ptr()
+    _elsewhere(x, dev, what)
     raise ValueError("%s must be %d contiguous elements of %s on the GPU" % (what, n, dtype))
 
 
-def _q8(q, rows, cols, what):
+def _q8(q, rows, cols, what, dev):
     """A zs_q8 (its bytes) of an 8-bit matrix (codes, scales), checked against rows x cols; None stays None."""
     if q is None:
         return None
@@ -737,13 +753,13 @@ def _q8(q, rows, cols, what):
         ld, step = codes.stride()
         lds, step_s = scales.stride()
         if (step == 1 and step_s == 1 and ld >= cols and lds >= blocks and not ld & 15 and codes.dtype in _CODES
-                and scales.dtype in _SCALES and codes.is_cuda and scales.is_cuda and codes.shape == (rows, cols)
-                and scales.shape == (rows, blocks)):
+                and scales.dtype in _SCALES and codes.get_device() == dev and scales.get_device() == dev
+                and codes.shape == (rows, cols) and scales.shape == (rows, blocks)):
             return _PACK_Q8(codes.data_ptr(), scales.data_ptr(), ld, lds)
     except ValueError:                     # not matrices
         pass
-    ld = _misfit(codes, rows, cols, _CODES, what + " codes")
-    lds = _misfit(scales, rows, blocks, _SCALES, what + " scales")
+    ld = _misfit(codes, rows, cols, _CODES, what + " codes", dev)
+    lds = _misfit(scales, rows, blocks, _SCALES, what + " scales", dev)
     if rows < 2:
         ld = max(16, (ld + 15) // 16 * 16)
     return _PACK_Q8(codes.data_ptr(), scales.data_ptr(), ld, lds)
@@ -751,78 +767,89 @@ def _q8(q, rows, cols, what):
 
 def zs_q8_encode(x, q=None, q_t=None, stream=None):
     """x (bf16 [rows, cols]) in 8 bits: as it is into q, transposed into q_t ([cols, rows])."""
+    dev = _device()
     shape = rows, cols = _shape(x, "x")
-    p, ld = _bf16(x, shape, "x")
-    return _check(_lib.zs_q8_encode(p, ld, rows, cols, _q8(q, rows, cols, "q"), _q8(q_t, cols, rows, "q_t"), _here(stream)))
+    p, ld = _bf16(x, shape, "x", dev)
+    return _check(_lib.zs_q8_encode(p, ld, rows, cols, _q8(q, rows, cols, "q", dev), _q8(q_t, cols, rows, "q_t", dev),
+                                    _here(stream, dev)))
 
 
 def zs_q8_decode(q, y, stream=None):
     """The values of q into y (bf16, same shape)."""
+    dev = _device()
     shape = rows, cols = _shape(y, "y")
-    p, ld = _bf16(y, shape, "y")
-    return _check(_lib.zs_q8_decode(_q8(q, rows, cols, "q"), rows, cols, p, ld, _here(stream)))
+    p, ld = _bf16(y, shape, "y", dev)
+    return _check(_lib.zs_q8_decode(_q8(q, rows, cols, "q", dev), rows, cols, p, ld, _here(stream, dev)))
 
 
 def zs_q8_transpose(q, q_t, stream=None):
     """q ([rows, cols]) encoded again as its transpose q_t ([cols, rows])."""
+    dev = _device()
     rows, cols = _shape(q[0], "q")
-    return _check(_lib.zs_q8_transpose(_q8(q, rows, cols, "q"), rows, cols, _q8(q_t, cols, rows, "q_t"), _here(stream)))
+    return _check(_lib.zs_q8_transpose(_q8(q, rows, cols, "q", dev), rows, cols, _q8(q_t, cols, rows, "q_t", dev),
+                                       _here(stream, dev)))
 
 
 def zs_q8_matmul(a, b, out, scale=1.0, first=True, stream=None):
     """out (bf16 [m, n]) = (0 if first else out) + scale * a b^T for 8-bit a ([m, k]) and b ([n, k])."""
+    dev = _device()
     shape = m, n = _shape(out, "out")
     k = _shape(a[0], "a")[1]
-    p, ld = _bf16(out, shape, "out")
-    return _check(_lib.zs_q8_matmul(_q8(a, m, k, "a"), _q8(b, n, k, "b"), m, n, k, scale, 1 if first else 0, p, ld,
-                                    _here(stream)))
+    p, ld = _bf16(out, shape, "out", dev)
+    return _check(_lib.zs_q8_matmul(_q8(a, m, k, "a", dev), _q8(b, n, k, "b", dev), m, n, k, scale, 1 if first else 0, p, ld,
+                                    _here(stream, dev)))
 
 
 def zs_rmsnorm_q8(x, residual, weight, eps, y, s=None, rstd=None, s_q8=None, stream=None):
     """RMS norm of x + residual (residual may be None) in 8 bits into y; the sum into s (bf16) and s_q8
     (8 bits), the rows' reciprocal norms into rstd (fp32), each when given."""
+    dev = _device()
     shape = rows, cols = _shape(x, "x")
-    px, ldx = _bf16(x, shape, "x")
-    pr, ldr = (None, 0) if residual is None else _bf16(residual, shape, "residual")
-    ps, lds = (None, 0) if s is None else _bf16(s, shape, "s")
-    return _check(_lib.zs_rmsnorm_q8(px, ldx, pr, ldr, _vector(weight, cols, _BF16, "weight"), eps, rows, cols,
-                                     _q8(y, rows, cols, "y"), ps, lds, _q8(s_q8, rows, cols, "s_q8"),
-                                     _vector(rstd, rows, _F32, "rstd"), _here(stream)))
+    px, ldx = _bf16(x, shape, "x", dev)
+    pr, ldr = (None, 0) if residual is None else _bf16(residual, shape, "residual", dev)
+    ps, lds = (None, 0) if s is None else _bf16(s, shape, "s", dev)
+    return _check(_lib.zs_rmsnorm_q8(px, ldx, pr, ldr, _vector(weight, cols, _BF16, "weight", dev), eps, rows, cols,
+                                     _q8(y, rows, cols, "y", dev), ps, lds, _q8(s_q8, rows, cols, "s_q8", dev),
+                                     _vector(rstd, rows, _F32, "rstd", dev), _here(stream, dev)))
 
 
 def zs_rmsnorm_backward(dy, s, weight, rstd, dx, dw, partials, ds=None, scale=1.0, first=True, stream=None):
     """Backward pass of zs_rmsnorm_q8.  s: the sum, a bf16 matrix or an 8-bit pair; partials: fp32 scratch
     [n, cols]; ds: gradient reaching the sum past the norm, added to dx."""
+    dev = _device()
     shape = rows, cols = _shape(dy, "dy")
-    py, ldy = _bf16(dy, shape, "dy")
+    py, ldy = _bf16(dy, shape, "dy", dev)
     if isinstance(s, tuple):
-        ps, lds, qs = None, 0, _q8(s, rows, cols, "s")
+        ps, lds, qs = None, 0, _q8(s, rows, cols, "s", dev)
     else:
-        (ps, lds), qs = _bf16(s, shape, "s"), None
-    pd, ldd = (None, 0) if ds is None else _bf16(ds, shape, "ds")
-    px, ldx = _bf16(dx, shape, "dx")
+        (ps, lds), qs = _bf16(s, shape, "s", dev), None
+    pd, ldd = (None, 0) if ds is None else _bf16(ds, shape, "ds", dev)
+    px, ldx = _bf16(dx, shape, "dx", dev)
     n = _shape(partials, "partials")[0]
     return _check(_lib.zs_rmsnorm_backward(
-        py, ldy, ps, lds, qs, _vector(weight, cols, _BF16, "weight"), _vector(rstd, rows, _F32, "rstd"), pd, ldd, rows, cols,
-        px, ldx, _vector(dw, cols, _BF16, "dw"), scale, 1 if first else 0, _vector(partials, n * cols, _F32, "partials"), n,
-        _here(stream)))
+        py, ldy, ps, lds, qs, _vector(weight, cols, _BF16, "weight", dev), _vector(rstd, rows, _F32, "rstd", dev), pd, ldd,
+        rows, cols, px, ldx, _vector(dw, cols, _BF16, "dw", dev), scale, 1 if first else 0,
+        _vector(partials, n * cols, _F32, "partials", dev), n, _here(stream, dev)))
 
 
 def zs_swiglu_q8(gate, up, h, gate_q=None, up_q=None, stream=None):
     """h = gate * sigmoid(gate) * up in 8 bits; gate and up kept in 8 bits where gate_q, up_q are given."""
+    dev = _device()
     shape = rows, cols = _shape(gate, "gate")
-    pg, ldg = _bf16(gate, shape, "gate")
-    pu, ldu = _bf16(up, shape, "up")
-    return _check(_lib.zs_swiglu_q8(pg, ldg, pu, ldu, rows, cols, _q8(h, rows, cols, "h"),
-                                    _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), _here(stream)))
+    pg, ldg = _bf16(gate, shape, "gate", dev)
+    pu, ldu = _bf16(up, shape, "up", dev)
+    return _check(_lib.zs_swiglu_q8(pg, ldg, pu, ldu, rows, cols, _q8(h, rows, cols, "h", dev),
+                                    _q8(gate_q, rows, cols, "gate_q", dev), _q8(up_q, rows, cols, "up_q", dev),
+                                    _here(stream, dev)))
 
 
 def zs_swiglu_backward_q8(dh, gate_q, up_q, dgate=None, dup=None, dgate_t=None, dup_t=None, h_t=None, stream=None):
     """Backward pass of zs_swiglu_q8 from the kept gate and up: the gradients in 8 bits as they are and
     transposed, and h recomputed and transposed, each where given."""
+    dev = _device()
     shape = rows, cols = _shape(dh, "dh")
-    p, ld = _bf16(dh, shape, "dh")
+    p, ld = _bf16(dh, shape, "dh", dev)
     return _check(_lib.zs_swiglu_backward_q8(
-        p, ld, _q8(gate_q, rows, cols, "gate_q"), _q8(up_q, rows, cols, "up_q"), rows, cols,
-        _q8(dgate, rows, cols, "dgate"), _q8(dup, rows, cols, "dup"), _q8(dgate_t, cols, rows, "dgate_t"),
-        _q8(dup_t, cols, rows, "dup_t"), _q8(h_t, cols, rows, "h_t"), _here(stream)))
+        p, ld, _q8(gate_q, rows, cols, "gate_q", dev), _q8(up_q, rows, cols, "up_q", dev), rows, cols,
+        _q8(dgate, rows, cols, "dgate", dev), _q8(dup, rows, cols, "dup", dev), _q8(dgate_t, cols, rows, "dgate_t", dev),
+        _q8(dup_t, cols, rows, "dup_t", dev), _q8(h_t, cols, rows, "h_t", dev), _here(stream, dev)))
