@@ -897,19 +897,30 @@ extern "C" int zs_swiglu_q8(const void* gate, int64_t ldg, const void* up, int64
     a.ldg = ldg;
     a.ldu = ldu;
     a.rows = rows;
-    a.cols = cols;
     // the CTA size of 64, 96 or 128 whose pieces leave the fewest threads without columns (larger CTAs leave the SM
     // less full: 148 us instead of 118 at 8192 x 11008 with 352 threads)
     const int64_t vecs = (cols + 15) / 16;
     int threads = zs::kGateMost;
     for (int t = 96; t >= 64; t -= 32)
         if ((vecs + t - 1) / t * t < (vecs + threads - 1) / threads * threads) threads = t;
-    const int64_t pieces = (vecs + threads - 1) / threads;
-    if (pieces > 65535) return fail(fn, "cols too large for one launch");
-    const dim3 grid((unsigned)rows, (unsigned)pieces), block(threads);
+    const bool w = wide(gate, ldg, 32) && wide(up, ldu, 32);
     const cudaStream_t st = (cudaStream_t)stream;
-    return cuda_status(fn, wide(gate, ldg, 32) && wide(up, ldu, 32) ? zs::launch_kernel(zs::k_swiglu_q8<true>, grid, block, 0, st, a)
-                                                            : zs::launch_kernel(zs::k_swiglu_q8<false>, grid, block, 0, st, a));
+    // as many columns at a time as a launch has pieces for: a column range that starts at a block is a matrix itself
+    const int64_t most = int64_t(65535) * threads * 16;
+    for (int64_t left = cols; left > 0; left -= most) {
+        a.cols = left < most ? left : most;
+        const dim3 grid((unsigned)rows, (unsigned)((a.cols + 16 * threads - 1) / (16 * threads))), block(threads);
+        ZS_Q8_TRY(cuda_status(fn, w ? zs::launch_kernel(zs::k_swiglu_q8<true>, grid, block, 0, st, a)
+                                    : zs::launch_kernel(zs::k_swiglu_q8<false>, grid, block, 0, st, a)));
+        a.gate += most;
+        a.up += most;
+        for (zs::Q8* q : {&a.h, &a.gate_q, &a.up_q}) {
+            if (!q->codes) continue;
+            q->codes += most;
+            q->scales += most / ZS_Q8_BLOCK;
+        }
+    }
+    return ZS_OK;
 }
 
 extern "C" int zs_swiglu_backward_q8(const void* dh, int64_t lddh, const zs_q8* gate_q, const zs_q8* up_q,
