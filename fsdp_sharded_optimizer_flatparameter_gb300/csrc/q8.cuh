@@ -5,6 +5,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <string>
 
@@ -159,15 +160,14 @@ inline int check_q8(const char* fn, const char* name, const zs_q8* q, int64_t ro
 inline bool wide(const void* p, int64_t ld, int bytes = 16) { return ((uintptr_t)p & (bytes - 1)) == 0 && (ld & (bytes / 2 - 1)) == 0; }
 
 inline int sm_count() {
-    static int cached[64] = {};
+    static std::atomic<int> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (!cached[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
-        cached[dev] = n;
-    }
-    return cached[dev];
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    cached[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace q8_host

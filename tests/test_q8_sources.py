@@ -24,3 +24,14 @@ def test_no_copy_is_multicast():
                 seen += 1
                 assert "multicast" not in line, "%s: %s" % (os.path.basename(path), line)
     assert seen >= 3
+
+
+def test_what_calls_remember_is_safe_between_threads():
+    """Calls may come from several threads: what the 8-bit operators' host code keeps between calls is constant or atomic."""
+    for path in SOURCES:
+        if not os.path.basename(path).startswith("q8"):
+            continue
+        with open(path) as f:
+            for n, line in enumerate(f, 1):
+                if re.match(r"\s*static ", line):
+                    assert re.match(r"\s*static (const\b|constexpr\b|std::atomic<)", line), "%s:%d: %s" % (path, n, line)
