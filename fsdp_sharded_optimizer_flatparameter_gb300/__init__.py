@@ -647,9 +647,6 @@ def zs_set_q8_wait_limit(limit_cycles=4 * 10 ** 9):
     return _check(_lib.zs_set_q8_wait_limit(int(limit_cycles)))
 
 
-__all__ = ["Plan", "ZsError", "zs_adamw_hparams", "LIB_PATH"] + EXPORTED + [
-    n for n in dir() if n.startswith("ZS_")]
-
 
 # ------------------------------------------------------------------ 8-bit training operators
 #
@@ -853,3 +850,8 @@ def zs_swiglu_backward_q8(dh, gate_q, up_q, dgate=None, dup=None, dgate_t=None, 
         p, ld, _q8(gate_q, rows, cols, "gate_q", dev), _q8(up_q, rows, cols, "up_q", dev), rows, cols,
         _q8(dgate, rows, cols, "dgate", dev), _q8(dup, rows, cols, "dup", dev), _q8(dgate_t, cols, rows, "dgate_t", dev),
         _q8(dup_t, cols, rows, "dup_t", dev), _q8(h_t, cols, rows, "h_t", dev), _here(stream, dev)))
+
+
+# the plan's calls are Plan's methods
+__all__ = ["Plan", "ZsError", "zs_adamw_hparams", "zs_q8", "q8_empty", "LIB_PATH"] + [
+    n for n in dir() if n in EXPORTED or n.startswith("ZS_")]

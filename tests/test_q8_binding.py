@@ -79,3 +79,10 @@ def test_nothing_is_enqueued_on_a_device_that_holds_none_of_the_tensors(monkeypa
     call, args = _calls()[i]
     with pytest.raises(ValueError, match="is on cuda:0 and the current device is cuda:1"):
         call(**args)
+
+
+def test_a_star_import_has_what_the_calls_take():
+    names = {}
+    exec("from fsdp_sharded_optimizer_flatparameter_gb300 import *", names)
+    assert {"q8_empty", "zs_q8", "ZS_Q8_BLOCK", "ZS_Q8_MAX_PARTIALS", "ZS_DEVERR_TILE_WAIT"} <= set(names)
+    assert {n for n in zs.EXPORTED if hasattr(zs, n)} <= set(names) and "Plan" in names
