@@ -11,9 +11,11 @@
 //
 // What bounds these kernels next to the bytes is the shared-memory pipe (shuffles, staging) and the issue of
 // instructions, hence the large thread tiles and the two-wide arithmetic.  Encoding 22016 x 4096 both ways (360 MB,
-// 53 us at the copy rate): 85 us with two rows per thread, full-width maxima and 18 instructions per value, 62-63 us
-// with 10.7.  The transpose issues 14 per value at 65 % of the issue rate (8192 x 4096: 20 us, bytes 10), the gate's
-// backward pass 55 at 54 % (5003 x 5504: 85 us, bytes 37).
+// 53 us at the copy rate): 85 us with two rows per thread, full-width maxima and 18 instructions per value, 63 us
+// with 11.4.  The transpose issues 14 per value at 63 % of the issue rate (8192 x 4096: 20 us, bytes 10).  The gate's
+// backward pass issues 58 at 47 % (5003 x 5504: 87 us, bytes 37) and saturates nothing: of the 8.3 cycles from one of a
+// warp's instructions to its next, with four warps to a scheduler, fixed latencies take 1.4, shared memory and the special
+// functions 1.0, the other warps' turns 0.9, global loads 0.8, the arithmetic pipe 0.6 and barriers 0.4.
 //
 // The next tiles' inputs arrive by tiled copies (a ring of stages) while a tile is worked on: with one tile per CTA
 // loaded into registers, its loads, arithmetic and stores took their times one after another (242 us for the
