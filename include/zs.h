@@ -637,12 +637,12 @@ int zs_zero3_step(zs_plan_t plan, void* shards, float* master, float* m, float* 
  *
  * bf16 matrices are given by a 2-byte aligned pointer and the elements between
  * rows (>= cols): views into flat parameter and gradient buffers at any
- * element.  The norm's passes and gate forward move 32 bytes per access where the pointers
- * and row distances of all their bf16 matrices are multiples of 32 bytes, and
- * shifted 16-byte pieces elsewhere; encode and gate backward use tiled copies
- * where they are multiples of 16 bytes, and shifted pieces elsewhere; decode
- * and the product's result move 16 bytes or more where they are multiples of
- * 16 bytes, and single elements elsewhere.  Sums are fp32.
+ * element.  The norm's passes and gate forward move 32 bytes per access where
+ * the pointers and row distances of all their bf16 matrices are multiples of
+ * 32 bytes, and shifted 16-byte pieces elsewhere; encode and gate backward use
+ * tiled copies where they are multiples of 16 bytes, and shifted pieces
+ * elsewhere; decode and the product's result move 16 bytes or more where they
+ * are multiples of 16 bytes, and single elements elsewhere.  Sums are fp32.
  * rows and cols are at most 2^31 - 256; cols >= 1; rows = 0 is an empty matrix
  * (nothing is read or written unless a call says so).  Inputs and outputs must
  * not overlap unless a call says so.  The calls only enqueue work on `stream`,
