@@ -35,6 +35,7 @@ ZS_LAYOUT_FSDP1, ZS_LAYOUT_FSDP2 = 0, 1
 ZS_DEVERR_NONE, ZS_DEVERR_PRODUCER_WAIT, ZS_DEVERR_CONSUMER_WAIT, ZS_DEVERR_SELFTEST = 0, 1, 2, 3
 ZS_DEVERR_GATHER_WAIT, ZS_DEVERR_MATMUL_WAIT, ZS_DEVERR_TILE_WAIT = 4, 5, 6
 ZS_Q8_BLOCK, ZS_Q8_MAX_PARTIALS = 128, 608
+ZS_MAX_CHOICES, ZS_MAX_EXPERTS, ZS_MAX_EXPERT_ALIGN, ZS_STATE_BLOCK = 32, 1024, 65536, 256
 
 c_i32, c_i64, c_f32, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 P_i64 = ctypes.POINTER(c_i64)
@@ -53,6 +54,11 @@ class zs_adamw_hparams(ctypes.Structure):
 
 class zs_q8(ctypes.Structure):
     _fields_ = [("codes", c_vp), ("scales", c_vp), ("ld", c_i64), ("ld_scales", c_i64)]
+
+
+class zs_tensor(ctypes.Structure):
+    _fields_ = [("n", c_i64), ("grad", c_vp), ("master", c_vp), ("param", c_vp), ("m", c_vp), ("v", c_vp),
+                ("m_scale", c_vp), ("v_scale", c_vp), ("no_decay", c_i32), ("reserved", c_i32)]
 
 
 def _sig(name, args, res=c_i32):
@@ -122,6 +128,15 @@ _sig("zs_rmsnorm_backward", [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c
                              c_f32, c_i32, c_vp, c_i64, c_vp])
 _sig("zs_swiglu_q8", [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp])
 _sig("zs_swiglu_backward_q8", [c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp])
+_sig("zs_expert_sort", [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp])
+_sig("zs_expert_dispatch", [c_vp, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_i32, c_i64, c_vp, c_vp, c_i64, c_vp])
+_sig("zs_expert_combine", [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp])
+_sig("zs_expert_combine_backward", [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_i32,
+                                    c_vp, c_vp, c_i64, c_vp, c_vp])
+_sig("zs_q8_matmul_experts", [c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_i64, c_vp])
+_sig("zs_q8_matmul_experts_grad", [c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_i64, c_vp])
+_sig("zs_adamw_tensors", [c_vp, c_i32, c_i32, c_i32, ctypes.POINTER(zs_adamw_hparams), c_i64, c_vp, ctypes.c_uint32, c_vp])
+_sig("zs_grad_norm", [c_vp, c_i32, c_i32, c_f32, c_vp, c_i64, c_vp, c_vp])
 
 EXPORTED = [
     "zs_plan_create", "zs_plan_destroy", "zs_plan_info", "zs_plan_unit", "zs_plan_bucket",
@@ -135,7 +150,8 @@ EXPORTED = [
     "zs_fsdp2_chunk_cat", "zs_fsdp2_copy_out", "zs_fused_step_buckets", "zs_set_dependent_launch",
     "zs_rank_shard_step", "zs_fused_step_accumulate", "zs_q8_encode", "zs_q8_decode", "zs_q8_transpose",
     "zs_q8_matmul", "zs_rmsnorm_q8", "zs_rmsnorm_backward", "zs_swiglu_q8", "zs_swiglu_backward_q8",
-    "zs_set_q8_wait_limit",
+    "zs_set_q8_wait_limit", "zs_expert_sort", "zs_expert_dispatch", "zs_expert_combine", "zs_expert_combine_backward",
+    "zs_q8_matmul_experts", "zs_q8_matmul_experts_grad", "zs_adamw_tensors", "zs_grad_norm",
 ]
 
 
@@ -852,6 +868,222 @@ def zs_swiglu_backward_q8(dh, gate_q, up_q, dgate=None, dup=None, dgate_t=None, 
         _q8(dup_t, cols, rows, "dup_t", dev), _q8(h_t, cols, rows, "h_t", dev), _here(stream, dev)))
 
 
+# ------------------------------------------------------------------ experts
+#
+# Integer tensors (row_of [tokens, choices], starts [n_experts + 1], counts [n_experts]) are int32 and contiguous.
+
+if _torch is not None:
+    _I32 = _torch.int32
+
+
+def expert_rows(tokens, choices, n_experts, align=1):
+    """Rows that hold every choice of every token, each expert's from a multiple of align on."""
+    pairs = tokens * choices
+    return (pairs + min(n_experts, pairs) * (align - 1) + align - 1) // align * align
+
+
+def _ints(x, shape, what, dev):
+    if x.dtype is _I32 and x.get_device() == dev and x.shape == shape and x.is_contiguous():
+        return x.data_ptr()
+    _elsewhere(x, dev, what)
+    raise ValueError("%s must be %s contiguous elements of torch.int32 on the GPU" % (what, " x ".join(map(str, shape))))
+
+
+def _weights(x, shape, what, dev):
+    if x is None or (x.dtype is _F32 and x.get_device() == dev and x.shape == shape and x.is_contiguous()):
+        return None if x is None else x.data_ptr()
+    _elsewhere(x, dev, what)
+    raise ValueError("%s must be %d x %d contiguous elements of torch.float32 on the GPU" % (what, *shape))
+
+
+def _places(row_of, starts, counts, tokens, dev):
+    """Addresses and sizes that a sort's results are passed with."""
+    choices, experts = _shape(row_of, "row_of")[1], counts.numel()
+    return (_ints(row_of, (tokens, choices), "row_of", dev), choices, _ints(starts, (experts + 1,), "starts", dev),
+            _ints(counts, (experts,), "counts", dev), experts)
+
+
+def zs_expert_sort(ids, align, row_of, starts, counts, stream=None):
+    """Rows of the choices ids (int32 or int64 [tokens, choices]; out of 0 .. n_experts - 1: dropped) into row_of,
+    the experts' first rows (multiples of align) into starts, their choices into counts."""
+    dev = _device()
+    shape = tokens, choices = _shape(ids, "ids")
+    _elsewhere(ids, dev, "ids")
+    if ids.dtype not in (_I32, _torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous elements of torch.int32 or torch.int64")
+    experts = counts.numel()
+    return _check(_lib.zs_expert_sort(ids.data_ptr(), ids.element_size(), tokens, choices, experts, int(align),
+                                      _ints(row_of, shape, "row_of", dev), _ints(starts, (experts + 1,), "starts", dev),
+                                      _ints(counts, (experts,), "counts", dev), _here(stream, dev)))
+
+
+def _rows_of(q, b, what):
+    """Rows of an 8-bit pair or a bf16 matrix of which one at least is given."""
+    if q is None and b is None:
+        raise ValueError("%s: neither the 8-bit nor the bf16 matrix is given" % what)
+    return _shape(q[0] if q is not None else b, what)[0]
+
+
+def zs_expert_dispatch(x, row_of, starts, counts, y=None, y_bf16=None, stream=None):
+    """x (bf16 [tokens, cols]) to the rows of its choices: y in 8 bits, y_bf16 as it is, zeros in rows without a token."""
+    dev = _device()
+    shape = tokens, cols = _shape(x, "x")
+    rows = _rows_of(y, y_bf16, "y")
+    px, ldx = _bf16(x, shape, "x", dev)
+    po, choices, ps, pc, experts = _places(row_of, starts, counts, tokens, dev)
+    pb, ldb = (None, 0) if y_bf16 is None else _bf16(y_bf16, (rows, cols), "y_bf16", dev)
+    return _check(_lib.zs_expert_dispatch(px, ldx, tokens, cols, po, choices, ps, pc, experts, rows, _q8(y, rows, cols, "y", dev), pb, ldb,
+                                          _here(stream, dev)))
+
+
+def zs_expert_combine(y, row_of, weights, out, residual=None, stream=None):
+    """out (bf16 [tokens, cols]) = residual + the weighted rows of y (bf16 [rows, cols]); weights None: 1."""
+    dev = _device()
+    shape = tokens, cols = _shape(out, "out")
+    rows = _shape(y, "y")[0]
+    py, ldy = _bf16(y, (rows, cols), "y", dev)
+    choices = _shape(row_of, "row_of")[1]
+    pr, ldr = (None, 0) if residual is None else _bf16(residual, shape, "residual", dev)
+    po, ldo = _bf16(out, shape, "out", dev)
+    return _check(_lib.zs_expert_combine(py, ldy, rows, cols, _ints(row_of, (tokens, choices), "row_of", dev),
+                                         _weights(weights, (tokens, choices), "weights", dev), tokens, choices, pr, ldr, po, ldo,
+                                         _here(stream, dev)))
+
+
+def zs_expert_combine_backward(dout, y, row_of, weights, starts, counts, dweights=None, dy=None, dy_bf16=None, stream=None):
+    """Backward pass of zs_expert_combine: the rows' gradients in 8 bits (dy) and as bf16 (dy_bf16), the weights'
+    (dweights, for which y is read; else it may be None)."""
+    dev = _device()
+    shape = tokens, cols = _shape(dout, "dout")
+    rows = _shape(y, "y")[0] if y is not None else _rows_of(dy, dy_bf16, "dy")
+    pd, ldd = _bf16(dout, shape, "dout", dev)
+    py, ldy = (None, 0) if y is None else _bf16(y, (rows, cols), "y", dev)
+    po, choices, ps, pc, experts = _places(row_of, starts, counts, tokens, dev)
+    pb, ldb = (None, 0) if dy_bf16 is None else _bf16(dy_bf16, (rows, cols), "dy_bf16", dev)
+    return _check(_lib.zs_expert_combine_backward(
+        pd, ldd, py, ldy, rows, cols, po, _weights(weights, (tokens, choices), "weights", dev), tokens, choices, ps, pc, experts,
+        _q8(dy, rows, cols, "dy", dev), pb, ldb, _weights(dweights, (tokens, choices), "dweights", dev), _here(stream, dev)))
+
+
+def zs_q8_matmul_experts(a, b, starts, out, scale=1.0, first=True, stream=None):
+    """Rows starts[e] .. starts[e + 1] of out (bf16 [m, n]) = (0 if first else out) + scale * those of a ([m, k]) times the
+    transpose of expert e's rows of b ([n_experts * n, k])."""
+    dev = _device()
+    shape = m, n = _shape(out, "out")
+    k, experts = _shape(a[0], "a")[1], starts.numel() - 1
+    p, ld = _bf16(out, shape, "out", dev)
+    return _check(_lib.zs_q8_matmul_experts(_q8(a, m, k, "a", dev), _q8(b, experts * n, k, "b", dev), _ints(starts, (experts + 1,), "starts", dev),
+                                            experts, m, n, k, scale, 1 if first else 0, p, ld, _here(stream, dev)))
+
+
+def zs_q8_matmul_experts_grad(a, b, starts, out, scale=1.0, first=True, stream=None):
+    """Expert e's m rows of out (bf16 [n_experts * m, n]) = (0 if first else out) + scale * the product of columns
+    starts[e] .. starts[e + 1] (multiples of 128) of a ([m, k]) and b ([n, k])."""
+    dev = _device()
+    shape = rows, n = _shape(out, "out")
+    (m, k), experts = _shape(a[0], "a"), starts.numel() - 1
+    if rows != experts * m:
+        raise ValueError("out must be %d x %d, not %s" % (experts * m, n, tuple(out.shape)))
+    p, ld = _bf16(out, shape, "out", dev)
+    return _check(_lib.zs_q8_matmul_experts_grad(_q8(a, m, k, "a", dev), _q8(b, n, k, "b", dev), _ints(starts, (experts + 1,), "starts", dev),
+                                                 experts, m, n, k, scale, 1 if first else 0, p, ld, _here(stream, dev)))
+
+
+# ------------------------------------------------------------------ many tensors at once
+
+def state_zeros(n, device="cuda"):
+    """An optimizer state of n elements in 8 bits before the first step: (codes, scales)."""
+    codes = _torch.zeros(n, dtype=_torch.uint8, device=device).view(_torch.float8_e4m3fn)
+    return codes, _torch.zeros((n + ZS_STATE_BLOCK - 1) // ZS_STATE_BLOCK, device=device)
+
+
+class TensorList:
+    """Tensors that are stepped together, checked once: contiguous CUDA tensors of one device, per tensor its
+    gradient (all bf16 or all fp32), fp32 master, m and v (fp32; with m_scales and v_scales, codes of one byte), and bf16
+    param where wanted.  no_decay: per tensor, whether weight decay is left out.  The list holds the tensors; set_grads
+    gives it other gradients of the same sizes."""
+
+    def __init__(self, grads, master, m, v, params=None, m_scales=None, v_scales=None, no_decay=None):
+        count = len(grads)
+        if (m_scales is None) != (v_scales is None):
+            raise ValueError("m_scales and v_scales belong together")
+        self.state_bits = 32 if m_scales is None else 8
+        lists = {"grads": grads, "master": master, "m": m, "v": v, "params": params, "m_scales": m_scales, "v_scales": v_scales,
+                 "no_decay": no_decay}
+        for name, xs in lists.items():
+            if xs is not None and len(xs) != count:
+                raise ValueError("%s holds %d tensors, grads %d" % (name, len(xs), count))
+        self.device = grads[0].get_device() if count else None
+        self._held = [list(xs) for xs in (master, m, v, params or [], m_scales or [], v_scales or [])]
+        self._array = (zs_tensor * max(count, 1))()
+        state = _CODES if self.state_bits == 8 else (_F32,)
+        self._sizes = [g.numel() for g in grads]
+        for i, n in enumerate(self._sizes):
+            t = self._array[i]
+            t.n = n
+            blocks = (n + ZS_STATE_BLOCK - 1) // ZS_STATE_BLOCK
+            t.master = self._tensor(master[i], n, (_F32,), ("master", i))
+            t.m = self._tensor(m[i], n, state, ("m", i))
+            t.v = self._tensor(v[i], n, state, ("v", i))
+            if params is not None and params[i] is not None:
+                t.param = self._tensor(params[i], n, (_BF16,), ("params", i))
+            if self.state_bits == 8:
+                t.m_scale = self._tensor(m_scales[i], blocks, (_F32,), ("m_scales", i))
+                t.v_scale = self._tensor(v_scales[i], blocks, (_F32,), ("v_scales", i))
+            t.no_decay = 1 if no_decay is not None and no_decay[i] else 0
+        self.set_grads(grads)
+
+    def __len__(self):
+        return len(self._sizes)
+
+    def _tensor(self, x, n, dtypes, what):
+        if x.dtype not in dtypes:
+            raise ValueError("%s must be %s, not %s" % (_name(what), " or ".join(str(d) for d in dtypes), x.dtype))
+        _elsewhere(x, self.device, _name(what))
+        if not x.is_contiguous():
+            raise ValueError("%s must be contiguous" % _name(what))
+        if x.numel() != n:
+            raise ValueError("%s must hold %d elements, not %d" % (_name(what), n, x.numel()))
+        return x.data_ptr()
+
+    def set_grads(self, grads):
+        if len(grads) != len(self._sizes):
+            raise ValueError("grads holds %d tensors, not %d" % (len(grads), len(self._sizes)))
+        dtype = grads[0].dtype if len(grads) else _BF16
+        if dtype not in (_BF16, _F32):
+            raise ValueError("grads must be torch.bfloat16 or torch.float32, not %s" % dtype)
+        at = [self._tensor(g, n, (dtype,), ("grads", i)) for i, (g, n) in enumerate(zip(grads, self._sizes))]
+        for t, p in zip(self._array, at):
+            t.grad = p
+        self.grad_bytes = dtype.itemsize
+        self._grads = list(grads)
+
+
+def _list_here(tensors):
+    """The current device, which a list's tensors have to be on."""
+    dev = _device()
+    if len(tensors) and tensors.device != dev:
+        raise ValueError("the tensors are on cuda:%s and the current device is cuda:%s" % (tensors.device, dev))
+    return dev
+
+
+def zs_adamw_tensors(tensors, hp, step, factor=None, seed=0, stream=None):
+    """One AdamW step on a TensorList.  factor: one fp32 value on the GPU that multiplies the gradients (NaN: no step
+    is taken); seed: of the 8-bit states' roundings (32 bits of it count), another one for every step."""
+    dev = _list_here(tensors)
+    return _check(_lib.zs_adamw_tensors(tensors._array, len(tensors), tensors.grad_bytes, tensors.state_bits, ctypes.byref(_hp(hp)), int(step),
+                                        _vector(factor, 1, _F32, "factor", dev), int(seed) & 0xffffffff, _here(stream, dev)))
+
+
+def zs_grad_norm(tensors, max_norm, partials, out, stream=None):
+    """The norm of a TensorList's gradients into out[0], the factor that clips it to max_norm into out[1] (fp32 [2]);
+    partials: fp32 scratch of any size."""
+    dev = _list_here(tensors)
+    return _check(_lib.zs_grad_norm(tensors._array, len(tensors), tensors.grad_bytes, float(max_norm),
+                                    _vector(partials, partials.numel(), _F32, "partials", dev), partials.numel(),
+                                    _vector(out, 2, _F32, "out", dev), _here(stream, dev)))
+
+
 # the plan's calls are Plan's methods
-__all__ = ["Plan", "ZsError", "zs_adamw_hparams", "zs_q8", "q8_empty", "LIB_PATH"] + [
+__all__ = ["Plan", "ZsError", "zs_adamw_hparams", "zs_q8", "q8_empty", "zs_tensor", "TensorList", "state_zeros", "expert_rows", "LIB_PATH"] + [
     n for n in dir() if n in EXPORTED or n.startswith("ZS_")]

@@ -1,0 +1,517 @@
+// Tokens to their experts' rows and back: sorted by expert, written there in 8 bits (or bf16), and brought back
+// weighted, with the gradients.  All of it moves bytes: a token's row is read once however many experts it goes to, and
+// an expert's row once.
+#include "q8_rows.cuh"
+
+namespace zs {
+
+namespace {
+
+// ------------------------------------------------------------------ sorting
+
+// A stable counting sort in one launch.  The pairs (token, choice) are cut into segments, one per warp of a cluster's
+// CTAs.  First pass: a warp counts its segment's pairs per expert, 32 at a time (the lanes of equal experts find each
+// other with one match instruction, so a counter has one writer and the order of the pairs is kept).  The counters
+// are summed over the warps, and over the cluster's CTAs through distributed shared memory; the second pass goes
+// through the segment again and gives each pair its place.  No atomics, no workspace: the same rows every time.
+constexpr int kSortWarps = 32;
+constexpr int kSortBatch = 8;        // ids per lane read at once
+
+struct SortArgs {
+    const void* ids;
+    int n, experts, align;
+    int seg;                         // pairs per warp, a multiple of 32
+    int *row_of, *starts, *counts;
+};
+
+template <typename ID>
+__global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_constant__ SortArgs a) {
+    extern __shared__ int sort_sh[];
+    const int E = a.experts;
+    int* hist = sort_sh;                         // [warp][expert]
+    int* total = hist + kSortWarps * E;          // this CTA's pairs per expert (read by the whole cluster)
+    int* first = total + E;                      // where this CTA's pairs of an expert go
+    __shared__ int scan[kSortWarps];
+    uint32_t rank, ctas;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kSortWarps * E; i += blockDim.x) hist[i] = 0;
+    dependent_launch_prologue();
+    __syncthreads();
+    const int64_t lo = (int64_t)(rank * kSortWarps + warp) * a.seg;
+    const int64_t hi = lo + a.seg < a.n ? lo + a.seg : a.n;
+    const ID* ids = static_cast<const ID*>(a.ids);
+    int* mine = hist + warp * E;
+    // f(pair, expert or -1, the lanes with the same expert) for every pair of the segment, in order
+    auto each = [&](auto f) {
+        for (int64_t base = lo; base < hi; base += 32 * kSortBatch) {
+            int id[kSortBatch];
+#pragma unroll
+            for (int j = 0; j < kSortBatch; ++j) {
+                const int64_t i = base + 32 * j + lane;
+                const ID x = i < hi ? ids[i] : (ID)-1;
+                id[j] = x >= 0 && x < (ID)E ? (int)x : -1;
+            }
+#pragma unroll
+            for (int j = 0; j < kSortBatch; ++j) {
+                if (base + 32 * j >= hi) break;
+                f(base + 32 * j + lane, id[j], __match_any_sync(~0u, id[j]));
+                __syncwarp();
+            }
+        }
+    };
+    each([&](int64_t, int id, uint32_t same) {
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+    });
+    __syncthreads();
+    const int e = threadIdx.x;                   // at most as many experts as threads
+    if (e < E) {
+        int sum = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int x = hist[w * E + e];
+            hist[w * E + e] = sum;
+            sum += x;
+        }
+        total[e] = sum;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    int before = 0, all = 0;
+    if (e < E) {
+        for (uint32_t c = 0; c < ctas; ++c) {
+            uint32_t at;
+            int x;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(su32(total + e)), "r"(c));
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+            before += c < rank ? x : 0;
+            all += x;
+        }
+    }
+    const int padded = (all + a.align - 1) / a.align * a.align;
+    int upto = padded;                           // sum over the experts up to this one
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int x = __shfl_up_sync(~0u, upto, k);
+        if (lane >= k) upto += x;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    if (warp == 0) {
+        int x = scan[lane];
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, k);
+            if (lane >= k) x += y;
+        }
+        scan[lane] = x;
+    }
+    __syncthreads();
+    if (warp > 0) upto += scan[warp - 1];
+    if (e < E) {
+        first[e] = upto - padded + before;
+        if (rank == 0) {
+            a.starts[e] = upto - padded;
+            a.counts[e] = all;
+            if (e == E - 1) a.starts[E] = upto;
+        }
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");       // the other CTAs' totals are read
+    each([&](int64_t i, int id, uint32_t same) {
+        const int at = id >= 0 ? mine[id] : 0;
+        __syncwarp();
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] = at + __popc(same);
+        if (i < hi) a.row_of[i] = id >= 0 ? first[id] + at + __popc(same & ((1u << lane) - 1)) : -1;
+    });
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");         // nobody reads this CTA's any more
+}
+
+// ------------------------------------------------------------------ to the experts
+
+// Rows [starts[e] + counts[e], starts[e + 1]) hold no token: zeros, for a later sum over an expert's rows.  kPadWarps
+// warps share an expert's.
+constexpr int kPadWarps = 16;
+
+struct Rows {
+    const int *row_of, *starts, *counts;
+    int64_t tokens, rows, cols;
+    int choices, experts, chunks;    // chunks of 512 columns
+    Q8 y;                            // either may be missing
+    uint16_t* y16;
+    int64_t ldy16;
+};
+
+template <bool WIDE>
+__device__ __forceinline__ void zero_padding(const Rows& a, int64_t warp, int64_t warps) {
+    const int lane = threadIdx.x & 31;
+    const V16 zero = {};
+    for (int64_t u = warp; u < (int64_t)a.experts * kPadWarps; u += warps) {
+        const int e = (int)(u / kPadWarps);
+        int64_t lo = (int64_t)a.starts[e] + a.counts[e], hi = a.starts[e + 1];
+        if (lo < 0) lo = 0;
+        if (hi > a.rows) hi = a.rows;
+        for (int64_t r = lo + u % kPadWarps; r < hi; r += kPadWarps)
+            for (int64_t c = lane * 16; c - lane * 16 < a.cols; c += 512) {
+                if (a.y.codes) store_code16(make_uint4(0, 0, 0, 0), 0, a.cols - c, a.y, r, c);
+                if (a.y16) store16<WIDE>(a.y16 + r * a.ldy16 + c, zero, a.cols - c);
+            }
+    }
+}
+
+// The row of choice j of a token, from the lane that holds it; -1 where there is none inside the matrix.
+__device__ __forceinline__ int64_t row_at(int held, int j, int64_t rows) {
+    const int r = __shfl_sync(~0u, held, j);
+    return r >= 0 && r < rows ? r : -1;
+}
+
+struct DispatchArgs {
+    Rows r;
+    const uint16_t* x;
+    int64_t ldx;
+};
+
+// A warp takes 512 columns of a token: read, encoded once, and written to every row that the token goes to.
+template <bool WIDE>
+__global__ void __launch_bounds__(256) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
+    dependent_launch_prologue();
+    const int64_t warp = gtid() >> 5, warps = gstride() >> 5;
+    const int lane = threadIdx.x & 31;
+    const Span sx = span_of(a.x, a.ldx, a.r.tokens, a.r.cols);
+    for (int64_t u = warp; u < a.r.tokens * a.r.chunks; u += warps) {
+        const int64_t t = u / a.r.chunks, c = (u - t * a.r.chunks) * 512 + lane * 16, n = a.r.cols - c;
+        const V16 v = load16<WIDE>(a.x + t * a.ldx + c, n, sx);
+        const int held = lane < a.r.choices ? a.r.row_of[t * a.r.choices + lane] : -1;
+        uint32_t byte = 0;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (a.r.y.codes) {
+            float2 f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = pair_of(v.w[i]);
+            w = code16(f, byte);
+        }
+        for (int j = 0; j < a.r.choices; ++j) {
+            const int64_t row = row_at(held, j, a.r.rows);
+            if (row < 0) continue;
+            if (a.r.y.codes) store_code16(w, byte, n, a.r.y, row, c);
+            if (a.r.y16) store16<WIDE>(a.r.y16 + row * a.r.ldy16 + c, v, n);
+        }
+    }
+    zero_padding<WIDE>(a.r, warp, warps);
+}
+
+// ------------------------------------------------------------------ back to the tokens
+
+constexpr int kAtOnce = 4;           // rows of a token read at once
+
+struct CombineArgs {
+    const uint16_t *y, *residual;
+    int64_t ldy, ldr, ldo, rows, cols, tokens;
+    const int* row_of;
+    const float* weights;            // nullptr: 1
+    int choices, chunks;
+    uint16_t* out;
+};
+
+// A warp takes 512 columns of a token: residual + sum of weight * row in the order of the choices, in fp32.
+template <bool WIDE>
+__global__ void __launch_bounds__(256) k_expert_combine(const __grid_constant__ CombineArgs a) {
+    dependent_launch_prologue();
+    const int64_t warp = gtid() >> 5, warps = gstride() >> 5;
+    const int lane = threadIdx.x & 31;
+    const Span sy = span_of(a.y, a.ldy, a.rows, a.cols), sr = span_of(a.residual, a.ldr, a.tokens, a.cols);
+    for (int64_t u = warp; u < a.tokens * a.chunks; u += warps) {
+        const int64_t t = u / a.chunks, c = (u - t * a.chunks) * 512 + lane * 16, n = a.cols - c;
+        const int held = lane < a.choices ? a.row_of[t * a.choices + lane] : -1;
+        const float weight = a.weights && lane < a.choices ? a.weights[t * a.choices + lane] : 1.f;
+        float2 f[8];
+        V16 v = {};
+        if (a.residual) v = load16<WIDE>(a.residual + t * a.ldr + c, n, sr);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = pair_of(v.w[i]);
+        for (int j0 = 0; j0 < a.choices; j0 += kAtOnce) {
+            V16 y[kAtOnce];
+            bool live[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int64_t row = j0 + j < a.choices ? row_at(held, j0 + j, a.rows) : -1;
+                live[j] = row >= 0;
+                if (live[j]) y[j] = load16<WIDE>(a.y + row * a.ldy + c, n, sy);
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const float w = __shfl_sync(~0u, weight, (j0 + j) & 31);
+                if (!live[j]) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = q8_fma2(pair_of(y[j].w[i]), make_float2(w, w), f[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(f[i].x, f[i].y);
+        store16<WIDE>(a.out + t * a.ldo + c, v, n);
+    }
+}
+
+struct CombineBackArgs {
+    Rows r;
+    const uint16_t *dout, *y;
+    int64_t lddout, ldy;
+    const float* weights;            // nullptr: 1
+    float* dweights;                 // nullptr: not wanted
+};
+
+constexpr int kMaxChoices = ZS_MAX_CHOICES;
+constexpr int kBackWarps = 8;        // at most, per token
+
+// A CTA takes a token, a warp of it 512 columns at a time.  The gradient row is read once; the largest magnitude of its
+// blocks serves every choice, as |weight| times it is the largest of the weighted ones (rounding keeps their order).
+template <bool WIDE>
+__global__ void __launch_bounds__(32 * kBackWarps) k_expert_combine_backward(const __grid_constant__ CombineBackArgs a) {
+    __shared__ float dots[2][kBackWarps][kMaxChoices];
+    dependent_launch_prologue();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = blockDim.x >> 5;
+    const Span sd = span_of(a.dout, a.lddout, a.r.tokens, a.r.cols), sy = span_of(a.y, a.ldy, a.r.rows, a.r.cols);
+    const int K = a.r.choices;
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < a.r.tokens; t += gridDim.x, turn ^= 1) {
+        const int held = lane < K ? a.r.row_of[t * K + lane] : -1;
+        const float weight = a.weights && lane < K ? a.weights[t * K + lane] : 1.f;
+        float* dot = dots[turn][warp];
+        if (lane < K) dot[lane] = 0.f;
+        __syncwarp();
+        for (int ch = warp; ch < a.r.chunks; ch += group) {
+            const int64_t c = (int64_t)ch * 512 + lane * 16, n = a.r.cols - c;
+            const V16 d = load16<WIDE>(a.dout + t * a.lddout + c, n, sd);
+            float2 f[8];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] = pair_of(d.w[i]);
+                top = q8_top2(top, f[i]);
+            }
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+            for (int j0 = 0; j0 < K; j0 += kAtOnce) {
+                V16 y[kAtOnce];
+                int64_t row[kAtOnce];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    row[j] = j0 + j < K ? row_at(held, j0 + j, a.r.rows) : -1;
+                    if (a.dweights && row[j] >= 0) y[j] = load16<WIDE>(a.y + row[j] * a.ldy + c, n, sy);
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const float w = __shfl_sync(~0u, weight, (j0 + j) & 31);
+                    if (row[j] < 0) continue;
+                    if (a.dweights) {
+                        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s = q8_fma2(f[i], pair_of(y[j].w[i]), s);
+                        float sum = s.x + s.y;
+#pragma unroll
+                        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+                        if (lane == 0) dot[j0 + j] += sum;
+                    }
+                    float2 g[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = q8_mul2(f[i], make_float2(w, w));
+                    if (a.r.y16) {
+                        V16 v;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(g[i].x, g[i].y);
+                        store16<WIDE>(a.r.y16 + row[j] * a.r.ldy16 + c, v, n);
+                    }
+                    if (a.r.y.codes) {
+                        const float most = top * fabsf(w);
+                        uint32_t byte;
+                        uint4 x;
+                        if (__any_sync(~0u, !(most < __int_as_float(0x7f800000)))) {
+                            x = code16(g, byte);         // infinities or NaN: found value by value
+                        } else {
+                            byte = q8_scale_byte(most);
+                            const float2 inv = make_float2(q8_inverse(byte), q8_inverse(byte));
+                            uint32_t q[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 p = q8_mul2(g[2 * k], inv), s = q8_mul2(g[2 * k + 1], inv);
+                                q[k] = q8_pack4(p.x, p.y, s.x, s.y);
+                            }
+                            x = make_uint4(q[0], q[1], q[2], q[3]);
+                        }
+                        store_code16(x, byte, n, a.r.y, row[j], c);
+                    }
+                }
+            }
+        }
+        if (a.dweights) {
+            __syncthreads();                     // the other of the two sums is free until the next token's barrier
+            if (threadIdx.x < K) {
+                float sum = 0.f;
+                for (int w = 0; w < group; ++w) sum += dots[turn][w][threadIdx.x];
+                a.dweights[t * K + threadIdx.x] = sum;
+            }
+        }
+    }
+    zero_padding<WIDE>(a.r, gtid() >> 5, gstride() >> 5);
+}
+
+// ------------------------------------------------------------------ host
+
+using q8_host::fail;
+
+int check_ints(const char* fn, const char* name, const void* p, bool needed) {
+    if (!p && needed) return fail(fn, std::string(name) + " is NULL");
+    if ((uintptr_t)p & 3) return fail(fn, std::string(name) + " is not 4-byte aligned");
+    return ZS_OK;
+}
+
+int check_routes(const char* fn, int64_t tokens, int32_t choices, int32_t experts) {
+    ZS_Q8_TRY(q8_host::check_dim(fn, "tokens", tokens, 0));
+    if (choices < 1 || choices > ZS_MAX_CHOICES) return fail(fn, "choices out of range");
+    if (experts < 1 || experts > ZS_MAX_EXPERTS) return fail(fn, "n_experts out of range");
+    return ZS_OK;
+}
+
+// CTAs of a grid whose `warps` warps of work are taken in turn, `per` to a CTA.
+unsigned grid_for(int64_t warps, int per, int resident) {
+    const int64_t ctas = (warps + per - 1) / per, most = (int64_t)q8_host::sm_count() * resident;
+    return (unsigned)(ctas < 1 ? 1 : ctas < most ? ctas : most);
+}
+
+}  // namespace
+
+}  // namespace zs
+
+using namespace zs::q8_host;
+
+extern "C" int zs_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t choices, int32_t n_experts, int32_t align,
+                              int32_t* row_of, int32_t* starts, int32_t* counts, void* stream) {
+    static const char* fn = "zs_expert_sort";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    ZS_Q8_TRY(zs::check_routes(fn, tokens, choices, n_experts));
+    if (id_bytes != 4 && id_bytes != 8) return fail(fn, "id_bytes must be 4 or 8");
+    const int64_t n = tokens * choices;
+    if (align < 1 || align > ZS_MAX_EXPERT_ALIGN) return fail(fn, "align out of range");
+    if (n + (int64_t)n_experts * (align - 1) > kMaxDim) return fail(fn, "the experts' rows pass 2^31 - 256");
+    if (!ids && n > 0) return fail(fn, "ids is NULL");
+    if ((uintptr_t)ids & (id_bytes - 1)) return fail(fn, "ids is not aligned to its elements");
+    ZS_Q8_TRY(zs::check_ints(fn, "row_of", row_of, n > 0));
+    ZS_Q8_TRY(zs::check_ints(fn, "starts", starts, true));
+    ZS_Q8_TRY(zs::check_ints(fn, "counts", counts, true));
+    zs::SortArgs a{ids, (int)n, n_experts, align, 0, row_of, starts, counts};
+    const int ctas = n <= 4096 ? 1 : 8;
+    a.seg = (int)((n + ctas * zs::kSortWarps * 32 - 1) / (ctas * zs::kSortWarps * 32) * 32);
+    const int smem = (zs::kSortWarps + 2) * n_experts * 4;
+    static std::atomic<uint64_t> ready32{0}, ready64{0};
+    const auto kern = id_bytes == 4 ? zs::k_expert_sort<int32_t> : zs::k_expert_sort<int64_t>;
+    ZS_Q8_TRY(cuda_status(fn, zs::ready_once(id_bytes == 4 ? ready32 : ready64, (const void*)kern,
+                                             (zs::kSortWarps + 2) * ZS_MAX_EXPERTS * 4)));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(zs::kSortWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = zs::dependent_launch() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) cudaGetLastError();
+    return cuda_status(fn, e);
+}
+
+namespace {
+
+// The places of the experts' rows and what goes there, as zs_expert_dispatch and zs_expert_combine_backward take them.
+int check_rows(const char* fn, const char* q_name, const char* b_name, const int32_t* row_of, int64_t tokens, int32_t choices,
+               const int32_t* starts, const int32_t* counts, int32_t n_experts, int64_t rows, int64_t cols, const zs_q8* q, void* b,
+               int64_t ldb, zs::Rows* out) {
+    ZS_Q8_TRY(zs::check_routes(fn, tokens, choices, n_experts));
+    ZS_Q8_TRY(check_dim(fn, "rows", rows, 0));
+    ZS_Q8_TRY(check_dim(fn, "cols", cols, 1));
+    ZS_Q8_TRY(zs::check_ints(fn, "row_of", row_of, tokens > 0));
+    ZS_Q8_TRY(zs::check_ints(fn, "starts", starts, true));
+    ZS_Q8_TRY(zs::check_ints(fn, "counts", counts, true));
+    *out = zs::Rows{row_of, starts, counts, tokens, rows, cols, choices, n_experts, (int)((cols + 511) / 512), {}, (uint16_t*)b, ldb};
+    ZS_Q8_TRY(check_q8(fn, q_name, q, rows, cols, true, &out->y));
+    if (b) ZS_Q8_TRY(check_bf16(fn, b_name, b, ldb, rows, cols));
+    return ZS_OK;
+}
+
+}  // namespace
+
+extern "C" int zs_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t cols, const int32_t* row_of, int32_t choices,
+                                  const int32_t* starts, const int32_t* counts, int32_t n_experts, int64_t rows, const zs_q8* y,
+                                  void* y_bf16, int64_t ldy, void* stream) {
+    static const char* fn = "zs_expert_dispatch";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    zs::DispatchArgs a{};
+    ZS_Q8_TRY(check_rows(fn, "y", "y_bf16", row_of, tokens, choices, starts, counts, n_experts, rows, cols, y, y_bf16, ldy, &a.r));
+    ZS_Q8_TRY(check_bf16(fn, "x", x, ldx, tokens, cols));
+    if (!y && !y_bf16) return fail(fn, "y and y_bf16 are both NULL");
+    if (tokens == 0 || rows == 0) return ZS_OK;
+    a.x = (const uint16_t*)x;
+    a.ldx = ldx;
+    const bool w = wide(x, ldx, 32) && (!y_bf16 || wide(y_bf16, ldy, 32));
+    int64_t work = tokens * a.r.chunks;
+    if (work < (int64_t)n_experts * zs::kPadWarps) work = (int64_t)n_experts * zs::kPadWarps;
+    return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_dispatch<true> : zs::k_expert_dispatch<false>,
+                                             dim3(zs::grid_for(work, 8, 8)), dim3(256), 0, (cudaStream_t)stream, a));
+}
+
+extern "C" int zs_expert_combine(const void* y, int64_t ldy, int64_t rows, int64_t cols, const int32_t* row_of, const float* weights,
+                                 int64_t tokens, int32_t choices, const void* residual, int64_t ldr, void* out, int64_t ldo,
+                                 void* stream) {
+    static const char* fn = "zs_expert_combine";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    ZS_Q8_TRY(zs::check_routes(fn, tokens, choices, 1));
+    ZS_Q8_TRY(check_dim(fn, "rows", rows, 0));
+    ZS_Q8_TRY(check_dim(fn, "cols", cols, 1));
+    ZS_Q8_TRY(check_bf16(fn, "y", y, ldy, rows, cols));
+    ZS_Q8_TRY(zs::check_ints(fn, "row_of", row_of, tokens > 0));
+    ZS_Q8_TRY(zs::check_ints(fn, "weights", weights, false));
+    if (residual) ZS_Q8_TRY(check_bf16(fn, "residual", residual, ldr, tokens, cols));
+    ZS_Q8_TRY(check_bf16(fn, "out", out, ldo, tokens, cols));
+    if (tokens == 0) return ZS_OK;
+    zs::CombineArgs a{(const uint16_t*)y, (const uint16_t*)residual, ldy, ldr, ldo, rows, cols, tokens, row_of, weights, choices,
+                      (int)((cols + 511) / 512), (uint16_t*)out};
+    const bool w = wide(y, ldy, 32) && (!residual || wide(residual, ldr, 32)) && wide(out, ldo, 32);
+    return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_combine<true> : zs::k_expert_combine<false>,
+                                             dim3(zs::grid_for(tokens * a.chunks, 8, 8)), dim3(256), 0, (cudaStream_t)stream, a));
+}
+
+extern "C" int zs_expert_combine_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int64_t rows, int64_t cols,
+                                          const int32_t* row_of, const float* weights, int64_t tokens, int32_t choices,
+                                          const int32_t* starts, const int32_t* counts, int32_t n_experts, const zs_q8* dy,
+                                          void* dy_bf16, int64_t lddy, float* dweights, void* stream) {
+    static const char* fn = "zs_expert_combine_backward";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    zs::CombineBackArgs a{};
+    ZS_Q8_TRY(check_rows(fn, "dy", "dy_bf16", row_of, tokens, choices, starts, counts, n_experts, rows, cols, dy, dy_bf16, lddy, &a.r));
+    ZS_Q8_TRY(check_bf16(fn, "dout", dout, lddout, tokens, cols));
+    ZS_Q8_TRY(zs::check_ints(fn, "weights", weights, false));
+    ZS_Q8_TRY(zs::check_ints(fn, "dweights", dweights, false));
+    if (!dy && !dy_bf16 && !dweights) return fail(fn, "dy, dy_bf16 and dweights are all NULL");
+    if (dweights) ZS_Q8_TRY(check_bf16(fn, "y", y, ldy, rows, cols));
+    if (tokens == 0) return ZS_OK;
+    a.dout = (const uint16_t*)dout;
+    a.lddout = lddout;
+    a.y = (const uint16_t*)y;
+    a.ldy = ldy;
+    a.weights = weights;
+    a.dweights = dweights;
+    const bool w = wide(dout, lddout, 32) && (!dweights || wide(y, ldy, 32)) && (!dy_bf16 || wide(dy_bf16, lddy, 32));
+    const int group = a.r.chunks < zs::kBackWarps ? a.r.chunks : zs::kBackWarps;
+    int64_t warps = tokens * group;
+    if (warps < (int64_t)n_experts * zs::kPadWarps) warps = (int64_t)n_experts * zs::kPadWarps;
+    return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_combine_backward<true> : zs::k_expert_combine_backward<false>,
+                                             dim3(zs::grid_for(warps, group, 32 / group)), dim3(32 * group), 0, (cudaStream_t)stream, a));
+}

@@ -238,6 +238,10 @@ struct MmArgs {
     int first;
     unsigned int* error;
     long long wait_limit;
+    const int* starts;           // of n_groups groups and the last one's end (the experts' products)
+    int n_groups;
+    int group_rows;              // rows of Q (kRowGroups) or of out (kSumGroups) that a group has
+    int most_tiles;              // of groups that do not overlap (kRowGroups)
 };
 
 // One row's scale bytes, kBatch groups of four blocks (16 bytes) at a time.  Rows of scales start at any
@@ -642,10 +646,19 @@ struct PairShape {
     static constexpr int kAccs = BN == 256 ? 1 : 2;
     static constexpr int kStageBytes = 128 * 128 + (BN / 2) * 128;
     static constexpr int kSmem = 1024 + kPairStages * kStageBytes + kPairSlots * kBatch * kPairScaleBytes + 8 * kStoreStage * 4 + 256;
+    static constexpr int kTable = (ZS_MAX_EXPERTS + 1) * 4;          // kRowGroups: the tiles before each group's
+    static_assert(kSmem + kTable <= 227 * 1024, "shared memory");
     static_assert(kAccs * BN + kScaleSets * kPairTmemScales <= 512, "tensor memory");
     static_assert(BN % 32 == 0 && (BN / 2) % 16 == 0, "halves of whole 16-column loads");
 };
 constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at about the same time
+
+// Products of groups in one launch, with the groups' places on the device: a group is an expert's rows.
+//   kRowGroups  P's rows starts[g] .. starts[g + 1] times the group's own group_rows rows of Q
+//   kSumGroups  the sum over columns starts[g] .. starts[g + 1] (multiples of 128) of both, one result per group
+// Starts out of range are read as the nearest inside; with overlapping groups (more tiles than there can be) nothing is
+// written, so that no tile lies outside.
+enum { kNoGroups = 0, kRowGroups = 1, kSumGroups = 2 };
 
 // What the barriers of a pair's CTA have been or will be sent by copies and products, each to its ring in turn.  A CTA
 // leaves only when all of it has arrived, after a wait that ran out as after the last tile: nothing may be under way
@@ -657,7 +670,20 @@ struct Sent {
     uint32_t sums;           // accumulators completed
 };
 
-template <int BN>
+// A pair's tile: its first rows of P and Q and where those that count end, its blocks of the sum, and its place in out.
+struct Tile {
+    int p0, q0, p_end, q_end;
+    int kb0, kbs;
+    int64_t out_row;             // row of out that P row 0 would have
+    int out_col;                 // Q row that column 0 of out has
+};
+// Start g of the groups, in order and in range.
+__device__ __forceinline__ int group_start(const MmArgs& a, int g, int most) {
+    const int x = a.starts[g];
+    return x < 0 ? 0 : x > most ? most : x;
+}
+
+template <int BN, int GROUPS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ MmArgs a) {
@@ -676,6 +702,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(settled + 1);
     uint32_t* gave_up = tmem_at + 1;             // set in both CTAs
     Sent* sent = reinterpret_cast<Sent*>(gave_up + 1);
+    int* before = reinterpret_cast<int*>(store_sh + 8 * kStoreStage) + 64;       // kRowGroups: tiles before each group's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();        // CTA 0 of the pair leads
     constexpr uint16_t kBoth = 3;
@@ -712,17 +739,70 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     wait_for_predecessor();
     const uint32_t tmem = *tmem_at, tmem_scales = tmem + kAccs * BN;
-    const int groups = (a.kblocks + 3) / 4;
     const int tiles_p = (int)(((int64_t)a.rows_p + 255) / 256);
-    const int64_t tiles = (int64_t)tiles_p * a.tiles_q;
+    int64_t tiles = (int64_t)tiles_p * a.tiles_q;
+    if constexpr (GROUPS == kSumGroups) tiles *= a.n_groups;
+    if constexpr (GROUPS == kRowGroups) {
+        // Tiles of the groups summed up: a thread adds a few neighbouring groups', the threads' sums are scanned.
+        const int each = (a.n_groups + kPairThreads - 1) / kPairThreads, g0 = threadIdx.x * each;
+        int64_t sum = 0;
+        for (int g = g0; g < g0 + each && g < a.n_groups; ++g) {
+            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
+            sum += hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
+        }
+        int64_t upto = sum;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, upto, k);
+            if (lane >= k) upto += x;
+        }
+        int64_t* warps = reinterpret_cast<int64_t*>(store_sh);
+        if (lane == 31) warps[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += warps[w];
+        int64_t at = upto - sum;
+        for (int g = g0; g < g0 + each && g < a.n_groups; ++g) {
+            before[g] = (int)at;
+            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
+            at += hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
+        }
+        if (threadIdx.x == kPairThreads - 1) before[a.n_groups] = upto <= a.most_tiles ? (int)upto : 0;
+        __syncthreads();
+        tiles = before[a.n_groups];
+    }
     const int64_t first_tile = blockIdx.x / 2, step = gridDim.x / 2;
     // the pair's tile t: kPairGroup P tiles at a time, within them Q tile by Q tile
-    auto place = [&](int64_t t, int& p0, int& q0) {
-        const int64_t per = (int64_t)kPairGroup * a.tiles_q;
-        const int g = (int)(t / per), in = (int)(t - g * per);
-        const int width = tiles_p - g * kPairGroup < kPairGroup ? tiles_p - g * kPairGroup : kPairGroup;
-        p0 = (g * kPairGroup + in % width) * 256;
-        q0 = (in / width) * BN;
+    auto place = [&](int64_t t) {
+        Tile x;
+        if constexpr (GROUPS == kRowGroups) {
+            int g = 0, past = a.n_groups;        // the last group with no more than t tiles before it
+            while (past - g > 1) {
+                const int mid = (g + past) >> 1;
+                if (before[mid] <= (int)t) g = mid;
+                else past = mid;
+            }
+            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
+            const int in = (int)t - before[g], high = (hi - lo + 255) / 256;
+            x = Tile{lo + in % high * 256, g * a.group_rows + in / high * BN, hi, (g + 1) * a.group_rows, 0, a.kblocks, 0, g * a.group_rows};
+        } else {
+            int g = 0;
+            if constexpr (GROUPS == kSumGroups) {
+                const int64_t per = (int64_t)tiles_p * a.tiles_q;
+                g = (int)(t / per);
+                t -= g * per;
+            }
+            const int64_t per = (int64_t)kPairGroup * a.tiles_q;
+            const int s = (int)(t / per), in = (int)(t - s * per);
+            const int width = tiles_p - s * kPairGroup < kPairGroup ? tiles_p - s * kPairGroup : kPairGroup;
+            x = Tile{(s * kPairGroup + in % width) * 256, (in / width) * BN, a.rows_p, a.rows_q, 0, a.kblocks, 0, 0};
+            if constexpr (GROUPS == kSumGroups) {
+                const int most = a.kblocks * 128, lo = group_start(a, g, most), hi = group_start(a, g + 1, most);
+                x.kb0 = lo / 128;
+                x.kbs = hi > lo ? (hi + 127) / 128 - x.kb0 : 0;
+                x.out_row = (int64_t)g * a.group_rows;
+            }
+        }
+        return x;
     };
     auto fail = [&] {
         cluster_st(at_rank(gave_up, 0), 1);
@@ -735,15 +815,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bool ok = true;
         const uint32_t full0 = at_rank(full, 0);
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
-            int p0, q0;
-            place(t, p0, q0);
-            for (int kb = 0; kb < a.kblocks; ++kb) {
+            const Tile x = place(t);
+            for (int kb = x.kb0; kb < x.kb0 + x.kbs; ++kb) {
                 if (ring.round > 0 && !(ok = warp_wait_or_look(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
                 uint8_t* at = base + ring.at * kStageBytes;
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kStageBytes);
-                    tma_load_pair(at, &map_p, kb * 128, p0 + (int)rank * 128, full0 + ring.at * 8);
-                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
+                    tma_load_pair(at, &map_p, kb * 128, x.p0 + (int)rank * 128, full0 + ring.at * 8);
+                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, x.q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
                 }
                 __syncwarp();
                 ring.next(kPairStages);
@@ -765,7 +844,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (acc.round > 0 && !(ok = warp_wait_cluster(acc_free + acc.at, acc.parity() ^ 1, a.wait_limit))) break;
             tc_fence_after();
             const uint32_t sums = tmem + acc.at * BN;
-            for (int kb = 0; kb < a.kblocks; ++kb) {
+            const int kbs = GROUPS == kSumGroups ? place(t).kbs : a.kblocks;
+            for (int kb = 0; kb < kbs; ++kb) {
                 if ((kb & 3) == 0) {
                     const int in = (kb >> 2) & (kBatch - 1);         // group of the batch
                     sfa = tmem_scales + set.at * kPairTmemScales;
@@ -774,7 +854,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         if (!(ok = warp_wait_cluster(sfull + slots.at, slots.parity(), a.wait_limit))) break;
                         tc_fence_after();
                     }
-                    const bool last = in == kBatch - 1 || kb + 4 >= a.kblocks;
+                    const bool last = in == kBatch - 1 || kb + 4 >= kbs;
                     if (elect_one()) {
                         const uint64_t from = sdesc0 + (((slots.at * kBatch + in) * kPairScaleBytes) >> 4);
                         tmem_copy_scales_pair(sfa, from);
@@ -818,12 +898,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int r = threadIdx.x - 64;
         uint8_t* mine = scale_sh + (r & 31) * 16 + (r >> 5) * 4;
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
-            int p0, q0;
-            place(t, p0, q0);
+            const Tile x = place(t);
+            const int groups = (x.kbs + 3) / 4;
             ScaleRow row[3];
-            row[0].start(a.sp, a.ldsp, (int64_t)p0 + rank * 128 + r, a.rows_p, 0, a.kblocks, a.kblocks);
-            row[1].start(a.sq, a.ldsq, (int64_t)q0 + r, a.rows_q, 0, a.kblocks, a.kblocks);
-            row[2].start(a.sq, a.ldsq, (int64_t)q0 + 128 + r, BN > 128 + r ? a.rows_q : 0, 0, a.kblocks, a.kblocks);
+            row[0].start(a.sp, a.ldsp, (int64_t)x.p0 + rank * 128 + r, a.rows_p, x.kb0, x.kbs, a.kblocks);
+            row[1].start(a.sq, a.ldsq, (int64_t)x.q0 + r, a.rows_q, x.kb0, x.kbs, a.kblocks);
+            row[2].start(a.sq, a.ldsq, (int64_t)x.q0 + 128 + r, BN > 128 + r ? a.rows_q : 0, x.kb0, x.kbs, a.kblocks);
             for (int g = 0; g < groups; g += kBatch) {
                 if (slots.round > 0 && !(ok = warp_wait_or_look(sempty + slots.at, slots.parity() ^ 1, a.wait_limit))) break;
 #pragma unroll
@@ -851,23 +931,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int sub = warp & 3, half = (warp - 6) >> 2;
         Ring acc;
         for (int64_t t = first_tile; t < tiles; t += step, acc.next(kAccs)) {
-            int p0, q0;
-            place(t, p0, q0);
+            const Tile x = place(t);
             if (!warp_wait_or_look(done + acc.at, acc.parity(), a.wait_limit)) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
-            const int64_t p = (int64_t)p0 + rank * 128 + sub * 32;               // the warp's first row
-            const int rows = a.rows_p - p < 32 ? (int)(a.rows_p - p) : 32;
-            const int qh = q0 + half * kHalf;
-            uint16_t* o = a.out + p * a.ldo + qh;
+            const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;             // the warp's first row
+            int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
+            const int qh = x.q0 + half * kHalf;
+            uint16_t* o = a.out + (x.out_row + p) * a.ldo + (qh - x.out_col);
+            const bool sum = GROUPS != kSumGroups || x.kbs > 0;                  // the empty sum: zeros, or out as it is
+            if (!sum && !a.first) rows = 0;
             const uint32_t from = tmem + acc.at * BN + half * kHalf + ((uint32_t)(sub * 32) << 16);
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 16) {
                 float f[16];
                 tmem_load16(from + c, f);
-                store_rows16(o + c, a.ldo, f, rows, a.rows_q - qh - c, a.align, a.scale, a.first,
+                if (GROUPS == kSumGroups && !sum) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] = 0.f;
+                }
+                store_rows16(o + c, a.ldo, f, rows, x.q_end - qh - c, a.align, a.scale, a.first,
                              store_sh + (warp - 6) * kStoreStage);
             }
             tc_fence_before();
@@ -963,18 +1048,25 @@ cudaError_t launch_mm_split(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cuda
 // CTA pairs that are resident at once.
 int64_t resident_pairs() { return q8_host::sm_count() / 2; }
 
-template <int BN>
+template <int BN, int GROUPS = kNoGroups>
 cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
-    constexpr int smem = PairShape<BN>::kSmem;
-    const auto kern = k_q8_matmul_pair<BN>;
+    constexpr int smem = PairShape<BN>::kSmem + (GROUPS == kRowGroups ? PairShape<BN>::kTable : 0);
+    const auto kern = k_q8_matmul_pair<BN, GROUPS>;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = ready_once(ready, (const void*)kern, smem);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq;
     e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2);
     if (e != cudaSuccess) return e;
-    a.tiles_q = (a.rows_q + BN - 1) / BN;
-    const int64_t tiles = ((int64_t)a.rows_p + 255) / 256 * a.tiles_q, room = resident_pairs();
+    const int64_t high = ((int64_t)a.rows_p + 255) / 256;
+    a.tiles_q = ((GROUPS == kRowGroups ? a.group_rows : a.rows_q) + BN - 1) / BN;
+    // at most: a group's last rows may be a tile of their own
+    const int64_t most = GROUPS == kRowGroups ? high + (a.n_groups < a.rows_p ? a.n_groups : a.rows_p) : GROUPS == kSumGroups ? high * a.n_groups : high;
+    const int64_t tiles = most * a.tiles_q, room = resident_pairs();
+    if (GROUPS == kRowGroups) {
+        if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        a.most_tiles = (int)tiles;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < room ? tiles : room)));
     cfg.blockDim = dim3(kPairThreads);
@@ -993,15 +1085,15 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
     return e;
 }
 
-// The tile width with the least time in the busiest pair: rounds of tiles times the time of one.  Measured per block of
+// The tile width with the least time in the busiest pair, for `tp` tiles of P: rounds of tiles times the time of one.  Measured per block of
 // the sum, one to three rounds of 4096 to 16384 columns, ns for tiles of 128 / 160 / 192 / 224 / 256 columns: 243 251
 // 266 284 302; where rows of codes are not 128 bytes apart, or a multiple, and each row of a box touches two lines,
 // 296 322 349 370 395.  Writing a tile out, 2.5 us, is hidden by the next tile's products but for the last one (and
 // for 256 columns).
-int pair_width(int64_t rows_p, int64_t rows_q, int64_t kblocks, bool lines) {
+int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines) {
     int best = 224;
     double least = 1e300;
-    const int64_t room = resident_pairs(), tp = (rows_p + 255) / 256;
+    const int64_t room = resident_pairs();
     for (int bn : {256, 224, 192, 160, 128}) {
         const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + room - 1) / room;
         const double block = lines ? 180 + 0.48 * bn : 200 + 0.765 * bn;
@@ -1014,11 +1106,108 @@ int pair_width(int64_t rows_p, int64_t rows_q, int64_t kblocks, bool lines) {
     return best;
 }
 
+// The products of groups, in the width of least time for groups of equal size (their sizes are on the device).
+template <int GROUPS>
+cudaError_t launch_mm_groups(const Q8& p, const Q8& q, int64_t k, MmArgs& a, int64_t rows_q, cudaStream_t st) {
+    const bool lines = ((p.ld | q.ld) & 127) == 0;
+    const int64_t n = a.n_groups;
+    const int64_t tp = GROUPS == kRowGroups ? n * ((a.rows_p / n + 255) / 256 + (a.rows_p < n)) : n * (((int64_t)a.rows_p + 255) / 256);
+    switch (pair_width(tp, rows_q, GROUPS == kRowGroups ? a.kblocks : (double)a.kblocks / n, lines)) {
+        case 256: return launch_mm_pair<256, GROUPS>(p, q, k, a, st);
+        case 224: return launch_mm_pair<224, GROUPS>(p, q, k, a, st);
+        case 192: return launch_mm_pair<192, GROUPS>(p, q, k, a, st);
+        case 160: return launch_mm_pair<160, GROUPS>(p, q, k, a, st);
+        default: return launch_mm_pair<128, GROUPS>(p, q, k, a, st);
+    }
+}
+
 }  // namespace
 
 }  // namespace zs
 
 using namespace zs::q8_host;
+
+namespace {
+
+int output_align(const void* out, int64_t ldo) { return ((uintptr_t)out & 31) == 0 && (ldo & 15) == 0 ? 32 : wide(out, ldo) ? 16 : 0; }
+
+// What the two products of groups share: `rows_q` rows of b, `out_rows` of out.
+int group_args(const char* fn, const zs::Q8& qa, const zs::Q8& qb, const int32_t* starts, int32_t n_groups, int64_t m, int64_t rows_q,
+               int64_t group_rows, int64_t n, int64_t k, int64_t out_rows, float scale, int32_t first, void* out, int64_t ldo, zs::MmArgs* g) {
+    if (!starts) return fail(fn, "starts is NULL");
+    if ((uintptr_t)starts & 3) return fail(fn, "starts is not 4-byte aligned");
+    if (!std::isfinite(scale)) return fail(fn, "scale must be finite");
+    ZS_Q8_TRY(check_bf16(fn, "out", out, ldo, out_rows, n));
+    *g = zs::MmArgs{};
+    g->sp = qa.scales;
+    g->sq = qb.scales;
+    g->ldsp = qa.lds;
+    g->ldsq = qb.lds;
+    g->rows_p = (int)m;
+    g->rows_q = (int)rows_q;
+    g->kblocks = (int)((k + 127) / 128);
+    g->starts = starts;
+    g->n_groups = n_groups;
+    g->group_rows = (int)group_rows;
+    g->out = (uint16_t*)out;
+    g->ldo = ldo;
+    g->align = output_align(out, ldo);
+    g->scale = scale;
+    g->first = first != 0;
+    g->wait_limit = zs::wait_limit().load(std::memory_order_relaxed);
+    return ZS_OK;
+}
+
+int check_groups(const char* fn, int32_t n_groups, int64_t m, int64_t n, int64_t k) {
+    if (n_groups < 1 || n_groups > ZS_MAX_EXPERTS) return fail(fn, "n_experts out of range");
+    ZS_Q8_TRY(check_dim(fn, "m", m, 0));
+    ZS_Q8_TRY(check_dim(fn, "n", n, 0));
+    return check_dim(fn, "k", k, 0);
+}
+
+}  // namespace
+
+extern "C" int zs_q8_matmul_experts(const zs_q8* a, const zs_q8* b, const int32_t* starts, int32_t n_experts, int64_t m, int64_t n,
+                                    int64_t k, float scale, int32_t first, void* out, int64_t ldo, void* stream) {
+    static const char* fn = "zs_q8_matmul_experts";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    zs::Q8 qa, qb;
+    zs::MmArgs g;
+    ZS_Q8_TRY(check_groups(fn, n_experts, m, n, k));
+    if (k < 1) return fail(fn, "k out of range");
+    ZS_Q8_TRY(check_dim(fn, "n_experts * n", n_experts * n, 0));
+    ZS_Q8_TRY(check_q8(fn, "a", a, m, k, false, &qa));
+    ZS_Q8_TRY(check_q8(fn, "b", b, n_experts * n, k, false, &qb));
+    ZS_Q8_TRY(group_args(fn, qa, qb, starts, n_experts, m, n_experts * n, n, n, k, m, scale, first, out, ldo, &g));
+    if (m == 0 || n == 0) return ZS_OK;
+    ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
+    return cuda_status(fn, zs::launch_mm_groups<zs::kRowGroups>(qa, qb, k, g, n, (cudaStream_t)stream));
+}
+
+extern "C" int zs_q8_matmul_experts_grad(const zs_q8* a, const zs_q8* b, const int32_t* starts, int32_t n_experts, int64_t m, int64_t n,
+                                         int64_t k, float scale, int32_t first, void* out, int64_t ldo, void* stream) {
+    static const char* fn = "zs_q8_matmul_experts_grad";
+    zs::TraceRange trace_(fn);
+    zs::clear_error();
+    zs::Q8 qa, qb;
+    zs::MmArgs g;
+    ZS_Q8_TRY(check_groups(fn, n_experts, m, n, k));
+    ZS_Q8_TRY(check_dim(fn, "n_experts * m", n_experts * m, 0));
+    ZS_Q8_TRY(check_q8(fn, "a", a, m, k, false, &qa));
+    ZS_Q8_TRY(check_q8(fn, "b", b, n, k, false, &qb));
+    ZS_Q8_TRY(group_args(fn, qa, qb, starts, n_experts, m, n, m, n, k, n_experts * m, scale, first, out, ldo, &g));
+    if (m == 0 || n == 0) return ZS_OK;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (k == 0) {
+        if (!first) return ZS_OK;
+        const int64_t rows = n_experts * m, blocks = (rows * n + 255) / 256;
+        return cuda_status(fn, zs::launch_kernel(zs::k_q8_empty_sum, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
+                                                 (uint16_t*)out, ldo, rows, n));
+    }
+    ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
+    return cuda_status(fn, zs::launch_mm_groups<zs::kSumGroups>(qa, qb, k, g, n, st));
+}
 
 extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n, int64_t k, float scale, int32_t first,
                             void* out, int64_t ldo, void* stream) {
@@ -1055,7 +1244,7 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     g.out = (uint16_t*)out;
     g.ldo = ldo;
     g.transposed = swap;
-    g.align = ((uintptr_t)out & 31) == 0 && (ldo & 15) == 0 ? 32 : wide(out, ldo) ? 16 : 0;
+    g.align = output_align(out, ldo);
     g.scale = scale;
     g.first = first != 0;
     g.wait_limit = zs::wait_limit().load(std::memory_order_relaxed);
@@ -1064,7 +1253,7 @@ extern "C" int zs_q8_matmul(const zs_q8* a, const zs_q8* b, int64_t m, int64_t n
     // 8192 x 64 x 4096: 11.8 and 13.0; 50000 x 64 x 2048: 22.8 and 22.1).
     cudaError_t e;
     if (!swap && n > 64 && ((m + 255) / 256) * ((n + 255) / 256) >= 24) {
-        switch (zs::pair_width(m, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0)) {
+        switch (zs::pair_width((m + 255) / 256, n, g.kblocks, ((qa.ld | qb.ld) & 127) == 0)) {
             case 256: e = zs::launch_mm_pair<256>(p, q, k, g, st); break;
             case 224: e = zs::launch_mm_pair<224>(p, q, k, g, st); break;
             case 192: e = zs::launch_mm_pair<192>(p, q, k, g, st); break;

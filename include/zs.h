@@ -735,6 +735,151 @@ int zs_swiglu_backward_q8(const void* dh, int64_t lddh, const zs_q8* gate_q, con
                           int64_t cols, const zs_q8* dgate, const zs_q8* dup, const zs_q8* dgate_t,
                           const zs_q8* dup_t, const zs_q8* h_t, void* stream);
 
+/* ------------------------------------------------------------------ experts
+ *
+ * A unit of experts in 8 bits: every token chooses some experts (`choices` of
+ * n_experts), its row goes to each of them, and what they give comes back
+ * weighted.  zs_expert_sort gives every choice a row; zs_expert_dispatch writes the
+ * tokens to their rows; the experts' products take their groups of rows from the
+ * device (no count comes to the host); zs_expert_combine brings the rows back.
+ * Backward: zs_expert_combine_backward, the products again, and zs_expert_combine
+ * without weights for the gradient of the tokens.  Rows that belong to no token are
+ * zeros all the way, so that sums over an expert's rows may take them along.
+ *
+ * Rows.  Expert e has the rows starts[e] .. starts[e + 1] of a matrix of `rows` rows,
+ * the first counts[e] of them with a token each, in the order of the tokens (and of a
+ * token's choices), the others zeros.  starts[e] is a multiple of `align`: 128 where
+ * sums over an expert's rows are wanted (zs_q8_matmul_experts_grad), else any.  `rows`
+ * is the caller's: tokens * choices + min(n_experts, tokens * choices) * (align - 1) is
+ * always enough.  What would lie at or past `rows` is left out, as a choice that goes
+ * nowhere is; rows from starts[n_experts] on are left as they are.
+ * The rest is as for the 8-bit training operators: matrices, alignment, empty
+ * matrices, repeatability, streams, errors.  row_of, starts, counts, weights and
+ * dweights are contiguous and 4-byte aligned. */
+#define ZS_MAX_CHOICES 32           /* of a token */
+#define ZS_MAX_EXPERTS 1024
+#define ZS_MAX_EXPERT_ALIGN 65536
+
+/* Gives every choice its row: with e = ids[t][j],
+ *     counts[e] = how many choices are e
+ *     starts[0] = 0, starts[e + 1] = starts[e] + counts[e] rounded up to a multiple of align
+ *     row_of[t][j] = starts[e] + how many choices before (t, j) are e
+ * and row_of[t][j] = -1 where e is not in 0 .. n_experts - 1 (a dropped choice).
+ *   ids      tokens x choices integers of id_bytes (4 or 8) bytes, contiguous.
+ *   row_of   tokens x choices;  starts  n_experts + 1;  counts  n_experts.
+ * One launch; no workspace. */
+int zs_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t choices, int32_t n_experts,
+                   int32_t align, int32_t* row_of, int32_t* starts, int32_t* counts, void* stream);
+
+/* The tokens x (bf16, tokens x cols) to their rows: y in 8 bits, y_bf16 as they are
+ * (either may be NULL), zeros in the rows without a token. */
+int zs_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t cols, const int32_t* row_of,
+                       int32_t choices, const int32_t* starts, const int32_t* counts, int32_t n_experts,
+                       int64_t rows, const zs_q8* y, void* y_bf16, int64_t ldy, void* stream);
+
+/* The rows of y (bf16, rows x cols) back at their tokens:
+ *     out[t] = bf16( residual[t] + sum over j of weights[t][j] * y[row_of[t][j]] )
+ * in fp32 in the order of the choices, dropped ones left out.  weights NULL: 1 (the
+ * gradient of zs_expert_dispatch's x, from its rows'); residual NULL: 0.  out may be
+ * residual (same row distance). */
+int zs_expert_combine(const void* y, int64_t ldy, int64_t rows, int64_t cols, const int32_t* row_of,
+                      const float* weights, int64_t tokens, int32_t choices, const void* residual, int64_t ldr,
+                      void* out, int64_t ldo, void* stream);
+
+/* Backward pass of zs_expert_combine from the gradient dout of its result (the
+ * residual's gradient is dout itself):
+ *     dy[row_of[t][j]] = weights[t][j] * dout[t]     in 8 bits (dy) and as bf16 (dy_bf16)
+ *     dweights[t][j]   = sum over columns of dout[t] * y[row_of[t][j]]      (dropped: 0)
+ * and zeros in the rows without a token.  Outputs that are NULL are not written; at
+ * least one is not.  y is read for dweights only. */
+int zs_expert_combine_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int64_t rows,
+                               int64_t cols, const int32_t* row_of, const float* weights, int64_t tokens,
+                               int32_t choices, const int32_t* starts, const int32_t* counts, int32_t n_experts,
+                               const zs_q8* dy, void* dy_bf16, int64_t lddy, float* dweights, void* stream);
+
+/* zs_q8_matmul for each expert's rows with the expert's own matrix: a (m x k), b
+ * (n_experts * n x k: expert e's n rows after the others'), and for the rows i of
+ * expert e, starts[e] <= i < starts[e + 1],
+ *     out[i][j] = bf16( (first ? 0 : out[i][j]) + scale * sum over l of a[i][l] * b[e * n + j][l] )
+ * Other rows of out are left as they are.  starts may be any, not only a sort's; starts
+ * out of range are read as the nearest inside, and where experts' rows overlap what is
+ * written is unspecified (inside out).  k >= 1; n_experts * n <= 2^31 - 256. */
+int zs_q8_matmul_experts(const zs_q8* a, const zs_q8* b, const int32_t* starts, int32_t n_experts, int64_t m,
+                         int64_t n, int64_t k, float scale, int32_t first, void* out, int64_t ldo, void* stream);
+
+/* The experts' weight gradients: a (m x k) and b (n x k) are operands whose columns are
+ * the experts' rows (transposes, zs_q8_transpose), and
+ *     out[e * m + i][j] = bf16( (first ? 0 : out[..]) + scale * sum over starts[e] <= l < starts[e + 1] of a[i][l] * b[j][l] )
+ * (an expert without rows: the empty sum).  starts are multiples of 128, as
+ * zs_expert_sort gives them with such an align; others are taken as the blocks of 128
+ * columns that they lie in.  n_experts * m <= 2^31 - 256. */
+int zs_q8_matmul_experts_grad(const zs_q8* a, const zs_q8* b, const int32_t* starts, int32_t n_experts, int64_t m,
+                              int64_t n, int64_t k, float scale, int32_t first, void* out, int64_t ldo, void* stream);
+
+/* ------------------------------------------------------------------ many tensors at once
+ *
+ * The AdamW update of zs_adamw_shard_step over a list of tensors, each with its own
+ * arrays, in as few launches as their table allows (448 tensors each): a unit of experts
+ * has hundreds of matrices, and so have a model's dense layers where they are not in one flat
+ * buffer.  The list is read before the call returns; it is host memory.
+ *
+ * States in 8 bits (zs_tensor.m_scale, v_scale).  m and r = sqrt(v) are e4m3 codes, and
+ * one fp32 scale per ZS_STATE_BLOCK elements of the tensor (the last block may be
+ * shorter): value = code * scale, scale = the block's largest magnitude / 448; blocks with
+ * none of at least 2^-100 are all zeros.  Two roundings differ from the nearest:
+ *   - A magnitude between two codes is rounded up with the probability of its distance
+ *     from the lower: to nearest, an average that moves by less than half a step per
+ *     update - v always, as 1 - beta2 of a change is far below an e4m3 step - would
+ *     stand still.  The random bits are a function of seed, the tensor's place in the
+ *     list and the element: with mix the finalizer of murmur3's 32-bit hash,
+ *         h = mix( (uint32)i ^ mix( mix( seed + 0x9e3779b9 * (tensor + 1) ) + (uint32)(i >> 32) ) )
+ *     the lower 16 bits m's, the upper r's.  Another seed for every step (the step number).
+ *   - r > 0 is never rounded to 0: an element whose r vanished beside its block's largest
+ *     and whose m did not would take a step without bound.
+ * The root of v is kept because v's range is the square of m's: codes of v itself would
+ * vanish where m's do not.  The update uses the new m and v before they are rounded.
+ * Infinities and NaN have the code NaN (0x7f) and leave their block's scale alone. */
+#define ZS_STATE_BLOCK 256
+
+typedef struct {
+    int64_t n;                  /* elements (0: nothing is read or written) */
+    const void* grad;           /* bf16 or fp32 (grad_bytes) */
+    float* master;              /* fp32, updated */
+    void* param;                /* bf16, written; NULL: not wanted */
+    void* m;                    /* fp32 or codes (state_bits), updated; zeros before the first step */
+    void* v;
+    float* m_scale;             /* states in 8 bits: ceil(n / ZS_STATE_BLOCK) floats; else unused */
+    float* v_scale;
+    int32_t no_decay;           /* != 0: weight_decay is 0 for this tensor */
+    int32_t reserved;
+} zs_tensor;
+
+/* One AdamW step (1-based `step`, arithmetic of zs_adamw_shard_step; with states of 32
+ * bits its results bit for bit) on every tensor of the list.
+ *   grad_bytes  2 (bf16) or 4 (fp32), for all tensors.
+ *   state_bits  32, or 8.
+ *   factor      device address of one float that multiplies the gradients (out[1] of
+ *               zs_grad_norm, a loss scale's inverse), NULL: 1.  NaN: nothing is written,
+ *               the step is left out.
+ *   seed        of the 8-bit states' roundings.
+ * Arrays are aligned to their elements; where grad, master (and 32-bit states) start at
+ * multiples of eight elements' bytes, param of 16 and codes of 8, eight elements are moved per
+ * access, elsewhere one (views into flat buffers at any element).  No two arrays of the list overlap.
+ * Errors: ZS_ERR_INVALID (nothing enqueued), ZS_ERR_CUDA. */
+int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, int32_t state_bits,
+                     const zs_adamw_hparams* hp, int64_t step, const float* factor, uint32_t seed, void* stream);
+
+/* The 2-norm of all gradients of the list and the factor that clips it:
+ *     out[0] = sqrt( sum of grad^2 ),   out[1] = min(1, max_norm / (out[0] + 1e-6))
+ * Squares are fp32 (|grad| below 1.8e19), their sums fp64 and rounded to fp32 once per
+ * partial sum.  A norm that is not finite gives out[1] = NaN.  Only n and grad of the
+ * tensors are used.
+ *   partials    caller's scratch, n_partials floats; at most 8 per SM are used, fewer make
+ *               the call slower.
+ *   out         two floats. */
+int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, float max_norm, float* partials,
+                 int64_t n_partials, float* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
