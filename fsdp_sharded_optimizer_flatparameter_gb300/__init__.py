@@ -33,7 +33,7 @@ ZS_FUSED_AUTO, ZS_FUSED_LDG, ZS_FUSED_TMA = 0, 1, 2
 ZS_BUCKETS_ONE_WALK, ZS_BUCKETS_PER_BUCKET = 0, 1
 ZS_LAYOUT_FSDP1, ZS_LAYOUT_FSDP2 = 0, 1
 ZS_DEVERR_NONE, ZS_DEVERR_PRODUCER_WAIT, ZS_DEVERR_CONSUMER_WAIT, ZS_DEVERR_SELFTEST = 0, 1, 2, 3
-ZS_DEVERR_GATHER_WAIT, ZS_DEVERR_MATMUL_WAIT, ZS_DEVERR_TILE_WAIT = 4, 5, 6
+ZS_DEVERR_GATHER_WAIT, ZS_DEVERR_MATMUL_WAIT, ZS_DEVERR_TILE_WAIT, ZS_DEVERR_TENSORS_WAIT = 4, 5, 6, 7
 ZS_Q8_BLOCK, ZS_Q8_MAX_PARTIALS = 128, 608
 ZS_MAX_CHOICES, ZS_MAX_EXPERTS, ZS_MAX_EXPERT_ALIGN, ZS_STATE_BLOCK = 32, 1024, 65536, 256
 

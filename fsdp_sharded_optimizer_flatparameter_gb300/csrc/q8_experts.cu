@@ -10,10 +10,11 @@ namespace {
 // ------------------------------------------------------------------ sorting
 
 // A stable counting sort in one launch.  The pairs (token, choice) are cut into segments, one per warp of a cluster's
-// CTAs.  First pass: a warp counts its segment's pairs per expert, 32 at a time (the lanes of equal experts find each
-// other with one match instruction, so a counter has one writer and the order of the pairs is kept).  The counters
-// are summed over the warps, and over the cluster's CTAs through distributed shared memory; the second pass goes
-// through the segment again and gives each pair its place.  No atomics, no workspace: the same rows every time.
+// CTAs.  First pass: a warp counts its segment's pairs per expert.  The counters are summed over the warps, and over
+// the cluster's CTAs through distributed shared memory; the second pass goes through the segment again, 32 pairs at a
+// time, and gives each its place: lanes of equal experts find each other by one vote per bit of the expert (the match
+// instruction takes its time once per different value: 131072 pairs of 64 experts in 28.7 us with it), a counter has one
+// writer, and the order of the pairs is kept.  No workspace, and the same rows every time.
 constexpr int kSortWarps = 32;
 constexpr int kSortBatch = 8;        // ids per lane read at once
 
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_co
     const int64_t hi = lo + a.seg < a.n ? lo + a.seg : a.n;
     const ID* ids = static_cast<const ID*>(a.ids);
     int* mine = hist + warp * E;
-    // f(pair, expert or -1, the lanes with the same expert) for every pair of the segment, in order
+    // f(pair, expert or -1) for every pair of the segment, 32 at a time in order
     auto each = [&](auto f) {
         for (int64_t base = lo; base < hi; base += 32 * kSortBatch) {
             int id[kSortBatch];
@@ -56,13 +57,12 @@ __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_co
 #pragma unroll
             for (int j = 0; j < kSortBatch; ++j) {
                 if (base + 32 * j >= hi) break;
-                f(base + 32 * j + lane, id[j], __match_any_sync(~0u, id[j]));
-                __syncwarp();
+                f(base + 32 * j + lane, id[j]);
             }
         }
     };
-    each([&](int64_t, int id, uint32_t same) {
-        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+    each([&](int64_t, int id) {
+        if (id >= 0) atomicAdd(mine + id, 1);
     });
     __syncthreads();
     const int e = threadIdx.x;                   // at most as many experts as threads
@@ -118,11 +118,18 @@ __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_co
     }
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");       // the other CTAs' totals are read
-    each([&](int64_t i, int id, uint32_t same) {
+    const int bits = 32 - __clz(E - 1);
+    each([&](int64_t i, int id) {
+        uint32_t same = __ballot_sync(~0u, id >= 0);
+        for (int b = 0; b < bits; ++b) {
+            const uint32_t set = __ballot_sync(~0u, id >> b & 1);
+            same &= id >> b & 1 ? set : ~set;
+        }
         const int at = id >= 0 ? mine[id] : 0;
         __syncwarp();
         if (id >= 0 && lane == __ffs(same) - 1) mine[id] = at + __popc(same);
         if (i < hi) a.row_of[i] = id >= 0 ? first[id] + at + __popc(same & ((1u << lane) - 1)) : -1;
+        __syncwarp();
     });
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");         // nobody reads this CTA's any more
 }
@@ -262,26 +269,52 @@ struct CombineBackArgs {
 
 constexpr int kMaxChoices = ZS_MAX_CHOICES;
 constexpr int kBackWarps = 8;        // at most, per token
+constexpr int kBackCtas = 4;         // resident (16384 x 2048, 8 choices: 149 us; 169 and 187 with 3 and 5)
 
-// A CTA takes a token, a warp of it 512 columns at a time.  The gradient row is read once; the largest magnitude of its
-// blocks serves every choice, as |weight| times it is the largest of the weighted ones (rounding keeps their order).
+// 16 columns of 8 neighbouring lanes, times w, in the format.  `top` is the block's largest finite magnitude before w:
+// |w| times it is the largest after (rounding keeps the order), and w and the block's inverse scale are one factor where
+// that is exact - where no value that matters comes near the ends of fp32's range.
+__device__ __forceinline__ uint4 code16_scaled(const float2 (&f)[8], float w, float top, uint32_t& byte) {
+    const float most = top * fabsf(w);
+    const bool plain = most >= 0x1p-100f && most < __int_as_float(0x7f800000) && top >= 0x1p-100f && top <= 0x1p100f;
+    if (!__all_sync(~0u, plain || (most == 0.f && top < 0x1p100f))) {
+        float2 g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = q8_mul2(f[i], make_float2(w, w));
+        return code16(g, byte);
+    }
+    byte = q8_scale_byte(most);
+    const float by = plain ? w * q8_inverse(byte) : 0.f;
+    uint32_t q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 a = q8_mul2(f[2 * k], make_float2(by, by)), b = q8_mul2(f[2 * k + 1], make_float2(by, by));
+        q[k] = q8_pack4(a.x, a.y, b.x, b.y);
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// A CTA takes a token, a warp of it 512 columns at a time: the gradient row stays in registers, and the expert's next row
+// is on its way while one is worked on.
 template <bool WIDE>
-__global__ void __launch_bounds__(32 * kBackWarps) k_expert_combine_backward(const __grid_constant__ CombineBackArgs a) {
-    __shared__ float dots[2][kBackWarps][kMaxChoices];
+__global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) k_expert_combine_backward(const __grid_constant__ CombineBackArgs a) {
+    __shared__ float dots[kBackWarps][kMaxChoices];
     dependent_launch_prologue();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = blockDim.x >> 5;
     const Span sd = span_of(a.dout, a.lddout, a.r.tokens, a.r.cols), sy = span_of(a.y, a.ldy, a.r.rows, a.r.cols);
     const int K = a.r.choices;
-    int turn = 0;
-    for (int64_t t = blockIdx.x; t < a.r.tokens; t += gridDim.x, turn ^= 1) {
+    const int64_t t = blockIdx.x;
+    if (t < a.r.tokens) {
         const int held = lane < K ? a.r.row_of[t * K + lane] : -1;
         const float weight = a.weights && lane < K ? a.weights[t * K + lane] : 1.f;
-        float* dot = dots[turn][warp];
-        if (lane < K) dot[lane] = 0.f;
+        if (lane < K) dots[warp][lane] = 0.f;
         __syncwarp();
         for (int ch = warp; ch < a.r.chunks; ch += group) {
             const int64_t c = (int64_t)ch * 512 + lane * 16, n = a.r.cols - c;
             const V16 d = load16<WIDE>(a.dout + t * a.lddout + c, n, sd);
+            int64_t row = row_at(held, 0, a.r.rows);
+            V16 y;
+            if (a.dweights && row >= 0) y = load16<WIDE>(a.y + row * a.ldy + c, n, sy);
             float2 f[8];
             float top = 0.f;
 #pragma unroll
@@ -291,63 +324,42 @@ __global__ void __launch_bounds__(32 * kBackWarps) k_expert_combine_backward(con
             }
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
-            for (int j0 = 0; j0 < K; j0 += kAtOnce) {
-                V16 y[kAtOnce];
-                int64_t row[kAtOnce];
+#pragma unroll 1
+            for (int j = 0; j < K; ++j) {
+                const int64_t here = row;
+                const float w = __shfl_sync(~0u, weight, j);
+                float2 s = make_float2(0.f, 0.f);
+                if (a.dweights && here >= 0) {
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    row[j] = j0 + j < K ? row_at(held, j0 + j, a.r.rows) : -1;
-                    if (a.dweights && row[j] >= 0) y[j] = load16<WIDE>(a.y + row[j] * a.ldy + c, n, sy);
+                    for (int i = 0; i < 8; ++i) s = q8_fma2(f[i], pair_of(y.w[i]), s);
                 }
+                row = j + 1 < K ? row_at(held, j + 1, a.r.rows) : -1;
+                if (a.dweights && row >= 0) y = load16<WIDE>(a.y + row * a.ldy + c, n, sy);
+                if (here < 0) continue;
+                if (a.r.y.codes) {
+                    uint32_t byte;
+                    const uint4 x = code16_scaled(f, w, top, byte);
+                    store_code16(x, byte, n, a.r.y, here, c);
+                }
+                if (a.r.y16) {
+                    V16 v;
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const float w = __shfl_sync(~0u, weight, (j0 + j) & 31);
-                    if (row[j] < 0) continue;
-                    if (a.dweights) {
-                        float2 s = make_float2(0.f, 0.f);
+                    for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(f[i].x * w, f[i].y * w);
+                    store16<WIDE>(a.r.y16 + here * a.r.ldy16 + c, v, n);
+                }
+                if (a.dweights) {
+                    float sum = s.x + s.y;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) s = q8_fma2(f[i], pair_of(y[j].w[i]), s);
-                        float sum = s.x + s.y;
-#pragma unroll
-                        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
-                        if (lane == 0) dot[j0 + j] += sum;
-                    }
-                    float2 g[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = q8_mul2(f[i], make_float2(w, w));
-                    if (a.r.y16) {
-                        V16 v;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(g[i].x, g[i].y);
-                        store16<WIDE>(a.r.y16 + row[j] * a.r.ldy16 + c, v, n);
-                    }
-                    if (a.r.y.codes) {
-                        const float most = top * fabsf(w);
-                        uint32_t byte;
-                        uint4 x;
-                        if (__any_sync(~0u, !(most < __int_as_float(0x7f800000)))) {
-                            x = code16(g, byte);         // infinities or NaN: found value by value
-                        } else {
-                            byte = q8_scale_byte(most);
-                            const float2 inv = make_float2(q8_inverse(byte), q8_inverse(byte));
-                            uint32_t q[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 p = q8_mul2(g[2 * k], inv), s = q8_mul2(g[2 * k + 1], inv);
-                                q[k] = q8_pack4(p.x, p.y, s.x, s.y);
-                            }
-                            x = make_uint4(q[0], q[1], q[2], q[3]);
-                        }
-                        store_code16(x, byte, n, a.r.y, row[j], c);
-                    }
+                    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+                    if (lane == 0) dots[warp][j] += sum;
                 }
             }
         }
         if (a.dweights) {
-            __syncthreads();                     // the other of the two sums is free until the next token's barrier
+            __syncthreads();
             if (threadIdx.x < K) {
                 float sum = 0.f;
-                for (int w = 0; w < group; ++w) sum += dots[turn][w][threadIdx.x];
+                for (int w = 0; w < group; ++w) sum += dots[w][threadIdx.x];
                 a.dweights[t * K + threadIdx.x] = sum;
             }
         }
@@ -372,9 +384,10 @@ int check_routes(const char* fn, int64_t tokens, int32_t choices, int32_t expert
     return ZS_OK;
 }
 
-// CTAs of a grid whose `warps` warps of work are taken in turn, `per` to a CTA.
-unsigned grid_for(int64_t warps, int per, int resident) {
-    const int64_t ctas = (warps + per - 1) / per, most = (int64_t)q8_host::sm_count() * resident;
+// CTAs for `warps` warps of work, `per` to a CTA, each with work of its own: CTAs that end make room for the next, so the
+// work goes to the SMs as they get through it.  Past 2^31 CTAs the kernels go round.
+unsigned grid_for(int64_t warps, int per) {
+    const int64_t ctas = (warps + per - 1) / per, most = 0x7fffffff;
     return (unsigned)(ctas < 1 ? 1 : ctas < most ? ctas : most);
 }
 
@@ -462,7 +475,7 @@ extern "C" int zs_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, in
     int64_t work = tokens * a.r.chunks;
     if (work < (int64_t)n_experts * zs::kPadWarps) work = (int64_t)n_experts * zs::kPadWarps;
     return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_dispatch<true> : zs::k_expert_dispatch<false>,
-                                             dim3(zs::grid_for(work, 8, 8)), dim3(256), 0, (cudaStream_t)stream, a));
+                                             dim3(zs::grid_for(work, 8)), dim3(256), 0, (cudaStream_t)stream, a));
 }
 
 extern "C" int zs_expert_combine(const void* y, int64_t ldy, int64_t rows, int64_t cols, const int32_t* row_of, const float* weights,
@@ -484,7 +497,7 @@ extern "C" int zs_expert_combine(const void* y, int64_t ldy, int64_t rows, int64
                       (int)((cols + 511) / 512), (uint16_t*)out};
     const bool w = wide(y, ldy, 32) && (!residual || wide(residual, ldr, 32)) && wide(out, ldo, 32);
     return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_combine<true> : zs::k_expert_combine<false>,
-                                             dim3(zs::grid_for(tokens * a.chunks, 8, 8)), dim3(256), 0, (cudaStream_t)stream, a));
+                                             dim3(zs::grid_for(tokens * a.chunks, 8)), dim3(256), 0, (cudaStream_t)stream, a));
 }
 
 extern "C" int zs_expert_combine_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int64_t rows, int64_t cols,
@@ -510,8 +523,8 @@ extern "C" int zs_expert_combine_backward(const void* dout, int64_t lddout, cons
     a.dweights = dweights;
     const bool w = wide(dout, lddout, 32) && (!dweights || wide(y, ldy, 32)) && (!dy_bf16 || wide(dy_bf16, lddy, 32));
     const int group = a.r.chunks < zs::kBackWarps ? a.r.chunks : zs::kBackWarps;
-    int64_t warps = tokens * group;
-    if (warps < (int64_t)n_experts * zs::kPadWarps) warps = (int64_t)n_experts * zs::kPadWarps;
+    // a token per CTA, and at least a few CTAs for the rows without one
+    const unsigned ctas = tokens < 64 ? 64 : (unsigned)tokens;
     return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_combine_backward<true> : zs::k_expert_combine_backward<false>,
-                                             dim3(zs::grid_for(warps, group, 32 / group)), dim3(32 * group), 0, (cudaStream_t)stream, a));
+                                             dim3(ctas), dim3(32 * group), 0, (cudaStream_t)stream, a));
 }

@@ -646,8 +646,9 @@ struct PairShape {
     static constexpr int kAccs = BN == 256 ? 1 : 2;
     static constexpr int kStageBytes = 128 * 128 + (BN / 2) * 128;
     static constexpr int kSmem = 1024 + kPairStages * kStageBytes + kPairSlots * kBatch * kPairScaleBytes + 8 * kStoreStage * 4 + 256;
-    static constexpr int kTable = (ZS_MAX_EXPERTS + 1) * 4;          // kRowGroups: the tiles before each group's
-    static_assert(kSmem + kTable <= 227 * 1024, "shared memory");
+    // kRowGroups: a table of the groups, their starts and the tiles before them
+    static constexpr int table(int n_groups) { return (n_groups + 1) * 8; }
+    static constexpr int kSmemMost = 227 * 1024;
     static_assert(kAccs * BN + kScaleSets * kPairTmemScales <= 512, "tensor memory");
     static_assert(BN % 32 == 0 && (BN / 2) % 16 == 0, "halves of whole 16-column loads");
 };
@@ -673,6 +674,7 @@ struct Sent {
 // A pair's tile: its first rows of P and Q and where those that count end, its blocks of the sum, and its place in out.
 struct Tile {
     int p0, q0, p_end, q_end;
+    int width;                   // columns: BN, or fewer so that a group's are shared out evenly
     int kb0, kbs;
     int64_t out_row;             // row of out that P row 0 would have
     int out_col;                 // Q row that column 0 of out has
@@ -702,7 +704,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(settled + 1);
     uint32_t* gave_up = tmem_at + 1;             // set in both CTAs
     Sent* sent = reinterpret_cast<Sent*>(gave_up + 1);
-    int* before = reinterpret_cast<int*>(store_sh + 8 * kStoreStage) + 64;       // kRowGroups: tiles before each group's
+    int* before = reinterpret_cast<int*>(store_sh + 8 * kStoreStage) + 64;       // kRowGroups: tiles before each group's,
+    int* start = before + a.n_groups + 1;                                         // and its first row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();        // CTA 0 of the pair leads
     constexpr uint16_t kBoth = 3;
@@ -745,11 +748,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if constexpr (GROUPS == kRowGroups) {
         // Tiles of the groups summed up: a thread adds a few neighbouring groups', the threads' sums are scanned.
         const int each = (a.n_groups + kPairThreads - 1) / kPairThreads, g0 = threadIdx.x * each;
+        for (int g = threadIdx.x; g <= a.n_groups; g += kPairThreads) start[g] = group_start(a, g, a.rows_p);
+        __syncthreads();
+        auto tiles_of = [&](int g) {
+            const int lo = start[g], hi = start[g + 1];
+            return hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
+        };
         int64_t sum = 0;
-        for (int g = g0; g < g0 + each && g < a.n_groups; ++g) {
-            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
-            sum += hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
-        }
+        for (int g = g0; g < g0 + each && g < a.n_groups; ++g) sum += tiles_of(g);
         int64_t upto = sum;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -763,44 +769,52 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int64_t at = upto - sum;
         for (int g = g0; g < g0 + each && g < a.n_groups; ++g) {
             before[g] = (int)at;
-            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
-            at += hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
+            at += tiles_of(g);
         }
         if (threadIdx.x == kPairThreads - 1) before[a.n_groups] = upto <= a.most_tiles ? (int)upto : 0;
         __syncthreads();
         tiles = before[a.n_groups];
     }
     const int64_t first_tile = blockIdx.x / 2, step = gridDim.x / 2;
-    // the pair's tile t: kPairGroup P tiles at a time, within them Q tile by Q tile
-    auto place = [&](int64_t t) {
+    // Tile q of tiles_q over a group's columns: units of 32 shared out evenly, so that no tile computes columns that are not
+    // there (2048 columns: two tiles in five of 224 columns and the others of 192, where ten of 224 compute 2240).
+    const int all = GROUPS == kRowGroups ? a.group_rows : a.rows_q;
+    const int units = (all + 31) / 32, few = units / a.tiles_q, wider = units - few * a.tiles_q;
+    auto columns = [&](Tile& x, int q) {
+        x.q0 = (q * few + (q < wider ? q : wider)) * 32;
+        x.width = (few + (q < wider)) * 32;
+    };
+    // Tile `in` of `high` x tiles_q: kPairGroup P tiles at a time, within them Q tile by Q tile.
+    auto strip = [&](int in, int high, int& p, int& q) {
+        const int per = kPairGroup * a.tiles_q, s = in / per, rest = in - s * per;
+        const int tall = high - s * kPairGroup < kPairGroup ? high - s * kPairGroup : kPairGroup;
+        q = rest / tall;
+        p = s * kPairGroup + rest - q * tall;
+    };
+    // the pair's tile t; g: the group of an earlier tile
+    auto place = [&](int64_t t, int& g) {
         Tile x;
+        int p, q;
         if constexpr (GROUPS == kRowGroups) {
-            int g = 0, past = a.n_groups;        // the last group with no more than t tiles before it
-            while (past - g > 1) {
-                const int mid = (g + past) >> 1;
-                if (before[mid] <= (int)t) g = mid;
-                else past = mid;
-            }
-            const int lo = group_start(a, g, a.rows_p), hi = group_start(a, g + 1, a.rows_p);
-            const int in = (int)t - before[g], high = (hi - lo + 255) / 256;
-            x = Tile{lo + in % high * 256, g * a.group_rows + in / high * BN, hi, (g + 1) * a.group_rows, 0, a.kblocks, 0, g * a.group_rows};
+            while (before[g + 1] <= (int)t) ++g;
+            const int lo = start[g], hi = start[g + 1];
+            strip((int)t - before[g], (hi - lo + 255) / 256, p, q);
+            x = Tile{lo + p * 256, 0, hi, (g + 1) * a.group_rows, 0, 0, a.kblocks, 0, g * a.group_rows};
+            columns(x, q);
+            x.q0 += x.out_col;
+        } else if constexpr (GROUPS == kSumGroups) {
+            const int per = tiles_p * a.tiles_q, most = a.kblocks * 128;
+            g = (int)t / per;
+            strip((int)t - g * per, tiles_p, p, q);
+            const int lo = group_start(a, g, most), hi = group_start(a, g + 1, most);
+            x = Tile{p * 256, 0, a.rows_p, a.rows_q, 0, lo / 128, 0, (int64_t)g * a.group_rows, 0};
+            x.kbs = hi > lo ? (hi + 127) / 128 - x.kb0 : 0;
+            columns(x, q);
         } else {
-            int g = 0;
-            if constexpr (GROUPS == kSumGroups) {
-                const int64_t per = (int64_t)tiles_p * a.tiles_q;
-                g = (int)(t / per);
-                t -= g * per;
-            }
             const int64_t per = (int64_t)kPairGroup * a.tiles_q;
             const int s = (int)(t / per), in = (int)(t - s * per);
             const int width = tiles_p - s * kPairGroup < kPairGroup ? tiles_p - s * kPairGroup : kPairGroup;
-            x = Tile{(s * kPairGroup + in % width) * 256, (in / width) * BN, a.rows_p, a.rows_q, 0, a.kblocks, 0, 0};
-            if constexpr (GROUPS == kSumGroups) {
-                const int most = a.kblocks * 128, lo = group_start(a, g, most), hi = group_start(a, g + 1, most);
-                x.kb0 = lo / 128;
-                x.kbs = hi > lo ? (hi + 127) / 128 - x.kb0 : 0;
-                x.out_row = (int64_t)g * a.group_rows;
-            }
+            x = Tile{(s * kPairGroup + in % width) * 256, (in / width) * BN, a.rows_p, a.rows_q, BN, 0, a.kblocks, 0, 0};
         }
         return x;
     };
@@ -813,16 +827,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 0) {
         Ring ring;
         bool ok = true;
+        int group = 0;
         const uint32_t full0 = at_rank(full, 0);
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
-            const Tile x = place(t);
+            const Tile x = place(t, group);
+            // rows of P that only the other CTA has are read as zeros past the matrix: neither fetched nor worth power
+            const int half = GROUPS == kNoGroups ? BN / 2 : x.width / 2, p = x.p0 + (int)rank * 128;
+            const int row = GROUPS == kRowGroups && p >= x.p_end ? a.rows_p : p;
             for (int kb = x.kb0; kb < x.kb0 + x.kbs; ++kb) {
                 if (ring.round > 0 && !(ok = warp_wait_or_look(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
                 uint8_t* at = base + ring.at * kStageBytes;
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + ring.at, 2 * kStageBytes);
-                    tma_load_pair(at, &map_p, kb * 128, x.p0 + (int)rank * 128, full0 + ring.at * 8);
-                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, x.q0 + (int)rank * (BN / 2), full0 + ring.at * 8);
+                    tma_load_pair(at, &map_p, kb * 128, row, full0 + ring.at * 8);
+                    tma_load_pair(at + 128 * 128, &map_q, kb * 128, x.q0 + (int)rank * half, full0 + ring.at * 8);
                 }
                 __syncwarp();
                 ring.next(kPairStages);
@@ -831,12 +849,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (lane == 0) sent->loads = ring.count(kPairStages);
         if (!ok && lane == 0) fail();
     } else if (warp == 1 && rank == 0) {
-        const uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
+        uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
         const uint64_t desc0 = operand_desc(su32(base));
         const uint64_t sdesc0 = scales_desc(su32(scale_sh));
         bool ok = true;
         Ring ring, slots, acc, set;
         uint32_t sfa = tmem_scales;
+        int group = 0;
+        Tile here;
+        if constexpr (GROUPS != kNoGroups) {
+            if (first_tile < tiles) here = place(first_tile, group);
+        }
         // A group's scales overwrite those of four groups before, whose products are complete: within a tile and into
         // the next they are nine blocks back or more, and the ring's six stages have been loaded again since; those
         // of the tile before that have been read out.
@@ -844,7 +867,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (acc.round > 0 && !(ok = warp_wait_cluster(acc_free + acc.at, acc.parity() ^ 1, a.wait_limit))) break;
             tc_fence_after();
             const uint32_t sums = tmem + acc.at * BN;
-            const int kbs = GROUPS == kSumGroups ? place(t).kbs : a.kblocks;
+            const int kbs = GROUPS == kNoGroups ? a.kblocks : here.kbs;
+            if constexpr (GROUPS != kNoGroups) idesc = ((uint32_t)(here.width >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24);
             for (int kb = 0; kb < kbs; ++kb) {
                 if ((kb & 3) == 0) {
                     const int in = (kb >> 2) & (kBatch - 1);         // group of the batch
@@ -881,6 +905,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (elect_one()) mma_commit_pair(done + acc.at, kBoth);
             __syncwarp();
             acc.next(kAccs);
+            if constexpr (GROUPS != kNoGroups) {
+                if (t + step < tiles) here = place(t + step, group);             // while the last products run
+            }
         }
         if (elect_one()) mma_commit_pair(settled, kBoth);
         __syncwarp();
@@ -896,9 +923,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         Ring slots;
         bool ok = true;
         const int r = threadIdx.x - 64;
+        int group = 0;
         uint8_t* mine = scale_sh + (r & 31) * 16 + (r >> 5) * 4;
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
-            const Tile x = place(t);
+            const Tile x = place(t, group);
             const int groups = (x.kbs + 3) / 4;
             ScaleRow row[3];
             row[0].start(a.sp, a.ldsp, (int64_t)x.p0 + rank * 128 + r, a.rows_p, x.kb0, x.kbs, a.kblocks);
@@ -927,11 +955,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= 6) {
-        constexpr int kHalf = BN / 2;            // columns of one warp
         const int sub = warp & 3, half = (warp - 6) >> 2;
         Ring acc;
+        int group = 0;
         for (int64_t t = first_tile; t < tiles; t += step, acc.next(kAccs)) {
-            const Tile x = place(t);
+            const Tile x = place(t, group);
             if (!warp_wait_or_look(done + acc.at, acc.parity(), a.wait_limit)) {
                 if (lane == 0) fail();
                 break;
@@ -939,6 +967,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc_fence_after();
             const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;             // the warp's first row
             int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
+            const int kHalf = GROUPS == kNoGroups ? BN / 2 : x.width / 2;                // columns of one warp
             const int qh = x.q0 + half * kHalf;
             uint16_t* o = a.out + (x.out_row + p) * a.ldo + (qh - x.out_col);
             const bool sum = GROUPS != kSumGroups || x.kbs > 0;                  // the empty sum: zeros, or out as it is
@@ -1050,10 +1079,10 @@ int64_t resident_pairs() { return q8_host::sm_count() / 2; }
 
 template <int BN, int GROUPS = kNoGroups>
 cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
-    constexpr int smem = PairShape<BN>::kSmem + (GROUPS == kRowGroups ? PairShape<BN>::kTable : 0);
+    const int smem = PairShape<BN>::kSmem + (GROUPS == kRowGroups ? PairShape<BN>::table(a.n_groups) : 0);
     const auto kern = k_q8_matmul_pair<BN, GROUPS>;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = ready_once(ready, (const void*)kern, smem);
+    cudaError_t e = ready_once(ready, (const void*)kern, GROUPS == kRowGroups ? PairShape<BN>::kSmemMost : smem);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq;
     e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2);
@@ -1063,8 +1092,8 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
     // at most: a group's last rows may be a tile of their own
     const int64_t most = GROUPS == kRowGroups ? high + (a.n_groups < a.rows_p ? a.n_groups : a.rows_p) : GROUPS == kSumGroups ? high * a.n_groups : high;
     const int64_t tiles = most * a.tiles_q, room = resident_pairs();
-    if (GROUPS == kRowGroups) {
-        if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (GROUPS != kNoGroups) {
+        if (tiles > 0x7fffffff - 2 * room) return cudaErrorInvalidConfiguration;
         a.most_tiles = (int)tiles;
     }
     cudaLaunchConfig_t cfg = {};
@@ -1090,11 +1119,12 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
 // 266 284 302; where rows of codes are not 128 bytes apart, or a multiple, and each row of a box touches two lines,
 // 296 322 349 370 395.  Writing a tile out, 2.5 us, is hidden by the next tile's products but for the last one (and
 // for 256 columns).
-int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines) {
-    int best = 224;
+int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines, int widest = 256) {
+    int best = 128;
     double least = 1e300;
     const int64_t room = resident_pairs();
     for (int bn : {256, 224, 192, 160, 128}) {
+        if (bn > widest) continue;
         const int64_t rounds = (tp * ((rows_q + bn - 1) / bn) + room - 1) / room;
         const double block = lines ? 180 + 0.48 * bn : 200 + 0.765 * bn;
         const double cost = (double)rounds * kblocks * block + 2500.0 * (bn == 256 ? rounds : 1);
@@ -1111,8 +1141,9 @@ template <int GROUPS>
 cudaError_t launch_mm_groups(const Q8& p, const Q8& q, int64_t k, MmArgs& a, int64_t rows_q, cudaStream_t st) {
     const bool lines = ((p.ld | q.ld) & 127) == 0;
     const int64_t n = a.n_groups;
+    const bool room256 = GROUPS != kRowGroups || PairShape<256>::kSmem + PairShape<256>::table(a.n_groups) <= PairShape<256>::kSmemMost;
     const int64_t tp = GROUPS == kRowGroups ? n * ((a.rows_p / n + 255) / 256 + (a.rows_p < n)) : n * (((int64_t)a.rows_p + 255) / 256);
-    switch (pair_width(tp, rows_q, GROUPS == kRowGroups ? a.kblocks : (double)a.kblocks / n, lines)) {
+    switch (pair_width(tp, rows_q, GROUPS == kRowGroups ? a.kblocks : (double)a.kblocks / n, lines, room256 ? 256 : 224)) {
         case 256: return launch_mm_pair<256, GROUPS>(p, q, k, a, st);
         case 224: return launch_mm_pair<224, GROUPS>(p, q, k, a, st);
         case 192: return launch_mm_pair<192, GROUPS>(p, q, k, a, st);

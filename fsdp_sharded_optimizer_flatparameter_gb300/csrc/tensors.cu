@@ -1,12 +1,12 @@
 // AdamW over many tensors at once, and the norm of their gradients (include/zs.h, "many tensors at once").
 //
 // A launch carries the table of up to kTableMost tensors in its parameters (no device memory, nothing to upload, and a
-// captured launch keeps it), and its warps take blocks of 256 elements in turn, whatever tensor they belong to.  All of it
-// moves bytes: with bf16 gradients 28 per element and states of 32 bits, 16.06 with states of 8 bits.
+// captured launch keeps it), and its CTAs take tiles of eight blocks of 256 elements in turn, whatever tensor they belong
+// to.  All of it moves bytes: with bf16 gradients 28 per element and states of 32 bits, 16.06 with states of 8 bits.
 #include <cmath>
 #include <cstring>
 
-#include "q8.cuh"
+#include "q8_tma.cuh"
 
 namespace zs {
 
@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kBlock = ZS_STATE_BLOCK;
 static_assert(kBlock == 256, "a warp's block: eight elements per lane");
+constexpr int kTileBlocks = 8, kTile = kTileBlocks * kBlock;         // a tile: a block for each of eight warps
 constexpr int kTableMost = 448, kTableFew = 48;      // a launch's parameters are at most 32764 bytes; few tensors: under 4 KB
 constexpr int64_t kAligned = int64_t(1) << 62, kNoDecay = int64_t(1) << 61, kCount = kNoDecay - 1;
 
@@ -29,21 +30,26 @@ struct Entry {
 template <int CAP>
 struct Table {
     Entry t[CAP];
-    uint32_t first[CAP];             // blocks of the tensors before
+    uint32_t first[CAP];             // tiles of the tensors before
     uint32_t key[CAP];               // of the tensor's random bits
-    uint32_t blocks;
+    uint32_t tiles;
     int count;
     AdamScalars s;
     float inv_root;                  // 1 / s.sqrt_bc2
+    float one;                       // 1, which the compiler does not know (sum2)
+    uint32_t run;                    // tiles of a CTA
     const float* factor;
     float* partials;
     int add;                         // the norm's partial sums: what earlier launches left counts too
+    unsigned int* error;
+    long long wait_limit;
 };
 static_assert(sizeof(Table<kTableMost>) <= 32764 && sizeof(Table<kTableFew>) <= 4096, "a launch's parameters");
 
-// The tensor that block u belongs to; u >= first[at].
+// The tensor that tile u belongs to, where an earlier tile belonged to `at`.
 template <int CAP>
 __device__ __forceinline__ int find(const Table<CAP>& a, uint32_t u, int at) {
+    if (at + 1 >= a.count || u < a.first[at + 1]) return at;
     int past = a.count;
     while (past - at > 1) {
         const int mid = (at + past) >> 1;
@@ -83,6 +89,11 @@ __device__ __forceinline__ float load_grad(const void* grad, int64_t at) {
 }
 
 // ------------------------------------------------------------------ states in 8 bits
+//
+// Every operation up to a code is rounded once, in the order of the definition, so that a state's bits do not depend on
+// the path that computed them.  With one instruction per operation a step takes about 80 per element, which is all that
+// can be issued while its 16 bytes pass; hence two values per instruction wherever there is one, and no test per value
+// for what is rare: blocks with infinities, NaN or magnitudes past kFastTop go through step8_any.
 
 // The finalizer of murmur3's 32-bit hash (A. Appleby): every bit of x changes every bit of the result about half the time.
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -91,164 +102,462 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// e4m3 code of |t| <= 448 (and rounding), up or down by 16 random bits.  Times 2^-120 the code's bits are fp32's from bit
-// 20 on, subnormal codes among them, and what lies below is the distance from the lower code.
-__device__ __forceinline__ uint32_t state_code(float t, uint32_t random16) {
-    const uint32_t c = (__float_as_uint(fabsf(t) * 0x1p-120f) + (random16 << 4)) >> 20;
-    return c < 0x7e ? c : 0x7e;
-}
-
 constexpr float kLeastTop = 0x1p-100f;       // blocks below are zeros: 448 / top would pass fp32's range
+constexpr float kFastTop = 0x1p14f;          // up to here 448 / top * 2^-120 is a normal number
 
-// A block's scale and what its values are multiplied by; top: the largest magnitude in the warp, as bits.
-__device__ __forceinline__ float block_scale(uint32_t top, float& inverse) {
-    const float t = __uint_as_float(top);
+// A block's scale and what its values are multiplied by; t: their largest magnitude.
+__device__ __forceinline__ float block_scale(float t, float& inverse) {
     const bool some = t >= kLeastTop;
-    inverse = some ? __fdividef(448.f, t) : 0.f;
-    return some ? t * (1.f / 448.f) : 0.f;
+    inverse = some ? __fmul_rn(448.f, __frcp_rn(t)) : 0.f;
+    return some ? __fmul_rn(t, 1.f / 448.f) : 0.f;
 }
 
-// The values x in 8 bits, POSITIVE: they are not negative, and what is above 0 gets no code 0.  `random`: 16 bits per
-// value, the lower or the upper half.  Infinities and NaN have the code NaN and leave the scale alone.
+// An element's two lots of 16 random bits: m's, r's.
+struct Random {
+    uint32_t m, r;
+};
+__device__ __forceinline__ Random random_bits(uint32_t x) {          // x: the hash before its last step
+    const uint32_t hi = x >> 16;
+    return {(x ^ hi) & 0xffffu, hi};
+}
+
+// Magnitudes times 2^-120 have their e4m3 code from bit 20 on, subnormal codes among them, and below it their distance from
+// that code: with 16 random bits added there (at most 2^20 - 16: a largest magnitude that rounding took a little past
+// 448 does not reach the next) the code is that of the lower neighbour or of the upper.
+__device__ __forceinline__ uint32_t raised(uint32_t bits, uint32_t random16) { return bits + (random16 << 4); }
+// Four codes in the order of their elements: bits 20 to 26, and the sign from bit 31.
+__device__ __forceinline__ uint32_t two_codes(uint32_t a, uint32_t b) {          // at bits 8 to 15 and 24 to 31
+    const uint32_t w = __byte_perm(a, b, 0x7632);
+    return ((w << 4) & 0x7fff7fffu) | (w & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t four_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(two_codes(a, b), two_codes(c, d), 0x7531);
+}
+
+// a + b, each sum rounded once, in a form that is not contracted with the products that a and b are (as mul.rn.f32x2 and
+// add.rn.f32x2 are, and a fused multiplication by a 1 that is known).
+__device__ __forceinline__ float2 sum2(float2 a, float one, float2 b) { return q8_fma2(a, make_float2(one, one), b); }
+
+// Square root rounded to nearest, given -2^66 y: from the hardware's reciprocal root one correction by the residual
+// y - s^2, which fused multiplication gives exactly (P. Markstein, 1990); equal to __fsqrt_rn for every y of [2^-126, 2^54).
+// 2^66 y has a normal root for every y > 0, and the result is exact to scale back; y = 0 gives 0.
+__device__ __forceinline__ float2 root2(float2 minus) {
+    float2 q;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(fmaxf(-minus.x, 0x1p-126f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(fmaxf(-minus.y, 0x1p-126f)));
+    const float2 s = q8_mul2(minus, q), h = q8_mul2(q, make_float2(0.5f, 0.5f));         // s: minus the root
+    return q8_mul2(q8_fma2(q8_fma2(s, s, minus), h, s), make_float2(-0x1p-33f, -0x1p-33f));
+}
+
+// max(top, |x.x|, |x.y|), NaN if one is.
+__device__ __forceinline__ float top_nan(float top, float2 x) {
+    float d;
+    asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %2;\n\tabs.f32 b, %3;\n\tmax.NaN.f32 %0, %1, a, b;\n\t}" : "=f"(d) : "f"(top), "f"(x.x), "f"(x.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Within one unit in the last place; a root above 0 is at least 2^-75, so nothing subnormal comes here.
+__device__ __forceinline__ float reciprocal(float x) {
+    float d;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
+
+struct Scalars8 {
+    float beta1, beta2, eps, decay, c1, c2, step_size, inv_root, one;
+};
+
+// A lane's eight elements.  m, v: their old codes; ms, vs: the block's scales.
+struct Codes8 {
+    uint2 m, v;
+    float ms, vs;
+};
+__device__ __forceinline__ void decode8(uint2 c, float scale, float2 (&f)[4]) {
+    f[0] = q8_mul2(q8_unpack2(c.x & 0xffffu), both(scale));
+    f[1] = q8_mul2(q8_unpack2(c.x >> 16), both(scale));
+    f[2] = q8_mul2(q8_unpack2(c.y & 0xffffu), both(scale));
+    f[3] = q8_mul2(q8_unpack2(c.y >> 16), both(scale));
+}
+
+// One step of eight elements per lane, a block per warp.  g: the gradients, p: the masters, updated; hash: element 0's
+// hash after its first shift, APART bits from one element's index to the next (0: neighbours, 5: 32 apart; below the
+// first shift, so they may be put in after it).  Returns whether the block was one for this path; c holds the new states.
+template <int APART>
+__device__ __forceinline__ bool step8(const float2 (&g)[4], float2 (&p)[4], Codes8& c, uint32_t hash, float factor, const Scalars8& s) {
+    float2 m[4], r[4];
+    decode8(c.m, c.ms, m);
+    decode8(c.v, c.vs, r);
+    constexpr float kUp = -0x1p66f;
+    float top_m = 0.f, top_r = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 x = q8_mul2(g[k], both(factor));
+        m[k] = sum2(q8_mul2(both(s.beta1), m[k]), s.one, q8_mul2(both(s.c1), x));
+        r[k] = root2(sum2(q8_mul2(both(s.beta2 * kUp), q8_mul2(r[k], r[k])), s.one, q8_mul2(both(s.c2 * kUp), q8_mul2(x, x))));
+        top_m = top_nan(top_m, m[k]);
+        top_r = top_nan(top_r, r[k]);
+    }
+    const uint32_t bits_m = __reduce_max_sync(~0u, __float_as_uint(top_m)), bits_r = __reduce_max_sync(~0u, __float_as_uint(top_r));
+    if (max(bits_m, bits_r) > __float_as_uint(kFastTop)) return false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 den = q8_fma2(r[k], both(s.inv_root), both(s.eps));
+        const float2 step = q8_mul2(m[k], make_float2(reciprocal(den.x), reciprocal(den.y)));
+        p[k] = q8_fma2(both(-s.step_size), step, q8_mul2(p[k], both(s.decay)));
+    }
+    float inv_m, inv_r;
+    c.ms = block_scale(__uint_as_float(bits_m), inv_m);
+    c.vs = block_scale(__uint_as_float(bits_r), inv_r);
+    inv_m *= 0x1p-120f;
+    inv_r *= 0x1p-120f;
+    const uint32_t least = c.vs > 0.f ? 1u << 20 : 0u;
+    uint32_t wm[8], wr[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 tm = q8_mul2(m[k], both(inv_m)), tr = q8_mul2(r[k], both(inv_r));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x = (hash ^ (uint32_t)((2 * k + h) << APART)) * 0x85ebca6bu;
+            x = (x ^ (x >> 13)) * 0xc2b2ae35u;
+            const Random random = random_bits(x);
+            wm[2 * k + h] = raised(__float_as_uint(h ? tm.y : tm.x), random.m);
+            // above 0 a root's bits are above `least`
+            wr[2 * k + h] = max(raised(__float_as_uint(h ? tr.y : tr.x), random.r), min(__float_as_uint(h ? r[k].y : r[k].x), least));
+        }
+    }
+    c.m = make_uint2(four_codes(wm[0], wm[1], wm[2], wm[3]), four_codes(wm[4], wm[5], wm[6], wm[7]));
+    c.v = make_uint2(four_codes(wr[0], wr[1], wr[2], wr[3]), four_codes(wr[4], wr[5], wr[6], wr[7]));
+    return true;
+}
+
+// A state's values in 8 bits, whatever they are: infinities and NaN have the code NaN and leave the scale alone.
 template <bool POSITIVE>
-__device__ __forceinline__ void encode_state(const float (&x)[8], const uint32_t (&random)[8], uint32_t (&code)[8], float& scale) {
+__device__ uint2 encode8_any(const float (&x)[8], const uint32_t (&random)[8], float& scale) {
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-    top = __reduce_max_sync(~0u, top);
-    const bool bad = top >= 0x7f800000u;
-    if (bad) {
-        top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(x[j]) & 0x7fffffffu;
-            if (b < 0x7f800000u) top = max(top, b);
-        }
-        top = __reduce_max_sync(~0u, top);
-    }
+    for (int j = 0; j < 8; ++j)
+        if (isfinite(x[j])) top = max(top, __float_as_uint(fabsf(x[j])));
     float inverse;
-    scale = block_scale(top, inverse);
+    scale = block_scale(__uint_as_float(__reduce_max_sync(~0u, top)), inverse);
+    uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = x[j] * inverse;
-        uint32_t c = state_code(t, POSITIVE ? random[j] >> 16 : random[j] & 0xffffu);
-        if (POSITIVE) c = c == 0 && t > 0.f ? 1 : c;
-        if (!POSITIVE) c |= (__float_as_uint(t) >> 24) & 0x80u;
-        if (bad && (__float_as_uint(x[j]) & 0x7fffffffu) >= 0x7f800000u) c = 0x7f;
-        code[j] = c;
+        const float t = __fmul_rn(x[j], inverse);
+        uint32_t c = raised(__float_as_uint(__fmul_rn(t, 0x1p-120f)), random[j]);
+        if (POSITIVE && t > 0.f) c = max(c, 1u << 20);
+        w[j] = isfinite(x[j]) ? c : 0x7f00000u;
+    }
+    return make_uint2(four_codes(w[0], w[1], w[2], w[3]), four_codes(w[4], w[5], w[6], w[7]));
+}
+// A block of any size at any address: lane l has elements l, l + 32, .. of it, so that unaligned arrays too are read and
+// written line by line.
+template <bool G32>
+struct Strided {
+    const Entry& t;
+    int64_t begin;
+    int left;                        // elements of the tensor from the block on, if fewer than a block
+    __device__ __forceinline__ Strided(const Entry& entry, int64_t block) : t(entry), begin(block * kBlock + (threadIdx.x & 31)) {
+        const int64_t n = (entry.n & kCount) - block * kBlock;
+        left = (n < kBlock ? (int)n : kBlock) - (int)(threadIdx.x & 31);
+    }
+    __device__ __forceinline__ bool live(int j) const { return 32 * j < left; }
+    __device__ __forceinline__ void load(float (&g)[8], float (&p)[8], Codes8& c, int64_t block) const {
+        uint32_t cm[8], cv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t i = begin + 32 * j;
+            g[j] = live(j) ? load_grad<G32>(t.grad, i) : 0.f;
+            p[j] = live(j) ? __ldcs(t.master + i) : 0.f;
+            cm[j] = live(j) ? __ldcs(static_cast<const uint8_t*>(t.m) + i) : 0;
+            cv[j] = live(j) ? __ldcs(static_cast<const uint8_t*>(t.v) + i) : 0;
+        }
+        auto pack4 = [](const uint32_t* x) { return x[0] | (x[1] << 8) | (x[2] << 16) | (x[3] << 24); };
+        c = Codes8{make_uint2(pack4(cm), pack4(cm + 4)), make_uint2(pack4(cv), pack4(cv + 4)), t.m_scale[block], t.v_scale[block]};
+    }
+    __device__ __forceinline__ void store(const float (&p)[8], const Codes8& c, int64_t block) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!live(j)) break;
+            const int64_t i = begin + 32 * j;
+            t.master[i] = p[j];
+            if (t.param) t.param[i] = f32_to_bf16(p[j]);
+            static_cast<uint8_t*>(t.m)[i] = (uint8_t)((j < 4 ? c.m.x : c.m.y) >> (8 * (j & 3)));
+            static_cast<uint8_t*>(t.v)[i] = (uint8_t)((j < 4 ? c.v.x : c.v.y) >> (8 * (j & 3)));
+        }
+        if ((threadIdx.x & 31) == 0) {
+            t.m_scale[block] = c.ms;
+            t.v_scale[block] = c.vs;
+        }
+    }
+};
+
+template <int CAP>
+__device__ __forceinline__ Scalars8 scalars8(const Table<CAP>& a, const Entry& t) {
+    return Scalars8{a.s.beta1, a.s.beta2, a.s.eps, t.n & kNoDecay ? 1.f : a.s.decay, a.s.c1, a.s.c2, a.s.step_size, a.inv_root, a.one};
+}
+// The hash of element i of a block's tensor after its first shift.
+template <int CAP>
+__device__ __forceinline__ uint32_t hash_of(const Table<CAP>& a, int e, int64_t i) {
+    const uint32_t x = (uint32_t)i ^ mix(a.key[e] + (uint32_t)(i >> 32));
+    return x ^ (x >> 16);
+}
+
+// A step of a block with whatever values.
+template <bool G32, int CAP>
+__device__ __noinline__ void step_any(const Table<CAP>& a, int e, int64_t block, float factor) {
+    const Strided<G32> at(a.t[e], block);
+    const Scalars8 s = scalars8(a, a.t[e]);
+    const uint32_t hash = hash_of(a, e, at.begin);
+    float g[8], p[8], m[8], r[8];
+    uint32_t random_m[8], random_r[8];
+    Codes8 c;
+    at.load(g, p, c, block);
+    q8_unpack4(c.m.x, c.ms, m);
+    q8_unpack4(c.m.y, c.ms, m + 4);
+    q8_unpack4(c.v.x, c.vs, r);
+    q8_unpack4(c.v.y, c.vs, r + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = __fmul_rn(g[j], factor);
+        m[j] = __fadd_rn(__fmul_rn(s.beta1, m[j]), __fmul_rn(s.c1, x));
+        r[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(r[j], r[j])), __fmul_rn(s.c2, __fmul_rn(x, x))));
+        p[j] = fmaf(-s.step_size, __fmul_rn(m[j], reciprocal(fmaf(r[j], s.inv_root, s.eps))), __fmul_rn(p[j], s.decay));
+        uint32_t h = (hash ^ (uint32_t)(32 * j)) * 0x85ebca6bu;
+        h = (h ^ (h >> 13)) * 0xc2b2ae35u;
+        const Random random = random_bits(h);
+        random_m[j] = random.m;
+        random_r[j] = random.r;
+    }
+    c.m = encode8_any<false>(m, random_m, c.ms);
+    c.v = encode8_any<true>(r, random_r, c.vs);
+    at.store(p, c, block);
+}
+
+__device__ __forceinline__ void to_pairs(const float (&f)[8], float2 (&d)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = make_float2(f[2 * k], f[2 * k + 1]);
+}
+__device__ __forceinline__ void of_pairs(const float2 (&d)[4], float (&f)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = d[k].x;
+        f[2 * k + 1] = d[k].y;
     }
 }
 
-__device__ __forceinline__ uint2 pack_codes(const uint32_t (&c)[8]) {
-    return make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+// A step of a block that is not whole or not aligned.
+template <bool G32, int CAP>
+__device__ __noinline__ void step_strided(const Table<CAP>& a, int e, int64_t block, float factor) {
+    const Strided<G32> at(a.t[e], block);
+    float gf[8], pf[8];
+    Codes8 c;
+    at.load(gf, pf, c, block);
+    float2 g[4], p[4];
+    to_pairs(gf, g);
+    to_pairs(pf, p);
+    if (!step8<5>(g, p, c, hash_of(a, e, at.begin), factor, scalars8(a, a.t[e]))) {
+        step_any<G32>(a, e, block, factor);
+        return;
+    }
+    of_pairs(p, pf);
+    at.store(pf, c, block);
 }
-__device__ __forceinline__ float code_value(uint32_t c) { return q8_unpack2(c).x; }
 
 // ------------------------------------------------------------------ the step
 
-// One block of a tensor per warp.
+// States of 32 bits: the arithmetic of the flat step, bit for bit, for a block that is not whole or not aligned.
+template <bool G32, int CAP>
+__device__ __noinline__ void step_strided32(const Table<CAP>& a, int e, int64_t block, float factor) {
+    const Entry& t = a.t[e];
+    const int64_t n = t.n & kCount, begin = block * kBlock + (threadIdx.x & 31);
+    float *tm = static_cast<float*>(t.m), *tv = static_cast<float*>(t.v);
+    float g[8], p[8], m[8], v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t i = begin + 32 * j;
+        const bool live = i < n;
+        g[j] = live ? load_grad<G32>(t.grad, i) : 0.f;
+        p[j] = live ? __ldcs(t.master + i) : 0.f;
+        m[j] = live ? __ldcs(tm + i) : 0.f;
+        v[j] = live ? __ldcs(tv + i) : 0.f;
+    }
+    AdamScalars s = a.s;
+    if (t.n & kNoDecay) s.decay = 1.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) adamw_elem(__fmul_rn(g[j], factor), p[j], m[j], v[j], s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t i = begin + 32 * j;
+        if (i >= n) break;
+        t.master[i] = p[j];
+        if (t.param) t.param[i] = f32_to_bf16(p[j]);
+        tm[i] = m[j];
+        tv[i] = v[j];
+    }
+}
+
+// A ring of tiles in shared memory: one warp brings whole aligned tiles there by bulk copies (their scales, at any 4-byte
+// address, by 4-byte copies that count on the same barrier), eight warps work on a block each and write it from
+// registers.  Of any other tile only its place is passed on, and the warps read its blocks themselves.
+template <bool G32, bool Q>
+struct Ring8 {
+    static constexpr int kGrad = kTile * (G32 ? 4 : 2), kState = kTile * (Q ? 1 : 4);
+    static constexpr int kScales = Q ? 2 * kTileBlocks * 4 : 0;
+    static constexpr int kBulk = kGrad + kTile * 4 + 2 * kState;     // a stage: gradients, masters, m, v, scales
+    static constexpr int kStage = kBulk + kScales;
+    static constexpr int kStages = Q ? (G32 ? 3 : 4) : 2;            // 57 to 66 KB, three CTAs per SM
+};
+struct Job {                         // a stage's tile
+    int64_t block;                   // of the tensor
+    int e;
+    uint32_t whole;
+};
+constexpr int kStepCtas = 3, kNormCtas = 8;          // resident CTAs per SM
+constexpr int kWorkers = 32 * kTileBlocks, kStepThreads = kWorkers + 32;
+template <bool G32, bool Q>
+constexpr int kStepSmem = Ring8<G32, Q>::kStages * (Ring8<G32, Q>::kStage + (int)sizeof(Job) + 16) + 64;
+
+// bytes (a multiple of 16) from src to dst, both 16-byte aligned, counted on bar.
+__device__ __forceinline__ void bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)), "l"(src),
+                 "r"(bytes), "r"(su32(bar))
+                 : "memory");
+}
+
 template <bool G32, bool Q, int CAP>
-__global__ void __launch_bounds__(256) k_adamw_tensors(const __grid_constant__ Table<CAP> a) {
+__global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const __grid_constant__ Table<CAP> a) {
+    using R = Ring8<G32, Q>;
+    extern __shared__ __align__(128) uint8_t ring_sh[];
+    Job* jobs = reinterpret_cast<Job*>(ring_sh + R::kStages * R::kStage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(jobs + R::kStages);
+    uint64_t* empty = full + R::kStages;
+    uint32_t* sent = reinterpret_cast<uint32_t*>(empty + R::kStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R::kStages; ++i) {
+            mbar_init(full + i, 33);             // the bulk copies' bytes, and what each of 32 lanes copies besides
+            mbar_init(empty + i, kTileBlocks);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     dependent_launch_prologue();
-    const int lane = threadIdx.x & 31;
-    const uint32_t warps = (uint32_t)(gstride() >> 5);
+    __syncthreads();
     const float factor = a.factor ? *a.factor : 1.f;
     if (isnan(factor)) return;                   // gradients that are not finite: no step
-    int e = 0;
-    for (uint32_t u = (uint32_t)(gtid() >> 5); u < a.blocks; u += warps) {
-        e = find(a, u, e);
-        const Entry& t = a.t[e];
-        const int64_t n = t.n & kCount, block = u - a.first[e], begin = block * kBlock;
-        const bool whole = (t.n & kAligned) && n - begin >= kBlock;
-        const int64_t at = begin + (whole ? lane * 8 : lane);
-        float g[8], p[8], m[8], v[8];
-        float ms = 0.f, vs = 0.f;
-        if (Q) {
-            ms = t.m_scale[block];
-            vs = t.v_scale[block];
+    const uint32_t begin = blockIdx.x * a.run, end = min(a.tiles, begin + a.run);
+    int at = 0;
+    uint32_t round = 0;
+    auto next = [&] {
+        if (++at == R::kStages) {
+            at = 0;
+            ++round;
         }
-        if (whole) {
-            load_grad8<G32>(t.grad, at, g);
-            load8(t.master + at, p);
-            if (Q) {
-                const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at));
-                const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + at));
-                q8_unpack4(cm.x, ms, m);
-                q8_unpack4(cm.y, ms, m + 4);
-                q8_unpack4(cv.x, vs, v);
-                q8_unpack4(cv.y, vs, v + 4);
-            } else {
-                load8(static_cast<const float*>(t.m) + at, m);
-                load8(static_cast<const float*>(t.v) + at, v);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t i = at + 32 * j;
-                const bool live = i < n;
-                g[j] = live ? load_grad<G32>(t.grad, i) : 0.f;
-                p[j] = live ? __ldcs(t.master + i) : 0.f;
-                if (Q) {
-                    m[j] = live ? code_value(static_cast<const uint8_t*>(t.m)[i]) * ms : 0.f;
-                    v[j] = live ? code_value(static_cast<const uint8_t*>(t.v)[i]) * vs : 0.f;
-                } else {
-                    m[j] = live ? __ldcs(static_cast<const float*>(t.m) + i) : 0.f;
-                    v[j] = live ? __ldcs(static_cast<const float*>(t.v) + i) : 0.f;
+    };
+    if (warp == kTileBlocks) {
+        int e = 0;
+        bool ok = true;
+        for (uint32_t u = begin; u < end; ++u) {
+            e = find(a, u, e);
+            const Entry& t = a.t[e];
+            const int64_t block = (int64_t)(u - a.first[e]) * kTileBlocks, i = block * kBlock;
+            const bool whole = (t.n & kAligned) && (t.n & kCount) - i >= kTile;
+            if (round > 0 && !(ok = __all_sync(~0u, mbar_wait_or_look(empty + at, (round & 1) ^ 1, a.wait_limit)))) break;
+            uint8_t* to = ring_sh + at * R::kStage;
+            if (lane == 0) jobs[at] = Job{block, e, whole};
+            if (whole) {
+                if (lane == 0) {
+                    mbar_expect_tx(full + at, R::kBulk);
+                    bulk(to, static_cast<const uint8_t*>(t.grad) + i * (G32 ? 4 : 2), R::kGrad, full + at);
+                    bulk(to + R::kGrad, t.master + i, kTile * 4, full + at);
+                    bulk(to + R::kGrad + kTile * 4, static_cast<const uint8_t*>(t.m) + i * (Q ? 1 : 4), R::kState, full + at);
+                    bulk(to + R::kGrad + kTile * 4 + R::kState, static_cast<const uint8_t*>(t.v) + i * (Q ? 1 : 4), R::kState, full + at);
                 }
-            }
-        }
-        AdamScalars s = a.s;
-        if (t.n & kNoDecay) s.decay = 1.f;
-        uint32_t cm[8], cv[8];
-        if (Q) {
-            const uint32_t key = mix(a.key[e] + (uint32_t)(begin >> 32));
-            uint32_t random[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = g[j] * factor;
-                m[j] = fmaf(s.beta1, m[j], s.c1 * x);
-                const float y = fmaf(s.beta2, v[j] * v[j], s.c2 * (x * x));
-                asm("sqrt.approx.f32 %0, %1;" : "=f"(v[j]) : "f"(y));
-                p[j] = fmaf(-s.step_size, __fdividef(m[j], fmaf(v[j], a.inv_root, s.eps)), p[j] * s.decay);
-                random[j] = mix((uint32_t)(at + (whole ? j : 32 * j)) ^ key);
-            }
-            encode_state<false>(m, random, cm, ms);
-            encode_state<true>(v, random, cv, vs);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) adamw_elem(__fmul_rn(g[j], factor), p[j], m[j], v[j], s);
-        }
-        if (whole) {
-            store8(t.master + at, p);
-            if (t.param) st_bf<8>(t.param + at, pack(p));
-            if (Q) {
-                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + at), pack_codes(cm));
-                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + at), pack_codes(cv));
-            } else {
-                store8(static_cast<float*>(t.m) + at, m);
-                store8(static_cast<float*>(t.v) + at, v);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t i = at + 32 * j;
-                if (i >= n) break;
-                t.master[i] = p[j];
-                if (t.param) t.param[i] = f32_to_bf16(p[j]);
-                if (Q) {
-                    static_cast<uint8_t*>(t.m)[i] = (uint8_t)cm[j];
-                    static_cast<uint8_t*>(t.v)[i] = (uint8_t)cv[j];
-                } else {
-                    static_cast<float*>(t.m)[i] = m[j];
-                    static_cast<float*>(t.v)[i] = v[j];
+                if (Q && lane < 2 * kTileBlocks) {
+                    const float* from = (lane < kTileBlocks ? t.m_scale : t.v_scale) + block + lane % kTileBlocks;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(to + R::kBulk + lane * 4)), "l"(from) : "memory");
                 }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(full + at)) : "memory");
+            } else {
+                if (lane == 0) mbar_arrive(full + at);
+                mbar_arrive(full + at);
             }
+            __syncwarp();
+            next();
         }
-        if (Q && lane == 0) {
-            t.m_scale[block] = ms;
-            t.v_scale[block] = vs;
+        if (lane == 0) *sent = round * R::kStages + at;
+        if (!ok && lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_TENSORS_WAIT);
+    } else {
+        for (uint32_t u = begin; u < end; ++u, next()) {
+            if (!__all_sync(~0u, mbar_wait_or_look(full + at, round & 1, a.wait_limit))) {
+                if (lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_TENSORS_WAIT);
+                break;
+            }
+            const Job job = jobs[at];
+            const Entry& t = a.t[job.e];
+            const int64_t block = job.block + warp, i = block * kBlock + lane * 8;
+            if (!job.whole) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + at);
+                if (block * kBlock < (t.n & kCount)) {
+                    if constexpr (Q) step_strided<G32>(a, job.e, block, factor);
+                    else step_strided32<G32>(a, job.e, block, factor);
+                }
+                continue;
+            }
+            const uint8_t* from = ring_sh + at * R::kStage;
+            const int mine = warp * kBlock + lane * 8;
+            float g[8], p[8];
+            auto floats = [](const uint8_t* q, float (&f)[8]) {
+                const float4 x = reinterpret_cast<const float4*>(q)[0], y = reinterpret_cast<const float4*>(q)[1];
+                f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+                f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+            };
+            if constexpr (G32) floats(from + mine * 4, g);
+            else unpack(BfVec<8>{*reinterpret_cast<const uint4*>(from + mine * 2)}, g);
+            from += R::kGrad;
+            floats(from + mine * 4, p);
+            from += kTile * 4;
+            if constexpr (Q) {
+                const float* scales = reinterpret_cast<const float*>(from + 2 * R::kState);
+                Codes8 c{*reinterpret_cast<const uint2*>(from + mine), *reinterpret_cast<const uint2*>(from + R::kState + mine), scales[warp],
+                         scales[kTileBlocks + warp]};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + at);
+                float2 gp[4], pp[4];
+                to_pairs(g, gp);
+                to_pairs(p, pp);
+                if (!step8<0>(gp, pp, c, hash_of(a, job.e, i), factor, scalars8(a, t))) {
+                    step_any<G32>(a, job.e, block, factor);
+                    continue;
+                }
+                of_pairs(pp, p);
+                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), c.m);
+                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), c.v);
+                if (lane == 0) {
+                    t.m_scale[block] = c.ms;
+                    t.v_scale[block] = c.vs;
+                }
+            } else {
+                float m[8], v[8];
+                floats(from + mine * 4, m);
+                floats(from + R::kState + mine * 4, v);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + at);
+                AdamScalars s = a.s;
+                if (t.n & kNoDecay) s.decay = 1.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) adamw_elem(__fmul_rn(g[j], factor), p[j], m[j], v[j], s);
+                store8(static_cast<float*>(t.m) + i, m);
+                store8(static_cast<float*>(t.v) + i, v);
+            }
+            store8(t.master + i, p);
+            if (t.param) st_bf<8>(t.param + i, pack(p));
         }
     }
+    __syncthreads();
+    if (warp == 0) ring_settled(full, R::kStages, *sent);        // no copy is under way when the CTA goes
 }
 
 // ------------------------------------------------------------------ the gradients' norm
@@ -266,8 +575,9 @@ __device__ __forceinline__ double block_sum(double x) {
     return x;
 }
 
-// A lane adds eight squares in fp32, and those sums in fp64.  The CTAs' sums are rounded to fp32 (they are as many as the
-// caller has room for, each of its own blocks, so the same bits every time) and added by one CTA.
+// A lane adds a tile's 64 squares in fp32, and those sums in fp64 (one fp64 addition per block of 256 alone took the
+// time of twice the bytes: 402 M bf16 gradients 210 us).  The CTAs' sums (as many as the caller has room for, each of
+// its own blocks, so the same bits every time) are kept as two fp32 words each and added by one CTA.
 template <bool G32, int CAP>
 __global__ void __launch_bounds__(256) k_grad_norm(const __grid_constant__ Table<CAP> a) {
     dependent_launch_prologue();
@@ -275,34 +585,49 @@ __global__ void __launch_bounds__(256) k_grad_norm(const __grid_constant__ Table
     const uint32_t warps = (uint32_t)(gstride() >> 5);
     double sum = 0.0;
     int e = 0;
-    for (uint32_t u = (uint32_t)(gtid() >> 5); u < a.blocks; u += warps) {
+    for (uint32_t u = (uint32_t)(gtid() >> 5); u < a.tiles; u += warps) {
         e = find(a, u, e);
         const Entry& t = a.t[e];
-        const int64_t n = t.n & kCount, begin = (int64_t)(u - a.first[e]) * kBlock;
-        const bool whole = (t.n & kAligned) && n - begin >= kBlock;
-        float g[8];
+        const int64_t n = t.n & kCount, begin = (int64_t)(u - a.first[e]) * kTile;
+        const bool whole = (t.n & kAligned) && n - begin >= kTile;
+        float q[kTileBlocks];
         if (whole) {
-            load_grad8<G32>(t.grad, begin + lane * 8, g);
+#pragma unroll
+            for (int b = 0; b < kTileBlocks; ++b) {
+                float g[8];
+                load_grad8<G32>(t.grad, begin + b * kBlock + lane * 8, g);
+                q[b] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[b] = fmaf(g[j], g[j], q[b]);
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t i = begin + lane + 32 * j;
-                g[j] = i < n ? load_grad<G32>(t.grad, i) : 0.f;
+            for (int b = 0; b < kTileBlocks; ++b) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t i = begin + b * kBlock + lane + 32 * j;
+                    const float g = i < n ? load_grad<G32>(t.grad, i) : 0.f;
+                    s = fmaf(g, g, s);
+                }
+                q[b] = s;
             }
         }
-        float q = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q = fmaf(g[j], g[j], q);
-        sum += q;
+        sum += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
     }
     sum = block_sum(sum);
-    if (threadIdx.x == 0) a.partials[blockIdx.x] = (float)(a.add ? sum + a.partials[blockIdx.x] : sum);
+    if (threadIdx.x == 0) {
+        float* p = a.partials + 2 * blockIdx.x;
+        if (a.add) sum += (double)p[0] + p[1];
+        p[0] = (float)sum;
+        p[1] = isfinite(p[0]) ? (float)(sum - p[0]) : 0.f;
+    }
 }
 
 __global__ void __launch_bounds__(256) k_grad_norm_end(const float* partials, int n, float max_norm, float* out) {
     dependent_launch_prologue();
     double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) sum += partials[i];
+    for (int i = threadIdx.x; i < n; i += 256) sum += (double)partials[2 * i] + partials[2 * i + 1];
     sum = block_sum(sum);
     if (threadIdx.x == 0) {
         const float norm = (float)sqrt(sum);
@@ -337,11 +662,12 @@ int check_tensor(const char* fn, const zs_tensor& t, int i, int grad_bytes, int 
     return ZS_OK;
 }
 
-// Whether a whole block's values are read and written eight at a time.
+// Whether whole tiles are copied, and values written eight at a time.
 bool wide_blocks(const zs_tensor& t, int grad_bytes, int state_bits, bool step) {
-    if (!aligned(t.grad, 8 * grad_bytes)) return false;
+    if (!aligned(t.grad, step ? 16 : 8 * grad_bytes)) return false;
     if (!step) return true;
-    return aligned(t.master, 32) && aligned(t.param, 16) && aligned(t.m, state_bits) && aligned(t.v, state_bits);
+    const uintptr_t state = state_bits == 8 ? 16 : 32;
+    return aligned(t.master, 32) && aligned(t.param, 16) && aligned(t.m, state) && aligned(t.v, state);
 }
 
 // Calls launch(table, first) for the tensors, as many at a time as a launch's parameters hold.
@@ -351,22 +677,22 @@ cudaError_t by_table(const zs_tensor* tensors, int count, int grad_bytes, int st
     int i = 0;
     do {
         a.count = 0;
-        uint64_t blocks = 0;
+        uint64_t tiles = 0;
         for (; i < count && a.count < CAP; ++i) {
             const zs_tensor& t = tensors[i];
             if (t.n == 0) continue;
-            const uint64_t more = (uint64_t)(t.n + kBlock - 1) / kBlock;
-            if (a.count && blocks + more > 0x7fffffffu) break;
+            const uint64_t more = (uint64_t)(t.n + kTile - 1) / kTile;
+            if (a.count && tiles + more > 0x7fffffffu) break;
             Entry& e = a.t[a.count];
             e = Entry{t.grad, t.master, (uint16_t*)t.param, t.m, t.v, t.m_scale, t.v_scale, t.n};
             if (wide_blocks(t, grad_bytes, state_bits, step)) e.n |= kAligned;
             if (t.no_decay) e.n |= kNoDecay;
-            a.first[a.count] = (uint32_t)blocks;
+            a.first[a.count] = (uint32_t)tiles;
             a.key[a.count] = mix(seed + 0x9e3779b9u * ((uint32_t)i + 1));
-            blocks += more;
+            tiles += more;
             ++a.count;
         }
-        a.blocks = (uint32_t)blocks;
+        a.tiles = (uint32_t)tiles;
         if (a.count || first) {
             const cudaError_t rc = launch(a, first);
             if (rc != cudaSuccess) return rc;
@@ -376,28 +702,38 @@ cudaError_t by_table(const zs_tensor* tensors, int count, int grad_bytes, int st
     return cudaSuccess;
 }
 
-constexpr int kStepCtas = 6, kNormCtas = 8;          // resident CTAs per SM
 
-unsigned grid_of(uint32_t blocks, int64_t most) {
-    const int64_t ctas = ((int64_t)blocks + 7) / 8;
-    return (unsigned)(ctas < 1 ? 1 : ctas < most ? ctas : most);
-}
+// Tiles of a CTA, at most.  CTAs that end and are replaced take the work as the SMs get through it, which a fixed share for
+// each does not (402 M elements with states in 8 bits, the norm before it: 1266 us in fixed shares; 1165, 1110, 1123 with
+// 4, 8 and 16 tiles.  139 M with states in 32 bits: 614; 546, 557, 573 with 2, 4 and 8).
+constexpr uint32_t kRun8 = 8, kRun32 = 3;
 
 template <bool G32, bool Q, int CAP>
 cudaError_t step_tensors(const zs_tensor* tensors, int count, uint32_t seed, Table<CAP>& a, cudaStream_t st) {
-    return by_table<CAP>(tensors, count, G32 ? 4 : 2, Q ? 8 : 32, true, seed, a, [&](const Table<CAP>& t, bool) {
+    constexpr int smem = kStepSmem<G32, Q>;
+    static_assert(kStepCtas * (smem + 1024) <= 228 * 1024, "resident CTAs");
+    static std::atomic<uint64_t> ready{0};
+    const auto kern = k_adamw_tensors<G32, Q, CAP>;
+    const cudaError_t e = ready_once(ready, (const void*)kern, smem);
+    if (e != cudaSuccess) return e;
+    const uint32_t room = (uint32_t)q8_host::sm_count() * kStepCtas, most = Q ? kRun8 : kRun32;
+    return by_table<CAP>(tensors, count, G32 ? 4 : 2, Q ? 8 : 32, true, seed, a, [&](Table<CAP>& t, bool) {
         if (!t.count) return cudaSuccess;
-        return launch_kernel(k_adamw_tensors<G32, Q, CAP>, dim3(grid_of(t.blocks, (int64_t)q8_host::sm_count() * kStepCtas)), dim3(256), 0, st, t);
+        t.run = t.tiles / (room * 4) < 1 ? 1 : t.tiles / (room * 4) < most ? t.tiles / (room * 4) : most;
+        return launch_kernel(kern, dim3((t.tiles + t.run - 1) / t.run), dim3(kStepThreads), smem, st, t);
     });
 }
 
 template <int CAP>
-cudaError_t step_any(const zs_tensor* tensors, int count, bool g32, bool q, uint32_t seed, const AdamScalars& s, const float* factor,
+cudaError_t step_list(const zs_tensor* tensors, int count, bool g32, bool q, uint32_t seed, const AdamScalars& s, const float* factor,
                      cudaStream_t st) {
     Table<CAP> a;
     a.s = s;
     a.inv_root = (float)(1.0 / (double)s.sqrt_bc2);
+    a.one = 1.f;
     a.factor = factor;
+    a.wait_limit = wait_limit().load(std::memory_order_relaxed);
+    if (const cudaError_t e = error_word(&a.error); e != cudaSuccess) return e;
     return g32 ? (q ? step_tensors<true, true>(tensors, count, seed, a, st) : step_tensors<true, false>(tensors, count, seed, a, st))
                : (q ? step_tensors<false, true>(tensors, count, seed, a, st) : step_tensors<false, false>(tensors, count, seed, a, st));
 }
@@ -442,10 +778,13 @@ extern "C" int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int
     float sc[8];
     ZS_Q8_TRY(zs_adamw_scalars(hp, step, sc));
     const zs::AdamScalars s{sc[0], sc[1], sc[2], sc[3], sc[4], sc[5], sc[6], sc[7]};
+    bool any = false;
+    for (int i = 0; i < n_tensors; ++i) any |= tensors[i].n > 0;
+    if (!any) return ZS_OK;
     const cudaStream_t st = (cudaStream_t)stream;
     return cuda_status(fn, n_tensors <= zs::kTableFew
-                               ? zs::step_any<zs::kTableFew>(tensors, n_tensors, grad_bytes == 4, state_bits == 8, seed, s, factor, st)
-                               : zs::step_any<zs::kTableMost>(tensors, n_tensors, grad_bytes == 4, state_bits == 8, seed, s, factor, st));
+                               ? zs::step_list<zs::kTableFew>(tensors, n_tensors, grad_bytes == 4, state_bits == 8, seed, s, factor, st)
+                               : zs::step_list<zs::kTableMost>(tensors, n_tensors, grad_bytes == 4, state_bits == 8, seed, s, factor, st));
 }
 
 extern "C" int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, float max_norm, float* partials,
@@ -455,14 +794,15 @@ extern "C" int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t
     zs::clear_error();
     if (!(max_norm > 0.f) || !std::isfinite(max_norm)) return fail(fn, "max_norm must be positive and finite");
     if (!partials || !zs::aligned(partials, 4)) return fail(fn, "partials is NULL or not 4-byte aligned");
-    if (n_partials < 1) return fail(fn, "n_partials must be at least 1");
+    if (n_partials < 2) return fail(fn, "n_partials must be at least 2");
     if (!out || !zs::aligned(out, 4)) return fail(fn, "out is NULL or not 4-byte aligned");
     ZS_Q8_TRY(zs::check_list(fn, tensors, n_tensors, grad_bytes, 32, false));
     const cudaStream_t st = (cudaStream_t)stream;
-    int64_t blocks = 0;
-    for (int i = 0; i < n_tensors; ++i) blocks += (tensors[i].n + zs::kBlock - 1) / zs::kBlock;
-    const int64_t most = (int64_t)sm_count() * zs::kNormCtas;
-    const int n = (int)zs::grid_of((uint32_t)(blocks < 0x7fffffff ? blocks : 0x7fffffff), n_partials < most ? n_partials : most);
+    int64_t tiles = 0;
+    for (int i = 0; i < n_tensors; ++i) tiles += (tensors[i].n + zs::kTile - 1) / zs::kTile;
+    int64_t most = (int64_t)sm_count() * zs::kNormCtas, ctas = (tiles + 7) / 8;
+    if (most > n_partials / 2) most = n_partials / 2;
+    const int n = (int)(ctas < 1 ? 1 : ctas < most ? ctas : most);
     const bool few = n_tensors <= zs::kTableFew;
     cudaError_t e;
     if (grad_bytes == 4) e = few ? zs::norm_tensors<true, zs::kTableFew>(tensors, n_tensors, partials, n, st) : zs::norm_tensors<true, zs::kTableMost>(tensors, n_tensors, partials, n, st);

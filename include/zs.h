@@ -115,6 +115,7 @@ extern "C" {
 #define ZS_DEVERR_GATHER_WAIT   4u   /* a bulk-store gather gave up waiting for its tile             */
 #define ZS_DEVERR_MATMUL_WAIT   5u   /* zs_q8_matmul gave up waiting for a tile or an accumulator    */
 #define ZS_DEVERR_TILE_WAIT     6u   /* an 8-bit encode, transpose, gate or norm backward gave up    */
+#define ZS_DEVERR_TENSORS_WAIT  7u   /* zs_adamw_tensors gave up waiting for a tile                  */
 
 typedef struct zs_plan_s* zs_plan_t;
 
@@ -256,7 +257,7 @@ int zs_device_status(uint32_t* code, int32_t clear);
  * Errors: ZS_ERR_INVALID for a limit out of range; ZS_ERR_CUDA. */
 int zs_selftest_wait_timeout(int64_t limit_cycles, void* stream);
 
-/* What a wait of the 8-bit operators' kernels may take, in SM cycles (0 .. 2^32; the
+/* What a wait of the 8-bit operators' kernels and of zs_adamw_tensors may take, in SM cycles (0 .. 2^32; the
  * default is 4 * 10^9, about 2 s), for calls of the whole process from now on.
  * With 0 a wait looks once and gives up, which is how a test sees it: the call
  * records its ZS_DEVERR_* code, lets everything under way arrive, and returns
@@ -871,11 +872,10 @@ int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_b
 
 /* The 2-norm of all gradients of the list and the factor that clips it:
  *     out[0] = sqrt( sum of grad^2 ),   out[1] = min(1, max_norm / (out[0] + 1e-6))
- * Squares are fp32 (|grad| below 1.8e19), their sums fp64 and rounded to fp32 once per
- * partial sum.  A norm that is not finite gives out[1] = NaN.  Only n and grad of the
- * tensors are used.
- *   partials    caller's scratch, n_partials floats; at most 8 per SM are used, fewer make
- *               the call slower.
+ * Squares and sums of 64 are fp32 (|grad| below 2e18), the sums of these fp64.  A
+ * norm that is not finite gives out[1] = NaN.  Only n and grad of the tensors are used.
+ *   partials    caller's scratch, n_partials >= 2 floats, two per partial sum; at most 16
+ *               per SM are used, fewer make the call slower.
  *   out         two floats. */
 int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, float max_norm, float* partials,
                  int64_t n_partials, float* out, void* stream);

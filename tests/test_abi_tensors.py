@@ -62,7 +62,7 @@ def test_step_refuses_a_missing_list():
 @pytest.mark.parametrize("change,says", [
     (dict(count=-1), "n_tensors"), (dict(grad_bytes=1), "grad_bytes"), (dict(max_norm=0.0), "max_norm"), (dict(max_norm=-1.0), "max_norm"),
     (dict(max_norm=NAN), "max_norm"), (dict(max_norm=INF), "max_norm"), (dict(partials=None), "partials"), (dict(partials=A + 1), "partials"),
-    (dict(n_partials=0), "n_partials"), (dict(out=None), "out"), (dict(out=A + 2), "out"), (dict(ts=_list(grad=None)), "grad of tensor 1")])
+    (dict(n_partials=0), "n_partials"), (dict(n_partials=1), "n_partials"), (dict(out=None), "out"), (dict(out=A + 2), "out"), (dict(ts=_list(grad=None)), "grad of tensor 1")])
 def test_norm_refuses_a_call(change, says):
     _refused(_norm(**change), "zs_grad_norm", says)
 

@@ -184,7 +184,7 @@ def test_lists_longer_than_a_table(count, bits):
     partials, out = torch.empty(500, device="cuda"), torch.empty(2, device="cuda")
     zs.zs_grad_norm(a.list(), 0.5, partials, out)
     norm, factor = tensors.grad_norm([g.double().cpu().numpy() for g in a.grad], 0.5)
-    # eight squares' chain in fp32, a partial sum's rounding, the root's and the quotient's
+    # squares rounded and eight in a chain, three more additions, halved by the root; a rounding each of the root and the norm
     assert abs(float(out[0]) - norm) <= 8 * U32 * norm and abs(float(out[1]) - factor) <= 12 * U32 * factor
     # the oracle of the update: each tensor's own, in the same place of a list of its own
     key = {}
@@ -295,7 +295,7 @@ def test_a_norm_that_is_not_finite_leaves_the_step_out(bits, bad):
 
 
 @pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("n_partials", [1, 7, 5000])
+@pytest.mark.parametrize("n_partials", [2, 7, 5000])
 @pytest.mark.parametrize("shift", [0, 5])
 def test_norm(grad, n_partials, shift):
     a = Arrays(SIZES + [3000001], 32, grad, shift, seed=8)
