@@ -153,6 +153,32 @@ __device__ __forceinline__ void tmem_load16(uint32_t tmem, float (&f)[16]) {
     for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// 32 columns.
+__device__ __forceinline__ void tmem_load32(uint32_t tmem, float (&f)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(tmem));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+// Tiled stores: a warp's 32 rows x 32 columns of bf16 from 2 KB of shared memory (64-byte swizzle) to column x and row y.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map), "r"(x), "r"(y),
+                 "r"(su32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Writes 16 columns of 32 rows of the result, one row per lane in f: row r of the warp at out + r * ldo.
 // `rows` and `n` are what is valid of them (the same in every lane).  With `align` 32 or 16, rows start at
 // multiples of that many bytes and a lane stores its own segment (a full sector at 32).  Otherwise the
@@ -240,7 +266,8 @@ struct MmArgs {
     long long wait_limit;
     const int* starts;           // of n_groups groups and the last one's end (the experts' products)
     int n_groups;
-    int group_rows;              // rows of Q (kRowGroups) or of out (kSumGroups) that a group has
+    int group_rows;              // rows of Q (kRowGroups), P (kFewRows) or out (kSumGroups) that a group has
+    int tiled;                   // out can be written by tiled copies
     int most_tiles;              // of groups that do not overlap (kRowGroups)
 };
 
@@ -656,10 +683,13 @@ constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at a
 
 // Products of groups in one launch, with the groups' places on the device: a group is an expert's rows.
 //   kRowGroups  P's rows starts[g] .. starts[g + 1] times the group's own group_rows rows of Q
+//   kFewRows    the same product with the operands' places exchanged: a tile is 256 of the group's own rows (of P now)
+//               times as many of the starts' rows as there are, 32 to BN.  A block of the sum takes 180 + 0.48 N ns, so few
+//               rows cost less as N than as 256 rows of P (37 tokens to 2 of 16 experts, 2048 x 4096: FEWFIG).
 //   kSumGroups  the sum over columns starts[g] .. starts[g + 1] (multiples of 128) of both, one result per group
 // Starts out of range are read as the nearest inside; with overlapping groups (more tiles than there can be) nothing is
 // written, so that no tile lies outside.
-enum { kNoGroups = 0, kRowGroups = 1, kSumGroups = 2 };
+enum { kNoGroups = 0, kRowGroups = 1, kSumGroups = 2, kFewRows = 3 };
 
 // What the barriers of a pair's CTA have been or will be sent by copies and products, each to its ring in turn.  A CTA
 // leaves only when all of it has arrived, after a wait that ran out as after the last tile: nothing may be under way
@@ -688,7 +718,7 @@ __device__ __forceinline__ int group_start(const MmArgs& a, int g, int most) {
 template <int BN, int GROUPS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_q8_matmul_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                     const __grid_constant__ MmArgs a) {
+                     const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MmArgs a) {
     constexpr int kStageBytes = PairShape<BN>::kStageBytes, kAccs = PairShape<BN>::kAccs;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (su32(raw) & 1023)) & 1023);
@@ -745,14 +775,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int tiles_p = (int)(((int64_t)a.rows_p + 255) / 256);
     int64_t tiles = (int64_t)tiles_p * a.tiles_q;
     if constexpr (GROUPS == kSumGroups) tiles *= a.n_groups;
-    if constexpr (GROUPS == kRowGroups) {
+    if constexpr (GROUPS == kRowGroups || GROUPS == kFewRows) {
         // Tiles of the groups summed up: a thread adds a few neighbouring groups', the threads' sums are scanned.
         const int each = (a.n_groups + kPairThreads - 1) / kPairThreads, g0 = threadIdx.x * each;
-        for (int g = threadIdx.x; g <= a.n_groups; g += kPairThreads) start[g] = group_start(a, g, a.rows_p);
+        for (int g = threadIdx.x; g <= a.n_groups; g += kPairThreads) start[g] = group_start(a, g, GROUPS == kRowGroups ? a.rows_p : a.rows_q);
         __syncthreads();
         auto tiles_of = [&](int g) {
             const int lo = start[g], hi = start[g + 1];
-            return hi > lo ? (int64_t)((hi - lo + 255) / 256) * a.tiles_q : 0;
+            constexpr int kRows = GROUPS == kRowGroups ? 256 : BN;
+            return hi > lo ? (int64_t)((hi - lo + kRows - 1) / kRows) * a.tiles_q : 0;
         };
         int64_t sum = 0;
         for (int g = g0; g < g0 + each && g < a.n_groups; ++g) sum += tiles_of(g);
@@ -802,6 +833,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             x = Tile{lo + p * 256, 0, hi, (g + 1) * a.group_rows, 0, 0, a.kblocks, 0, g * a.group_rows};
             columns(x, q);
             x.q0 += x.out_col;
+        } else if constexpr (GROUPS == kFewRows) {
+            while (before[g + 1] <= (int)t) ++g;
+            const int in = (int)t - before[g];                                   // of tiles_q x ceil(rows / BN)
+            q = in / a.tiles_q;
+            p = in - q * a.tiles_q;
+            x = Tile{g * a.group_rows + p * 256, start[g] + q * BN, (g + 1) * a.group_rows, start[g + 1], 0, 0, a.kblocks, 0, g * a.group_rows};
+            x.width = x.q_end - x.q0 < BN ? (x.q_end - x.q0 + 31) / 32 * 32 : BN;
         } else if constexpr (GROUPS == kSumGroups) {
             const int per = tiles_p * a.tiles_q, most = a.kblocks * 128;
             g = (int)t / per;
@@ -831,9 +869,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t full0 = at_rank(full, 0);
         for (int64_t t = first_tile; t < tiles && ok; t += step) {
             const Tile x = place(t, group);
-            // rows of P that only the other CTA has are read as zeros past the matrix: neither fetched nor worth power
+            // where a group's rows end in the pair's first half, the second reads zeros past the matrix: not fetched, little power
             const int half = GROUPS == kNoGroups ? BN / 2 : x.width / 2, p = x.p0 + (int)rank * 128;
-            const int row = GROUPS == kRowGroups && p >= x.p_end ? a.rows_p : p;
+            const int row = (GROUPS == kRowGroups || GROUPS == kFewRows) && p >= x.p_end ? a.rows_p : p;
             for (int kb = x.kb0; kb < x.kb0 + x.kbs; ++kb) {
                 if (ring.round > 0 && !(ok = warp_wait_or_look(empty + ring.at, ring.parity() ^ 1, a.wait_limit))) break;
                 uint8_t* at = base + ring.at * kStageBytes;
@@ -965,29 +1003,92 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 break;
             }
             tc_fence_after();
-            const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;             // the warp's first row
-            int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
-            const int kHalf = GROUPS == kNoGroups ? BN / 2 : x.width / 2;                // columns of one warp
-            const int qh = x.q0 + half * kHalf;
-            uint16_t* o = a.out + (x.out_row + p) * a.ldo + (qh - x.out_col);
-            const bool sum = GROUPS != kSumGroups || x.kbs > 0;                  // the empty sum: zeros, or out as it is
-            if (!sum && !a.first) rows = 0;
-            const uint32_t from = tmem + acc.at * BN + half * kHalf + ((uint32_t)(sub * 32) << 16);
+            if constexpr (GROUPS == kFewRows) {
+                // lanes hold neighbouring columns of out, the accumulator's columns are its rows
+                const int col = x.p0 - x.out_col + (int)rank * 128 + sub * 32 + lane;
+                const uint32_t from = tmem + acc.at * BN + ((uint32_t)(sub * 32) << 16);
 #pragma unroll 1
-            for (int c = 0; c < kHalf; c += 16) {
-                float f[16];
-                tmem_load16(from + c, f);
-                if (GROUPS == kSumGroups && !sum) {
+                for (int c = half * 32; c < x.width; c += 64) {
+                    float f[32];
+                    tmem_load32(from + c, f);
+                    uint16_t* o = a.out + (int64_t)(x.q0 + c) * a.ldo + col;
+                    const int rows = col < a.group_rows ? x.q_end - x.q0 - c : 0;
+                    if (!a.first) {
+                        uint16_t was[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = 0.f;
+                        for (int j = 0; j < 32; ++j) was[j] = j < rows ? o[j * a.ldo] : 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = fmaf(f[j], a.scale, bf16_to_f32(was[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] *= a.scale;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < rows) o[j * a.ldo] = f32_to_bf16(f[j]);
                 }
-                store_rows16(o + c, a.ldo, f, rows, x.q_end - qh - c, a.align, a.scale, a.first,
-                             store_sh + (warp - 6) * kStoreStage);
+            } else if constexpr (GROUPS != kNoGroups) {
+                // Pieces of 32 columns, in turn for the two halves of the warps.  Whole pieces that are only written go by tiled
+                // copies: 64 bytes of a row at once and nothing of the warp's time, where its own stores touch 32 lines for 32
+                // bytes each (8 x 5504 x 2048 over 750 rows each, whose tiles are written about as fast as they are
+                // computed: STOREFIG).
+                const bool sum = GROUPS != kSumGroups || x.kbs > 0;              // the empty sum: zeros, or out as it is
+                const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;         // the warp's first row
+                int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
+                if (!sum && !a.first) rows = 0;
+                const bool tiled = a.tiled && rows == 32;
+                const uint32_t from = tmem + acc.at * BN + ((uint32_t)(sub * 32) << 16);
+                float* stage = store_sh + (warp - 6) * kStoreStage;
+#pragma unroll 1
+                for (int c = half * 32; c < x.width; c += 64) {
+                    float f[32];
+                    tmem_load32(from + c, f);
+                    if (GROUPS == kSumGroups && !sum) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = 0.f;
+                    }
+                    if (lane == 0) tma_stores_read();                            // the piece before has left the staging
+                    __syncwarp();
+                    const int q = x.q0 - x.out_col + c;
+                    if (tiled) {
+                        uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(stage) + lane * 64);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[8 * k + 2 * j] * a.scale, f[8 * k + 2 * j + 1] * a.scale);
+                            to[k ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) tma_store(&map_out, stage, q, (int)(x.out_row + p));
+                    } else {
+                        uint16_t* o = a.out + (x.out_row + p) * a.ldo + q;
+                        const int n = x.q_end - x.out_col - q;
+                        store_rows16(o, a.ldo, reinterpret_cast<float(&)[16]>(f[0]), rows, n, a.align, a.scale, a.first, stage);
+                        store_rows16(o + 16, a.ldo, reinterpret_cast<float(&)[16]>(f[16]), rows, n - 16, a.align, a.scale, a.first, stage);
+                    }
+                }
+            } else {
+                const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;         // the warp's first row
+                const int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
+                constexpr int kHalf = BN / 2;                                    // columns of one warp
+                const int qh = x.q0 + half * kHalf;
+                uint16_t* o = a.out + p * a.ldo + qh;
+                const uint32_t from = tmem + acc.at * BN + half * kHalf + ((uint32_t)(sub * 32) << 16);
+#pragma unroll 1
+                for (int c = 0; c < kHalf; c += 16) {
+                    float f[16];
+                    tmem_load16(from + c, f);
+                    store_rows16(o + c, a.ldo, f, rows, x.q_end - qh - c, a.align, a.scale, a.first,
+                                 store_sh + (warp - 6) * kStoreStage);
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(at_rank(acc_free + acc.at, 0));
         }
+        if ((GROUPS == kRowGroups || GROUPS == kSumGroups) && lane == 0) tma_stores_done();
     }
     __syncthreads();
     cluster_sync();                              // nobody issues anything any more, and what was issued is known
@@ -1079,18 +1180,27 @@ int64_t resident_pairs() { return q8_host::sm_count() / 2; }
 
 template <int BN, int GROUPS = kNoGroups>
 cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaStream_t st) {
-    const int smem = PairShape<BN>::kSmem + (GROUPS == kRowGroups ? PairShape<BN>::table(a.n_groups) : 0);
+    constexpr bool kTable = GROUPS == kRowGroups || GROUPS == kFewRows;
+    const int smem = PairShape<BN>::kSmem + (kTable ? PairShape<BN>::table(a.n_groups) : 0);
     const auto kern = k_q8_matmul_pair<BN, GROUPS>;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = ready_once(ready, (const void*)kern, GROUPS == kRowGroups ? PairShape<BN>::kSmemMost : smem);
+    cudaError_t e = ready_once(ready, (const void*)kern, kTable ? PairShape<BN>::kSmemMost : smem);
     if (e != cudaSuccess) return e;
-    CUtensorMap mp, mq;
+    CUtensorMap mp, mq, mo;
     e = make_maps(&mp, &mq, p, q, a, k, 128, BN / 2);
     if (e != cudaSuccess) return e;
+    mo = mp;
+    if ((GROUPS == kRowGroups || GROUPS == kSumGroups) && a.tiled) {
+        const int64_t rows = GROUPS == kRowGroups ? a.rows_p : (int64_t)a.rows_p * a.n_groups, cols = GROUPS == kRowGroups ? a.group_rows : a.rows_q;
+        e = make_map(&mo, a.out, true, rows, cols, a.ldo * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t high = ((int64_t)a.rows_p + 255) / 256;
-    a.tiles_q = ((GROUPS == kRowGroups ? a.group_rows : a.rows_q) + BN - 1) / BN;
+    a.tiles_q = GROUPS == kFewRows ? (a.group_rows + 255) / 256 : ((GROUPS == kRowGroups ? a.group_rows : a.rows_q) + BN - 1) / BN;
     // at most: a group's last rows may be a tile of their own
-    const int64_t most = GROUPS == kRowGroups ? high + (a.n_groups < a.rows_p ? a.n_groups : a.rows_p) : GROUPS == kSumGroups ? high * a.n_groups : high;
+    auto with_ends = [&](int64_t tiles, int64_t rows) { return tiles + (a.n_groups < rows ? a.n_groups : rows); };
+    const int64_t most = GROUPS == kRowGroups ? with_ends(high, a.rows_p) : GROUPS == kFewRows ? with_ends(((int64_t)a.rows_q + BN - 1) / BN, a.rows_q)
+                         : GROUPS == kSumGroups ? high * a.n_groups : high;
     const int64_t tiles = most * a.tiles_q, room = resident_pairs();
     if (GROUPS != kNoGroups) {
         if (tiles > 0x7fffffff - 2 * room) return cudaErrorInvalidConfiguration;
@@ -1109,7 +1219,7 @@ cudaError_t launch_mm_pair(const Q8& p, const Q8& q, int64_t k, MmArgs& a, cudaS
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, mp, mq, a);
+    e = cudaLaunchKernelEx(&cfg, kern, mp, mq, mo, a);
     if (e != cudaSuccess) cudaGetLastError();
     return e;
 }
@@ -1135,6 +1245,8 @@ int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines, int wides
     }
     return best;
 }
+
+constexpr int kFewAverage = 96;
 
 // The products of groups, in the width of least time for groups of equal size (their sizes are on the device).
 template <int GROUPS>
@@ -1185,6 +1297,7 @@ int group_args(const char* fn, const zs::Q8& qa, const zs::Q8& qb, const int32_t
     g->align = output_align(out, ldo);
     g->scale = scale;
     g->first = first != 0;
+    g->tiled = g->first && g->align && ldo * 2 < (int64_t(1) << 40);
     g->wait_limit = zs::wait_limit().load(std::memory_order_relaxed);
     return ZS_OK;
 }
@@ -1213,6 +1326,13 @@ extern "C" int zs_q8_matmul_experts(const zs_q8* a, const zs_q8* b, const int32_
     ZS_Q8_TRY(group_args(fn, qa, qb, starts, n_experts, m, n_experts * n, n, n, k, m, scale, first, out, ldo, &g));
     if (m == 0 || n == 0) return ZS_OK;
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
+    // On average FEWROWS rows of an expert or fewer: see kFewRows.
+    if (m <= (int64_t)zs::kFewAverage * n_experts) {
+        std::swap(g.sp, g.sq);
+        std::swap(g.ldsp, g.ldsq);
+        std::swap(g.rows_p, g.rows_q);
+        return cuda_status(fn, zs::launch_mm_pair<128, zs::kFewRows>(qb, qa, k, g, (cudaStream_t)stream));
+    }
     return cuda_status(fn, zs::launch_mm_groups<zs::kRowGroups>(qa, qb, k, g, n, (cudaStream_t)stream));
 }
 

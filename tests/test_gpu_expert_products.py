@@ -34,7 +34,8 @@ def _starts(sizes):
 
 ROWS = [([1], 1, 1), ([3, 0, 5], 40, 100), ([0, 0, 7], 128, 128), ([256, 1, 255, 257], 300, 513), ([128] * 5, 256, 640),
         ([0, 600, 0, 3, 1, 0], 129, 1100), (list(range(40)), 65, 200), ([5] * 100, 24, 385), ([2000, 3], 1000, 300),
-        ([1] * 1024, 17, 130), ([70, 900, 20], 700, 1)]
+        ([1] * 1024, 17, 130), ([70, 900, 20], 700, 1),
+        ([300, 0, 0, 0, 2], 300, 600), ([1, 31, 33, 64, 0, 129], 513, 385), ([17] * 9, 1000, 2048), ([130, 0, 60, 96], 70, 300)]
 
 
 @pytest.mark.parametrize("sizes,n,k", ROWS)
