@@ -899,6 +899,10 @@ def _weights(x, shape, what, dev):
 def _places(row_of, starts, counts, tokens, dev):
     """Addresses and sizes that a sort's results are passed with."""
     choices, experts = _shape(row_of, "row_of")[1], counts.numel()
+    if (row_of.dtype is _I32 and starts.dtype is _I32 and counts.dtype is _I32 and row_of.shape[0] == tokens and starts.numel() == experts + 1
+            and row_of.get_device() == dev and starts.get_device() == dev and counts.get_device() == dev
+            and row_of.is_contiguous() and starts.is_contiguous() and counts.is_contiguous()):
+        return row_of.data_ptr(), choices, starts.data_ptr(), counts.data_ptr(), experts
     return (_ints(row_of, (tokens, choices), "row_of", dev), choices, _ints(starts, (experts + 1,), "starts", dev),
             _ints(counts, (experts,), "counts", dev), experts)
 
@@ -907,14 +911,15 @@ def zs_expert_sort(ids, align, row_of, starts, counts, stream=None):
     """Rows of the choices ids (int32 or int64 [tokens, choices]; out of 0 .. n_experts - 1: dropped) into row_of,
     the experts' first rows (multiples of align) into starts, their choices into counts."""
     dev = _device()
-    shape = tokens, choices = _shape(ids, "ids")
-    _elsewhere(ids, dev, "ids")
-    if ids.dtype not in (_I32, _torch.int64) or not ids.is_contiguous():
+    tokens, choices = _shape(ids, "ids")
+    size = 4 if ids.dtype is _I32 else 8
+    if ids.get_device() != dev or not ids.is_contiguous() or (size == 8 and ids.dtype is not _torch.int64):
+        _elsewhere(ids, dev, "ids")
         raise ValueError("ids must be contiguous elements of torch.int32 or torch.int64")
-    experts = counts.numel()
-    return _check(_lib.zs_expert_sort(ids.data_ptr(), ids.element_size(), tokens, choices, experts, int(align),
-                                      _ints(row_of, shape, "row_of", dev), _ints(starts, (experts + 1,), "starts", dev),
-                                      _ints(counts, (experts,), "counts", dev), _here(stream, dev)))
+    po, width, ps, pc, experts = _places(row_of, starts, counts, tokens, dev)
+    if width != choices:
+        raise ValueError("row_of must be %d x %d, not %s" % (tokens, choices, tuple(row_of.shape)))
+    return _check(_lib.zs_expert_sort(ids.data_ptr(), size, tokens, choices, experts, align, po, ps, pc, _here(stream, dev)))
 
 
 def _rows_of(q, b, what):

@@ -10,13 +10,13 @@ namespace {
 // ------------------------------------------------------------------ sorting
 
 // A stable counting sort in one launch.  The pairs (token, choice) are cut into segments, one per warp of a cluster's
-// CTAs.  First pass: a warp counts its segment's pairs per expert.  The counters are summed over the warps, and over
-// the cluster's CTAs through distributed shared memory; the second pass goes through the segment again, 32 pairs at a
-// time, and gives each its place: lanes of equal experts find each other by one vote per bit of the expert (the match
-// instruction takes its time once per different value: 131072 pairs of 64 experts in 28.7 us with it), a counter has one
-// writer, and the order of the pairs is kept.  No workspace, and the same rows every time.
+// CTAs.  First pass: a warp counts its segment's pairs per expert, 32 at a time: lanes of equal experts find each other by
+// one vote per bit of the expert, and one of them adds their number.  The counters are summed over the warps, and over
+// the cluster's CTAs through distributed shared memory; the second pass goes through the segment again, with what the
+// first found where it fits in registers, and gives each pair its place.  A counter has one writer at a time and the order
+// of the pairs is kept: the same rows every time, without a workspace.  131072 pairs of 64 experts: SORTFIG; 12.5 with
+// atomics for the counts, 28.7 with the match instruction, which takes its time once per different value.
 constexpr int kSortWarps = 32;
-constexpr int kSortBatch = 8;        // ids per lane read at once
 
 struct SortArgs {
     const void* ids;
@@ -25,7 +25,7 @@ struct SortArgs {
     int *row_of, *starts, *counts;
 };
 
-template <typename ID>
+template <typename ID, int BATCH>
 __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_constant__ SortArgs a) {
     extern __shared__ int sort_sh[];
     const int E = a.experts;
@@ -44,26 +44,34 @@ __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_co
     const int64_t hi = lo + a.seg < a.n ? lo + a.seg : a.n;
     const ID* ids = static_cast<const ID*>(a.ids);
     int* mine = hist + warp * E;
-    // f(pair, expert or -1) for every pair of the segment, 32 at a time in order
-    auto each = [&](auto f) {
-        for (int64_t base = lo; base < hi; base += 32 * kSortBatch) {
-            int id[kSortBatch];
+    // A batch of the segment: each lane's experts (-1: none) and the lanes with the same one.
+    const int bits = 32 - __clz(E - 1);
+    int id[BATCH];
+    uint32_t same[BATCH];
+    auto read = [&](int64_t base) {
 #pragma unroll
-            for (int j = 0; j < kSortBatch; ++j) {
-                const int64_t i = base + 32 * j + lane;
-                const ID x = i < hi ? ids[i] : (ID)-1;
-                id[j] = x >= 0 && x < (ID)E ? (int)x : -1;
-            }
-#pragma unroll
-            for (int j = 0; j < kSortBatch; ++j) {
-                if (base + 32 * j >= hi) break;
-                f(base + 32 * j + lane, id[j]);
-            }
+        for (int j = 0; j < BATCH; ++j) {
+            const int64_t i = base + 32 * j + lane;
+            const ID x = i < hi ? ids[i] : (ID)-1;
+            id[j] = x >= 0 && x < (ID)E ? (int)x : -1;
         }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) same[j] = __ballot_sync(~0u, id[j] >= 0);
+        for (int b = 0; b < bits; ++b)
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const uint32_t set = __ballot_sync(~0u, id[j] >> b & 1);
+                same[j] &= id[j] >> b & 1 ? set : ~set;
+            }
     };
-    each([&](int64_t, int id) {
-        if (id >= 0) atomicAdd(mine + id, 1);
-    });
+    for (int64_t base = lo; base < hi; base += 32 * BATCH) {
+        read(base);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (id[j] >= 0 && lane == __ffs(same[j]) - 1) mine[id[j]] += __popc(same[j]);
+            __syncwarp();
+        }
+    }
     __syncthreads();
     const int e = threadIdx.x;                   // at most as many experts as threads
     if (e < E) {
@@ -118,32 +126,31 @@ __global__ void __launch_bounds__(kSortWarps * 32) k_expert_sort(const __grid_co
     }
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");       // the other CTAs' totals are read
-    const int bits = 32 - __clz(E - 1);
-    each([&](int64_t i, int id) {
-        uint32_t same = __ballot_sync(~0u, id >= 0);
-        for (int b = 0; b < bits; ++b) {
-            const uint32_t set = __ballot_sync(~0u, id >> b & 1);
-            same &= id >> b & 1 ? set : ~set;
+    for (int64_t base = lo; base < hi; base += 32 * BATCH) {
+        if (hi - lo > 32 * BATCH) read(base);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int64_t i = base + 32 * j + lane;
+            const int at = id[j] >= 0 ? mine[id[j]] : 0;
+            __syncwarp();
+            if (id[j] >= 0 && lane == __ffs(same[j]) - 1) mine[id[j]] = at + __popc(same[j]);
+            if (i < hi) a.row_of[i] = id[j] >= 0 ? first[id[j]] + at + __popc(same[j] & ((1u << lane) - 1)) : -1;
+            __syncwarp();
         }
-        const int at = id >= 0 ? mine[id] : 0;
-        __syncwarp();
-        if (id >= 0 && lane == __ffs(same) - 1) mine[id] = at + __popc(same);
-        if (i < hi) a.row_of[i] = id >= 0 ? first[id] + at + __popc(same & ((1u << lane) - 1)) : -1;
-        __syncwarp();
-    });
+    }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");         // nobody reads this CTA's any more
 }
 
 // ------------------------------------------------------------------ to the experts
 
-// Rows [starts[e] + counts[e], starts[e + 1]) hold no token: zeros, for a later sum over an expert's rows.  kPadWarps
+// Rows [starts[e] + counts[e], starts[e + 1]) hold no token: zeros, for a later sum over an expert's rows.  pad_warps
 // warps share an expert's.
-constexpr int kPadWarps = 16;
 
 struct Rows {
     const int *row_of, *starts, *counts;
     int64_t tokens, rows, cols;
     int choices, experts, chunks;    // chunks of 512 columns
+    int pad_warps;
     Q8 y;                            // either may be missing
     uint16_t* y16;
     int64_t ldy16;
@@ -153,12 +160,12 @@ template <bool WIDE>
 __device__ __forceinline__ void zero_padding(const Rows& a, int64_t warp, int64_t warps) {
     const int lane = threadIdx.x & 31;
     const V16 zero = {};
-    for (int64_t u = warp; u < (int64_t)a.experts * kPadWarps; u += warps) {
-        const int e = (int)(u / kPadWarps);
+    for (int64_t u = warp; u < (int64_t)a.experts * a.pad_warps; u += warps) {
+        const int e = (int)(u / a.pad_warps);
         int64_t lo = (int64_t)a.starts[e] + a.counts[e], hi = a.starts[e + 1];
         if (lo < 0) lo = 0;
         if (hi > a.rows) hi = a.rows;
-        for (int64_t r = lo + u % kPadWarps; r < hi; r += kPadWarps)
+        for (int64_t r = lo + u % a.pad_warps; r < hi; r += a.pad_warps)
             for (int64_t c = lane * 16; c - lane * 16 < a.cols; c += 512) {
                 if (a.y.codes) store_code16(make_uint4(0, 0, 0, 0), 0, a.cols - c, a.y, r, c);
                 if (a.y16) store16<WIDE>(a.y16 + r * a.ldy16 + c, zero, a.cols - c);
@@ -384,6 +391,71 @@ int check_routes(const char* fn, int64_t tokens, int32_t choices, int32_t expert
     return ZS_OK;
 }
 
+// CTAs of the sort's cluster: one up to 1024 pairs (3.2 us; 4096 pairs take 4.8 in one and 3.5 in eight), eight, and sixteen
+// past 65536 (131072: SIXTEEN; 11.4 in eight) where the device has room for such clusters.
+constexpr int kSortOne = 1024, kSortEight = 65536;
+
+template <typename ID, int BATCH>
+cudaError_t launch_sort(const SortArgs& a, int ctas, cudaStream_t st) {
+    constexpr int per = (kSortWarps + 2) * 4;
+    static std::atomic<uint64_t> ready{0};
+    const auto kern = k_expert_sort<ID, BATCH>;
+    cudaError_t e = ready_once(ready, (const void*)kern, per * ZS_MAX_EXPERTS);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kSortWarps * 32);
+    cfg.dynamicSmemBytes = per * ZS_MAX_EXPERTS;         // what the occupancy is asked for
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = dependent_launch() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (ctas > 8) {                              // past the portable size: asked for once per device
+        static std::atomic<uint64_t> asked{0}, fits{0};
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        const uint64_t bit = dev < kMaxDevices ? uint64_t(1) << dev : 0;
+        if (!(asked.load(std::memory_order_acquire) & bit)) {
+            int clusters = 0;
+            if (cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0)
+                fits.fetch_or(bit, std::memory_order_release);
+            cudaGetLastError();
+            asked.fetch_or(bit, std::memory_order_release);
+        }
+        if (!(fits.load(std::memory_order_acquire) & bit)) return cudaErrorNotSupported;
+    }
+    cfg.dynamicSmemBytes = per * a.experts;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
+// The sort with `ctas` CTAs: each warp's part of the pairs, and as many ids at once as it has (16 at once for a part of
+// eight cost as much as for sixteen: 65536 pairs 11.0 us and 6.9).
+template <typename ID>
+cudaError_t launch_sort(SortArgs a, int ctas, cudaStream_t st) {
+    const int64_t per = (int64_t)ctas * kSortWarps * 32;
+    a.seg = (int)((a.n + per - 1) / per * 32);
+    return a.seg <= 32    ? launch_sort<ID, 1>(a, ctas, st)
+           : a.seg <= 128 ? launch_sort<ID, 4>(a, ctas, st)
+           : a.seg <= 256 ? launch_sort<ID, 8>(a, ctas, st)
+                          : launch_sort<ID, 16>(a, ctas, st);
+}
+template <typename ID>
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t st) {
+    if (a.n > kSortEight) {
+        const cudaError_t e = launch_sort<ID>(a, 16, st);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    return launch_sort<ID>(a, a.n <= kSortOne ? 1 : 8, st);
+}
+
 // CTAs for `warps` warps of work, `per` to a CTA, each with work of its own: CTAs that end make room for the next, so the
 // work goes to the SMs as they get through it.  Past 2^31 CTAs the kernels go round.
 unsigned grid_for(int64_t warps, int per) {
@@ -413,28 +485,8 @@ extern "C" int zs_expert_sort(const void* ids, int32_t id_bytes, int64_t tokens,
     ZS_Q8_TRY(zs::check_ints(fn, "starts", starts, true));
     ZS_Q8_TRY(zs::check_ints(fn, "counts", counts, true));
     zs::SortArgs a{ids, (int)n, n_experts, align, 0, row_of, starts, counts};
-    const int ctas = n <= 4096 ? 1 : 8;
-    a.seg = (int)((n + ctas * zs::kSortWarps * 32 - 1) / (ctas * zs::kSortWarps * 32) * 32);
-    const int smem = (zs::kSortWarps + 2) * n_experts * 4;
-    static std::atomic<uint64_t> ready32{0}, ready64{0};
-    const auto kern = id_bytes == 4 ? zs::k_expert_sort<int32_t> : zs::k_expert_sort<int64_t>;
-    ZS_Q8_TRY(cuda_status(fn, zs::ready_once(id_bytes == 4 ? ready32 : ready64, (const void*)kern,
-                                             (zs::kSortWarps + 2) * ZS_MAX_EXPERTS * 4)));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(zs::kSortWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = zs::dependent_launch() ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess) cudaGetLastError();
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = id_bytes == 4 ? zs::launch_sort<int32_t>(a, st) : zs::launch_sort<int64_t>(a, st);
     return cuda_status(fn, e);
 }
 
@@ -450,7 +502,10 @@ int check_rows(const char* fn, const char* q_name, const char* b_name, const int
     ZS_Q8_TRY(zs::check_ints(fn, "row_of", row_of, tokens > 0));
     ZS_Q8_TRY(zs::check_ints(fn, "starts", starts, true));
     ZS_Q8_TRY(zs::check_ints(fn, "counts", counts, true));
-    *out = zs::Rows{row_of, starts, counts, tokens, rows, cols, choices, n_experts, (int)((cols + 511) / 512), {}, (uint16_t*)b, ldb};
+    *out = zs::Rows{row_of, starts, counts, tokens, rows, cols, choices, n_experts, (int)((cols + 511) / 512), 1, {}, (uint16_t*)b, ldb};
+    // an expert's rows without a token: about half of what `rows` has beyond the choices, if all are kept
+    const int64_t beyond = (rows - tokens * choices) / n_experts;
+    out->pad_warps = beyond < 4 ? 4 : beyond < 128 ? (int)beyond : 128;
     ZS_Q8_TRY(check_q8(fn, q_name, q, rows, cols, true, &out->y));
     if (b) ZS_Q8_TRY(check_bf16(fn, b_name, b, ldb, rows, cols));
     return ZS_OK;
@@ -473,7 +528,7 @@ extern "C" int zs_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, in
     a.ldx = ldx;
     const bool w = wide(x, ldx, 32) && (!y_bf16 || wide(y_bf16, ldy, 32));
     int64_t work = tokens * a.r.chunks;
-    if (work < (int64_t)n_experts * zs::kPadWarps) work = (int64_t)n_experts * zs::kPadWarps;
+    if (work < (int64_t)n_experts * a.r.pad_warps) work = (int64_t)n_experts * a.r.pad_warps;
     return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_dispatch<true> : zs::k_expert_dispatch<false>,
                                              dim3(zs::grid_for(work, 8)), dim3(256), 0, (cudaStream_t)stream, a));
 }
