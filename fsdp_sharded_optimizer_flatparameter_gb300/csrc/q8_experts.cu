@@ -14,8 +14,9 @@ namespace {
 // one vote per bit of the expert, and one of them adds their number.  The counters are summed over the warps, and over
 // the cluster's CTAs through distributed shared memory; the second pass goes through the segment again, with what the
 // first found where it fits in registers, and gives each pair its place.  A counter has one writer at a time and the order
-// of the pairs is kept: the same rows every time, without a workspace.  131072 pairs of 64 experts: SORTFIG; 12.5 with
-// atomics for the counts, 28.7 with the match instruction, which takes its time once per different value.
+// of the pairs is kept: the same rows every time, without a workspace.  131072 pairs of 64 experts: 7.3 us; in eight
+// CTAs 11.4, 12.5 with atomics for the counts, 28.7 with the match instruction, which takes its time once per different
+// value.  What bounds it is the issue of the votes and counts on the cluster's SMs.
 constexpr int kSortWarps = 32;
 
 struct SortArgs {
@@ -185,7 +186,8 @@ struct DispatchArgs {
     int64_t ldx;
 };
 
-// A warp takes 512 columns of a token: read, encoded once, and written to every row that the token goes to.
+// A warp takes 512 columns of a token: read, encoded once, and written to every row that the token goes to.  Bound by the
+// bytes: 16384 x 2048 to 8 of 64 experts 54 us (338 MB, 50 at the copy rate), and 60 with a fixed share for each CTA.
 template <bool WIDE>
 __global__ void __launch_bounds__(256) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
     dependent_launch_prologue();
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(256) k_expert_dispatch(const __grid_constant__
 
 constexpr int kAtOnce = 4;           // rows of a token read at once
 
+
 struct CombineArgs {
     const uint16_t *y, *residual;
     int64_t ldy, ldr, ldo, rows, cols, tokens;
@@ -227,7 +230,9 @@ struct CombineArgs {
     uint16_t* out;
 };
 
-// A warp takes 512 columns of a token: residual + sum of weight * row in the order of the choices, in fp32.
+// A warp takes 512 columns of a token: residual + sum of weight * row in the order of the choices, in fp32.  Bound by the
+// bytes, four rows of a token on their way at once: 16384 x 2048 from 8 experts 91 us (605 MB, 89 at the copy rate).  With
+// registers for 32 warps per SM in the place of 24, and some of them spilled, 118.
 template <bool WIDE>
 __global__ void __launch_bounds__(256) k_expert_combine(const __grid_constant__ CombineArgs a) {
     dependent_launch_prologue();
@@ -276,22 +281,21 @@ struct CombineBackArgs {
 
 constexpr int kMaxChoices = ZS_MAX_CHOICES;
 constexpr int kBackWarps = 8;        // at most, per token
-constexpr int kBackCtas = 4;         // resident (16384 x 2048, 8 choices: 149 us; 169 and 187 with 3 and 5)
+constexpr int kBackCtas = 4;         // resident (with rows in registers 149 us; 169 and 187 with 3 and 5)
 
 // 16 columns of 8 neighbouring lanes, times w, in the format.  `top` is the block's largest finite magnitude before w:
 // |w| times it is the largest after (rounding keeps the order), and w and the block's inverse scale are one factor where
-// that is exact - where no value that matters comes near the ends of fp32's range.
-__device__ __forceinline__ uint4 code16_scaled(const float2 (&f)[8], float w, float top, uint32_t& byte) {
-    const float most = top * fabsf(w);
-    const bool plain = most >= 0x1p-100f && most < __int_as_float(0x7f800000) && top >= 0x1p-100f && top <= 0x1p100f;
-    if (!__all_sync(~0u, plain || (most == 0.f && top < 0x1p100f))) {
+// that is exact: where no value that matters comes near the ends of fp32's range (usual: top is in 2^-100 .. 2^100).
+__device__ __forceinline__ uint4 code16_scaled(const float2 (&f)[8], float w, float top, bool usual, uint32_t& byte) {
+    const float most = top * fabsf(w);           // and so |w| is above 2^-200 and below 2^228
+    if (!__all_sync(~0u, most >= 0x1p-100f && most < __int_as_float(0x7f800000) && usual)) {
         float2 g[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = q8_mul2(f[i], make_float2(w, w));
         return code16(g, byte);
     }
     byte = q8_scale_byte(most);
-    const float by = plain ? w * q8_inverse(byte) : 0.f;
+    const float by = w * q8_inverse(byte);
     uint32_t q[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -301,27 +305,48 @@ __device__ __forceinline__ uint4 code16_scaled(const float2 (&f)[8], float w, fl
     return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-// A CTA takes a token, a warp of it 512 columns at a time: the gradient row stays in registers, and the expert's next row
-// is on its way while one is worked on.
+// A CTA takes a token, a warp of it 512 columns at a time: the gradient row stays in registers, and the experts' next rows
+// are on their way to shared memory, to each lane's own places in it, while one is worked on.  What bounds it is how much
+// is on its way: 16384 x 2048 with 8 choices takes 133 us (its 876 MB 129 at the copy rate) with three rows or four, 160 with
+// six, for which fewer CTAs fit an SM, and took 150 with the next row in registers.
+template <bool WIDE>
+constexpr int kBackSlot = WIDE ? 32 : kSlot;             // bytes of a lane's 16 columns
+constexpr int kBackRows = 3;                             // rows under way, the one worked on among them
 template <bool WIDE>
 __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) k_expert_combine_backward(const __grid_constant__ CombineBackArgs a) {
     __shared__ float dots[kBackWarps][kMaxChoices];
+    extern __shared__ __align__(16) uint8_t back_sh[];   // [warp][row][lane]
     dependent_launch_prologue();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = blockDim.x >> 5;
+    uint8_t* slots = back_sh + (warp * kBackRows * 32 + lane) * kBackSlot<WIDE>;
     const Span sd = span_of(a.dout, a.lddout, a.r.tokens, a.r.cols), sy = span_of(a.y, a.ldy, a.r.rows, a.r.cols);
     const int K = a.r.choices;
     const int64_t t = blockIdx.x;
     if (t < a.r.tokens) {
         const int held = lane < K ? a.r.row_of[t * K + lane] : -1;
         const float weight = a.weights && lane < K ? a.weights[t * K + lane] : 1.f;
-        if (lane < K) dots[warp][lane] = 0.f;
-        __syncwarp();
+        float dot = 0.f;                         // of choice `lane`
         for (int ch = warp; ch < a.r.chunks; ch += group) {
             const int64_t c = (int64_t)ch * 512 + lane * 16, n = a.r.cols - c;
             const V16 d = load16<WIDE>(a.dout + t * a.lddout + c, n, sd);
-            int64_t row = row_at(held, 0, a.r.rows);
-            V16 y;
-            if (a.dweights && row >= 0) y = load16<WIDE>(a.y + row * a.ldy + c, n, sy);
+            auto slot = [&](int j) { return slots + j % kBackRows * (32 * kBackSlot<WIDE>); };
+            auto fetch = [&](int j) {
+                const int64_t row = j < K ? row_at(held, j & 31, a.r.rows) : -1;
+                if (a.dweights && row >= 0) {
+                    const uint16_t* from = a.y + row * a.ldy + c;
+                    if (WIDE) {
+                        if (n >= 8) async16(slot(j), reinterpret_cast<const uint8_t*>(from), 16);
+                        else if (n > 0) async16(slot(j), reinterpret_cast<const uint8_t*>(from), (int)n * 2);
+                        if (n >= 16) async16(slot(j) + 16, reinterpret_cast<const uint8_t*>(from + 8), 16);
+                        else if (n > 8) async16(slot(j) + 16, reinterpret_cast<const uint8_t*>(from + 8), (int)(n - 8) * 2);
+                    } else {
+                        fetch16(slot(j), from, n, sy);
+                    }
+                }
+                async_commit();
+            };
+#pragma unroll
+            for (int j = 0; j < kBackRows - 1; ++j) fetch(j);
             float2 f[8];
             float top = 0.f;
 #pragma unroll
@@ -331,38 +356,49 @@ __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) k_expert_combine_b
             }
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+            const bool usual = top >= 0x1p-100f && top <= 0x1p100f;
 #pragma unroll 1
             for (int j = 0; j < K; ++j) {
-                const int64_t here = row;
+                fetch(j + kBackRows - 1);
+                const int64_t row = row_at(held, j, a.r.rows);
                 const float w = __shfl_sync(~0u, weight, j);
-                float2 s = make_float2(0.f, 0.f);
-                if (a.dweights && here >= 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s = q8_fma2(f[i], pair_of(y.w[i]), s);
-                }
-                row = j + 1 < K ? row_at(held, j + 1, a.r.rows) : -1;
-                if (a.dweights && row >= 0) y = load16<WIDE>(a.y + row * a.ldy + c, n, sy);
-                if (here < 0) continue;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kBackRows - 1) : "memory");
+                if (row < 0) continue;
                 if (a.r.y.codes) {
                     uint32_t byte;
-                    const uint4 x = code16_scaled(f, w, top, byte);
-                    store_code16(x, byte, n, a.r.y, here, c);
+                    const uint4 x = code16_scaled(f, w, top, usual, byte);
+                    store_code16(x, byte, n, a.r.y, row, c);
                 }
                 if (a.r.y16) {
                     V16 v;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v.w[i] = pack_bf16x2(f[i].x * w, f[i].y * w);
-                    store16<WIDE>(a.r.y16 + here * a.r.ldy16 + c, v, n);
+                    store16<WIDE>(a.r.y16 + row * a.r.ldy16 + c, v, n);
                 }
                 if (a.dweights) {
-                    float sum = s.x + s.y;
+                    float sum = 0.f;
+                    if (n > 0) {                 // elsewhere nothing was read
+                        V16 y;
+                        if (WIDE) {
+                            const uint4 x0 = reinterpret_cast<const uint4*>(slot(j))[0], x1 = reinterpret_cast<const uint4*>(slot(j))[1];
+                            y = V16{{x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}};
+                            if (n <= 8) y.w[4] = y.w[5] = y.w[6] = y.w[7] = 0;
+                        } else {
+                            y = take16(slot(j), a.y + row * a.ldy + c, n);
+                        }
+                        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s = q8_fma2(f[i], pair_of(y.w[i]), s);
+                        sum = s.x + s.y;
+                    }
 #pragma unroll
                     for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
-                    if (lane == 0) dots[warp][j] += sum;
+                    if (lane == j) dot += sum;
                 }
             }
         }
         if (a.dweights) {
+            if (lane < K) dots[warp][lane] = dot;
             __syncthreads();
             if (threadIdx.x < K) {
                 float sum = 0.f;
@@ -392,7 +428,7 @@ int check_routes(const char* fn, int64_t tokens, int32_t choices, int32_t expert
 }
 
 // CTAs of the sort's cluster: one up to 1024 pairs (3.2 us; 4096 pairs take 4.8 in one and 3.5 in eight), eight, and sixteen
-// past 65536 (131072: SIXTEEN; 11.4 in eight) where the device has room for such clusters.
+// past 65536 (131072: 7.3 us; 11.4 in eight) where the device has room for such clusters.
 constexpr int kSortOne = 1024, kSortEight = 65536;
 
 template <typename ID, int BATCH>
@@ -454,6 +490,15 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t st) {
         if (e != cudaErrorNotSupported) return e;
     }
     return launch_sort<ID>(a, a.n <= kSortOne ? 1 : 8, st);
+}
+
+template <bool WIDE>
+cudaError_t launch_back(const CombineBackArgs& a, unsigned ctas, int group, cudaStream_t st) {
+    constexpr int per = kBackRows * 32 * kBackSlot<WIDE>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = ready_once(ready, (const void*)k_expert_combine_backward<WIDE>, per * kBackWarps);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(k_expert_combine_backward<WIDE>, dim3(ctas), dim3(32 * group), a.dweights ? per * group : 0, st, a);
 }
 
 // CTAs for `warps` warps of work, `per` to a CTA, each with work of its own: CTAs that end make room for the next, so the
@@ -580,6 +625,6 @@ extern "C" int zs_expert_combine_backward(const void* dout, int64_t lddout, cons
     const int group = a.r.chunks < zs::kBackWarps ? a.r.chunks : zs::kBackWarps;
     // a token per CTA, and at least a few CTAs for the rows without one
     const unsigned ctas = tokens < 64 ? 64 : (unsigned)tokens;
-    return cuda_status(fn, zs::launch_kernel(w ? zs::k_expert_combine_backward<true> : zs::k_expert_combine_backward<false>,
-                                             dim3(ctas), dim3(32 * group), 0, (cudaStream_t)stream, a));
+    const cudaStream_t st = (cudaStream_t)stream;
+    return cuda_status(fn, w ? zs::launch_back<true>(a, ctas, group, st) : zs::launch_back<false>(a, ctas, group, st));
 }

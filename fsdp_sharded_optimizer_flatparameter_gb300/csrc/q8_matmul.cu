@@ -685,7 +685,7 @@ constexpr int kPairGroup = 8;        // P tiles that share the same Q tiles at a
 //   kRowGroups  P's rows starts[g] .. starts[g + 1] times the group's own group_rows rows of Q
 //   kFewRows    the same product with the operands' places exchanged: a tile is 256 of the group's own rows (of P now)
 //               times as many of the starts' rows as there are, 32 to BN.  A block of the sum takes 180 + 0.48 N ns, so few
-//               rows cost less as N than as 256 rows of P (37 tokens to 2 of 16 experts, 2048 x 4096: FEWFIG).
+//               rows cost less as N than as 256 rows of P (37 tokens to 2 of 16 experts, 2048 x 4096: 27 us, 33 as 256 rows).
 //   kSumGroups  the sum over columns starts[g] .. starts[g + 1] (multiples of 128) of both, one result per group
 // Starts out of range are read as the nearest inside; with overlapping groups (more tiles than there can be) nothing is
 // written, so that no tile lies outside.
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 // Pieces of 32 columns, in turn for the two halves of the warps.  Whole pieces that are only written go by tiled
                 // copies: 64 bytes of a row at once and nothing of the warp's time, where its own stores touch 32 lines for 32
                 // bytes each (8 x 5504 x 2048 over 750 rows each, whose tiles are written about as fast as they are
-                // computed: STOREFIG).
+                // computed: 82 us, 91 by the warps).
                 const bool sum = GROUPS != kSumGroups || x.kbs > 0;              // the empty sum: zeros, or out as it is
                 const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;         // the warp's first row
                 int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
@@ -1246,6 +1246,9 @@ int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines, int wides
     return best;
 }
 
+// Rows of an expert, on average, up to which they are the narrow operand.  Microseconds as such and as P for 16, 64, 96 and
+// 128 rows each: 16 experts of 2048 x 4096 29 31 35 38 and 34 35 35 36; 64 of 2048 x 2048 48 54 57 62 and 58 59 62 65;
+// 8 of 5504 x 2048 23 24 25 28 and 25 25 25 27.
 constexpr int kFewAverage = 96;
 
 // The products of groups, in the width of least time for groups of equal size (their sizes are on the device).
@@ -1326,7 +1329,6 @@ extern "C" int zs_q8_matmul_experts(const zs_q8* a, const zs_q8* b, const int32_
     ZS_Q8_TRY(group_args(fn, qa, qb, starts, n_experts, m, n_experts * n, n, n, k, m, scale, first, out, ldo, &g));
     if (m == 0 || n == 0) return ZS_OK;
     ZS_Q8_TRY(cuda_status(fn, zs::error_word(&g.error)));
-    // On average FEWROWS rows of an expert or fewer: see kFewRows.
     if (m <= (int64_t)zs::kFewAverage * n_experts) {
         std::swap(g.sp, g.sq);
         std::swap(g.ldsp, g.ldsq);
