@@ -1036,6 +1036,9 @@ class TensorList:
                 t.m_scale = self._tensor(m_scales[i], blocks, (_F32,), ("m_scales", i))
                 t.v_scale = self._tensor(v_scales[i], blocks, (_F32,), ("v_scales", i))
             t.no_decay = 1 if no_decay is not None and no_decay[i] else 0
+        written = [p for t in self._array[:count] if t.n for p in (t.master, t.param, t.m, t.v, t.m_scale, t.v_scale) if p]
+        if len(set(written)) < len(written):
+            raise ValueError("an array is in the list twice, and would be stepped twice at once")
         self.set_grads(grads)
 
     def __len__(self):

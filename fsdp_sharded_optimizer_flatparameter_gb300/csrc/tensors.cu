@@ -3,8 +3,8 @@
 // A launch carries the table of up to kTableMost tensors in its parameters (no device memory, nothing to upload, and a
 // captured launch keeps it), and its CTAs take tiles of eight blocks of 256 elements in turn, whatever tensor they belong
 // to.  All of it moves bytes: with bf16 gradients 28 per element and states of 32 bits, 16.06 with states of 8 bits.
+#include <cfloat>
 #include <cmath>
-#include <cstring>
 
 #include "q8_tma.cuh"
 
@@ -36,6 +36,7 @@ struct Table {
     int count;
     AdamScalars s;
     float inv_root;                  // 1 / s.sqrt_bc2
+    float eps;                       // s.eps, not subnormal
     float one;                       // 1, which the compiler does not know (sum2)
     uint32_t run;                    // tiles of a CTA
     const float* factor;
@@ -158,7 +159,7 @@ __device__ __forceinline__ float top_nan(float top, float2 x) {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Within one unit in the last place; a root above 0 is at least 2^-75, so nothing subnormal comes here.
+// Within one unit in the last place; a root above 0 is at least 2^-75 and eps not subnormal, so nothing subnormal comes here.
 __device__ __forceinline__ float reciprocal(float x) {
     float d;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
@@ -295,7 +296,7 @@ struct Strided {
 
 template <int CAP>
 __device__ __forceinline__ Scalars8 scalars8(const Table<CAP>& a, const Entry& t) {
-    return Scalars8{a.s.beta1, a.s.beta2, a.s.eps, t.n & kNoDecay ? 1.f : a.s.decay, a.s.c1, a.s.c2, a.s.step_size, a.inv_root, a.one};
+    return Scalars8{a.s.beta1, a.s.beta2, a.eps, t.n & kNoDecay ? 1.f : a.s.decay, a.s.c1, a.s.c2, a.s.step_size, a.inv_root, a.one};
 }
 // The hash of element i of a block's tensor after its first shift.
 template <int CAP>
@@ -730,6 +731,7 @@ cudaError_t step_list(const zs_tensor* tensors, int count, bool g32, bool q, uin
     Table<CAP> a;
     a.s = s;
     a.inv_root = (float)(1.0 / (double)s.sqrt_bc2);
+    a.eps = s.eps > 0.f && s.eps < FLT_MIN ? FLT_MIN : s.eps;
     a.one = 1.f;
     a.factor = factor;
     a.wait_limit = wait_limit().load(std::memory_order_relaxed);

@@ -78,8 +78,15 @@ def test_the_structure_is_the_headers():
     assert ctypes.sizeof(zs.zs_tensor) == 72 and zs.zs_tensor.no_decay.offset == 64
 
 
+class _At(_Placed):
+    """A tensor on GPU 0 with an address of its own."""
+
+    def data_ptr(self):
+        return id(self) * 64
+
+
 def _arrays(**change):
-    P = lambda n, dtype, **kw: _Placed(n, dtype=dtype, **kw)  # noqa: E731
+    P = lambda n, dtype, **kw: _At(n, dtype=dtype, **kw)  # noqa: E731
     a = dict(grads=[P(300, BF16), P(5, BF16)], master=[P(300, F32), P(5, F32)], m=[P(300, U8), P(5, U8)], v=[P(300, U8), P(5, U8)],
              params=[P(300, BF16), None], m_scales=[P(2, F32), P(1, F32)], v_scales=[P(2, F32), P(1, F32)])
     return dict(a, **change)
@@ -115,3 +122,16 @@ def test_other_gradients_have_to_fit_too():
         ts.set_grads([_Placed(300, dtype=F32)])
     with pytest.raises(ValueError, match="must hold 300"):
         ts.set_grads([_Placed(301, dtype=F32), _Placed(5, dtype=F32)])
+
+
+def test_a_list_refuses_an_array_twice():
+    a = _arrays()
+    a["m"][1] = a["v"][1]
+    with pytest.raises(ValueError, match="twice"):
+        zs.TensorList(**a)
+    a = _arrays(grads=[_At(300, dtype=BF16)] * 2, master=[_At(300, dtype=F32)] * 2, m=[_At(300, dtype=U8) for _ in "ab"],
+                v=[_At(300, dtype=U8) for _ in "ab"], params=None, m_scales=[_At(2, dtype=F32) for _ in "ab"], v_scales=[_At(2, dtype=F32) for _ in "ab"])
+    with pytest.raises(ValueError, match="twice"):
+        zs.TensorList(**a)
+    a["master"] = [_At(300, dtype=F32) for _ in "ab"]
+    assert len(zs.TensorList(**a)) == 2                        # gradients are only read

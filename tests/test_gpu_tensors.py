@@ -387,3 +387,75 @@ def test_decoded_codes_are_the_formats():
     assert np.array_equal(np.isnan(got), np.isnan(want))
     fine = ~np.isnan(want)
     assert np.all(np.abs(got[fine] - want[fine]) <= 16 * U32 * np.abs(want[fine]))
+
+
+def test_no_decay_of_states_of_8_bits():
+    sizes = [3000, 3000, 77, 77]
+    a = Arrays(sizes, 8, seed=5)
+    before = a.numpy()
+    zs.zs_adamw_tensors(a.list(no_decay=[True, False, True, False]), HP, 3, seed=1)
+    for i, n in enumerate(sizes):
+        m, r = tensors.decode(before["m"][i], before["ms"][i]), tensors.decode(before["v"][i], before["vs"][i])
+        hp = dict(HP, weight_decay=0.0 if i % 2 == 0 else HP["weight_decay"])
+        want, m1, v1 = tensors.adamw(before["grad"][i], before["master"][i], m, r * r, hp, 3)
+        size = tensors.scalars(hp, 3)[6]
+        err = 3 * U32 * np.abs(before["master"][i]) + 24 * U32 * size * (np.abs(m) + np.abs(before["grad"][i])) / (np.sqrt(v1) / tensors.scalars(hp, 3)[7] + HP["eps"])
+        assert np.all(np.abs(a.master[i].double().cpu().numpy() - want) <= err)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_steps_in_a_row_do_not_need_plain_launches(bits):
+    """Launches that overlap the one before and launches that do not: the same bits after many steps without a wait,
+    over tensors whose tiles and scales change hands between the SMs."""
+    sizes, runs = [3 << 20, 5000, 1 << 20, 77777], []
+    for dependent in (1, 0):
+        a = Arrays(sizes, bits, seed=12)
+        ts = a.list()
+        partials, out = torch.empty(1216, device="cuda"), torch.empty(2, device="cuda")
+        torch.cuda.synchronize()
+        zs.zs_set_dependent_launch(dependent)
+        try:
+            for t in range(1, 13):
+                zs.zs_grad_norm(ts, 0.01, partials, out)
+                zs.zs_adamw_tensors(ts, HP, t, factor=out[1:], seed=t)
+        finally:
+            zs.zs_set_dependent_launch(1)
+        runs.append(a.snapshot())
+    assert all(torch.equal(runs[0][k], runs[1][k]) for k in runs[0])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_waits_that_run_out(bits, grad):
+    """The call reports it, leaves nothing under way, writes nothing outside, and the next call on fresh arrays is right."""
+    sizes = [1 << 20, 3000, 1 << 19]
+    want = Arrays(sizes, bits, grad, seed=3)
+    zs.zs_adamw_tensors(want.list(), HP, 2, seed=2)
+    want = want.snapshot()
+    try:
+        for limit in (0, 0, 0, 1, 300, 3000):
+            a = Arrays(sizes, bits, grad, seed=3)
+            torch.cuda.synchronize()
+            zs.zs_set_q8_wait_limit(limit)
+            zs.zs_adamw_tensors(a.list(), HP, 2, seed=2)
+            torch.cuda.synchronize()
+            assert zs.zs_device_status(clear=True) in ((zs.ZS_DEVERR_TENSORS_WAIT,) if limit == 0 else (zs.ZS_DEVERR_NONE, zs.ZS_DEVERR_TENSORS_WAIT))
+            a.assert_untouched_outside()
+            zs.zs_set_q8_wait_limit()
+            a = Arrays(sizes, bits, grad, seed=3)
+            zs.zs_adamw_tensors(a.list(), HP, 2, seed=2)
+            assert all(torch.equal(x, want[k]) for k, x in a.snapshot().items())
+            assert zs.zs_device_status() == zs.ZS_DEVERR_NONE
+    finally:
+        zs.zs_set_q8_wait_limit()
+
+
+def test_an_eps_that_is_subnormal_or_none():
+    """Elements without a gradient and states of zeros: 0 / eps is 0 for any eps above 0."""
+    grad = torch.zeros(512, device="cuda")
+    grad[:256] = torch.randn(256, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    for eps in (1e-42, 1e-38, 1e-30):
+        (m, ms), (v, vs) = zs.state_zeros(512), zs.state_zeros(512)
+        master = torch.ones(512, device="cuda")
+        zs.zs_adamw_tensors(zs.TensorList([grad], [master], [m], [v], m_scales=[ms], v_scales=[vs]), dict(HP, eps=eps, weight_decay=0.0), 1)
+        assert bool((master[256:] == 1).all()) and bool(torch.isfinite(master).all()) and bool((master[:256] != 1).all())
