@@ -35,7 +35,7 @@ def _starts(sizes):
 ROWS = [([1], 1, 1), ([3, 0, 5], 40, 100), ([0, 0, 7], 128, 128), ([256, 1, 255, 257], 300, 513), ([128] * 5, 256, 640),
         ([0, 600, 0, 3, 1, 0], 129, 1100), (list(range(40)), 65, 200), ([5] * 100, 24, 385), ([2000, 3], 1000, 300),
         ([1] * 1024, 17, 130), ([70, 900, 20], 700, 1),
-        ([300, 0, 0, 0, 2], 300, 600), ([1, 31, 33, 64, 0, 129], 513, 385), ([17] * 9, 1000, 2048), ([130, 0, 60, 96], 70, 300)]
+        ([300, 0, 0, 0, 2], 300, 600), ([1, 31, 33, 64, 0, 129], 513, 385), ([17] * 9, 1000, 2048), ([130, 0, 60, 96], 70, 300), ([0, 0], 5, 10)]
 
 
 @pytest.mark.parametrize("sizes,n,k", ROWS)
@@ -63,7 +63,7 @@ def test_rows(sizes, n, k):
 
 
 SUMS = [([128], 1, 1), ([128, 0, 256], 40, 100), ([0, 0, 1280], 128, 128), ([256, 128, 2304, 128], 300, 513), ([0] * 6 + [128], 70, 30),
-        ([128] * 60, 65, 200), ([640, 0] * 9, 257, 300), ([2048, 128, 128, 0], 600, 1100)]
+        ([128] * 60, 65, 200), ([640, 0] * 9, 257, 300), ([2048, 128, 128, 0], 600, 1100), ([0, 0, 0], 300, 70)]
 
 
 @pytest.mark.parametrize("sizes,m,n", SUMS)
