@@ -41,6 +41,8 @@ struct Table {
     uint32_t run;                    // tiles of a CTA
     const float* factor;
     float* partials;
+    float* out;                      // where one CTA has all of the norm's sum
+    float max_norm;
     int add;                         // the norm's partial sums: what earlier launches left counts too
     unsigned int* error;
     long long wait_limit;
@@ -62,8 +64,8 @@ __device__ __forceinline__ int find(const Table<CAP>& a, uint32_t u, int at) {
 
 // ------------------------------------------------------------------ eight values per lane
 
-// A lane's values of a block: neighbours (8 * lane + j) where the block is whole and every array aligned, else
-// 32 * j + lane, so that unaligned arrays too are read and written line by line.
+// A lane's values of a block: neighbours (8 * lane + j) where every array is aligned, else 32 * j + lane, so that unaligned
+// arrays too are read and written line by line.
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
     asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
@@ -94,7 +96,7 @@ __device__ __forceinline__ float load_grad(const void* grad, int64_t at) {
 // Every operation up to a code is rounded once, in the order of the definition, so that a state's bits do not depend on
 // the path that computed them.  With one instruction per operation a step takes about 80 per element, which is all that
 // can be issued while its 16 bytes pass; hence two values per instruction wherever there is one, and no test per value
-// for what is rare: blocks with infinities, NaN or magnitudes past kFastTop go through step8_any.
+// for what is rare: blocks with infinities, NaN or magnitudes past kFastTop go through step_any.
 
 // The finalizer of murmur3's 32-bit hash (A. Appleby): every bit of x changes every bit of the result about half the time.
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -399,26 +401,35 @@ __device__ __noinline__ void step_strided32(const Table<CAP>& a, int e, int64_t 
     }
 }
 
-// A ring of tiles in shared memory: one warp brings whole aligned tiles there by bulk copies (their scales, at any 4-byte
-// address, by 4-byte copies that count on the same barrier), eight warps work on a block each and write it from
-// registers.  Of any other tile only its place is passed on, and the warps read its blocks themselves.
+// A ring of tiles in shared memory: one warp brings whole tiles there by bulk copies (their scales, at any 4-byte address, by
+// 4-byte copies that count on the same barrier), eight warps work on a block each and write it from registers.  Arrays at
+// other addresses come as the 16-byte chunks that cover the tile, each with its own offset, and go back by bulk copies too
+// (step_shifted), where those chunks lie inside the tensor.  Of any other tile - a tensor's last, and its first where the
+// arrays are shifted - only the place is passed on, and the warps read its blocks themselves.  402 M elements with states in
+// 8 bits: 969 us (6.46 GB, 950 at the copy rate); 139 M in 32 bits 549 (558).  All arrays three elements off: 59 % and 85 %
+// of the copy rate, bound by the single-element accesses to shared memory; 34 % and 58 % before, with global ones.
 template <bool G32, bool Q>
 struct Ring8 {
     static constexpr int kGrad = kTile * (G32 ? 4 : 2), kState = kTile * (Q ? 1 : 4);
     static constexpr int kScales = Q ? 2 * kTileBlocks * 4 : 0;
-    static constexpr int kBulk = kGrad + kTile * 4 + 2 * kState;     // a stage: gradients, masters, m, v, scales
-    static constexpr int kStage = kBulk + kScales;
+    static constexpr int kBulk = kGrad + kTile * 4 + 2 * kState;     // what an aligned tile has
+    // a stage: gradients, masters, m, v, each with room for an offset, and the scales
+    static constexpr int kMaster = kGrad + 16, kM = kMaster + kTile * 4 + 16, kV = kM + kState + 16, kScale = kV + kState + 16;
+    static constexpr int kStage = kScale + kScales;
     static constexpr int kStages = Q ? (G32 ? 3 : 4) : 2;            // 57 to 66 KB, three CTAs per SM
 };
+enum { kElsewhere = 0, kInPlace = 1, kShifted = 2 };
 struct Job {                         // a stage's tile
     int64_t block;                   // of the tensor
     int e;
-    uint32_t whole;
+    uint32_t how;
 };
-constexpr int kStepCtas = 3, kNormCtas = 8;          // resident CTAs per SM
+constexpr int kStepCtas = 3, kNormCtas = 4;          // resident CTAs per SM
 constexpr int kWorkers = 32 * kTileBlocks, kStepThreads = kWorkers + 32;
 template <bool G32, bool Q>
 constexpr int kStepSmem = Ring8<G32, Q>::kStages * (Ring8<G32, Q>::kStage + (int)sizeof(Job) + 16) + 64;
+
+__device__ __forceinline__ uint32_t offset16(const void* p) { return (uint32_t)((uintptr_t)p & 15); }
 
 // bytes (a multiple of 16) from src to dst, both 16-byte aligned, counted on bar.
 __device__ __forceinline__ void bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -427,20 +438,126 @@ __device__ __forceinline__ void bulk(void* dst, const void* src, uint32_t bytes,
                  : "memory");
 }
 
+// The bytes [to, to + n) from shared memory at an address that is the same modulo 16; a warp, elements of `size` bytes.  The
+// caller waits until the copy has read.
+__device__ __forceinline__ void write_back(uint8_t* to, const uint8_t* from, int n, int size) {
+    const int lane = threadIdx.x & 31, head = (16 - (int)offset16(to)) & 15, body = (n - head) & ~15, tail = head + body;
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + head), "r"(su32(from + head)), "r"(body) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    // what is left on either side, an element per lane
+    const int at = lane * size < head ? lane * size : tail + lane * size - head;
+    if (at >= n) return;
+    if (size == 1) to[at] = from[at];
+    else if (size == 2) *reinterpret_cast<uint16_t*>(to + at) = *reinterpret_cast<const uint16_t*>(from + at);
+    else *reinterpret_cast<uint32_t*>(to + at) = *reinterpret_cast<const uint32_t*>(from + at);
+}
+
+// A tile whose arrays have offsets.  The eight warps read their blocks of the stage, write the results to the same places
+// (the parameters to the gradients', once all have read), and four of them bring an array each back.  `read` and
+// `written`: barriers of the eight warps, `parity` theirs for this tile.  False: a wait ran out.
 template <bool G32, bool Q, int CAP>
+__device__ __noinline__ bool step_shifted(const Table<CAP>& a, int e, int64_t block0, uint8_t* stage, uint64_t* read, uint64_t* written,
+                                          uint32_t parity, float factor) {
+    using R = Ring8<G32, Q>;
+    const Entry& t = a.t[e];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp * kBlock + lane;
+    const int64_t block = block0 + warp, i = block0 * kBlock;
+    constexpr int kStateSize = Q ? 1 : 4;
+    uint8_t* sg = stage + offset16(t.grad);
+    uint8_t* sp = stage + R::kMaster + offset16(t.master);
+    uint8_t* sm = stage + R::kM + offset16(t.m);
+    uint8_t* sv = stage + R::kV + offset16(t.v);
+    uint8_t* sb = stage + offset16(t.param);                 // where the parameters go
+    float g[8], p[8], m[8], v[8];
+    Codes8 c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = mine + 32 * j;
+        g[j] = G32 ? reinterpret_cast<const float*>(sg)[k] : bf16_to_f32(reinterpret_cast<const uint16_t*>(sg)[k]);
+        p[j] = reinterpret_cast<const float*>(sp)[k];
+        if (!Q) {
+            m[j] = reinterpret_cast<const float*>(sm)[k];
+            v[j] = reinterpret_cast<const float*>(sv)[k];
+        }
+    }
+    if (Q) {
+        auto four = [&](const uint8_t* q) { return q[mine] | (q[mine + 32] << 8) | (q[mine + 64] << 16) | ((uint32_t)q[mine + 96] << 24); };
+        const float* scales = reinterpret_cast<const float*>(stage + R::kScale);
+        c = Codes8{make_uint2(four(sm), four(sm + 128)), make_uint2(four(sv), four(sv + 128)), scales[warp], scales[kTileBlocks + warp]};
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(read);
+    if constexpr (Q) {
+        float2 gp[4], pp[4];
+        to_pairs(g, gp);
+        to_pairs(p, pp);
+        if (step8<5>(gp, pp, c, hash_of(a, e, block * kBlock + lane), factor, scalars8(a, t))) {
+            of_pairs(pp, p);
+        } else {                                 // in place, and from there into the stage like the other blocks
+            step_any<G32>(a, e, block, factor);
+            __syncwarp();
+            Strided<G32>(t, block).load(g, p, c, block);
+        }
+        if (lane == 0) {
+            t.m_scale[block] = c.ms;
+            t.v_scale[block] = c.vs;
+        }
+    } else {
+        AdamScalars s = a.s;
+        if (t.n & kNoDecay) s.decay = 1.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) adamw_elem(__fmul_rn(g[j], factor), p[j], m[j], v[j], s);
+    }
+    if (!__all_sync(~0u, mbar_wait(read, parity, a.wait_limit))) return false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = mine + 32 * j;
+        reinterpret_cast<float*>(sp)[k] = p[j];
+        if (t.param) reinterpret_cast<uint16_t*>(sb)[k] = f32_to_bf16(p[j]);
+        if (Q) {
+            sm[k] = (uint8_t)((j < 4 ? c.m.x : c.m.y) >> (8 * (j & 3)));
+            sv[k] = (uint8_t)((j < 4 ? c.v.x : c.v.y) >> (8 * (j & 3)));
+        } else {
+            reinterpret_cast<float*>(sm)[k] = m[j];
+            reinterpret_cast<float*>(sv)[k] = v[j];
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(written);
+    if (warp >= 4) return true;
+    if (!__all_sync(~0u, mbar_wait(written, parity, a.wait_limit))) return false;
+    if (warp == 0) write_back(reinterpret_cast<uint8_t*>(t.master + i), sp, kTile * 4, 4);
+    if (warp == 1) write_back(static_cast<uint8_t*>(t.m) + i * kStateSize, sm, kTile * kStateSize, kStateSize);
+    if (warp == 2) write_back(static_cast<uint8_t*>(t.v) + i * kStateSize, sv, kTile * kStateSize, kStateSize);
+    if (warp == 3 && t.param) write_back(reinterpret_cast<uint8_t*>(t.param + i), sb, kTile * 2, 2);
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    return true;
+}
+
+// SHIFTS: some tensor of the list has arrays with offsets.  (With that path in it, though it is never taken, the kernel for
+// others keeps fewer values in registers: 402 M elements in 8 bits 1186 us for 1110.)
+template <bool G32, bool Q, bool SHIFTS, int CAP>
 __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const __grid_constant__ Table<CAP> a) {
     using R = Ring8<G32, Q>;
     extern __shared__ __align__(128) uint8_t ring_sh[];
     Job* jobs = reinterpret_cast<Job*>(ring_sh + R::kStages * R::kStage);
     uint64_t* full = reinterpret_cast<uint64_t*>(jobs + R::kStages);
     uint64_t* empty = full + R::kStages;
-    uint32_t* sent = reinterpret_cast<uint32_t*>(empty + R::kStages);
+    uint64_t* read = empty + R::kStages;         // step_shifted's
+    uint64_t* written = read + 1;
+    uint32_t* sent = reinterpret_cast<uint32_t*>(written + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::kStages; ++i) {
             mbar_init(full + i, 33);             // the bulk copies' bytes, and what each of 32 lanes copies besides
             mbar_init(empty + i, kTileBlocks);
         }
+        mbar_init(read, kTileBlocks);
+        mbar_init(written, kTileBlocks);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     dependent_launch_prologue();
@@ -463,21 +580,35 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
             e = find(a, u, e);
             const Entry& t = a.t[e];
             const int64_t block = (int64_t)(u - a.first[e]) * kTileBlocks, i = block * kBlock;
-            const bool whole = (t.n & kAligned) && (t.n & kCount) - i >= kTile;
+            const int64_t left = (t.n & kCount) - i;
+            const uint32_t how = t.n & kAligned ? (left >= kTile ? kInPlace : kElsewhere)
+                                 : SHIFTS && block > 0 && left >= kTile + 16   ? kShifted
+                                                                               : kElsewhere;
             if (round > 0 && !(ok = __all_sync(~0u, mbar_wait_or_look(empty + at, (round & 1) ^ 1, a.wait_limit)))) break;
             uint8_t* to = ring_sh + at * R::kStage;
-            if (lane == 0) jobs[at] = Job{block, e, whole};
-            if (whole) {
+            if (lane == 0) jobs[at] = Job{block, e, how};
+            if (how != kElsewhere) {
                 if (lane == 0) {
-                    mbar_expect_tx(full + at, R::kBulk);
-                    bulk(to, static_cast<const uint8_t*>(t.grad) + i * (G32 ? 4 : 2), R::kGrad, full + at);
-                    bulk(to + R::kGrad, t.master + i, kTile * 4, full + at);
-                    bulk(to + R::kGrad + kTile * 4, static_cast<const uint8_t*>(t.m) + i * (Q ? 1 : 4), R::kState, full + at);
-                    bulk(to + R::kGrad + kTile * 4 + R::kState, static_cast<const uint8_t*>(t.v) + i * (Q ? 1 : 4), R::kState, full + at);
+                    const uint8_t *g = static_cast<const uint8_t*>(t.grad) + i * (G32 ? 4 : 2), *p = reinterpret_cast<const uint8_t*>(t.master + i),
+                                  *m = static_cast<const uint8_t*>(t.m) + i * (Q ? 1 : 4), *v = static_cast<const uint8_t*>(t.v) + i * (Q ? 1 : 4);
+                    if (!SHIFTS || how == kInPlace) {
+                        mbar_expect_tx(full + at, R::kBulk);
+                        bulk(to, g, R::kGrad, full + at);
+                        bulk(to + R::kMaster, p, kTile * 4, full + at);
+                        bulk(to + R::kM, m, R::kState, full + at);
+                        bulk(to + R::kV, v, R::kState, full + at);
+                    } else {                     // the chunks that cover them: one more where there is an offset
+                        auto more = [](const void* q) { return offset16(q) ? 16u : 0u; };
+                        mbar_expect_tx(full + at, R::kBulk + more(g) + more(p) + more(m) + more(v));
+                        bulk(to, g - offset16(g), R::kGrad + more(g), full + at);
+                        bulk(to + R::kMaster, p - offset16(p), kTile * 4 + more(p), full + at);
+                        bulk(to + R::kM, m - offset16(m), R::kState + more(m), full + at);
+                        bulk(to + R::kV, v - offset16(v), R::kState + more(v), full + at);
+                    }
                 }
                 if (Q && lane < 2 * kTileBlocks) {
                     const float* from = (lane < kTileBlocks ? t.m_scale : t.v_scale) + block + lane % kTileBlocks;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(to + R::kBulk + lane * 4)), "l"(from) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(to + R::kScale + lane * 4)), "l"(from) : "memory");
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(full + at)) : "memory");
             } else {
@@ -490,6 +621,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
         if (lane == 0) *sent = round * R::kStages + at;
         if (!ok && lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_TENSORS_WAIT);
     } else {
+        uint32_t shifted = 0;                    // tiles so far
         for (uint32_t u = begin; u < end; ++u, next()) {
             if (!__all_sync(~0u, mbar_wait_or_look(full + at, round & 1, a.wait_limit))) {
                 if (lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_TENSORS_WAIT);
@@ -498,7 +630,15 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
             const Job job = jobs[at];
             const Entry& t = a.t[job.e];
             const int64_t block = job.block + warp, i = block * kBlock + lane * 8;
-            if (!job.whole) {
+            if (SHIFTS && job.how == kShifted) {
+                if (!step_shifted<G32, Q>(a, job.e, job.block, ring_sh + at * R::kStage, read, written, shifted++ & 1, factor)) {
+                    if (lane == 0) atomicCAS(a.error, 0u, ZS_DEVERR_TENSORS_WAIT);
+                    break;
+                }
+                if (lane == 0) mbar_arrive(empty + at);
+                continue;
+            }
+            if (job.how == kElsewhere) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + at);
                 if (block * kBlock < (t.n & kCount)) {
@@ -507,7 +647,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
                 }
                 continue;
             }
-            const uint8_t* from = ring_sh + at * R::kStage;
+            const uint8_t* stage = ring_sh + at * R::kStage;
             const int mine = warp * kBlock + lane * 8;
             float g[8], p[8];
             auto floats = [](const uint8_t* q, float (&f)[8]) {
@@ -515,14 +655,12 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
                 f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
                 f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
             };
-            if constexpr (G32) floats(from + mine * 4, g);
-            else unpack(BfVec<8>{*reinterpret_cast<const uint4*>(from + mine * 2)}, g);
-            from += R::kGrad;
-            floats(from + mine * 4, p);
-            from += kTile * 4;
+            if constexpr (G32) floats(stage + mine * 4, g);
+            else unpack(BfVec<8>{*reinterpret_cast<const uint4*>(stage + mine * 2)}, g);
+            floats(stage + R::kMaster + mine * 4, p);
             if constexpr (Q) {
-                const float* scales = reinterpret_cast<const float*>(from + 2 * R::kState);
-                Codes8 c{*reinterpret_cast<const uint2*>(from + mine), *reinterpret_cast<const uint2*>(from + R::kState + mine), scales[warp],
+                const float* scales = reinterpret_cast<const float*>(stage + R::kScale);
+                Codes8 c{*reinterpret_cast<const uint2*>(stage + R::kM + mine), *reinterpret_cast<const uint2*>(stage + R::kV + mine), scales[warp],
                          scales[kTileBlocks + warp]};
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + at);
@@ -542,8 +680,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
                 }
             } else {
                 float m[8], v[8];
-                floats(from + mine * 4, m);
-                floats(from + R::kState + mine * 4, v);
+                floats(stage + R::kM + mine * 4, m);
+                floats(stage + R::kV + mine * 4, v);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + at);
                 AdamScalars s = a.s;
@@ -557,6 +695,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
             if (t.param) st_bf<8>(t.param + i, pack(p));
         }
     }
+    if (SHIFTS && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncthreads();
     if (warp == 0) ring_settled(full, R::kStages, *sent);        // no copy is under way when the CTA goes
 }
@@ -566,21 +705,34 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const
 // Sum over the CTA's 256 threads, in thread 0.
 __device__ __forceinline__ double block_sum(double x) {
     __shared__ double sh[8];
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(~0u, x, k);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    if (lane == 0) sh[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < 8; ++w) x += sh[w];
+    if (threadIdx.x >= 32) return 0.0;
+    x = lane < 8 ? sh[lane] : 0.0;
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) x += __shfl_xor_sync(~0u, x, k);
     return x;
 }
 
+// The norm and the factor from the sum of squares.
+__device__ __forceinline__ void norm_and_factor(double sum, float max_norm, float* out) {
+    // the root of the nearest fp32 number, corrected by what that leaves (a division in fp64 takes longer than the rest)
+    const float r = sqrtf((float)sum);
+    const bool inside = r > 0.f && isfinite(r);
+    const float norm = inside ? (float)((double)r + (sum - (double)r * r) * (double)(0.5f / r)) : r;
+    out[0] = norm;
+    // not finite: no factor, and a step given it is not taken
+    out[1] = isfinite(norm) ? fminf(__fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f)), 1.f) : __int_as_float(0x7fffffff);
+}
+
 // A lane adds a tile's 64 squares in fp32, and those sums in fp64 (one fp64 addition per block of 256 alone took the
-// time of twice the bytes: 402 M bf16 gradients 210 us).  The CTAs' sums (as many as the caller has room for, each of
+// time of twice the bytes: 402 M bf16 gradients 210 us, now 117; 118 at the copy rate).  The CTAs' sums (as many as the caller has room for, each of
 // its own blocks, so the same bits every time) are kept as two fp32 words each and added by one CTA.
 template <bool G32, int CAP>
-__global__ void __launch_bounds__(256) k_grad_norm(const __grid_constant__ Table<CAP> a) {
+__global__ void __launch_bounds__(256, kNormCtas) k_grad_norm(const __grid_constant__ Table<CAP> a) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
     const uint32_t warps = (uint32_t)(gstride() >> 5);
@@ -588,31 +740,43 @@ __global__ void __launch_bounds__(256) k_grad_norm(const __grid_constant__ Table
     int e = 0;
     for (uint32_t u = (uint32_t)(gtid() >> 5); u < a.tiles; u += warps) {
         e = find(a, u, e);
+        // tiles from the tensor's first element at 8 elements' bytes on; the first tile takes those before it along
         const Entry& t = a.t[e];
+        constexpr int kSize = G32 ? 4 : 2;
         const int64_t n = t.n & kCount, begin = (int64_t)(u - a.first[e]) * kTile;
-        const bool whole = (t.n & kAligned) && n - begin >= kTile;
+        const int64_t head = min(n, (int64_t)((0 - (uintptr_t)t.grad) & (8 * kSize - 1)) / kSize), left = n - head - begin;
+        const uint8_t* from = static_cast<const uint8_t*>(t.grad) + (head + begin) * kSize;
         float q[kTileBlocks];
-        if (whole) {
+        auto squares = [](const float (&g)[8]) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
+            return s;
+        };
+        if (left >= kTile) {
 #pragma unroll
             for (int b = 0; b < kTileBlocks; ++b) {
                 float g[8];
-                load_grad8<G32>(t.grad, begin + b * kBlock + lane * 8, g);
-                q[b] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[b] = fmaf(g[j], g[j], q[b]);
+                load_grad8<G32>(from, b * kBlock + lane * 8, g);
+                q[b] = squares(g);
             }
         } else {
 #pragma unroll
             for (int b = 0; b < kTileBlocks; ++b) {
-                float s = 0.f;
+                const int at = b * kBlock + lane * 8;
+                float g[8];
+                if (at + 8 <= left) {
+                    load_grad8<G32>(from, at, g);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int64_t i = begin + b * kBlock + lane + 32 * j;
-                    const float g = i < n ? load_grad<G32>(t.grad, i) : 0.f;
-                    s = fmaf(g, g, s);
+                    for (int j = 0; j < 8; ++j) g[j] = at + j < left ? load_grad<G32>(from, at + j) : 0.f;
                 }
-                q[b] = s;
+                q[b] = squares(g);
             }
+        }
+        if (begin == 0 && lane < head) {
+            const float g = load_grad<G32>(t.grad, lane);
+            q[0] = fmaf(g, g, q[0]);
         }
         sum += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
     }
@@ -622,6 +786,7 @@ __global__ void __launch_bounds__(256) k_grad_norm(const __grid_constant__ Table
         if (a.add) sum += (double)p[0] + p[1];
         p[0] = (float)sum;
         p[1] = isfinite(p[0]) ? (float)(sum - p[0]) : 0.f;
+        if (a.out) norm_and_factor(sum, a.max_norm, a.out);          // the only CTA
     }
 }
 
@@ -630,13 +795,7 @@ __global__ void __launch_bounds__(256) k_grad_norm_end(const float* partials, in
     double sum = 0.0;
     for (int i = threadIdx.x; i < n; i += 256) sum += (double)partials[2 * i] + partials[2 * i + 1];
     sum = block_sum(sum);
-    if (threadIdx.x == 0) {
-        const float norm = (float)sqrt(sum);
-        // not finite: no factor, and a step given it is not taken
-        const float factor = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
-        out[0] = norm;
-        out[1] = isfinite(norm) ? fminf(factor, 1.f) : __int_as_float(0x7fffffff);
-    }
+    if (threadIdx.x == 0) norm_and_factor(sum, max_norm, out);
 }
 
 // ------------------------------------------------------------------ host
@@ -663,17 +822,15 @@ int check_tensor(const char* fn, const zs_tensor& t, int i, int grad_bytes, int 
     return ZS_OK;
 }
 
-// Whether whole tiles are copied, and values written eight at a time.
-bool wide_blocks(const zs_tensor& t, int grad_bytes, int state_bits, bool step) {
-    if (!aligned(t.grad, step ? 16 : 8 * grad_bytes)) return false;
-    if (!step) return true;
+// Whether the step's tiles are copied as they are, and values written eight at a time.
+bool in_place(const zs_tensor& t, int state_bits) {
     const uintptr_t state = state_bits == 8 ? 16 : 32;
-    return aligned(t.master, 32) && aligned(t.param, 16) && aligned(t.m, state) && aligned(t.v, state);
+    return aligned(t.grad, 16) && aligned(t.master, 32) && aligned(t.param, 16) && aligned(t.m, state) && aligned(t.v, state);
 }
 
 // Calls launch(table, first) for the tensors, as many at a time as a launch's parameters hold.
 template <int CAP, typename F>
-cudaError_t by_table(const zs_tensor* tensors, int count, int grad_bytes, int state_bits, bool step, uint32_t seed, Table<CAP>& a, F launch) {
+cudaError_t by_table(const zs_tensor* tensors, int count, int state_bits, uint32_t seed, Table<CAP>& a, F launch) {
     bool first = true;
     int i = 0;
     do {
@@ -686,7 +843,7 @@ cudaError_t by_table(const zs_tensor* tensors, int count, int grad_bytes, int st
             if (a.count && tiles + more > 0x7fffffffu) break;
             Entry& e = a.t[a.count];
             e = Entry{t.grad, t.master, (uint16_t*)t.param, t.m, t.v, t.m_scale, t.v_scale, t.n};
-            if (wide_blocks(t, grad_bytes, state_bits, step)) e.n |= kAligned;
+            if (in_place(t, state_bits)) e.n |= kAligned;
             if (t.no_decay) e.n |= kNoDecay;
             a.first[a.count] = (uint32_t)tiles;
             a.key[a.count] = mix(seed + 0x9e3779b9u * ((uint32_t)i + 1));
@@ -709,19 +866,26 @@ cudaError_t by_table(const zs_tensor* tensors, int count, int grad_bytes, int st
 // 4, 8 and 16 tiles.  139 M with states in 32 bits: 614; 546, 557, 573 with 2, 4 and 8).
 constexpr uint32_t kRun8 = 8, kRun32 = 3;
 
-template <bool G32, bool Q, int CAP>
-cudaError_t step_tensors(const zs_tensor* tensors, int count, uint32_t seed, Table<CAP>& a, cudaStream_t st) {
+template <bool G32, bool Q, bool SHIFTS, int CAP>
+cudaError_t launch_step(Table<CAP>& t, cudaStream_t st) {
     constexpr int smem = kStepSmem<G32, Q>;
     static_assert(kStepCtas * (smem + 1024) <= 228 * 1024, "resident CTAs");
     static std::atomic<uint64_t> ready{0};
-    const auto kern = k_adamw_tensors<G32, Q, CAP>;
+    const auto kern = k_adamw_tensors<G32, Q, SHIFTS, CAP>;
     const cudaError_t e = ready_once(ready, (const void*)kern, smem);
     if (e != cudaSuccess) return e;
-    const uint32_t room = (uint32_t)q8_host::sm_count() * kStepCtas, most = Q ? kRun8 : kRun32;
-    return by_table<CAP>(tensors, count, G32 ? 4 : 2, Q ? 8 : 32, true, seed, a, [&](Table<CAP>& t, bool) {
+    const uint32_t room = (uint32_t)q8_host::sm_count() * kStepCtas, most = Q ? kRun8 : kRun32, run = t.tiles / (room * 4);
+    t.run = run < 1 ? 1 : run < most ? run : most;
+    return launch_kernel(kern, dim3((t.tiles + t.run - 1) / t.run), dim3(kStepThreads), smem, st, t);
+}
+
+template <bool G32, bool Q, int CAP>
+cudaError_t step_tensors(const zs_tensor* tensors, int count, uint32_t seed, Table<CAP>& a, cudaStream_t st) {
+    return by_table<CAP>(tensors, count, Q ? 8 : 32, seed, a, [&](Table<CAP>& t, bool) {
         if (!t.count) return cudaSuccess;
-        t.run = t.tiles / (room * 4) < 1 ? 1 : t.tiles / (room * 4) < most ? t.tiles / (room * 4) : most;
-        return launch_kernel(kern, dim3((t.tiles + t.run - 1) / t.run), dim3(kStepThreads), smem, st, t);
+        bool shifts = false;
+        for (int i = 0; i < t.count; ++i) shifts |= !(t.t[i].n & kAligned) && (t.t[i].n & kCount) > 2 * kTile;
+        return shifts ? launch_step<G32, Q, true>(t, st) : launch_step<G32, Q, false>(t, st);
     });
 }
 
@@ -741,10 +905,12 @@ cudaError_t step_list(const zs_tensor* tensors, int count, bool g32, bool q, uin
 }
 
 template <bool G32, int CAP>
-cudaError_t norm_tensors(const zs_tensor* tensors, int count, float* partials, int n_partials, cudaStream_t st) {
+cudaError_t norm_tensors(const zs_tensor* tensors, int count, float* partials, int n_partials, float max_norm, float* out, cudaStream_t st) {
     Table<CAP> a;
     a.partials = partials;
-    return by_table<CAP>(tensors, count, G32 ? 4 : 2, 32, false, 0, a, [&](Table<CAP>& t, bool first) {
+    a.max_norm = max_norm;
+    a.out = n_partials == 1 ? out : nullptr;     // overwritten by later launches, if there are any
+    return by_table<CAP>(tensors, count, 32, 0, a, [&](Table<CAP>& t, bool first) {
         t.add = !first;
         return launch_kernel(k_grad_norm<G32, CAP>, dim3((unsigned)n_partials), dim3(256), 0, st, t);
     });
@@ -807,8 +973,8 @@ extern "C" int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t
     const int n = (int)(ctas < 1 ? 1 : ctas < most ? ctas : most);
     const bool few = n_tensors <= zs::kTableFew;
     cudaError_t e;
-    if (grad_bytes == 4) e = few ? zs::norm_tensors<true, zs::kTableFew>(tensors, n_tensors, partials, n, st) : zs::norm_tensors<true, zs::kTableMost>(tensors, n_tensors, partials, n, st);
-    else e = few ? zs::norm_tensors<false, zs::kTableFew>(tensors, n_tensors, partials, n, st) : zs::norm_tensors<false, zs::kTableMost>(tensors, n_tensors, partials, n, st);
-    if (e == cudaSuccess) e = zs::launch_kernel(zs::k_grad_norm_end, dim3(1), dim3(256), 0, st, (const float*)partials, n, max_norm, out);
+    if (grad_bytes == 4) e = few ? zs::norm_tensors<true, zs::kTableFew>(tensors, n_tensors, partials, n, max_norm, out, st) : zs::norm_tensors<true, zs::kTableMost>(tensors, n_tensors, partials, n, max_norm, out, st);
+    else e = few ? zs::norm_tensors<false, zs::kTableFew>(tensors, n_tensors, partials, n, max_norm, out, st) : zs::norm_tensors<false, zs::kTableMost>(tensors, n_tensors, partials, n, max_norm, out, st);
+    if (e == cudaSuccess && n > 1) e = zs::launch_kernel(zs::k_grad_norm_end, dim3(1), dim3(256), 0, st, (const float*)partials, n, max_norm, out);
     return cuda_status(fn, e);
 }

@@ -874,8 +874,8 @@ int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_b
  *     out[0] = sqrt( sum of grad^2 ),   out[1] = min(1, max_norm / (out[0] + 1e-6))
  * Squares and sums of 64 are fp32 (|grad| below 2e18), the sums of these fp64.  A
  * norm that is not finite gives out[1] = NaN.  Only n and grad of the tensors are used.
- *   partials    caller's scratch, n_partials >= 2 floats, two per partial sum; at most 16
- *               per SM are used, fewer make the call slower.
+ *   partials    caller's scratch, n_partials >= 2 floats, two per partial sum; at most 8
+ *               per SM are used (1216), fewer make the call slower.
  *   out         two floats. */
 int zs_grad_norm(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, float max_norm, float* partials,
                  int64_t n_partials, float* out, void* stream);

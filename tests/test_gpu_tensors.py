@@ -75,7 +75,7 @@ def _f32(x):
     return x.astype(np.float32)
 
 
-@pytest.mark.parametrize("shift", [0, 1, 8])
+@pytest.mark.parametrize("shift", [0, 1, 8, 13])
 @pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("params", [True, False])
 def test_states_of_32_bits_are_the_flat_steps(shift, grad, params):
@@ -129,7 +129,7 @@ def _check_state(codes, scale, x, err, random, positive):
     assert np.all((got >= a) & (got <= b)), "a code: %s" % np.nonzero((got < a) | (got > b))[0][:5]
 
 
-@pytest.mark.parametrize("shift", [0, 1, 8])
+@pytest.mark.parametrize("shift", [0, 1, 8, 13])
 @pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("factor", [None, 0.37])
 def test_states_of_8_bits(shift, grad, factor):
@@ -459,3 +459,68 @@ def test_an_eps_that_is_subnormal_or_none():
         master = torch.ones(512, device="cuda")
         zs.zs_adamw_tensors(zs.TensorList([grad], [master], [m], [v], m_scales=[ms], v_scales=[vs]), dict(HP, eps=eps, weight_decay=0.0), 1)
         assert bool((master[256:] == 1).all()) and bool(torch.isfinite(master).all()) and bool((master[:256] != 1).all())
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_any_offset_of_any_array(bits, grad):
+    """Each array at an offset of its own, tensors of many tiles, with values that are not finite, far too large and of zero
+    in some blocks: the same bits as at aligned addresses, and nothing written beside them."""
+    n, rng = 25000, np.random.default_rng(bits)
+    names = ["grad", "master", "m", "v", "param"]
+    a = Arrays([n], bits, grad, seed=7)
+    for where, value in ((3000, float("nan")), (9000, float("inf")), (12345, 1e9), (24999, -1e9), (0, 1e5)):
+        a.grad[0][where] = value
+    a.grad[0][5000:7000] = 0.0
+    for run in range(6):
+        b = Arrays([n], bits, grad, seed=7)
+        shifts = {k: int(rng.integers(0, 16)) for k in names}
+        moved, bufs = {}, {}
+        for k in names:
+            x, fill = getattr(a, k)[0], 3
+            bufs[k] = torch.full((n + 64,), fill, dtype=x.dtype, device="cuda")
+            moved[k] = bufs[k][16 + shifts[k]:16 + shifts[k] + n]
+            moved[k].copy_(x)
+        scales = [[a.ms[0].clone()], [a.vs[0].clone()]] if bits == 8 else [None, None]
+        ts = zs.TensorList([moved["grad"]], [moved["master"]], [moved["m"]], [moved["v"]], params=[moved["param"]], m_scales=scales[0], v_scales=scales[1])
+        for k in ("master", "m", "v"):
+            getattr(b, k)[0].copy_(getattr(a, k)[0])
+        b.grad[0].copy_(a.grad[0])
+        if bits == 8:
+            b.ms[0].copy_(a.ms[0])
+            b.vs[0].copy_(a.vs[0])
+        for t in (1, 2):
+            zs.zs_adamw_tensors(ts, HP, t, seed=t)
+            zs.zs_adamw_tensors(b.list(), HP, t, seed=t)
+        for k in names[1:]:
+            # a NaN is a NaN, whichever
+            x, y = (v if v.dtype == torch.uint8 else torch.nan_to_num(v, nan=7.5) for v in (moved[k], getattr(b, k)[0]))
+            assert torch.equal(x, y), (k, shifts)
+            outside = bufs[k].clone()
+            outside[16 + shifts[k]:16 + shifts[k] + n] = 3
+            assert bool((outside == 3).all()), (k, shifts)
+        if bits == 8:
+            assert torch.equal(scales[0][0], b.ms[0]) and torch.equal(scales[1][0], b.vs[0])
+
+
+def test_waits_that_run_out_in_shifted_tiles():
+    sizes = [1 << 19, 3000]
+    want = Arrays(sizes, 8, shift=3, seed=3)
+    zs.zs_adamw_tensors(want.list(), HP, 2, seed=2)
+    want = want.snapshot()
+    try:
+        for limit in (0, 0, 1, 300, 3000, 30000):
+            a = Arrays(sizes, 8, shift=3, seed=3)
+            torch.cuda.synchronize()
+            zs.zs_set_q8_wait_limit(limit)
+            zs.zs_adamw_tensors(a.list(), HP, 2, seed=2)
+            torch.cuda.synchronize()
+            assert zs.zs_device_status(clear=True) in (zs.ZS_DEVERR_NONE, zs.ZS_DEVERR_TENSORS_WAIT)
+            a.assert_untouched_outside()
+            zs.zs_set_q8_wait_limit()
+            a = Arrays(sizes, 8, shift=3, seed=3)
+            zs.zs_adamw_tensors(a.list(), HP, 2, seed=2)
+            assert all(torch.equal(x, want[k]) for k, x in a.snapshot().items())
+            assert zs.zs_device_status() == zs.ZS_DEVERR_NONE
+    finally:
+        zs.zs_set_q8_wait_limit()
