@@ -113,7 +113,7 @@ extern "C" {
 #define ZS_DEVERR_CONSUMER_WAIT 2u   /* a staged kernel's consumer gave up waiting for its data     */
 #define ZS_DEVERR_SELFTEST      3u   /* zs_selftest_wait_timeout ran its wait out (expected)         */
 #define ZS_DEVERR_GATHER_WAIT   4u   /* a bulk-store gather gave up waiting for its tile             */
-#define ZS_DEVERR_MATMUL_WAIT   5u   /* zs_q8_matmul gave up waiting for a tile or an accumulator    */
+#define ZS_DEVERR_MATMUL_WAIT   5u   /* an 8-bit product gave up waiting for a tile or an accumulator */
 #define ZS_DEVERR_TILE_WAIT     6u   /* an 8-bit encode, transpose, gate or norm backward gave up    */
 #define ZS_DEVERR_TENSORS_WAIT  7u   /* zs_adamw_tensors gave up waiting for a tile                  */
 

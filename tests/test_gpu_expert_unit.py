@@ -144,3 +144,56 @@ def test_two_units_at_once_on_two_streams():
                 _step(unit, x, t)
     for unit, want in zip(units, wants):
         assert all(torch.equal(a, b) for a, b in zip(_state(unit), want))
+
+
+FIRST_CALLS = """
+import torch
+import fsdp_sharded_optimizer_flatparameter_gb300 as zs
+T, K, E, C, N = 16384, 8, 64, 256, 256
+i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+b = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+ids = torch.arange(T * K, device="cuda").view(T, K) % E
+row_of, starts, counts = i32(T, K), i32(E + 1), i32(E)
+rows = zs.expert_rows(T, K, E, 128)
+x, y, w, out, result = torch.ones_like(b(T, C)), zs.q8_empty(rows, C), zs.q8_empty(E * N, C), b(rows, N), b(T, N)
+y_t, grad = zs.q8_empty(C, rows), b(E * C, C)
+zs_w = torch.ones_like(b(E * N, C))
+n = 700
+g = [torch.ones(n + i, device="cuda") for i in range(60)]
+states = [(zs.state_zeros(n + i), zs.state_zeros(n + i)) for i in range(60)]
+master = [torch.zeros(n + i, device="cuda") for i in range(60)]
+ts = zs.TensorList(g, master, [s[0][0] for s in states], [s[1][0] for s in states], m_scales=[s[0][1] for s in states], v_scales=[s[1][1] for s in states])
+norm, partials = torch.zeros(2, device="cuda"), torch.zeros(64, device="cuda")
+dw, dy = torch.zeros(T, K, device="cuda"), zs.q8_empty(rows, N)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    zs.zs_q8_encode(zs_w, w)
+    zs.zs_expert_sort(ids, 128, row_of, starts, counts)
+    zs.zs_expert_dispatch(x, row_of, starts, counts, y=y)
+    zs.zs_q8_matmul_experts(y, w, starts, out)
+    zs.zs_expert_combine(out, row_of, None, result)
+    zs.zs_expert_combine_backward(result, out, row_of, None, starts, counts, dw, dy=dy)
+    zs.zs_q8_transpose(y, y_t)
+    zs.zs_q8_matmul_experts_grad(y_t, y_t, starts, grad)
+    zs.zs_grad_norm(ts, 1e9, partials, norm)
+    zs.zs_adamw_tensors(ts, dict(lr=1.0, beta1=0.5, beta2=0.5, eps=0.0, weight_decay=0.0), 1, factor=norm[1:])
+graph.replay()
+torch.cuda.synchronize()
+assert zs.zs_device_status() == zs.ZS_DEVERR_NONE
+assert counts.tolist() == [T * K // E] * E
+assert bool((result == K * C).all()) and bool((dw == N * K * C * C).all())
+assert bool((grad.float() == T * K // E).all())
+assert abs(float(norm[0]) - sum(len(x) for x in g) ** 0.5) < 1e-2 and all(bool((m + 1).abs().max() < 1e-5) for m in master)
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    got = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, cwd=ROOT, timeout=300, env=dict(os.environ, PYTHONPATH=ROOT))
+    assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
