@@ -863,9 +863,10 @@ typedef struct {
  *               zs_grad_norm, a loss scale's inverse), NULL: 1.  NaN: nothing is written,
  *               the step is left out.
  *   seed        of the 8-bit states' roundings.
- * Arrays are aligned to their elements; where grad, master (and 32-bit states) start at
- * multiples of eight elements' bytes, param of 16 and codes of 8, eight elements are moved per
- * access, elsewhere one (views into flat buffers at any element).  No two arrays of the list overlap.
+ * Arrays are aligned to their elements.  Where master and 32-bit states start at multiples of 32
+ * bytes and grad, param and codes of 16, eight elements are moved per access; arrays elsewhere
+ * (views into flat buffers at any element) go through shared memory element by element.  The same
+ * bits either way.  No two arrays of the list overlap.
  * Errors: ZS_ERR_INVALID (nothing enqueued), ZS_ERR_CUDA. */
 int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_bytes, int32_t state_bits,
                      const zs_adamw_hparams* hp, int64_t step, const float* factor, uint32_t seed, void* stream);
