@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int64_t p = (int64_t)x.p0 + rank * 128 + sub * 32;         // the warp's first row
                 int rows = x.p_end - p < 32 ? (int)(x.p_end - p) : 32;
                 if (!sum && !a.first) rows = 0;
-                const bool tiled = a.tiled && rows == 32;
+                const bool whole_rows = a.tiled && rows == 32;
                 const uint32_t from = tmem + acc.at * BN + ((uint32_t)(sub * 32) << 16);
                 float* stage = store_sh + (warp - 6) * kStoreStage;
 #pragma unroll 1
@@ -1049,8 +1049,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     if (lane == 0) tma_stores_read();                            // the piece before has left the staging
                     __syncwarp();
-                    const int q = x.q0 - x.out_col + c;
-                    if (tiled) {
+                    const int q = x.q0 - x.out_col + c, n = x.q_end - x.out_col - q;
+                    // A group's last columns by the warps: a tiled store cut off inside 16 bytes writes all 16, and what lies
+                    // between the rows is the caller's.
+                    if (whole_rows && n >= 32) {
                         uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(stage) + lane * 64);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -1064,7 +1066,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         if (lane == 0) tma_store(&map_out, stage, q, (int)(x.out_row + p));
                     } else {
                         uint16_t* o = a.out + (x.out_row + p) * a.ldo + q;
-                        const int n = x.q_end - x.out_col - q;
                         store_rows16(o, a.ldo, reinterpret_cast<float(&)[16]>(f[0]), rows, n, a.align, a.scale, a.first, stage);
                         store_rows16(o + 16, a.ldo, reinterpret_cast<float(&)[16]>(f[16]), rows, n - 16, a.align, a.scale, a.first, stage);
                     }

@@ -174,3 +174,27 @@ def test_waits_that_run_out(grad):
         zs.zs_set_q8_wait_limit()
         call()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n", [1, 7, 20, 31, 33, 44, 97, 230, 700])
+@pytest.mark.parametrize("align", [8, 16])
+@pytest.mark.parametrize("grad", [False, True])
+def test_out_as_the_first_columns_of_wider_rows(grad, align, n):
+    """Rows of out that start on 16 or 32 bytes and end inside them: the columns beside keep what they hold."""
+    rng = np.random.default_rng(n + align)
+    k = 384 if grad else 200
+    sizes = [128, 0, 256] if grad else [300, 0, 160, 500]          # past the few rows of an expert
+    E, starts = len(sizes), _starts(sizes)
+    rows = 300 if grad else sum(sizes)
+    a, av = encoded(rng, rows, k)
+    b, bv = encoded(rng, n if grad else E * n, k)
+    oracle, call = (experts.product_grad, zs.zs_q8_matmul_experts_grad) if grad else (experts.product, zs.zs_q8_matmul_experts)
+    host = starts.tolist()
+    want, size = oracle(av, bv, host), oracle(np.abs(av), np.abs(bv), host)
+    for more in (0, align):
+        out = Bf16Matrix(len(want), n, pad=-n % align + more)
+        out.t.fill_(float("nan"))
+        for _ in range(3):
+            call(a.pair, b.pair, starts, out.t)
+        check_close(to64(out.t), want, _bound(size, want, k) + 1e-38, "out")
+        out.assert_untouched_outside()
