@@ -1085,7 +1085,7 @@ def zs_adamw_tensors(tensors, hp, step, factor=None, seed=0, stream=None):
 
 def zs_grad_norm(tensors, max_norm, partials, out, stream=None):
     """The norm of a TensorList's gradients into out[0], the factor that clips it to max_norm into out[1] (fp32 [2]);
-    partials: fp32 scratch of any size."""
+    partials: fp32 scratch of at least 2 elements."""
     dev = _list_here(tensors)
     return _check(_lib.zs_grad_norm(tensors._array, len(tensors), tensors.grad_bytes, float(max_norm),
                                     _vector(partials, partials.numel(), _F32, "partials", dev), partials.numel(),

@@ -717,12 +717,27 @@ __device__ __forceinline__ double block_sum(double x) {
     return x;
 }
 
+// A CTA's sum among the partial ones: the fp64 number in two words, as sums of fp32 squares go past fp32's range.
+__device__ __forceinline__ double partial_sum(const float* partials, int i) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(partials) + 2 * i;
+    return __hiloint2double((int)p[1], (int)p[0]);
+}
+__device__ __forceinline__ void keep_partial_sum(float* partials, int i, double sum) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(partials) + 2 * i;
+    p[0] = (uint32_t)__double2loint(sum);
+    p[1] = (uint32_t)__double2hiint(sum);
+}
+
 // The norm and the factor from the sum of squares.
 __device__ __forceinline__ void norm_and_factor(double sum, float max_norm, float* out) {
-    // the root of the nearest fp32 number, corrected by what that leaves (a division in fp64 takes longer than the rest)
-    const float r = sqrtf((float)sum);
+    // the root of the nearest fp32 number, corrected by what that leaves (a division in fp64 takes longer than the rest);
+    // sums past fp32's range are scaled into it, finite ones are below 2^128 times the number of tiles and lanes
+    const bool large = sum > 0x1p120;
+    const double s = large ? sum * 0x1p-128 : sum;
+    const float r = sqrtf((float)s);
     const bool inside = r > 0.f && isfinite(r);
-    const float norm = inside ? (float)((double)r + (sum - (double)r * r) * (double)(0.5f / r)) : r;
+    const float root = inside ? (float)((double)r + (s - (double)r * r) * (double)(0.5f / r)) : r;
+    const float norm = large ? root * 0x1p64f : root;
     out[0] = norm;
     // not finite: no factor, and a step given it is not taken
     out[1] = isfinite(norm) ? fminf(__fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f)), 1.f) : __int_as_float(0x7fffffff);
@@ -730,7 +745,7 @@ __device__ __forceinline__ void norm_and_factor(double sum, float max_norm, floa
 
 // A lane adds a tile's 64 squares in fp32, and those sums in fp64 (one fp64 addition per block of 256 alone took the
 // time of twice the bytes: 402 M bf16 gradients 210 us, now 117; 118 at the copy rate).  The CTAs' sums (as many as the caller has room for, each of
-// its own blocks, so the same bits every time) are kept as two fp32 words each and added by one CTA.
+// its own blocks, so the same bits every time) are kept in two words each and added by one CTA.
 template <bool G32, int CAP>
 __global__ void __launch_bounds__(256, kNormCtas) k_grad_norm(const __grid_constant__ Table<CAP> a) {
     dependent_launch_prologue();
@@ -782,10 +797,8 @@ __global__ void __launch_bounds__(256, kNormCtas) k_grad_norm(const __grid_const
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) {
-        float* p = a.partials + 2 * blockIdx.x;
-        if (a.add) sum += (double)p[0] + p[1];
-        p[0] = (float)sum;
-        p[1] = isfinite(p[0]) ? (float)(sum - p[0]) : 0.f;
+        if (a.add) sum += partial_sum(a.partials, (int)blockIdx.x);
+        keep_partial_sum(a.partials, (int)blockIdx.x, sum);
         if (a.out) norm_and_factor(sum, a.max_norm, a.out);          // the only CTA
     }
 }
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(256, kNormCtas) k_grad_norm(const __grid_const
 __global__ void __launch_bounds__(256) k_grad_norm_end(const float* partials, int n, float max_norm, float* out) {
     dependent_launch_prologue();
     double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) sum += (double)partials[2 * i] + partials[2 * i + 1];
+    for (int i = threadIdx.x; i < n; i += 256) sum += partial_sum(partials, i);
     sum = block_sum(sum);
     if (threadIdx.x == 0) norm_and_factor(sum, max_norm, out);
 }

@@ -873,8 +873,11 @@ int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_b
 
 /* The 2-norm of all gradients of the list and the factor that clips it:
  *     out[0] = sqrt( sum of grad^2 ),   out[1] = min(1, max_norm / (out[0] + 1e-6))
- * Squares and sums of 64 are fp32 (|grad| below 2e18), the sums of these fp64.  A
- * norm that is not finite gives out[1] = NaN.  Only n and grad of the tensors are used.
+ * Squares and sums of 64 are fp32 (|grad| below 2e18), the sums of these fp64.  The
+ * squares of small gradients are rounded to multiples of 2^-149 (those of |grad| below
+ * 2^-75 to 0): out[0]^2 is off by 2^-150 for each at most, besides the relative
+ * roundings.  A norm that is not finite gives out[1] = NaN.  Only n and grad of the
+ * tensors are used.
  *   partials    caller's scratch, n_partials >= 2 floats, two per partial sum; at most 8
  *               per SM are used (1216), fewer make the call slower.
  *   out         two floats. */

@@ -524,3 +524,44 @@ def test_waits_that_run_out_in_shifted_tiles():
             assert zs.zs_device_status() == zs.ZS_DEVERR_NONE
     finally:
         zs.zs_set_q8_wait_limit()
+
+
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_partials", [2, 5000])
+@pytest.mark.parametrize("sizes", [[100000, 3, 70001], [300] * 500])
+def test_norm_of_gradients_near_their_bound(grad, n_partials, sizes):
+    """Gradients up to 2e18: the sum of their squares is far past fp32's range, their norm is not, and the step is taken."""
+    a = Arrays(sizes, 32, grad, 5, seed=8)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for g in a.grad:
+        g.copy_(1.9e18 * (1 - 0.5 * torch.rand(len(g), generator=gen, device="cuda")))
+    partials, out = torch.empty(n_partials, device="cuda"), torch.empty(2, device="cuda")
+    zs.zs_grad_norm(a.list(), 1.0, partials, out)
+    norm, factor = tensors.grad_norm([g.double().cpu().numpy() for g in a.grad], 1.0)
+    assert norm > 2.0 ** 64
+    # as in test_norm
+    assert abs(float(out[0]) - norm) <= 8 * U32 * norm and abs(float(out[1]) - factor) <= 12 * U32 * factor
+    before = [x.clone() for x in a.master]
+    zs.zs_adamw_tensors(a.list(), HP, 2, factor=out[1:])
+    assert all(bool(torch.isfinite(x).all()) and not torch.equal(x, y) for x, y in zip(a.master, before))
+
+
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_norm_of_tiny_gradients(grad):
+    """Near fp32's least number a sum of squares is off by half of it for every square besides what is relative, so the root
+    by that over the norm; gradients below 2^-75 have no square."""
+    a = Arrays([50000, 7], 32, grad, 3, seed=8)
+    partials, out = torch.empty(64, device="cuda"), torch.empty(2, device="cuda")
+    for scale in (1e-17, 1e-18):                                     # of gradients of about 1e-3
+        for g in a.grad:
+            g.copy_(g.float() * scale)
+        zs.zs_grad_norm(a.list(), 1e-7, partials, out)
+        norm, factor = tensors.grad_norm([g.double().cpu().numpy() for g in a.grad], 1e-7)
+        assert abs(float(out[0]) - norm) <= 8 * U32 * norm + 50007 * 2.0 ** -150 / norm
+        assert abs(float(out[1]) - factor) <= 12 * U32 * factor
+        for g in a.grad:
+            g.copy_(g.float() / scale)
+    for g in a.grad:
+        g.fill_(2.5e-23)
+    zs.zs_grad_norm(a.list(), 1e-7, partials, out)
+    assert float(out[0]) == 0 and abs(float(out[1]) - 0.1) <= 4 * U32 * 0.1
