@@ -142,14 +142,16 @@ __device__ __forceinline__ uint32_t four_codes(uint32_t a, uint32_t b, uint32_t 
 __device__ __forceinline__ float2 sum2(float2 a, float one, float2 b) { return q8_fma2(a, make_float2(one, one), b); }
 
 // Square root rounded to nearest, given -2^66 y: from the hardware's reciprocal root one correction by the residual
-// y - s^2, which fused multiplication gives exactly (P. Markstein, 1990); equal to __fsqrt_rn for every y of [2^-126, 2^54).
-// 2^66 y has a normal root for every y > 0, and the result is exact to scale back; y = 0 gives 0.
+// y - s^2, which fused multiplication gives exactly (P. Markstein, 1990).  Compared with __fsqrt_rn for every y of
+// [2^-168, 2^54): equal; below, where the residual loses bits, 25 of the 2^26 values down to 2^-176 differ.
+// 2^66 y has a normal root for every y > 0, and the result is exact to scale back; 0 is added to it so that y = 0 gives 0
+// and not -0, whose sign would be kept in the code.
 __device__ __forceinline__ float2 root2(float2 minus) {
     float2 q;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(fmaxf(-minus.x, 0x1p-126f)));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(fmaxf(-minus.y, 0x1p-126f)));
     const float2 s = q8_mul2(minus, q), h = q8_mul2(q, make_float2(0.5f, 0.5f));         // s: minus the root
-    return q8_mul2(q8_fma2(q8_fma2(s, s, minus), h, s), make_float2(-0x1p-33f, -0x1p-33f));
+    return q8_fma2(q8_fma2(q8_fma2(s, s, minus), h, s), make_float2(-0x1p-33f, -0x1p-33f), make_float2(0.f, 0.f));
 }
 
 // max(top, |x.x|, |x.y|), NaN if one is.

@@ -565,3 +565,21 @@ def test_norm_of_tiny_gradients(grad):
         g.fill_(2.5e-23)
     zs.zs_grad_norm(a.list(), 1e-7, partials, out)
     assert float(out[0]) == 0 and abs(float(out[1]) - 0.1) <= 4 * U32 * 0.1
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_a_root_of_zero_has_the_code_of_zero(shift):
+    """v = 0 is the code 0 without a sign, whichever path stores it: in blocks of nothing, beside other elements, beside one
+    that is not finite, in whole tiles and parts of one; a code 0x80 that is there already is read as 0."""
+    n = 3 * 2048 + 100
+    a = Arrays([n], 8, shift=shift, seed=3)
+    a.m[0].zero_()
+    a.v[0].zero_()
+    a.v[0][::7] = 0x80
+    a.grad[0][::3] = 0.0
+    a.grad[0][3000:5000] = 0.0
+    a.grad[0][5001] = float("inf")
+    zs.zs_adamw_tensors(a.list(), HP, 2, seed=1)
+    none = a.grad[0] == 0
+    assert not bool(a.v[0][none].any()) and not bool((a.m[0][none] & 0x7f).any())
+    assert bool((a.v[0][~none] > 0).all()) and bool((a.v[0] < 0x80).all())
