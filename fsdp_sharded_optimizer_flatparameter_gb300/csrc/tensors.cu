@@ -170,6 +170,8 @@ __device__ __forceinline__ float reciprocal(float x) {
     return d;
 }
 
+constexpr float kUp = -0x1p66f;              // what the sums under roots are multiplied by
+
 struct Scalars8 {
     float beta1, beta2, eps, decay, c1, c2, step_size, inv_root, one;
 };
@@ -194,7 +196,6 @@ __device__ __forceinline__ bool step8(const float2 (&g)[4], float2 (&p)[4], Code
     float2 m[4], r[4];
     decode8(c.m, c.ms, m);
     decode8(c.v, c.vs, r);
-    constexpr float kUp = -0x1p66f;
     float top_m = 0.f, top_r = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -244,14 +245,17 @@ __device__ uint2 encode8_any(const float (&x)[8], const uint32_t (&random)[8], f
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (isfinite(x[j])) top = max(top, __float_as_uint(fabsf(x[j])));
+    const float most = __uint_as_float(__reduce_max_sync(~0u, top));
     float inverse;
-    scale = block_scale(__uint_as_float(__reduce_max_sync(~0u, top)), inverse);
+    scale = block_scale(most, inverse);
+    // one product, rounded once, as in step8 where that can be; beyond kFastTop the two factors have to stay apart
+    const bool once = most <= kFastTop;
+    const float by = once ? inverse * 0x1p-120f : inverse, then = once ? 1.f : 0x1p-120f;
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = __fmul_rn(x[j], inverse);
-        uint32_t c = raised(__float_as_uint(__fmul_rn(t, 0x1p-120f)), random[j]);
-        if (POSITIVE && t > 0.f) c = max(c, 1u << 20);
+        uint32_t c = raised(__float_as_uint(__fmul_rn(__fmul_rn(x[j], by), then)), random[j]);
+        if (POSITIVE && scale > 0.f && x[j] > 0.f) c = max(c, 1u << 20);
         w[j] = isfinite(x[j]) ? c : 0x7f00000u;
     }
     return make_uint2(four_codes(w[0], w[1], w[2], w[3]), four_codes(w[4], w[5], w[6], w[7]));
@@ -309,6 +313,14 @@ __device__ __forceinline__ uint32_t hash_of(const Table<CAP>& a, int e, int64_t 
     return x ^ (x >> 16);
 }
 
+// sqrt(beta2 * rr + c2 * xx): as step8 has it, sum and root of 2^66 times as much, wherever that path has a result (sums below
+// fp32's normal numbers would be rounded to other values, and so to other codes, beside a value that is not finite).
+__device__ __forceinline__ float root_any(float rr, float xx, const Scalars8& s) {
+    const float minus = __fadd_rn(__fmul_rn(s.beta2 * kUp, rr), __fmul_rn(s.c2 * kUp, xx));
+    if (minus > -0x1p120f) return root2(make_float2(minus, minus)).x;
+    return __fsqrt_rn(__fadd_rn(__fmul_rn(s.beta2, rr), __fmul_rn(s.c2, xx)));
+}
+
 // A step of a block with whatever values.
 template <bool G32, int CAP>
 __device__ __noinline__ void step_any(const Table<CAP>& a, int e, int64_t block, float factor) {
@@ -327,7 +339,7 @@ __device__ __noinline__ void step_any(const Table<CAP>& a, int e, int64_t block,
     for (int j = 0; j < 8; ++j) {
         const float x = __fmul_rn(g[j], factor);
         m[j] = __fadd_rn(__fmul_rn(s.beta1, m[j]), __fmul_rn(s.c1, x));
-        r[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(r[j], r[j])), __fmul_rn(s.c2, __fmul_rn(x, x))));
+        r[j] = root_any(__fmul_rn(r[j], r[j]), __fmul_rn(x, x), s);
         p[j] = fmaf(-s.step_size, __fmul_rn(m[j], reciprocal(fmaf(r[j], s.inv_root, s.eps))), __fmul_rn(p[j], s.decay));
         uint32_t h = (hash ^ (uint32_t)(32 * j)) * 0x85ebca6bu;
         h = (h ^ (h >> 13)) * 0xc2b2ae35u;

@@ -583,3 +583,41 @@ def test_a_root_of_zero_has_the_code_of_zero(shift):
     none = a.grad[0] == 0
     assert not bool(a.v[0][none].any()) and not bool((a.m[0][none] & 0x7f).any())
     assert bool((a.v[0][~none] > 0).all()) and bool((a.v[0] < 0x80).all())
+
+
+@pytest.mark.parametrize("beta2", [0.0, 0.3, 0.95])
+def test_a_block_beside_a_value_that_is_not_finite_keeps_its_bits(beta2):
+    """A block with an infinity or NaN takes another path, with the library's root: its other elements have the same bits, for
+    gradients of every exponent whose squares are not zero, 2^23 - 2^15 significands of each, squares below fp32's normal
+    numbers among them."""
+    n = 1 << 23
+    hp = dict(lr=1.0, beta1=0.0, beta2=beta2, eps=0.0, weight_decay=0.0)
+    significands = 1 + torch.arange(n, device="cuda", dtype=torch.float64) / n
+    for e in range(-74, 14):
+        runs = []
+        for special in (0.0, float("inf")):
+            grad = (significands * 2.0 ** e).float()
+            grad[::256] = special
+            (m, ms), (v, vs) = zs.state_zeros(n), zs.state_zeros(n)
+            master = torch.zeros(n, device="cuda")
+            zs.zs_adamw_tensors(zs.TensorList([grad], [master], [m], [v], m_scales=[ms], v_scales=[vs]), hp, 1, seed=e & 0xff)
+            runs.append([x.view(torch.uint8).view(n // 256, -1) for x in (master, m, v, ms, vs)])
+        for name, x, y, skip in zip(("master", "m", "v", "m's scales", "v's scales"), *runs, (4, 1, 1, 0, 0)):
+            assert torch.equal(x[:, skip:], y[:, skip:]), (name, e)
+
+
+def test_small_codes_beside_a_value_that_is_not_finite():
+    """Blocks whose magnitudes span 2^20, so that many codes are subnormal: the same bits with and without an infinity."""
+    n = 1 << 26
+    hp = dict(lr=1.0, beta1=0.0, beta2=0.0, eps=0.0, weight_decay=0.0)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for seed in range(6):
+        small = torch.exp2(-20 * torch.rand(n, generator=gen, device="cuda")) * 2.0 ** (4 * seed - 12)
+        runs = []
+        for special in (0.0, float("inf")):
+            grad = small.clone()
+            grad[::256] = special
+            (m, ms), (v, vs) = zs.state_zeros(n), zs.state_zeros(n)
+            zs.zs_adamw_tensors(zs.TensorList([grad], [torch.zeros(n, device="cuda")], [m], [v], m_scales=[ms], v_scales=[vs]), hp, 1, seed=seed)
+            runs.append([m.view(torch.uint8).view(-1, 256)[:, 1:], v.view(torch.uint8).view(-1, 256)[:, 1:], ms, vs])
+        assert [int((x != y).sum()) for x, y in zip(*runs)] == [0, 0, 0, 0]
