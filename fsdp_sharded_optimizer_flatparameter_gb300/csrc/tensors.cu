@@ -128,13 +128,16 @@ __device__ __forceinline__ Random random_bits(uint32_t x) {          // x: the h
 // that code: with 16 random bits added there (at most 2^20 - 16: a largest magnitude that rounding took a little past
 // 448 does not reach the next) the code is that of the lower neighbour or of the upper.
 __device__ __forceinline__ uint32_t raised(uint32_t bits, uint32_t random16) { return bits + (random16 << 4); }
-// Four codes in the order of their elements: bits 20 to 26, and the sign from bit 31.
+// Four codes in the order of their elements: bits 20 to 26, and m's sign from bit 31 (a root has none, though root2 gives -0 for 0).
+template <bool SIGN>
 __device__ __forceinline__ uint32_t two_codes(uint32_t a, uint32_t b) {          // at bits 8 to 15 and 24 to 31
     const uint32_t w = __byte_perm(a, b, 0x7632);
-    return ((w << 4) & 0x7fff7fffu) | (w & 0x80008000u);
+    return ((w << 4) & 0x7fff7fffu) | (SIGN ? w & 0x80008000u : 0u);
 }
-__device__ __forceinline__ uint32_t four_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    return __byte_perm(two_codes(a, b), two_codes(c, d), 0x7531);
+template <bool SIGN>
+__device__ __forceinline__ uint2 eight_codes(const uint32_t (&w)[8]) {
+    return make_uint2(__byte_perm(two_codes<SIGN>(w[0], w[1]), two_codes<SIGN>(w[2], w[3]), 0x7531),
+                      __byte_perm(two_codes<SIGN>(w[4], w[5]), two_codes<SIGN>(w[6], w[7]), 0x7531));
 }
 
 // a + b, each sum rounded once, in a form that is not contracted with the products that a and b are (as mul.rn.f32x2 and
@@ -144,14 +147,13 @@ __device__ __forceinline__ float2 sum2(float2 a, float one, float2 b) { return q
 // Square root rounded to nearest, given -2^66 y: from the hardware's reciprocal root one correction by the residual
 // y - s^2, which fused multiplication gives exactly (P. Markstein, 1990).  Compared with __fsqrt_rn for every y of
 // [2^-168, 2^54): equal; below, where the residual loses bits, 25 of the 2^26 values down to 2^-176 differ.
-// 2^66 y has a normal root for every y > 0, and the result is exact to scale back; 0 is added to it so that y = 0 gives 0
-// and not -0, whose sign would be kept in the code.
+// 2^66 y has a normal root for every y > 0, and the result is exact to scale back; y = 0 gives -0.
 __device__ __forceinline__ float2 root2(float2 minus) {
     float2 q;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(fmaxf(-minus.x, 0x1p-126f)));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(fmaxf(-minus.y, 0x1p-126f)));
     const float2 s = q8_mul2(minus, q), h = q8_mul2(q, make_float2(0.5f, 0.5f));         // s: minus the root
-    return q8_fma2(q8_fma2(q8_fma2(s, s, minus), h, s), make_float2(-0x1p-33f, -0x1p-33f), make_float2(0.f, 0.f));
+    return q8_mul2(q8_fma2(q8_fma2(s, s, minus), h, s), make_float2(-0x1p-33f, -0x1p-33f));
 }
 
 // max(top, |x.x|, |x.y|), NaN if one is.
@@ -233,14 +235,14 @@ __device__ __forceinline__ bool step8(const float2 (&g)[4], float2 (&p)[4], Code
             wr[2 * k + h] = max(raised(__float_as_uint(h ? tr.y : tr.x), random.r), min(__float_as_uint(h ? r[k].y : r[k].x), least));
         }
     }
-    c.m = make_uint2(four_codes(wm[0], wm[1], wm[2], wm[3]), four_codes(wm[4], wm[5], wm[6], wm[7]));
-    c.v = make_uint2(four_codes(wr[0], wr[1], wr[2], wr[3]), four_codes(wr[4], wr[5], wr[6], wr[7]));
+    c.m = eight_codes<true>(wm);
+    c.v = eight_codes<false>(wr);
     return true;
 }
 
 // A state's values in 8 bits, whatever they are: infinities and NaN have the code NaN and leave the scale alone.
 template <bool POSITIVE>
-__device__ uint2 encode8_any(const float (&x)[8], const uint32_t (&random)[8], float& scale) {
+__device__ __forceinline__ uint2 encode8_any(const float (&x)[8], uint32_t hash, float& scale) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -254,11 +256,14 @@ __device__ uint2 encode8_any(const float (&x)[8], const uint32_t (&random)[8], f
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        uint32_t c = raised(__float_as_uint(__fmul_rn(__fmul_rn(x[j], by), then)), random[j]);
+        uint32_t h = (hash ^ (uint32_t)(32 * j)) * 0x85ebca6bu;
+        h = (h ^ (h >> 13)) * 0xc2b2ae35u;
+        const Random random = random_bits(h);
+        uint32_t c = raised(__float_as_uint(__fmul_rn(__fmul_rn(x[j], by), then)), POSITIVE ? random.r : random.m);
         if (POSITIVE && scale > 0.f && x[j] > 0.f) c = max(c, 1u << 20);
         w[j] = isfinite(x[j]) ? c : 0x7f00000u;
     }
-    return make_uint2(four_codes(w[0], w[1], w[2], w[3]), four_codes(w[4], w[5], w[6], w[7]));
+    return eight_codes<!POSITIVE>(w);
 }
 // A block of any size at any address: lane l has elements l, l + 32, .. of it, so that unaligned arrays too are read and
 // written line by line.
@@ -328,7 +333,6 @@ __device__ __noinline__ void step_any(const Table<CAP>& a, int e, int64_t block,
     const Scalars8 s = scalars8(a, a.t[e]);
     const uint32_t hash = hash_of(a, e, at.begin);
     float g[8], p[8], m[8], r[8];
-    uint32_t random_m[8], random_r[8];
     Codes8 c;
     at.load(g, p, c, block);
     q8_unpack4(c.m.x, c.ms, m);
@@ -341,14 +345,9 @@ __device__ __noinline__ void step_any(const Table<CAP>& a, int e, int64_t block,
         m[j] = __fadd_rn(__fmul_rn(s.beta1, m[j]), __fmul_rn(s.c1, x));
         r[j] = root_any(__fmul_rn(r[j], r[j]), __fmul_rn(x, x), s);
         p[j] = fmaf(-s.step_size, __fmul_rn(m[j], reciprocal(fmaf(r[j], s.inv_root, s.eps))), __fmul_rn(p[j], s.decay));
-        uint32_t h = (hash ^ (uint32_t)(32 * j)) * 0x85ebca6bu;
-        h = (h ^ (h >> 13)) * 0xc2b2ae35u;
-        const Random random = random_bits(h);
-        random_m[j] = random.m;
-        random_r[j] = random.r;
     }
-    c.m = encode8_any<false>(m, random_m, c.ms);
-    c.v = encode8_any<true>(r, random_r, c.vs);
+    c.m = encode8_any<false>(m, hash, c.ms);
+    c.v = encode8_any<true>(r, hash, c.vs);
     at.store(p, c, block);
 }
 
