@@ -621,3 +621,38 @@ def test_small_codes_beside_a_value_that_is_not_finite():
             zs.zs_adamw_tensors(zs.TensorList([grad], [torch.zeros(n, device="cuda")], [m], [v], m_scales=[ms], v_scales=[vs]), hp, 1, seed=seed)
             runs.append([m.view(torch.uint8).view(-1, 256)[:, 1:], v.view(torch.uint8).view(-1, 256)[:, 1:], ms, vs])
         assert [int((x != y).sum()) for x, y in zip(*runs)] == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_a_step_that_gives_up_has_stepped_a_block_or_left_it(bits, shift):
+    """A limit of 0 is reported; at any limit a block's arrays are all as before the step or all as after it.  Tensors of 19
+    tiles and a part: some CTAs begin with a tile that the warps read themselves, while the next one arrives."""
+    sizes = [20 * 2048 - 256] * 448
+    blocks = lambda a, k: torch.cat([x.view(len(x) // 256 if len(x) > 200 else len(x), -1) for x in getattr(a, k)])  # noqa: E731
+    names = ["master", "param", "m", "v"] + (["ms", "vs"] if bits == 8 else [])
+    a = Arrays(sizes, bits, shift=shift, seed=3)
+    kept = {k: b.clone() for k, (b, _) in a.bufs.items()}
+    left = [blocks(a, k) for k in names]
+    zs.zs_adamw_tensors(a.list(), HP, 2, seed=2)
+    stepped = [blocks(a, k) for k in names]
+    assert bool((left[0] != stepped[0]).any(1).all())
+    try:
+        for limit in (0,) * 12 + (1, 100, 1000, 3000, 10000, 30000) * 2:
+            for k, (b, _) in a.bufs.items():
+                b.copy_(kept[k])
+            ts = a.list()
+            torch.cuda.synchronize()
+            zs.zs_set_q8_wait_limit(limit)
+            zs.zs_adamw_tensors(ts, HP, 2, seed=2)
+            torch.cuda.synchronize()
+            code = zs.zs_device_status(clear=True)
+            assert code in ((zs.ZS_DEVERR_TENSORS_WAIT,) if limit == 0 else (zs.ZS_DEVERR_NONE, zs.ZS_DEVERR_TENSORS_WAIT))
+            now = [blocks(a, k) for k in names]
+            new, old = ([(x == y).all(1) for x, y in zip(now, ref)] for ref in (stepped, left))
+            new, old = torch.stack(new).all(0), torch.stack(old).all(0)
+            assert bool((new | old).all()), "%d of %d blocks in part, limit %d" % (int((~(new | old)).sum()), len(new), limit)
+            assert code != zs.ZS_DEVERR_NONE or bool(new.all())
+            a.assert_untouched_outside()
+    finally:
+        zs.zs_set_q8_wait_limit()
