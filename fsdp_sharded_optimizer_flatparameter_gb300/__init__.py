@@ -1075,10 +1075,13 @@ def _list_here(tensors):
     return dev
 
 
-def zs_adamw_tensors(tensors, hp, step, factor=None, seed=0, stream=None):
+def zs_adamw_tensors(tensors, hp, step, factor=None, seed=None, stream=None):
     """One AdamW step on a TensorList.  factor: one fp32 value on the GPU that multiplies the gradients (NaN: no step
-    is taken); seed: of the 8-bit states' roundings (32 bits of it count), another one for every step."""
+    is taken); seed: of the 8-bit states' roundings (32 bits of it count), another one for every step (None: the step's
+    number).  A captured call repeats its step and seed at every replay, and with the seed its roundings, which then do not
+    average out: with states in 8 bits the step belongs behind the graph."""
     dev = _list_here(tensors)
+    seed = step if seed is None else seed
     return _check(_lib.zs_adamw_tensors(tensors._array, len(tensors), tensors.grad_bytes, tensors.state_bits, ctypes.byref(_hp(hp)), int(step),
                                         _vector(factor, 1, _F32, "factor", dev), int(seed) & 0xffffffff, _here(stream, dev)))
 

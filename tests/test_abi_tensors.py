@@ -135,3 +135,18 @@ def test_a_list_refuses_an_array_twice():
         zs.TensorList(**a)
     a["master"] = [_At(300, dtype=F32) for _ in "ab"]
     assert len(zs.TensorList(**a)) == 2                        # gradients are only read
+
+
+def test_the_seed_is_the_steps_number_where_none_is_given(monkeypatch):
+    class Library:
+        def zs_adamw_tensors(self, *args):
+            seen.append((args[5], args[7]))
+            return 0
+    seen = []
+    ts = zs.TensorList(**_arrays())
+    monkeypatch.setattr(zs, "_lib", Library())
+    monkeypatch.setattr(zs, "_device", lambda: 0)
+    monkeypatch.setattr(zs, "_here", lambda stream, dev: 7)
+    for step, kw in ((1, {}), (2, {}), ((1 << 32) + 3, {}), (4, dict(seed=0)), (5, dict(seed=9)), (6, dict(seed=(1 << 32) + 5))):
+        zs.zs_adamw_tensors(ts, HP, step, **kw)
+    assert seen == [(1, 1), (2, 2), ((1 << 32) + 3, 3), (4, 0), (5, 9), (6, 5)]
