@@ -863,6 +863,9 @@ typedef struct {
  *               zs_grad_norm, a loss scale's inverse), NULL: 1.  NaN: nothing is written,
  *               the step is left out.
  *   seed        of the 8-bit states' roundings.
+ * step and seed are the launch's: a captured call repeats them at every replay, with states in 8
+ * bits the roundings too, which then do not average out (an element whose random bits are low
+ * stands still).  Such a step belongs behind the graph.
  * Arrays are aligned to their elements.  Where master and 32-bit states start at multiples of 32
  * bytes and grad, param and codes of 16, eight elements are moved per access; arrays elsewhere
  * (views into flat buffers at any element) go through shared memory element by element.  The same
@@ -877,7 +880,8 @@ int zs_adamw_tensors(const zs_tensor* tensors, int32_t n_tensors, int32_t grad_b
  * squares of small gradients are rounded to multiples of 2^-149 (those of |grad| below
  * 2^-75 to 0): out[0]^2 is off by 2^-150 for each at most, besides the relative
  * roundings.  A norm that is not finite gives out[1] = NaN.  Only n and grad of the
- * tensors are used.
+ * tensors are used.  Gradients of two types are two lists, and the norm of both is the
+ * caller's to form from the two.
  *   partials    caller's scratch, n_partials >= 2 floats, two per partial sum; at most 8
  *               per SM are used (1216), fewer make the call slower.
  *   out         two floats. */

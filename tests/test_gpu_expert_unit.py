@@ -197,3 +197,43 @@ def test_first_calls_of_a_process_may_be_captured():
     from conftest import ROOT
     got = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, cwd=ROOT, timeout=300, env=dict(os.environ, PYTHONPATH=ROOT))
     assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
+
+
+def test_steps_behind_a_captured_pass():
+    """Forward and backward as a graph, the step called behind each replay with its own number and seed: training's bits."""
+    shape = (200, 2, 6, 256, 128)
+    inputs = _inputs(*shape[:4], dropped=0.1)
+    unit = example_expert_unit.ExpertUnit(*shape)
+    for t in range(1, 6):
+        _step(unit, inputs, t)
+    want = _state(unit)
+    unit = example_expert_unit.ExpertUnit(*shape)
+    x, ids, weights, dout = inputs
+    _step(unit, inputs, 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        unit.forward(x, ids, weights)
+        unit.backward(dout, weights)
+    for t in range(2, 6):
+        graph.replay()
+        unit.step(t)
+    assert all(torch.equal(a, b) for a, b in zip(_state(unit), want))
+
+
+def test_a_captured_step_repeats_its_number_and_its_seed():
+    shape = (200, 2, 6, 256, 128)
+    inputs = _inputs(*shape[:4], dropped=0.1)
+    states = []
+    for captured in (False, True):
+        unit = example_expert_unit.ExpertUnit(*shape)
+        _step(unit, inputs, 1)
+        torch.cuda.synchronize()
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                _step(unit, inputs, 2)
+        for _ in range(3):
+            graph.replay() if captured else _step(unit, inputs, 2)
+        states.append(_state(unit))
+    assert all(torch.equal(a, b) for a, b in zip(*states))
