@@ -1247,9 +1247,10 @@ int pair_width(int64_t tp, int64_t rows_q, double kblocks, bool lines, int wides
     return best;
 }
 
-// Rows of an expert, on average, up to which they are the narrow operand.  Microseconds as such and as P for 16, 64, 96 and
-// 128 rows each: 16 experts of 2048 x 4096 29 31 35 38 and 34 35 35 36; 64 of 2048 x 2048 48 54 57 62 and 58 59 62 65;
-// 8 of 5504 x 2048 23 24 25 28 and 25 25 25 27.
+// Rows of out for an expert, on average, up to which they are the narrow operand: the caller's matrix decides, as the rows in
+// use are known on the device only (with align 128 it has more, and so few tokens run as P there).  Microseconds as such and
+// as P for 16, 64, 96 and 128 rows each, align 1: 16 experts of 2048 x 4096 29 31 35 38 and 34 35 35 36; 64 of 2048 x 2048
+// 48 54 57 62 and 58 59 62 65; 8 of 5504 x 2048 23 24 25 28 and 25 25 25 27.
 constexpr int kFewAverage = 96;
 
 // The products of groups, in the width of least time for groups of equal size (their sizes are on the device).
@@ -1258,7 +1259,7 @@ cudaError_t launch_mm_groups(const Q8& p, const Q8& q, int64_t k, MmArgs& a, int
     const bool lines = ((p.ld | q.ld) & 127) == 0;
     const int64_t n = a.n_groups;
     const bool room256 = GROUPS != kRowGroups || PairShape<256>::kSmem + PairShape<256>::table(a.n_groups) <= PairShape<256>::kSmemMost;
-    const int64_t tp = GROUPS == kRowGroups ? n * ((a.rows_p / n + 255) / 256 + (a.rows_p < n)) : n * (((int64_t)a.rows_p + 255) / 256);
+    const int64_t tp = GROUPS == kRowGroups ? n * ((a.rows_p / n + 255) / 256) : n * (((int64_t)a.rows_p + 255) / 256);
     switch (pair_width(tp, rows_q, GROUPS == kRowGroups ? a.kblocks : (double)a.kblocks / n, lines, room256 ? 256 : 224)) {
         case 256: return launch_mm_pair<256, GROUPS>(p, q, k, a, st);
         case 224: return launch_mm_pair<224, GROUPS>(p, q, k, a, st);
