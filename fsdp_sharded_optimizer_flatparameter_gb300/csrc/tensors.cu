@@ -419,7 +419,7 @@ __device__ __noinline__ void step_strided32(const Table<CAP>& a, int e, int64_t 
 // other addresses come as the 16-byte chunks that cover the tile, each with its own offset, and go back by bulk copies too
 // (step_shifted), where those chunks lie inside the tensor.  Of any other tile - a tensor's last, and its first where the
 // arrays are shifted - only the place is passed on, and the warps read its blocks themselves.  402 M elements with states in
-// 8 bits: 969 us (6.46 GB, 950 at the copy rate); 139 M in 32 bits 549 (558).  All arrays three elements off: 59 % and 85 %
+// 8 bits: 932 us (6.46 GB, 950 at the copy rate); 139 M in 32 bits 551 (558).  All arrays three elements off: 60 % and 84 %
 // of the copy rate, bound by the single-element accesses to shared memory; 34 % and 58 % before, with global ones.
 template <bool G32, bool Q>
 struct Ring8 {
@@ -572,7 +572,7 @@ __device__ __noinline__ bool step_shifted(const Table<CAP>& a, int e, int64_t bl
 }
 
 // SHIFTS: some tensor of the list has arrays with offsets.  (With that path in it, though it is never taken, the kernel for
-// others keeps fewer values in registers: 402 M elements in 8 bits 1186 us for 1110.)
+// others keeps fewer values in registers: 402 M elements in 8 bits, the norm before it, 1131 us for 1074.)
 template <bool G32, bool Q, bool SHIFTS, int CAP>
 __global__ void __launch_bounds__(kStepThreads, kStepCtas) k_adamw_tensors(const __grid_constant__ Table<CAP> a) {
     using R = Ring8<G32, Q>;
@@ -914,8 +914,8 @@ cudaError_t by_table(const zs_tensor* tensors, int count, int state_bits, uint32
 
 
 // Tiles of a CTA, at most.  CTAs that end and are replaced take the work as the SMs get through it, which a fixed share for
-// each does not (402 M elements with states in 8 bits, the norm before it: 1266 us in fixed shares; 1165, 1110, 1123 with
-// 4, 8 and 16 tiles.  139 M with states in 32 bits: 614; 546, 557, 573 with 2, 4 and 8).
+// each does not (402 M elements with states in 8 bits, the norm before it: 1121, 1074, 1087 us with 4, 8 and 16 tiles, and
+// about 150 more in fixed shares.  139 M with states in 32 bits: 549, 551, 574 with 2, 3 and 8, and 65 more).
 constexpr uint32_t kRun8 = 8, kRun32 = 3;
 
 template <bool G32, bool Q, bool SHIFTS, int CAP>
